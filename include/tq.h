@@ -64,6 +64,7 @@ typedef enum tq_status {
 #define TQ_DEVERR_BAD_ID 1u      /* an expert id outside [0, experts) */
 #define TQ_DEVERR_TIMEOUT 2u     /* a bounded spin-wait gave up */
 #define TQ_DEVERR_BAD_BOOK 4u    /* a ternary codebook that is not {c0, c0+d, c0+2d} */
+#define TQ_DEVERR_BAD_PAGE 8u    /* a cache slot, page id or sequence length out of range */
 
 typedef enum tq_dtype { TQ_F32 = 0, TQ_BF16 = 1, TQ_F16 = 2 } tq_dtype;
 
@@ -400,6 +401,130 @@ tq_status tq_kv_attend_noalloc(const void* q, tq_dtype qdt, int32_t Hq, int32_t 
                                const uint16_t* kscales, const uint32_t* vcodes, const uint16_t* vscales, float* o,
                                void* stream);
 size_t tq_kv_attend_noalloc_max_scratch_bytes(void);
+
+/* ------------------------------------------------------------------ rotary positions */
+
+/* Rotary positions (Su et al. 2021).  The first `rotary` elements of a head
+ * vector form rotary/2 pairs; pair i of a token at position p turns by the angle
+ * p * w_i: y_a = f (a cos - b sin), y_b = f (a sin + b cos).  Elements past
+ * `rotary` are copied.  layout TQ_ROPE_HALF pairs element i with i + rotary/2,
+ * TQ_ROPE_INTERLEAVED elements 2i and 2i + 1.
+ * steps: device uint64[rotary/2], w_i as a fraction of a turn times 2^64.  The
+ * product with a position is taken mod 2^64, so whole turns drop out exactly and
+ * the angle is as accurate at position 2^30 as at 1. */
+typedef enum tq_rope_layout { TQ_ROPE_HALF = 0, TQ_ROPE_INTERLEAVED = 1 } tq_rope_layout;
+typedef struct tq_rope_t {
+    int32_t dim;     /* elements of a head vector */
+    int32_t rotary;  /* rotated leading elements: even, 2 .. dim */
+    int32_t layout;  /* tq_rope_layout */
+    float factor;    /* f above: 1, or the long-context factor of tq_rope_steps */
+    const uint64_t* steps;
+} tq_rope_t;
+
+/* Scaling of the frequencies for contexts longer than `original` positions.
+ * LINEAR: every w_i divided by `factor`.  BASE: the base raised to base *
+ * factor^(rotary / (rotary - 2)), which leaves the fastest pair alone and divides
+ * the slowest one's w by `factor`.  PARTS (YaRN, Peng et al. 2023): with r = the
+ * turns of pair i over `original` positions, w_i keeps its value where r >=
+ * fast_turns, is divided by `factor` where r <= slow_turns, and is a linear blend
+ * between; the factor on the elements is 0.1 ln(factor) + 1. */
+typedef enum tq_rope_scaling_kind {
+    TQ_ROPE_NONE = 0, TQ_ROPE_LINEAR = 1, TQ_ROPE_BASE = 2, TQ_ROPE_PARTS = 3
+} tq_rope_scaling_kind;
+typedef struct tq_rope_scaling_t {
+    int32_t kind;
+    double factor;                 /* >= 1 */
+    double original;               /* PARTS: positions the model was trained on, > 0 */
+    double slow_turns, fast_turns; /* PARTS: 0 <= slow_turns < fast_turns (1 and 32 are usual) */
+} tq_rope_scaling_t;
+
+/* Host: steps[rotary/2] (host uint64) of w_i = base^(-2i/rotary), scaled (scaling
+ * NULL: not), and the factor on the rotated elements (factor may be NULL).
+ * TQ_ERR_INVALID: rotary odd or < 2, base <= 1, or a scaling out of range. */
+tq_status tq_rope_steps(int32_t rotary, double base, const tq_rope_scaling_t* scaling, uint64_t* steps, float* factor);
+
+/* Rotary positions of the query heads and, in the same launch, the key heads of
+ * `tokens` tokens.  q: device [tokens][Hq][dim] of dt (f32, bf16 or f16), tokens
+ * q_stride elements apart (>= Hq*dim), heads dim apart; k: the same with Hkv and
+ * k_stride, or NULL with Hkv = 0.  yq, yk: as q and k with their own strides;
+ * yq == q (with the same stride) works in place, any other overlap does not.
+ * positions: device int32 [tokens] (any value; negative ones turn backwards).
+ * inverse != 0 turns by -p w_i (the transpose of the same rotation, times f).
+ * Angles and products are in fp32; results are rounded once to dt. */
+tq_status tq_rope(const tq_rope_t* rope, const int32_t* positions, int64_t tokens, tq_dtype dt, int32_t inverse,
+                  const void* q, int64_t q_stride, int32_t Hq, void* yq, int64_t yq_stride,
+                  const void* k, int64_t k_stride, int32_t Hkv, void* yk, int64_t yk_stride, void* stream);
+
+/* ------------------------------------------------------------------ paged compressed KV cache */
+
+/* A compressed KV cache in pages.  "How it works", "The KV cache" and "Running a
+ * 1T-Parameter Model on a Laptop", update_and_fetch: vectors are rotated,
+ * scaled by group and snapped as tq_kv_quantize does; here the tokens of many
+ * sequences share one pool of pages.  Page p holds `page` consecutive tokens of
+ * one sequence for every kv head; the cache row of token slot p*page + i and head
+ * h is p*page_stride + h*head_stride + i, and row r has its codes at kcodes +
+ * r*tq_row_words(kcb.levels, D) and its scales at kscales + r*(D/group), the same
+ * for v.  A pool [pages][Hkv][page] has page_stride = Hkv*page and head_stride =
+ * page; a contiguous cache of tq_kv_quantize has page_stride = page and
+ * head_stride = capacity.
+ * D: 128.  page: 16, 32, 64, 128 or 256.  kcb.levels: 16 or 256, vcb.levels: 8 or
+ * 16.  group: 16, 32, 64 or 128.  Strides: multiples of 16 rows.  The four arrays
+ * start 16-byte aligned. */
+typedef struct tq_kv_pages_t {
+    uint32_t* kcodes;
+    uint16_t* kscales;
+    uint32_t* vcodes;
+    uint16_t* vscales;
+    int32_t Hkv, D, group, page;
+    int64_t pages, page_stride, head_stride;
+    tq_codebook_t kcb, vcb;
+    tq_rotation_t rot; /* dim = block = D */
+} tq_kv_pages_t;
+
+/* Writes T tokens to their slots: [rope k,] rotate, group RMS, snap, pack.
+ * k, v: device [T][Hkv][D] of dt (f32 or bf16), tokens k_stride / v_stride
+ * elements apart (a multiple of 16 bytes; 16-byte aligned).  slots: device int32
+ * [T]; a negative slot is skipped (a rejected draft), one past the pool too, with
+ * TQ_DEVERR_BAD_PAGE.  Two tokens with one slot leave either's row, or a mixture.
+ * rope: rotary positions of k on the way (NULL: none; positions: device int32
+ * [T]); TQ_ERR_UNSUPPORTED unless rotary is 32, 64 or 128.  The rotated keys are
+ * not rounded to dt between the two rotations. */
+tq_status tq_kv_append(const tq_kv_pages_t* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       tq_dtype dt, int64_t T, const int32_t* slots, const tq_rope_t* rope, const int32_t* positions,
+                       uint32_t* err, void* stream);
+
+/* Reads T tokens back: unpack, scale, rotate back ("update_and_fetch": the cache
+ * is dequantized and de-rotated).  slots: device int32 [T]; a negative slot (and,
+ * with TQ_DEVERR_BAD_PAGE, one past the pool) gives zeros.  k, v: device [T][Hkv][D]
+ * of dt (f32, bf16 or f16), 16-byte aligned; either may be NULL. */
+tq_status tq_kv_fetch(const tq_kv_pages_t* cache, const int32_t* slots, int64_t T, void* k, void* v, tq_dtype dt,
+                      uint32_t* err, void* stream);
+
+/* Attention of B trees of up to n drafted tokens each over the compressed context
+ * of their sequences and over the drafted tokens themselves.
+ * Row (b, i, h) sees the first lens[b] tokens of sequence b, whose pages are
+ * table[b*table_stride + 0, 1, ...], and the drafted tokens j whose bit is set:
+ * bit j%64 of mask[(b*n + i)*ceil(n/64) + j/64] (mask NULL: j <= i, a chain).
+ *   o[b, i, h] = sum_t p_t v_t,  p = softmax(scale * q . k),  kv head h / (Hq/Hkv)
+ * A row that sees nothing gives zeros; so do rows i >= n_tok[b] (n_tok NULL: all n
+ * are in use).  What a row does not see never reaches it, whatever it holds.
+ * q: device bf16 [B][n][Hq][D], token (b, i) at (b*n + i)*q_stride; k_new, v_new:
+ * the drafted tokens' own keys and values, bf16 [B][n][Hkv][D] with strides (keys
+ * with their positions, not rotated by cache->rot); both NULL: only the context is
+ * seen.  Strides are multiples of 8 elements, pointers 16-byte aligned.  dt: BF16.
+ * lens: device int32 [B]; max_len: a host bound on them, <= table_stride*page.  A
+ * length outside [0, max_len], or a page id outside the pool among those a length
+ * reaches, sets TQ_DEVERR_BAD_PAGE; the length is clamped, the page's tokens are
+ * left out.  Entries of table past a sequence's pages are not read.
+ * o: device bf16 [B][n][Hq][D].  Cached keys, values and their weights are fp16
+ * tensor-core operands; scores, softmax statistics and sums are fp32.  ws: 16-byte
+ * aligned device scratch of tq_kv_attend_tree_workspace_bytes(...) bytes. */
+tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q, int64_t q_stride, tq_dtype dt, int32_t B,
+                            int32_t n, int32_t Hq, const int32_t* table, int32_t table_stride, const int32_t* lens,
+                            int64_t max_len, const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                            const uint64_t* mask, const int32_t* n_tok, float scale, void* o, void* ws,
+                            size_t ws_bytes, uint32_t* err, void* stream);
+size_t tq_kv_attend_tree_workspace_bytes(const tq_kv_pages_t* cache, int32_t B, int32_t n, int32_t Hq, int64_t max_len);
 
 /* ------------------------------------------------------------------ fused decode layer */
 

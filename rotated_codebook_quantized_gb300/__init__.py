@@ -18,7 +18,9 @@ LIB_PATH = os.path.join(_PKG, "libtq.so")
 
 TQ_F32, TQ_BF16, TQ_F16 = 0, 1, 2
 TQ_OK, TQ_ERR_INVALID, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA, TQ_ERR_TIMEOUT, TQ_ERR_DEVICE = range(6)
-TQ_DEVERR_BAD_ID, TQ_DEVERR_TIMEOUT, TQ_DEVERR_BAD_BOOK = 1, 2, 4
+TQ_DEVERR_BAD_ID, TQ_DEVERR_TIMEOUT, TQ_DEVERR_BAD_BOOK, TQ_DEVERR_BAD_PAGE = 1, 2, 4, 8
+TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
+TQ_ROPE_NONE, TQ_ROPE_LINEAR, TQ_ROPE_BASE, TQ_ROPE_PARTS = range(4)
 
 _c_p = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -39,6 +41,21 @@ class tq_qweight_t(ctypes.Structure):
     _fields_ = [("codes", _c_p), ("scales", _c_p), ("experts", _i32), ("rows", _i32), ("cols", _i32),
                 ("group", _i32), ("row_stride_words", _i64), ("expert_stride_words", _i64),
                 ("expert_stride_scales", _i64), ("cb", tq_codebook_t)]
+
+
+class tq_rope_t(ctypes.Structure):
+    _fields_ = [("dim", _i32), ("rotary", _i32), ("layout", _i32), ("factor", ctypes.c_float), ("steps", _c_p)]
+
+
+class tq_rope_scaling_t(ctypes.Structure):
+    _fields_ = [("kind", _i32), ("factor", ctypes.c_double), ("original", ctypes.c_double),
+                ("slow_turns", ctypes.c_double), ("fast_turns", ctypes.c_double)]
+
+
+class tq_kv_pages_t(ctypes.Structure):
+    _fields_ = [("kcodes", _c_p), ("kscales", _c_p), ("vcodes", _c_p), ("vscales", _c_p), ("Hkv", _i32), ("D", _i32),
+                ("group", _i32), ("page", _i32), ("pages", _i64), ("page_stride", _i64), ("head_stride", _i64),
+                ("kcb", tq_codebook_t), ("vcb", tq_codebook_t), ("rot", tq_rotation_t)]
 
 
 class tq_layer_desc_t(ctypes.Structure):
@@ -94,6 +111,15 @@ _SIGS = {
     "tq_moe_decode_layer_workspace_bytes": (_sz, [_P(tq_qweight_t), _P(tq_qweight_t), _i32]),
     "tq_moe_decode_layer": (_i32, [_P(tq_qweight_t), _P(tq_qweight_t), _P(tq_rotation_t), _P(tq_rotation_t), _c_p,
                                    _c_p, _i32, _i32, _c_p, _i32, _c_p, _sz, _c_p, _c_p]),
+    "tq_rope_steps": (_i32, [_i32, ctypes.c_double, _P(tq_rope_scaling_t), _c_p, _P(ctypes.c_float)]),
+    "tq_rope": (_i32, [_P(tq_rope_t), _c_p, _i64, _i32, _i32, _c_p, _i64, _i32, _c_p, _i64, _c_p, _i64, _i32, _c_p,
+                       _i64, _c_p]),
+    "tq_kv_append": (_i32, [_P(tq_kv_pages_t), _c_p, _i64, _c_p, _i64, _i32, _i64, _c_p, _P(tq_rope_t), _c_p, _c_p,
+                            _c_p]),
+    "tq_kv_fetch": (_i32, [_P(tq_kv_pages_t), _c_p, _i64, _c_p, _c_p, _i32, _c_p, _c_p]),
+    "tq_kv_attend_tree": (_i32, [_P(tq_kv_pages_t), _c_p, _i64, _i32, _i32, _i32, _i32, _c_p, _i32, _c_p, _i64, _c_p,
+                                 _i64, _c_p, _i64, _c_p, _c_p, ctypes.c_float, _c_p, _c_p, _sz, _c_p, _c_p]),
+    "tq_kv_attend_tree_workspace_bytes": (_sz, [_P(tq_kv_pages_t), _i32, _i32, _i32, _i64]),
     "tq_check_error": (_i32, [_c_p, _P(_u32), _c_p]),
     "tq_set_wait_budget": (_i32, [_i64]),
     "tq_rotation_dense": (_i32, [ctypes.c_uint64, _i32, _P(ctypes.c_double)]),
@@ -545,6 +571,234 @@ def kv_attend_noalloc(cache: KVCache, q, ctx: int | None = None):
                                        ctypes.byref(r), ctypes.byref(kb), ctypes.byref(vb), cache.group,
                                        _ptr(cache.kcodes), _ptr(cache.kscales), _ptr(cache.vcodes),
                                        _ptr(cache.vscales), _ptr(o), _stream()), "tq_kv_attend_noalloc")
+    return o
+
+
+# ---------------------------------------------------------------- rotary positions
+
+class Rope:
+    """Rotary positions of heads of length ``dim``: the first ``rotary`` elements (default: all) turn.
+
+    ``layout``: "half" (element i pairs with i + rotary/2) or "interleaved" (2i with 2i + 1).  ``scaling``
+    for long contexts: None or a dict with "kind" ("linear", "base" or "parts"), "factor" and, for
+    parts, "original" (positions) and optionally "slow_turns" / "fast_turns" (1 and 32); see tq_rope_steps
+    in include/tq.h.  ``steps`` (int64 [rotary/2], the phase per position in 2^-64 turns) and ``factor``
+    take the place of ``base`` and ``scaling`` where a model brings frequencies of its own.
+    """
+
+    def __init__(self, dim: int, rotary: int | None = None, base: float = 10000.0, layout: str = "half",
+                 scaling: dict | None = None, steps=None, factor: float | None = None, device="cuda"):
+        torch = _torch()
+        self.dim, self.rotary = int(dim), int(dim if rotary is None else rotary)
+        if layout not in ("half", "interleaved"):
+            raise ValueError(f"layout must be 'half' or 'interleaved', not {layout!r}")
+        self.layout = layout
+        if not 2 <= self.rotary <= self.dim or self.rotary % 2:
+            raise ValueError(f"rotary must be even and between 2 and dim = {self.dim}, not {self.rotary}")
+        if steps is None:
+            host, own = rope_steps(self.rotary, base, scaling)
+            steps, factor = torch.from_numpy(host), own if factor is None else factor
+        elif scaling is not None:
+            raise ValueError("steps are the scaled frequencies: scaling must be None")
+        if steps.dtype != torch.int64 or steps.numel() != self.rotary // 2:
+            raise ValueError(f"steps must be int64 [{self.rotary // 2}]")
+        self.steps = steps.to(device).contiguous()
+        self.factor = 1.0 if factor is None else float(factor)
+
+    def c(self) -> tq_rope_t:
+        return tq_rope_t(self.dim, self.rotary, TQ_ROPE_INTERLEAVED if self.layout == "interleaved" else TQ_ROPE_HALF,
+                         self.factor, self.steps.data_ptr())
+
+
+def rope_steps(rotary: int, base: float = 10000.0, scaling: dict | None = None):
+    """(steps int64 [rotary/2], factor) of scaled rotary frequencies, on the host."""
+    steps = np.zeros(max(rotary // 2, 1), np.int64)
+    factor = ctypes.c_float(1.0)
+    sc = None
+    if scaling is not None:
+        kinds = {"linear": TQ_ROPE_LINEAR, "base": TQ_ROPE_BASE, "parts": TQ_ROPE_PARTS}
+        if scaling.get("kind") not in kinds:
+            raise ValueError(f"scaling kind must be one of {sorted(kinds)}, not {scaling.get('kind')!r}")
+        sc = ctypes.byref(tq_rope_scaling_t(kinds[scaling["kind"]], float(scaling["factor"]),
+                                            float(scaling.get("original", 0.0)), float(scaling.get("slow_turns", 1.0)),
+                                            float(scaling.get("fast_turns", 32.0))))
+    _check(load().tq_rope_steps(rotary, float(base), sc, steps.ctypes.data, ctypes.byref(factor)), "tq_rope_steps")
+    return steps, float(factor.value)
+
+
+def _heads(x, name, dim):
+    """(tokens, heads, token stride) of x [..., heads, dim] whose heads lie one after another."""
+    if not x.is_cuda or x.dim() < 3 or x.shape[-1] != dim:
+        raise ValueError(f"{name} must be a CUDA tensor [..., heads, {dim}]")
+    lead, stride = x.shape[:-2], x.stride()
+    if x.numel() and (stride[-1] != 1 or (x.shape[-2] > 1 and stride[-2] != dim)):
+        raise ValueError(f"{name}'s heads must lie one after another")
+    tokens, step = 1, None
+    for size, st in zip(reversed(lead), reversed(stride[:-2])):
+        if size == 1:
+            continue
+        if step is None:
+            step = st
+        elif st != step * tokens:
+            raise ValueError(f"{name}'s tokens must lie at one stride")
+        tokens *= size
+    return (0 if 0 in lead else tokens), x.shape[-2], (x.shape[-2] * dim if step is None else step)
+
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on {ref.device}")
+
+
+def _ints(t, name, count, dtype=None):
+    torch = _torch()
+    if not t.is_cuda or t.dtype != (dtype or torch.int32) or not t.is_contiguous() or t.numel() != count:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {count} {dtype or torch.int32}")
+    return t
+
+
+def rope(q, positions, r: Rope, k=None, inverse: bool = False, inplace: bool = False):
+    """Rotary positions of q [..., Hq, dim] and, in the same launch, k [..., Hkv, dim] (views of a fused
+    projection are fine); positions: int32 with one entry per token.  Returns q's result, or (q's, k's)."""
+    torch = _torch()
+    T, hq, qs = _heads(q, "q", r.dim)
+    _ints(positions, "positions", T)
+    _same_device(q, positions=positions, k=k, steps=r.steps)
+    yq, yqs = (q, qs) if inplace else (torch.empty(q.shape, dtype=q.dtype, device=q.device), hq * r.dim)
+    yk, hk, ks, yks = None, 0, 0, 0
+    if k is not None:
+        Tk, hk, ks = _heads(k, "k", r.dim)
+        if Tk != T or k.dtype != q.dtype:
+            raise ValueError("k must have q's tokens and dtype")
+        yk, yks = (k, ks) if inplace else (torch.empty(k.shape, dtype=k.dtype, device=k.device), hk * r.dim)
+    c = r.c()
+    _check(load().tq_rope(ctypes.byref(c), _ptr(positions), T, _dt(q), int(inverse), _ptr(q), qs, hq, _ptr(yq), yqs,
+                          _ptr(k), ks, hk, _ptr(yk), yks, _stream()), "tq_rope")
+    return yq if k is None else (yq, yk)
+
+
+# ---------------------------------------------------------------- paged compressed KV cache
+
+class PagedKVCache:
+    """A compressed KV cache in pages shared by many sequences: codes and fp16 scales [pages, heads, page, ...].
+
+    ``page`` tokens to a page; a token's slot is page id * page + offset.  Which pages a sequence owns is
+    the caller's table.  ``storage``: (kcodes, kscales, vcodes, vscales) tensors to use instead of new ones.
+    """
+
+    def __init__(self, pages: int, page: int, heads: int, dim: int, group: int, kcb: Codebook, vcb: Codebook,
+                 rot: Rotation, device="cuda", storage=None):
+        torch = _torch()
+        self.pages, self.page, self.heads, self.dim, self.group = int(pages), int(page), int(heads), int(dim), int(group)
+        self.kcb, self.vcb, self.rot = kcb, vcb, rot
+        self.kw, self.vw = row_words(kcb.levels, dim), row_words(vcb.levels, dim)
+        self.page_stride, self.head_stride = self.heads * self.page, self.page
+        lead = (self.pages, self.heads, self.page)
+        if storage is None:
+            self.kcodes = torch.zeros((*lead, self.kw), dtype=torch.int32, device=device)
+            self.vcodes = torch.zeros((*lead, self.vw), dtype=torch.int32, device=device)
+            self.kscales = torch.zeros((*lead, dim // group), dtype=torch.int16, device=device)
+            self.vscales = torch.zeros((*lead, dim // group), dtype=torch.int16, device=device)
+        else:
+            self.kcodes, self.kscales, self.vcodes, self.vscales = storage
+            for t, width, size in ((self.kcodes, self.kw, 4), (self.kscales, dim // group, 2), (self.vcodes, self.vw, 4),
+                                   (self.vscales, dim // group, 2)):
+                if tuple(_contig(t, "storage").shape) != (*lead, width) or t.element_size() != size:
+                    raise ValueError(f"storage must be contiguous [{self.pages}, {self.heads}, {self.page}, words or groups]")
+
+    @classmethod
+    def of(cls, cache: KVCache, page: int = 64) -> "PagedKVCache":
+        """One sequence's contiguous cache seen as pages, in order (its capacity a multiple of the page)."""
+        if cache.capacity % page:
+            raise ValueError("the cache's capacity must be a multiple of the page")
+        self = cls.__new__(cls)
+        self.pages, self.page, self.heads, self.dim, self.group = (cache.capacity // page, int(page), cache.heads,
+                                                                   cache.dim, cache.group)
+        self.kcb, self.vcb, self.rot, self.kw, self.vw = cache.kcb, cache.vcb, cache.rot, cache.kw, cache.vw
+        self.page_stride, self.head_stride = self.page, cache.capacity
+        self.kcodes, self.kscales, self.vcodes, self.vscales = cache.kcodes, cache.kscales, cache.vcodes, cache.vscales
+        return self
+
+    def c(self) -> tq_kv_pages_t:
+        return tq_kv_pages_t(self.kcodes.data_ptr(), self.kscales.data_ptr(), self.vcodes.data_ptr(),
+                             self.vscales.data_ptr(), self.heads, self.dim, self.group, self.page, self.pages,
+                             self.page_stride, self.head_stride, self.kcb.c(), self.vcb.c(), self.rot.c())
+
+
+def kv_append(cache: PagedKVCache, k, v, slots, rope: Rope | None = None, positions=None, err=None):
+    """Write tokens k, v [..., heads, dim] (f32 or bf16) to ``slots`` (int32, one per token; negative: skipped).
+
+    With ``rope`` and ``positions`` the keys get their rotary positions on the way."""
+    T, h, ks = _heads(k, "k", cache.dim)
+    Tv, hv, vs = _heads(v, "v", cache.dim)
+    if (T, h) != (Tv, hv) or h != cache.heads or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same tokens, the cache's heads and one dtype")
+    _ints(slots, "slots", T)
+    if rope is not None:
+        if positions is None:
+            raise ValueError("rope needs positions")
+        _ints(positions, "positions", T)
+    _same_device(k, v=v, slots=slots, positions=positions, cache=cache.kcodes)
+    c, r = cache.c(), rope.c() if rope is not None else None
+    _check(load().tq_kv_append(ctypes.byref(c), _ptr(k), ks, _ptr(v), vs, _dt(k), T, _ptr(slots),
+                               ctypes.byref(r) if r is not None else None, _ptr(positions), _ptr(err), _stream()),
+           "tq_kv_append")
+
+
+def kv_fetch(cache: PagedKVCache, slots, out_dtype=None, err=None):
+    """The tokens of ``slots`` (int32 [T]) as (k, v) [T, heads, dim], bf16 unless told otherwise; a negative slot is zeros."""
+    torch = _torch()
+    T = slots.numel()
+    _ints(slots, "slots", T)
+    _same_device(slots, cache=cache.kcodes)
+    k = torch.empty((T, cache.heads, cache.dim), dtype=out_dtype or torch.bfloat16, device=slots.device)
+    v = torch.empty_like(k)
+    c = cache.c()
+    _check(load().tq_kv_fetch(ctypes.byref(c), _ptr(slots), T, _ptr(k), _ptr(v), _dt(k), _ptr(err), _stream()),
+           "tq_kv_fetch")
+    return k, v
+
+
+def kv_attend_tree(cache: PagedKVCache, q, table, lens, k_new=None, v_new=None, mask=None, n_tok=None,
+                   max_len: int | None = None, scale: float | None = None, err=None, ws=None):
+    """Attention of drafted tokens q [B, n, Hq, dim] (bf16) over each sequence's cached context and over the drafts.
+
+    table: int32 [B, pages] page ids in order; lens: int32 [B] cached tokens; max_len: a bound on lens that
+    the host knows (default: what the table can hold).  k_new, v_new: the drafts' own keys and values
+    [B, n, heads, dim] (bf16); mask: int64 [B, n, ceil(n/64)], bit j of row i set where draft i sees draft j
+    (None: a chain, j <= i); n_tok: int32 [B] drafts in use.  Returns [B, n, Hq, dim] bf16."""
+    torch = _torch()
+    if q.dim() != 4:
+        raise ValueError("q must be [B, n, heads, dim]")
+    B, n = q.shape[:2]
+    _, hq, qs = _heads(q, "q", cache.dim)
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"table must be [{B}, pages]")
+    _ints(table, "table", table.numel())
+    _ints(lens, "lens", B)
+    ks = vs = 0
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    if k_new is not None:
+        for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+            if tuple(t.shape) != (B, n, cache.heads, cache.dim) or t.dtype != q.dtype:
+                raise ValueError(f"{name} must be [{B}, {n}, {cache.heads}, {cache.dim}] of q's dtype")
+        ks, vs = _heads(k_new, "k_new", cache.dim)[2], _heads(v_new, "v_new", cache.dim)[2]
+    if mask is not None:
+        _ints(mask, "mask", B * n * (-(-n // 64)), torch.int64)
+    if n_tok is not None:
+        _ints(n_tok, "n_tok", B)
+    _same_device(q, table=table, lens=lens, k_new=k_new, v_new=v_new, mask=mask, n_tok=n_tok, cache=cache.kcodes)
+    max_len = table.shape[1] * cache.page if max_len is None else int(max_len)
+    o = torch.empty((B, n, hq, cache.dim), dtype=torch.bfloat16, device=q.device)
+    c = cache.c()
+    nb = int(load().tq_kv_attend_tree_workspace_bytes(ctypes.byref(c), B, n, hq, max_len))
+    ws = _workspace(nb, q.device, ws)
+    _check(load().tq_kv_attend_tree(ctypes.byref(c), _ptr(q), qs, _dt(q), B, n, hq, _ptr(table), table.shape[1],
+                                    _ptr(lens), max_len, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(mask), _ptr(n_tok),
+                                    cache.dim ** -0.5 if scale is None else scale, _ptr(o), _ptr(ws), nb, _ptr(err),
+                                    _stream()), "tq_kv_attend_tree")
     return o
 
 
