@@ -3,9 +3,16 @@
 // o = softmax(scale * q K^T) V over a sequence's cached tokens and, through an ancestor
 // mask, over the drafted tokens.  As in tq_kv_attend the rotation moves off the cache:
 // q . k = (R q) . (R k), and sum_t p_t v_t = R^T sum_t p_t (R v_t), one de-rotation per row.
-// The drafted tokens come as they are (bf16, not rotated), so their part is a partial
-// result of its own, added after the de-rotation.
+//
+// Two launches.  kv_tree_context_kernel: the cached tokens.  The work is cut into steps of
+// 16 tokens of one (sequence, kv head, tile of 16 query rows); one persistent CTA per SM
+// takes an equal run of the steps of the whole batch, whatever the sequences' lengths, and
+// leaves a partial result (maximum, sum, weighted values of 16 rows) wherever its run
+// crosses into another tile.  kv_tree_finish_kernel: the drafted tokens, then the join of a
+// tile's partial results, the de-rotation and the output.
 #include <math.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "kv_pages.cuh"
@@ -14,8 +21,14 @@ using namespace tq;
 
 namespace {
 
-constexpr int kChunk = 512;  // cached tokens per CTA
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kInvSqrtD = 0.08838834764831845f;  // 1 / sqrt(128)
+constexpr int kStep = 16;                           // tokens of a step, rows of a tile
+constexpr int kCtxWarps = 12;                       // 168 registers a thread: 64 of sums, 32 of queries
+constexpr int kDepth = 3;                           // steps of a warp's ring: two in flight while one is decoded
+constexpr float kSlack = 8.0f;                      // a running maximum may be this far (log2) below the true one
+constexpr int kFinWarps = 8, kDraftWarps = 4;
+constexpr int kFragPad = 33;  // floats of a fragment register over the lanes, padded
 
 struct TreeArgs {
     KvPages c;
@@ -27,154 +40,830 @@ struct TreeArgs {
     const int32_t* lens;
     const uint64_t* mask;
     const int32_t* n_tok;
-    int B, n, Hq, table_stride, splits;  // splits: of the context; one more partial for the drafts
-    float scale2;                        // scale * log2(e)
+    int B, n, Hq, ratio, table_stride, ctas;  // ratio: query heads per kv head; ctas: of the context launch
+    float scale2;                             // scale * log2(e)
     __nv_bfloat16* o;
-    float* part;  // [row][splits + 1][2 + 128]: (max, sum, weighted values)
+    float2* stat;  // [slot][16]: running maximum (log2 units) and sum of a row
+    float* part;   // [slot][16][128]: weighted values, rotated
     uint32_t* err;
 };
 
-// One CTA (4 warps) per row and context chunk; the last chunk index is the drafts.
-template <int KL, int VL>
-__global__ void __launch_bounds__(128) kv_tree_kernel(TreeArgs a) {
-    __shared__ float kl[KL], vl[VL], qr[kPD], sc[kChunk], red[4];
-    __shared__ int64_t rows[kChunk];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t r = blockIdx.x;
-    const int hq = (int)(r % a.Hq), i = (int)(r / a.Hq % a.n), b = (int)(r / a.Hq / a.n);
-    const int h = hq / (a.Hq / a.c.Hkv), split = blockIdx.y;
-    float* dst = a.part + (r * (a.splits + 1) + split) * (2 + kPD);
-    const int live = a.n_tok ? a.n_tok[b] : a.n;
-    const bool drafts = split == a.splits;
-    int64_t len = a.lens[b];
-    if (len < 0 || len > a.max_len) {
-        if (tid == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
-        len = len < 0 ? 0 : a.max_len;
+// ---------------------------------------------------------------- the batch's work, counted on the device
+
+TQ_DEVFN int seq_len(const TreeArgs& a, int b) {
+    const int len = a.lens[b];
+    return len < 0 ? 0 : (int)min((int64_t)len, a.max_len);
+}
+TQ_DEVFN int seq_live(const TreeArgs& a, int b) { return a.n_tok ? min(max(a.n_tok[b], 0), a.n) : a.n; }
+TQ_DEVFN int seq_tiles(const TreeArgs& a, int b) { return (seq_live(a, b) * a.ratio + kStep - 1) / kStep; }
+TQ_DEVFN int seq_steps(const TreeArgs& a, int b) { return (seq_len(a, b) + kStep - 1) / kStep; }
+
+struct Work {
+    long long steps;  // steps of the sequences before this one
+    int units;        // (kv head, tile) units of the sequences before this one
+};
+
+// Steps and units of the sequences before b, and of all (one warp).
+TQ_DEVFN void count_work(const TreeArgs& a, int b, Work& before, long long& total) {
+    const int lane = threadIdx.x & 31;
+    long long s = 0, all = 0;
+    int u = 0;
+    for (int i = lane; i < a.B; i += 32) {
+        const int units = seq_tiles(a, i) * a.c.Hkv;
+        const long long w = (long long)units * seq_steps(a, i);
+        all += w;
+        if (i < b) {
+            s += w;
+            u += units;
+        }
     }
-    const int64_t t0 = (int64_t)split * kChunk;
-    const int64_t end = drafts ? (a.kn ? a.n : 0) : min(len, t0 + kChunk);
-    float m = -INFINITY, l = 0.f, acc = 0.f;
-    if (i < live && (drafts ? end > 0 : t0 < end)) {
-        for (int x = tid; x < KL; x += 128) kl[x] = a.c.kcent[x];
-        for (int x = tid; x < VL; x += 128) vl[x] = a.c.vcent[x];
-        const __nv_bfloat16* q = a.q + ((int64_t)b * a.n + i) * a.qs + (int64_t)hq * kPD;
-        if (drafts) {
-            qr[tid] = __bfloat162float(q[tid]) * a.scale2;
-        } else if (warp == 0) {
-            float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __bfloat162float(q[lane * 4 + e]) * (float)a.c.signs[lane * 4 + e];
+    for (int m = 16; m; m >>= 1) {
+        s += __shfl_xor_sync(kFull, s, m);
+        all += __shfl_xor_sync(kFull, all, m);
+        u += __shfl_xor_sync(kFull, u, m);
+    }
+    before = {s, u};
+    total = all;
+}
+
+// Steps of one CTA's run: an equal share, and no fewer than one for each of its warps.
+TQ_DEVFN long long steps_per_cta(const TreeArgs& a, long long total) {
+    return max((total + a.ctas - 1) / a.ctas, (long long)kCtxWarps);
+}
+
+// ---------------------------------------------------------------- fragments
+
+TQ_DEVFN uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(s));
+    return d;
+}
+TQ_DEVFN uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// D[16, 8] += A[16, 16] B[16, 8], fp32 sums.
+TQ_DEVFN void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+TQ_DEVFN void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+TQ_DEVFN uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+TQ_DEVFN float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+TQ_DEVFN void cp16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+// 2^-e just above x's magnitude, as an exponent: 0 for 0, infinities and NaN.
+TQ_DEVFN int exponent_above(float x) {
+    const int e = (__float_as_int(x) >> 23) & 255;
+    return e == 0 || e == 255 ? 0 : e - 126;
+}
+
+// One step of a ring: 16 tokens' codes and scales.
+template <int KL, int VL>
+struct Stage {
+    static constexpr int kKRow = KvBook<KL>::kWords * 4;            // bytes of a key row
+    static constexpr int kVRow = VL == 16 ? 80 : 52;                // of a value row: 4-bit rows (64) spread over the banks
+    static constexpr int kK = 0, kV = kStep * kKRow, kKs = kV + kStep * kVRow, kVs = kKs + 256, kBytes = kVs + 256;
+};
+constexpr int kLutBytes = 256 * 256;
+
+template <int KL, int VL>
+constexpr size_t context_smem() {
+    const size_t rings = (size_t)kCtxWarps * kDepth * Stage<KL, VL>::kBytes;
+    const size_t join = (size_t)kCtxWarps * (64 * kFragPad * sizeof(float) + kStep * sizeof(float2));  // over the rings
+    return kLutBytes + kStep * kPD * 2 + kStep * 4 + (rings > join ? rings : join);
+}
+
+template <int KL, int VL>
+__global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(TreeArgs a) {
+    using S = Stage<KL, VL>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* lut = smem;                                                   // [256][key lanes 32 | value lanes 32] words
+    __half* qh = reinterpret_cast<__half*>(smem + kLutBytes);              // [16][128] rotated queries
+    float* qf = reinterpret_cast<float*>(qh + kStep * kPD);                // [16] factor from a row's products to log2 scores
+    uint8_t* rings = reinterpret_cast<uint8_t*>(qf + kStep);
+    __shared__ Work s_before;
+    __shared__ long long s_total;
+    __shared__ int s_b;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+    pdl_trigger();
+    if (warp == 0) {
+        // where this CTA's run begins: the last sequence with at most P0 steps before it
+        Work w;
+        long long total;
+        count_work(a, 0, w, total);
+        const long long P0 = blockIdx.x * steps_per_cta(a, total);
+        long long base = 0;
+        int units = 0, b = 0;
+        if (P0 < total) {
+            for (int b0 = 0; b0 < a.B; b0 += 32) {
+                const int i = b0 + lane;
+                const int u = i < a.B ? seq_tiles(a, i) * a.c.Hkv : 0;
+                long long s = i < a.B ? (long long)u * seq_steps(a, i) : 0, incl = s;
+                int ui = u;
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const long long x = __shfl_up_sync(kFull, incl, m);
+                    const int y = __shfl_up_sync(kFull, ui, m);
+                    if (lane >= m) {
+                        incl += x;
+                        ui += y;
+                    }
+                }
+                const unsigned hit = __ballot_sync(kFull, base + incl > P0);
+                if (hit) {
+                    const int src = __ffs(hit) - 1;
+                    base += __shfl_sync(kFull, incl - s, src);
+                    units += __shfl_sync(kFull, ui - u, src);
+                    b = b0 + src;
+                    break;
+                }
+                base += __shfl_sync(kFull, incl, 31);
+                units += __shfl_sync(kFull, ui, 31);
+            }
+        }
+        if (lane == 0) {
+            s_before = {base, units};
+            s_total = total;
+            s_b = b;
+        }
+    }
+    // The books as fp16 over a power of two just above their largest centroid, a copy for each lane
+    // (bank = lane), so a decoded value over 2^e is at most its group's scale and never overflows fp16.
+    // Row c: the key centroid of code c (8-bit), or the centroids of the two 4-bit codes of byte c; the
+    // same pair for 4-bit values in the upper half of the row.
+    const int ek = exponent_above(fmaxf(fabsf(a.c.kcent[0]), fabsf(a.c.kcent[KL - 1])));
+    const int ev = exponent_above(fmaxf(fabsf(a.c.vcent[0]), fabsf(a.c.vcent[VL - 1])));
+    const float kd = exp2f((float)-ek), vd = exp2f((float)-ev);
+    for (int c = warp; c < 256; c += kCtxWarps) {
+        uint32_t* row = reinterpret_cast<uint32_t*>(lut + c * 256);
+        row[lane] = KL == 256 ? pack_f16(a.c.kcent[c % KL] * kd, 0.f)
+                              : pack_f16(a.c.kcent[(c & 15) % KL] * kd, a.c.kcent[(c >> 4) % KL] * kd);
+        if (VL == 16) row[32 + lane] = pack_f16(a.c.vcent[(c & 15) % VL] * vd, a.c.vcent[(c >> 4) % VL] * vd);
+    }
+    // An 8-level value book lives in four registers: low and high bytes of its fp16 centroids.
+    uint32_t tl[2] = {0, 0}, th[2] = {0, 0};
+    if (VL == 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t h = __half_as_ushort(__float2half_rn(a.c.vcent[i % VL] * vd));
+            tl[i >> 2] |= (h & 255u) << (8 * (i & 3));
+            th[i >> 2] |= (h >> 8) << (8 * (i & 3));
+        }
+    }
+    __syncthreads();
+
+    const long long total = s_total, per = steps_per_cta(a, total);
+    long long p = blockIdx.x * per;
+    const long long pend = min(p + per, total);
+    int b = s_b;
+    long long base = s_before.steps;
+    int ubase = s_before.units;
+    const int ng = kPD >> a.c.lgroup;
+    uint8_t* ring = rings + warp * kDepth * S::kBytes;
+    const uint32_t lane4 = lane * 4;
+
+    while (p < pend) {
+        int steps = seq_steps(a, b), tiles = seq_tiles(a, b);
+        while (p >= base + (long long)steps * tiles * a.c.Hkv) {  // into the next sequence that has any
+            base += (long long)steps * tiles * a.c.Hkv;
+            ubase += tiles * a.c.Hkv;
+            ++b;
+            steps = seq_steps(a, b);
+            tiles = seq_tiles(a, b);
+        }
+        const int unit = (int)((p - base) / steps);
+        const int s0 = (int)(p - base - (long long)unit * steps);
+        const int s1 = (int)min((long long)steps, s0 + (pend - p));
+        const int h = unit / tiles, tile = unit - h * tiles;
+        const int len = seq_len(a, b), rows = min(kStep, seq_live(a, b) * a.ratio - tile * kStep);
+
+        // queries of the tile: rotated, over a power of two of their own, fp16
+        for (int row = warp; row < kStep; row += kCtxWarps) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            if (row < rows) {
+                const int x = tile * kStep + row, i = x / a.ratio, g = x - i * a.ratio;
+                const uint2 raw = *reinterpret_cast<const uint2*>(a.q + ((int64_t)b * a.n + i) * a.qs +
+                                                                  (int64_t)(h * a.ratio + g) * kPD + lane * 4);
+                const uint32_t sg = *reinterpret_cast<const uint32_t*>(a.c.signs + lane * 4);
+                v[0] = __uint_as_float(raw.x << 16) * (float)(int8_t)sg;
+                v[1] = __uint_as_float(raw.x & 0xffff0000u) * (float)(int8_t)(sg >> 8);
+                v[2] = __uint_as_float(raw.y << 16) * (float)(int8_t)(sg >> 16);
+                v[3] = __uint_as_float(raw.y & 0xffff0000u) * (float)(int8_t)(sg >> 24);
+            }
             fwht_warp128(v);
+            float mx = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) qr[lane * 4 + e] = v[e] * (0.08838834764831845f * a.scale2);
+            for (int m = 16; m; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, m));
+            const int e = exponent_above(mx);
+            const float d = exp2f((float)-e);
+            *reinterpret_cast<uint2*>(qh + row * kPD + lane * 4) =
+                make_uint2(pack_f16(v[0] * d, v[1] * d), pack_f16(v[2] * d, v[3] * d));
+            if (lane == 0) qf[row] = exp2f((float)(e + ek)) * (kInvSqrtD * a.scale2);
         }
         __syncthreads();
-        for (int64_t base = drafts ? 0 : t0; base < end; base += kChunk) {  // the drafts may take several rounds
-            const int cnt = (int)min((int64_t)kChunk, end - base);
-            for (int x = tid; x < cnt; x += 128) {
-                const int64_t t = base + x;
-                float s = -INFINITY;
-                if (drafts) {
-                    const bool see = t < live && (a.mask ? (a.mask[((int64_t)b * a.n + i) * ((a.n + 63) / 64) + t / 64] >> (t % 64)) & 1 : t <= i);
-                    if (see) {
-                        const __nv_bfloat16* k = a.kn + ((int64_t)b * a.n + t) * a.ks + (int64_t)h * kPD;
-                        s = 0.f;
-                        for (int d = 0; d < kPD; ++d) s = fmaf(qr[d], __bfloat162float(k[d]), s);
+        // A operand of product step s: the lane's rows r and r + 8, dims 32 j + 4 s .. + 3.  Any order
+        // of the dims will do as long as the keys' follows it; this one gives a lane whole words of a key.
+        uint32_t qa[8][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 lo = *reinterpret_cast<const uint4*>(qh + r * kPD + 32 * j + 8 * i);
+            const uint4 hi = *reinterpret_cast<const uint4*>(qh + (r + 8) * kPD + 32 * j + 8 * i);
+            qa[2 * i][0] = lo.x, qa[2 * i][2] = lo.y, qa[2 * i + 1][0] = lo.z, qa[2 * i + 1][2] = lo.w;
+            qa[2 * i][1] = hi.x, qa[2 * i][3] = hi.y, qa[2 * i + 1][1] = hi.z, qa[2 * i + 1][3] = hi.w;
+        }
+        const float f0 = qf[r], f1 = qf[r + 8];
+
+        const int cnt = s1 - s0 > warp ? (s1 - s0 - warp + kCtxWarps - 1) / kCtxWarps : 0;  // steps of this warp
+        const int32_t* tab = a.table + (int64_t)b * a.table_stride;
+        uint32_t okbits = 0;
+        auto page_of = [&](int it) {
+            return it < cnt ? __ldg(tab + (((s0 + warp + it * kCtxWarps) * kStep) >> a.c.lpage)) : 0;
+        };
+        int page_next = page_of(0);
+        auto issue = [&](int it) {  // step `it` of this warp into its ring
+            const int page = page_next;
+            page_next = page_of(it + 1);
+            if (it < cnt) {
+                const int t = (s0 + warp + it * kCtxWarps) * kStep;
+                const bool ok = page >= 0 && page < a.c.pages;
+                okbits = (okbits & ~(1u << (it & 31))) | ((uint32_t)ok << (it & 31));
+                if (ok) {
+                    const int64_t row = (int64_t)page * a.c.page_stride + (int64_t)h * a.c.head_stride +
+                                        (t & ((1 << a.c.lpage) - 1));
+                    uint8_t* st = ring + (it % kDepth) * S::kBytes;
+                    const uint8_t* kc = reinterpret_cast<const uint8_t*>(a.c.kcodes) + row * S::kKRow;
+#pragma unroll
+                    for (int x = 0; x < kStep * S::kKRow / 512; ++x) {
+                        const int c = lane + 32 * x;
+                        // 128-byte rows: chunks of odd rows swapped in pairs, so that eight lanes of a read
+                        // (two rows, every other chunk) meet all banks
+                        const int d = KL == 256 ? c ^ ((c >> 3) & 1) : c;
+                        cp16(st + S::kK + d * 16, kc + c * 16);
+                    }
+                    const uint8_t* vc = reinterpret_cast<const uint8_t*>(a.c.vcodes) + row * (KvBook<VL>::kWords * 4);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int c = lane + 32 * x;
+                        if (c < kStep * KvBook<VL>::kWords / 4)
+                            cp16(st + S::kV + (VL == 16 ? (c >> 2) * S::kVRow + (c & 3) * 16 : c * 16), vc + c * 16);
+                    }
+                    const int c = lane & 15;
+                    if (c < 2 * ng)
+                        cp16(st + (lane < 16 ? S::kKs : S::kVs) + c * 16,
+                             reinterpret_cast<const uint8_t*>((lane < 16 ? a.c.kscales : a.c.vscales) + row * ng) + c * 16);
+                } else if (lane == 0 && a.err) {
+                    atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+
+        float o[16][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int it = 0; it < kDepth - 1; ++it) issue(it);
+        // scale places of the lane: keys' dims 32 j and 32 j + 16, values' dims 16 r
+        const int gk0 = (32 * j) >> a.c.lgroup, gk1 = (32 * j + 16) >> a.c.lgroup, gv = (16 * r) >> a.c.lgroup;
+        // 3-bit values: dims 16 r .. + 15 begin at code `rem` of word w0 (ten to a word)
+        const int w0 = (16 * r) / 10, rem = (16 * r) % 10;
+        const int sh0 = 3 * rem, sh1 = rem == 0 ? 24 : 3 * (rem - 2);
+#pragma unroll 1
+        for (int it = 0; it < cnt; ++it) {
+            issue(it + kDepth - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            __syncwarp();
+            if ((okbits >> (it & 31)) & 1) {
+                const uint8_t* st = ring + (it % kDepth) * S::kBytes;
+                const int t0 = (s0 + warp + it * kCtxWarps) * kStep, left = len - t0;  // tokens of the step
+                // ---- scores of tokens r (tile 0) and r + 8 (tile 1)
+                float sc[2][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int tok = r + 8 * e;
+                    sc[e][0] = sc[e][1] = sc[e][2] = sc[e][3] = 0.f;
+                    const uint16_t* ks = reinterpret_cast<const uint16_t*>(st + S::kKs) + tok * ng;
+                    const uint32_t s_lo = ks[gk0] * 0x10001u, s_hi = ks[gk1] * 0x10001u;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t s2 = half ? s_hi : s_lo;
+                        if constexpr (KL == 256) {
+                            const uint4 w4 = *reinterpret_cast<const uint4*>(st + S::kK + tok * 128 +
+                                                                             ((2 * j + half) ^ (r & 1)) * 16);
+                            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t v[4];
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)  // byte 1: the code, byte 0: the lane's bank
+                                    v[c] = *reinterpret_cast<const uint32_t*>(lut + prmt(w[i], lane4, 0x5504u | (c << 4)));
+                                mma_f16(sc[e], qa[4 * half + i], mul2(prmt(v[0], v[1], 0x5410), s2),
+                                        mul2(prmt(v[2], v[3], 0x5410), s2));
+                            }
+                        } else {
+                            const uint2 w2 = *reinterpret_cast<const uint2*>(st + S::kK + tok * 64 + j * 16 + half * 8);
+                            const uint32_t w[2] = {w2.x, w2.y};
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t v[4];
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    v[c] = *reinterpret_cast<const uint32_t*>(lut + prmt(w[i], lane4, 0x5504u | (c << 4)));
+                                mma_f16(sc[e], qa[4 * half + 2 * i], mul2(v[0], s2), mul2(v[1], s2));
+                                mma_f16(sc[e], qa[4 * half + 2 * i + 1], mul2(v[2], s2), mul2(v[3], s2));
+                            }
+                        }
+                    }
+                }
+                // ---- log2 scores, tokens past the end left out; columns 8 e + 2 j + {0, 1}
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const bool in = 8 * e + 2 * j + (c & 1) < left;
+                        sc[e][c] = in ? sc[e][c] * (c < 2 ? f0 : f1) : -INFINITY;
+                    }
+                const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+                const float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+                // the maximum follows only when a score passes it by kSlack: weights stay below 2^8, well inside fp16
+                if (__any_sync(kFull, x0 > m0 + kSlack || x1 > m1 + kSlack)) {
+                    float n0 = x0, n1 = x1;
+#pragma unroll
+                    for (int m = 1; m < 4; m <<= 1) {
+                        n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, m));
+                        n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, m));
+                    }
+                    n0 = fmaxf(n0, m0);
+                    n1 = fmaxf(n1, m1);
+                    const float g0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0), g1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
+                    m0 = n0;
+                    m1 = n1;
+                    l0 *= g0;
+                    l1 *= g1;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        o[i][0] *= g0;
+                        o[i][1] *= g0;
+                        o[i][2] *= g1;
+                        o[i][3] *= g1;
+                    }
+                }
+                const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+                uint32_t pa[4];  // weights as the A operand: the score fragment is already in its order
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float w00 = fast_exp2(sc[e][0] - b0), w01 = fast_exp2(sc[e][1] - b0);
+                    const float w10 = fast_exp2(sc[e][2] - b1), w11 = fast_exp2(sc[e][3] - b1);
+                    l0 += w00 + w01;
+                    l1 += w10 + w11;
+                    pa[2 * e] = pack_f16(w00, w01);
+                    pa[2 * e + 1] = pack_f16(w10, w11);
+                }
+                // ---- weighted values: tokens 2 j, 2 j + 1 and 2 j + 8, 2 j + 9, dims 16 r + i in tile i
+                const uint16_t* vs = reinterpret_cast<const uint16_t*>(st + S::kVs);
+                uint32_t s2[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int tok = 8 * e + 2 * j;
+                    const uint32_t sa = tok < left ? vs[tok * ng + gv] : 0u, sb = tok + 1 < left ? vs[(tok + 1) * ng + gv] : 0u;
+                    s2[e] = sa | (sb << 16);
+                }
+                if constexpr (VL == 8) {
+                    uint32_t bits[2][2][2];  // [pair][token][dims 8 q .. + 7]
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t* w = reinterpret_cast<const uint32_t*>(st + S::kV) + (8 * e + 2 * j + x) * 13 + w0;
+                            const uint32_t wa = w[0], wb = w[1], wc = r == 7 ? 0u : w[2];
+                            bits[e][x][0] = (wa >> sh0) | (wb << (30 - sh0));
+                            bits[e][x][1] = rem == 0 ? (wa >> 24) | (wb << 6) : (wb >> sh1) | (wc << (30 - sh1));
+                        }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t v[2][8];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t u[2];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {  // two codes to a byte
+                                const uint32_t b24 = bits[e][x][q];
+                                const uint32_t t = (b24 & 0x0000ffffu) | ((b24 << 4) & 0xffff0000u);
+                                u[x] = (t & 0x00ff00ffu) | ((t << 2) & 0xff00ff00u);
+                            }
+                            // selectors: nibbles (token a, token b) of dims 0, 2, 4, 6 and of dims 1, 3, 5, 7
+                            const uint32_t ev0 = ((u[0] & 0x0f0f0f0fu) | ((u[1] << 4) & 0xf0f0f0f0u)) & 0x77777777u;
+                            const uint32_t od0 = (((u[0] >> 3) & 0x0f0f0f0fu) | ((u[1] << 1) & 0xf0f0f0f0u)) & 0x77777777u;
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const uint32_t sel = (y & 1 ? od0 : ev0) >> (16 * (y >> 1));
+                                const uint32_t lo = prmt(tl[0], tl[1], sel), hi = prmt(th[0], th[1], sel);
+                                v[e][4 * (y >> 1) + (y & 1)] = mul2(prmt(lo, hi, 0x5140), s2[e]);
+                                v[e][4 * (y >> 1) + (y & 1) + 2] = mul2(prmt(lo, hi, 0x7362), s2[e]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) mma_f16(o[8 * q + i], pa, v[0][i], v[1][i]);
                     }
                 } else {
-                    const int page = a.table[(int64_t)b * a.table_stride + (t >> a.c.lpage)];
-                    rows[x] = -1;
-                    if (page >= 0 && page < a.c.pages) {
-                        const int64_t row = (int64_t)page * a.c.page_stride + (int64_t)h * a.c.head_stride + (t & ((1 << a.c.lpage) - 1));
-                        rows[x] = row;
-                        const uint32_t* w = a.c.kcodes + row * KvBook<KL>::kWords;
-                        const uint16_t* z = a.c.kscales + (row << (7 - a.c.lgroup));
-                        s = 0.f;
-                        for (int d = 0; d < kPD; ++d) {
-                            const uint32_t c = (w[d / KvBook<KL>::kCW] >> (KvBook<KL>::kBits * (d % KvBook<KL>::kCW))) & (KL - 1);
-                            s = fmaf(qr[d], kl[c] * half_bits_to_float(z[d >> a.c.lgroup]), s);
+                    uint2 w[2][2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            w[e][x] = *reinterpret_cast<const uint2*>(st + S::kV + (8 * e + 2 * j + x) * S::kVRow + r * 8);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {  // byte y of the 16 dims: dims 2 y and 2 y + 1
+                        uint32_t lo[2], hi[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t v[2];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                v[x] = *reinterpret_cast<const uint32_t*>(
+                                    lut + 128 + prmt(y < 4 ? w[e][x].x : w[e][x].y, lane4, 0x5504u | ((y & 3) << 4)));
+                            lo[e] = mul2(prmt(v[0], v[1], 0x5410), s2[e]);
+                            hi[e] = mul2(prmt(v[0], v[1], 0x7632), s2[e]);
                         }
-                    } else if (a.err) {
-                        atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
+                        mma_f16(o[2 * y], pa, lo[0], lo[1]);
+                        mma_f16(o[2 * y + 1], pa, hi[0], hi[1]);
                     }
                 }
-                sc[x] = s;
             }
-            __syncthreads();
-            float mx = -INFINITY;
-            for (int x = lane; x < cnt; x += 32) mx = mx != mx ? mx : (sc[x] != sc[x] ? sc[x] : fmaxf(mx, sc[x]));
-            for (int o = 16; o; o >>= 1) {
-                const float y = __shfl_xor_sync(kFull, mx, o);
-                mx = mx != mx ? mx : (y != y ? y : fmaxf(mx, y));
+            __syncwarp();  // the ring slot is free for the copy after next
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+        // ---- join the warps: fragments through shared memory (over the rings)
+        l0 += __shfl_xor_sync(kFull, l0, 1);
+        l0 += __shfl_xor_sync(kFull, l0, 2);
+        l1 += __shfl_xor_sync(kFull, l1, 1);
+        l1 += __shfl_xor_sync(kFull, l1, 2);
+        __syncthreads();
+        const int act = min(kCtxWarps, s1 - s0);
+        float* frag = reinterpret_cast<float*>(rings);                 // [warp][64][33]
+        float2* ml = reinterpret_cast<float2*>(frag + kCtxWarps * 64 * kFragPad);  // [warp][16]
+        if (warp < act) {
+            float* f = frag + warp * 64 * kFragPad + lane;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) f[(4 * i + c) * kFragPad] = o[i][c];
+            if (j == 0) {
+                ml[warp * kStep + r] = make_float2(m0, l0);
+                ml[warp * kStep + r + 8] = make_float2(m1, l1);
             }
-            if (!(mx == -INFINITY)) {
-                const float nm = mx != mx || m != m ? NAN : fmaxf(m, mx), f = m == -INFINITY ? 0.f : exp2f(m - nm);
-                acc *= f;
-                l *= f;
-                m = nm;
-                float sum = 0.f;
-                for (int x = 0; x < cnt; ++x) {
-                    const float p = sc[x] == -INFINITY ? 0.f : exp2f(sc[x] - nm);
-                    if (sc[x] == -INFINITY) continue;  // not seen: its value never enters
-                    sum += p;
-                    if (drafts) {
-                        acc = fmaf(p, __bfloat162float(a.vn[((int64_t)b * a.n + base + x) * a.vs + (int64_t)h * kPD + tid]), acc);
-                    } else if (rows[x] >= 0) {
-                        const uint32_t w = a.c.vcodes[rows[x] * KvBook<VL>::kWords + tid / KvBook<VL>::kCW];
-                        const uint32_t c = (w >> (KvBook<VL>::kBits * (tid % KvBook<VL>::kCW))) & (VL - 1);
-                        acc = fmaf(p, vl[c] * half_bits_to_float(a.c.vscales[(rows[x] << (7 - a.c.lgroup)) + (tid >> a.c.lgroup)]), acc);
+        }
+        __syncthreads();
+        const int64_t slot = (int64_t)blockIdx.x + ubase + unit;
+        const float vscale = exp2f((float)ev);
+        for (int x = threadIdx.x; x < rows * kPD; x += 32 * kCtxWarps) {
+            const int row = x >> 7, d = x & 127, i = d & 15, nn = d >> 4;
+            const int at = (4 * i + 2 * (row >> 3) + (nn & 1)) * kFragPad + (row & 7) * 4 + (nn >> 1);
+            float M = -INFINITY;
+            for (int w = 0; w < act; ++w) M = fmaxf(M, ml[w * kStep + row].x);
+            float L = 0.f, acc = 0.f;
+            for (int w = 0; w < act; ++w) {
+                const float2 s = ml[w * kStep + row];
+                const float g = s.x == -INFINITY ? 1.f : fast_exp2(s.x - M);  // nothing seen: zeros, or NaN scores
+                L = fmaf(g, s.y, L);
+                acc = fmaf(g, frag[w * 64 * kFragPad + at], acc);
+            }
+            a.part[(slot * kStep + row) * kPD + d] = acc * vscale;
+            if (d == 0) a.stat[slot * kStep + row] = make_float2(M, L);
+        }
+        __syncthreads();  // the rings and the queries are free
+        p += s1 - s0;
+    }
+}
+
+// ---------------------------------------------------------------- drafted tokens, join, output
+
+// Whether draft i of sequence b sees draft t.
+TQ_DEVFN bool sees(const TreeArgs& a, int b, int i, int t, int live) {
+    if (t >= live) return false;
+    if (!a.mask) return t <= i;
+    return (a.mask[((int64_t)b * a.n + i) * ((a.n + 63) >> 6) + (t >> 6)] >> (t & 63)) & 1;
+}
+
+// One CTA per (sequence, kv head, tile of 16 rows).  The drafted tokens come as they are: bf16 queries, keys
+// and values on the tensor cores, exact but for the weights, which are split in two bf16 halves.
+__global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs a, int tiles_max) {
+    __shared__ float frag[kDraftWarps][64][kFragPad];
+    __shared__ float2 ml[kDraftWarps][kStep];
+    __shared__ __align__(16) float joined[kFinWarps][kPD];
+    __shared__ float2 jml[kFinWarps];
+    __shared__ Work s_before;
+    __shared__ long long s_total;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+    const int tile = blockIdx.x % tiles_max, bh = blockIdx.x / tiles_max, h = bh % a.c.Hkv, b = bh / a.c.Hkv;
+    const int live = seq_live(a, b), all = a.n * a.ratio;
+    const int rows = min(kStep, all - tile * kStep);           // rows of the output
+    const int used = min(rows, live * a.ratio - tile * kStep);  // of which in use (may be none)
+    // A operand rows r and r + 8 of the tile
+    const int x0 = tile * kStep + r, x1 = x0 + 8;
+    const int i0 = x0 / a.ratio, i1 = x1 / a.ratio;
+    const int dsteps = a.kn && used > 0 ? (live + kStep - 1) / kStep : 0;
+    const int dact = min(dsteps, kDraftWarps);
+    if (warp < dact) {
+        uint32_t qa[8][4];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int x = y ? x1 : x0, i = y ? i1 : i0;
+            const bool in = x < live * a.ratio;
+            const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * a.n + i) * a.qs +
+                                                              (int64_t)(h * a.ratio + x - i * a.ratio) * kPD + 32 * j);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const uint4 v = in ? src[z] : make_uint4(0u, 0u, 0u, 0u);
+                qa[2 * z][y] = v.x, qa[2 * z][2 + y] = v.y, qa[2 * z + 1][y] = v.z, qa[2 * z + 1][2 + y] = v.w;
+            }
+        }
+        float o[16][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+        for (int st = warp; st < dsteps; st += kDraftWarps) {
+            const int t0 = st * kStep;
+            float sc[2][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = t0 + 8 * e + r;
+                sc[e][0] = sc[e][1] = sc[e][2] = sc[e][3] = 0.f;
+                const uint4* src = reinterpret_cast<const uint4*>(a.kn + ((int64_t)b * a.n + t) * a.ks + (int64_t)h * kPD + 32 * j);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const uint4 v = t < live ? src[z] : make_uint4(0u, 0u, 0u, 0u);
+                    mma_bf16(sc[e], qa[2 * z], v.x, v.y);
+                    mma_bf16(sc[e], qa[2 * z + 1], v.z, v.w);
+                }
+            }
+            float x[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int t = t0 + 8 * e + 2 * j + (c & 1);
+                    sc[e][c] = sees(a, b, min(c < 2 ? i0 : i1, a.n - 1), t, live) ? sc[e][c] * a.scale2 : -INFINITY;
+                    x[c >> 1] = fmaxf(x[c >> 1], sc[e][c]);
+                }
+#pragma unroll
+            for (int m = 1; m < 4; m <<= 1) {
+                x[0] = fmaxf(x[0], __shfl_xor_sync(kFull, x[0], m));
+                x[1] = fmaxf(x[1], __shfl_xor_sync(kFull, x[1], m));
+            }
+            const float n0 = fmaxf(m0, x[0]), n1 = fmaxf(m1, x[1]);
+            const float g0 = m0 == -INFINITY ? 1.f : exp2f(m0 - n0), g1 = m1 == -INFINITY ? 1.f : exp2f(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= g0;
+            l1 *= g1;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                o[i][0] *= g0;
+                o[i][1] *= g0;
+                o[i][2] *= g1;
+                o[i][3] *= g1;
+            }
+            const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+            uint32_t ph[4], pl[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float wa = exp2f(sc[e][2 * y] - (y ? b1 : b0)), wb = exp2f(sc[e][2 * y + 1] - (y ? b1 : b0));
+                    (y ? l1 : l0) += wa + wb;
+                    sc[e][2 * y] = wa;
+                    sc[e][2 * y + 1] = wb;
+                    const __nv_bfloat162 hi = __floats2bfloat162_rn(wa, wb);
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(wa - __low2float(hi), wb - __high2float(hi));
+                    ph[2 * e + y] = *reinterpret_cast<const uint32_t*>(&hi);
+                    pl[2 * e + y] = *reinterpret_cast<const uint32_t*>(&lo);
+                }
+            // values of tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9, dims 16 r .. + 15; what is not finite is taken
+            // out (0 times it would reach rows that do not see it) and added below to those that do
+            uint32_t bad = 0;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                uint32_t w[2][2][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int t = t0 + 8 * e + 2 * j + y;
+                        const uint4 v = t < live ? reinterpret_cast<const uint4*>(a.vn + ((int64_t)b * a.n + t) * a.vs +
+                                                                                  (int64_t)h * kPD + 16 * r)[z]
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+                        w[e][y][0] = v.x, w[e][y][1] = v.y, w[e][y][2] = v.z, w[e][y][3] = v.w;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t inf = ((w[e][y][k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                            bad |= inf;
+                            w[e][y][k] &= ~((inf >> 15) * 0xffffu);
+                        }
+                    }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t lo0 = prmt(w[0][0][k], w[0][1][k], 0x5410), lo1 = prmt(w[1][0][k], w[1][1][k], 0x5410);
+                    const uint32_t hi0 = prmt(w[0][0][k], w[0][1][k], 0x7632), hi1 = prmt(w[1][0][k], w[1][1][k], 0x7632);
+                    mma_bf16(o[8 * z + 2 * k], ph, lo0, lo1);
+                    mma_bf16(o[8 * z + 2 * k], pl, lo0, lo1);
+                    mma_bf16(o[8 * z + 2 * k + 1], ph, hi0, hi1);
+                    mma_bf16(o[8 * z + 2 * k + 1], pl, hi0, hi1);
+                }
+            }
+            if (__any_sync(kFull, bad != 0)) {
+#pragma unroll
+                for (int col = 0; col < kStep; ++col) {
+                    const int t = t0 + col, from = (lane & ~3) | ((col & 7) >> 1);
+                    const float w0 = __shfl_sync(kFull, sc[col >> 3][col & 1], from);
+                    const float w1 = __shfl_sync(kFull, sc[col >> 3][2 + (col & 1)], from);
+                    if (t < live) {
+                        const bool see0 = sees(a, b, min(i0, a.n - 1), t, live), see1 = sees(a, b, min(i1, a.n - 1), t, live);
+                        const __nv_bfloat16* v = a.vn + ((int64_t)b * a.n + t) * a.vs + (int64_t)h * kPD;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const float x = __bfloat162float(v[16 * (2 * j + y) + i]);
+                                if (!isfinite(x)) {
+                                    if (see0) o[i][y] += w0 * x;
+                                    if (see1) o[i][2 + y] += w1 * x;
+                                }
+                            }
                     }
                 }
-                l += sum;
             }
-            __syncthreads();
+        }
+        l0 += __shfl_xor_sync(kFull, l0, 1);
+        l0 += __shfl_xor_sync(kFull, l0, 2);
+        l1 += __shfl_xor_sync(kFull, l1, 1);
+        l1 += __shfl_xor_sync(kFull, l1, 2);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) frag[warp][4 * i + c][lane] = o[i][c];
+        if (j == 0) {
+            ml[warp][r] = make_float2(m0, l0);
+            ml[warp][r + 8] = make_float2(m1, l1);
         }
     }
-    if (tid == 0) {
-        dst[0] = m;
-        dst[1] = l;
+    if (blockIdx.x == 0 && a.err)
+        for (int i = threadIdx.x; i < a.B; i += 32 * kFinWarps)
+            if (a.lens[i] < 0 || a.lens[i] > a.max_len) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
+    if (warp == kFinWarps - 1) {
+        Work w;
+        long long total;
+        count_work(a, b, w, total);
+        if (lane == 0) {
+            s_before = w;
+            s_total = total;
+        }
     }
-    dst[2 + tid] = acc;
+    __syncthreads();
+    pdl_wait();  // the context's partial results
+
+    // Partial results of this tile: runs first .. last, each at slot run + unit.  Warps share a row where rows are few.
+    const long long per = steps_per_cta(a, s_total);
+    const int steps = seq_steps(a, b), unit = s_before.units + h * seq_tiles(a, b) + tile;
+    const long long at = s_before.steps + (long long)(h * seq_tiles(a, b) + tile) * steps;
+    const int first = used > 0 && steps ? (int)(at / per) : 0;
+    const int count = used > 0 && steps ? (int)((at + steps - 1) / per) - first + 1 : 0;
+    int share = 1;
+    while (share * 2 * rows <= kFinWarps) share *= 2;  // warps of a row
+    for (int row0 = 0; row0 < rows; row0 += kFinWarps / share) {
+        const int row = row0 + warp / share;
+        float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (row < used) {
+            const int64_t slot0 = (int64_t)first + unit;
+            for (int x = warp % share; x < count; x += share) M = fmaxf(M, a.stat[(slot0 + x) * kStep + row].x);
+#pragma unroll 4
+            for (int x = warp % share; x < count; x += share) {
+                const float2 s = a.stat[(slot0 + x) * kStep + row];
+                const float4 y = *reinterpret_cast<const float4*>(a.part + ((slot0 + x) * kStep + row) * kPD + lane * 4);
+                const float g = s.x == -INFINITY ? 1.f : exp2f(s.x - M);
+                L = fmaf(g, s.y, L);
+                v[0] = fmaf(g, y.x, v[0]);
+                v[1] = fmaf(g, y.y, v[1]);
+                v[2] = fmaf(g, y.z, v[2]);
+                v[3] = fmaf(g, y.w, v[3]);
+            }
+        }
+        if (share > 1) {
+            __syncthreads();  // the last round's reads
+            *reinterpret_cast<float4*>(&joined[warp][lane * 4]) = make_float4(v[0], v[1], v[2], v[3]);
+            if (lane == 0) jml[warp] = make_float2(M, L);
+            __syncthreads();
+            if (warp % share == 0) {
+                float N = -INFINITY;
+                for (int x = 0; x < share; ++x) N = fmaxf(N, jml[warp + x].x);
+                M = N;
+                L = v[0] = v[1] = v[2] = v[3] = 0.f;
+                for (int x = 0; x < share; ++x) {
+                    const float2 s = jml[warp + x];
+                    const float4 y = *reinterpret_cast<const float4*>(&joined[warp + x][lane * 4]);
+                    const float g = s.x == -INFINITY ? 1.f : exp2f(s.x - N);
+                    L = fmaf(g, s.y, L);
+                    v[0] = fmaf(g, y.x, v[0]);
+                    v[1] = fmaf(g, y.y, v[1]);
+                    v[2] = fmaf(g, y.z, v[2]);
+                    v[3] = fmaf(g, y.w, v[3]);
+                }
+            }
+        }
+        if (row < rows && warp % share == 0) {
+            float N = M;
+            for (int w = 0; w < dact; ++w) N = fmaxf(N, ml[w][row].x);
+            const float g = M == -INFINITY ? 1.f : exp2f(M - N);
+            fwht_warp128(v);
+            L *= g;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= g * kInvSqrtD * (float)a.c.signs[lane * 4 + e];
+            for (int w = 0; w < dact; ++w) {
+                const float2 s = ml[w][row];
+                const float f = s.x == -INFINITY ? 1.f : exp2f(s.x - N);
+                L = fmaf(f, s.y, L);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int d = lane * 4 + e, i = d & 15, nn = d >> 4;
+                    v[e] = fmaf(f, frag[w][4 * i + 2 * (row >> 3) + (nn & 1)][(row & 7) * 4 + (nn >> 1)], v[e]);
+                }
+            }
+            // no weight at all: zeros.  A NaN sum stays NaN.
+            const float inv = L == 0.f || row >= used ? 0.f : 1.0f / L;
+            const int x = tile * kStep + row, i = x / a.ratio;
+            __nv_bfloat162 y[2];
+            y[0] = row >= used ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(v[0] * inv, v[1] * inv);
+            y[1] = row >= used ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(v[2] * inv, v[3] * inv);
+            *reinterpret_cast<uint2*>(a.o + (((int64_t)b * a.n + i) * a.Hq + h * a.ratio + x - i * a.ratio) * kPD + lane * 4) =
+                make_uint2(*reinterpret_cast<uint32_t*>(&y[0]), *reinterpret_cast<uint32_t*>(&y[1]));
+        }
+    }
 }
 
-// Joins the partial results of a row: the context's, de-rotated, and the drafts'.  One warp per row.
-__global__ void __launch_bounds__(128) kv_tree_join_kernel(TreeArgs a) {
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (r >= (int64_t)a.B * a.n * a.Hq) return;
-    const int lane = threadIdx.x & 31;
-    const float* p = a.part + r * (a.splits + 1) * (2 + kPD);
-    float M = -INFINITY;
-    bool bad = false;
-    for (int s = 0; s <= a.splits; ++s) {
-        const float m = p[s * (2 + kPD)];
-        bad |= m != m;
-        M = fmaxf(M, m);
-    }
-    float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s <= a.splits; ++s) {
-        const float* x = p + s * (2 + kPD);
-        if (x[0] == -INFINITY) continue;
-        const float f = exp2f(x[0] - M);
-        L = fmaf(f, x[1], L);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) (s == a.splits ? d : v)[e] = fmaf(f, x[2 + lane * 4 + e], (s == a.splits ? d : v)[e]);
-    }
-    fwht_warp128(v);
-    const float inv = bad ? NAN : (L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : NAN));
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        a.o[r * kPD + lane * 4 + e] =
-            __float2bfloat16_rn((v[e] * 0.08838834764831845f * (float)a.c.signs[lane * 4 + e] + d[e]) * inv);
+int sm_count() {
+    static const int n = [] {
+        int dev = 0, v = 0;
+        cudaGetDevice(&dev);
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+        return v > 0 ? v : 1;
+    }();
+    return n;
 }
 
-int64_t context_splits(int64_t max_len) { return (max_len + kChunk - 1) / kChunk; }
+struct Plan {
+    int64_t tiles, units, slots;  // tiles of 16 rows, (sequence, kv head, tile) units, partial results at most
+    int ctas;
+};
+
+// Workspace of a call.  Runs (CTAs) and units both ascend along the work, so run + unit numbers every partial result once.
+Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, int sms) {
+    Plan p{};
+    p.tiles = ((int64_t)n * (Hq / Hkv) + kStep - 1) / kStep;
+    p.units = p.tiles * Hkv * B;
+    const int64_t steps = (max_len + kStep - 1) / kStep;
+    const int64_t runs = (p.units * steps + kCtxWarps - 1) / kCtxWarps;
+    p.ctas = (int)std::min<int64_t>(sms, runs);
+    p.slots = p.ctas ? p.units + p.ctas : 0;
+    return p;
+}
+
+template <int KL, int VL>
+tq_status launch_context(const TreeArgs& a, cudaStream_t st) {
+    if (ensure_smem((const void*)kv_tree_context_kernel<KL, VL>, context_smem<KL, VL>()) != cudaSuccess) return TQ_ERR_CUDA;
+    kv_tree_context_kernel<KL, VL><<<a.ctas, 32 * kCtxWarps, context_smem<KL, VL>(), st>>>(a);
+    return launch_status();
+}
+
+constexpr int kMaxSms = 256;  // bound on the SMs that the workspace is sized for
 
 }  // namespace
 
 extern "C" size_t tq_kv_attend_tree_workspace_bytes(const tq_kv_pages_t* cache, int32_t B, int32_t n, int32_t Hq,
                                                     int64_t max_len) {
-    if (kv_pages_check(cache, false) != TQ_OK || B <= 0 || n <= 0 || Hq <= 0 || max_len < 0) return 0;
-    return (size_t)B * n * Hq * (context_splits(max_len) + 1) * (2 + kPD) * sizeof(float);
+    if (kv_pages_check(cache, false) != TQ_OK || B <= 0 || n <= 0 || Hq <= 0 || Hq % cache->Hkv || max_len < 0) return 0;
+    const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, kMaxSms);
+    return 16 + (size_t)p.slots * kStep * (kPD * sizeof(float) + sizeof(float2));
 }
 
 extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q, int64_t q_stride, tq_dtype dt,
@@ -199,8 +888,9 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
         !aligned(mask, 8))
         return TQ_ERR_INVALID;
     if (ws_bytes < tq_kv_attend_tree_workspace_bytes(cache, B, n, Hq, max_len)) return TQ_ERR_INVALID;
-    const int64_t rows = (int64_t)B * n * Hq, splits = context_splits(max_len);
-    if (rows > 0x7fffffffll || splits > 65534) return TQ_ERR_UNSUPPORTED;
+    const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, std::min(sm_count(), kMaxSms));
+    if ((int64_t)n * (Hq / cache->Hkv) > 0x3fffffffll || p.units > 0x3fffffffll || max_len > 0x7fffffffll - kStep)
+        return TQ_ERR_UNSUPPORTED;
     TreeArgs a{};
     a.c = kv_pages_view(cache);
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -217,20 +907,22 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
     a.B = B;
     a.n = n;
     a.Hq = Hq;
+    a.ratio = Hq / cache->Hkv;
     a.table_stride = table_stride;
-    a.splits = (int)splits;
+    a.ctas = std::max(p.ctas, 1);
     a.scale2 = scale * kLog2e;
     a.o = static_cast<__nv_bfloat16*>(o);
     a.part = static_cast<float*>(ws);
+    a.stat = reinterpret_cast<float2*>(a.part + (size_t)p.slots * kStep * kPD);
     a.err = err;
     cudaStream_t st = as_stream(stream);
-    const dim3 grid((unsigned)rows, (unsigned)splits + 1);
-    if (cache->kcb.levels == 256 && cache->vcb.levels == 8) kv_tree_kernel<256, 8><<<grid, 128, 0, st>>>(a);
-    else if (cache->kcb.levels == 256) kv_tree_kernel<256, 16><<<grid, 128, 0, st>>>(a);
-    else if (cache->vcb.levels == 8) kv_tree_kernel<16, 8><<<grid, 128, 0, st>>>(a);
-    else kv_tree_kernel<16, 16><<<grid, 128, 0, st>>>(a);
-    const tq_status s = launch_status();
-    if (s != TQ_OK) return s;
-    kv_tree_join_kernel<<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a);
+    if (p.ctas) {
+        tq_status s;
+        if (cache->kcb.levels == 256) s = cache->vcb.levels == 8 ? launch_context<256, 8>(a, st) : launch_context<256, 16>(a, st);
+        else s = cache->vcb.levels == 8 ? launch_context<16, 8>(a, st) : launch_context<16, 16>(a, st);
+        if (s != TQ_OK) return s;
+        return launch_pdl(kv_tree_finish_kernel, dim3((unsigned)p.units), dim3(32 * kFinWarps), 0, st, a, (int)p.tiles);
+    }
+    kv_tree_finish_kernel<<<(unsigned)p.units, 32 * kFinWarps, 0, st>>>(a, (int)p.tiles);
     return launch_status();
 }
