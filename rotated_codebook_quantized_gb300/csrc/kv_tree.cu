@@ -124,9 +124,38 @@ TQ_DEVFN float fast_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-TQ_DEVFN void cp16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
+TQ_DEVFN void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+TQ_DEVFN uint32_t lds32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+TQ_DEVFN uint32_t lds16(uint32_t at) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+    return v;
+}
+TQ_DEVFN uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+TQ_DEVFN uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+// The lane's entry of a table of 256-byte rows: the row is byte `c` of w (asm without volatile: the table
+// does not change after it is built, so the compiler may order these reads as it likes).
+template <int C>
+TQ_DEVFN uint32_t table(uint32_t w, uint32_t lane_base) {
+    uint32_t v;
+    asm("{\n .reg .b32 a;\n prmt.b32 a, %1, %2, %3;\n ld.shared.u32 %0, [a];\n}\n"
+        : "=r"(v)
+        : "r"(w), "r"(lane_base), "n"(0x6504 | (C << 4)));
+    return v;
 }
 // 2^-e just above x's magnitude, as an exponent: 0 for 0, infinities and NaN.
 TQ_DEVFN int exponent_above(float x) {
@@ -141,23 +170,34 @@ struct Stage {
     static constexpr int kVRow = VL == 16 ? 80 : 52;                // of a value row: 4-bit rows (64) spread over the banks
     static constexpr int kK = 0, kV = kStep * kKRow, kKs = kV + kStep * kVRow, kVs = kKs + 256, kBytes = kVs + 256;
 };
-constexpr int kLutBytes = 256 * 256;
-
+// Shared memory of the context kernel.  The decode table (256 rows of 256 bytes) starts at shared address
+// 64 K, so that one byte permute builds the address of an entry (64 K + code * 256 + lane * 4); the rings of
+// the first kLowWarps warps lie below it, the others above.
+constexpr uint32_t kTable = 65536, kTableEnd = 131072;
+constexpr int kLowWarps = 5;
+constexpr uint32_t kSmemStart = 1024 + 512;  // of the space below: the system's first KB, then the static variables
+constexpr uint32_t kQueries = kSmemStart, kFactors = kQueries + kStep * kPD * 2, kRingsLow = kFactors + kStep * 4;
 template <int KL, int VL>
-constexpr size_t context_smem() {
-    const size_t rings = (size_t)kCtxWarps * kDepth * Stage<KL, VL>::kBytes;
-    const size_t join = (size_t)kCtxWarps * (64 * kFragPad * sizeof(float) + kStep * sizeof(float2));  // over the rings
-    return kLutBytes + kStep * kPD * 2 + kStep * 4 + (rings > join ? rings : join);
+constexpr uint32_t warp_region() {  // a warp's ring, and its fragments of the join over it
+    const uint32_t ring = kDepth * Stage<KL, VL>::kBytes, join = 64 * kFragPad * 4 + kStep * 8;
+    return ((ring > join ? ring : join) + 127) / 128 * 128;
+}
+template <int KL, int VL>
+constexpr uint32_t context_smem_end() {
+    static_assert(kRingsLow % 16 == 0 && kRingsLow + kLowWarps * warp_region<KL, VL>() <= kTable, "rings below the table");
+    return kTableEnd + (kCtxWarps - kLowWarps) * warp_region<KL, VL>();
 }
 
 template <int KL, int VL>
 __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(TreeArgs a) {
     using S = Stage<KL, VL>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* lut = smem;                                                   // [256][key lanes 32 | value lanes 32] words
-    __half* qh = reinterpret_cast<__half*>(smem + kLutBytes);              // [16][128] rotated queries
-    float* qf = reinterpret_cast<float*>(qh + kStep * kPD);                // [16] factor from a row's products to log2 scores
-    uint8_t* rings = reinterpret_cast<uint8_t*>(qf + kStep);
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t* const space = smem - (uint32_t)__cvta_generic_to_shared(smem);  // shared address 0
+    __half* qh = reinterpret_cast<__half*>(space + kQueries);  // [16][128] rotated queries
+    float* qf = reinterpret_cast<float*>(space + kFactors);    // [16] factor from a row's products to log2 scores
+    auto region = [&](int w) {  // of a warp
+        return w < kLowWarps ? kRingsLow + w * warp_region<KL, VL>() : kTableEnd + (w - kLowWarps) * warp_region<KL, VL>();
+    };
     __shared__ Work s_before;
     __shared__ long long s_total;
     __shared__ int s_b;
@@ -213,7 +253,7 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
     const int ev = exponent_above(fmaxf(fabsf(a.c.vcent[0]), fabsf(a.c.vcent[VL - 1])));
     const float kd = exp2f((float)-ek), vd = exp2f((float)-ev);
     for (int c = warp; c < 256; c += kCtxWarps) {
-        uint32_t* row = reinterpret_cast<uint32_t*>(lut + c * 256);
+        uint32_t* row = reinterpret_cast<uint32_t*>(space + kTable + c * 256);
         row[lane] = KL == 256 ? pack_f16(a.c.kcent[c % KL] * kd, 0.f)
                               : pack_f16(a.c.kcent[(c & 15) % KL] * kd, a.c.kcent[(c >> 4) % KL] * kd);
         if (VL == 16) row[32 + lane] = pack_f16(a.c.vcent[(c & 15) % VL] * vd, a.c.vcent[(c >> 4) % VL] * vd);
@@ -237,8 +277,21 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
     long long base = s_before.steps;
     int ubase = s_before.units;
     const int ng = kPD >> a.c.lgroup;
-    uint8_t* ring = rings + warp * kDepth * S::kBytes;
-    const uint32_t lane4 = lane * 4;
+    const uint32_t ring = region(warp), ring_end = ring + kDepth * S::kBytes;
+    // bytes 0 .. 2 of a table address beside the code: lane * 4 in byte 0, the table's 64 K in byte 2
+    const uint32_t lane_k = lane * 4 | 0x100, lane_v = lane_k + 128;
+    // rows by the 16 (all strides are whole 16s): 32 bits are enough
+    const uint32_t page16 = (uint32_t)(a.c.page_stride >> 4), head16 = (uint32_t)(a.c.head_stride >> 4);
+    const uint32_t in_page = (1u << (a.c.lpage - 4)) - 1;
+    const uint8_t* kc = reinterpret_cast<const uint8_t*>(a.c.kcodes) + lane * 16;
+    const uint8_t* vc = reinterpret_cast<const uint8_t*>(a.c.vcodes) + lane * 16;
+    const uint8_t* zc = reinterpret_cast<const uint8_t*>(lane < 16 ? a.c.kscales : a.c.vscales) + (lane & 15) * 16;
+    // places of the lane's 16-byte pieces in a stage.  128-byte key rows: chunks of odd rows swapped in pairs, so
+    // that eight lanes of a read (two rows, every other chunk) meet all banks.
+    const uint32_t dk = S::kK + (KL == 256 ? lane ^ ((lane >> 3) & 1) : lane) * 16;
+    const uint32_t dv = S::kV + (VL == 16 ? (lane >> 2) * S::kVRow + (lane & 3) * 16 : lane * 16);
+    const uint32_t dz = (lane < 16 ? S::kKs : S::kVs) + (lane & 15) * 16;
+    const bool copies_z = (lane & 15) < 2 * ng;
 
     while (p < pend) {
         int steps = seq_steps(a, b), tiles = seq_tiles(a, b);
@@ -273,10 +326,10 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
 #pragma unroll
             for (int m = 16; m; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, m));
             const int e = exponent_above(mx);
-            const float d = exp2f((float)-e);
+            const float d = a.scale2 < 0.f ? -exp2f((float)-e) : exp2f((float)-e);  // a factor below is not negative
             *reinterpret_cast<uint2*>(qh + row * kPD + lane * 4) =
                 make_uint2(pack_f16(v[0] * d, v[1] * d), pack_f16(v[2] * d, v[3] * d));
-            if (lane == 0) qf[row] = exp2f((float)(e + ek)) * (kInvSqrtD * a.scale2);
+            if (lane == 0) qf[row] = exp2f((float)(e + ek)) * (kInvSqrtD * fabsf(a.scale2));
         }
         __syncthreads();
         // A operand of product step s: the lane's rows r and r + 8, dims 32 j + 4 s .. + 3.  Any order
@@ -291,119 +344,100 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
         }
         const float f0 = qf[r], f1 = qf[r + 8];
 
-        const int cnt = s1 - s0 > warp ? (s1 - s0 - warp + kCtxWarps - 1) / kCtxWarps : 0;  // steps of this warp
         const int32_t* tab = a.table + (int64_t)b * a.table_stride;
         uint32_t okbits = 0;
-        auto page_of = [&](int it) {
-            return it < cnt ? __ldg(tab + (((s0 + warp + it * kCtxWarps) * kStep) >> a.c.lpage)) : 0;
-        };
-        int page_next = page_of(0);
-        auto issue = [&](int it) {  // step `it` of this warp into its ring
+        auto page_of = [&](int st) { return st < s1 ? __ldg(tab + (st >> (a.c.lpage - 4))) : 0; };
+        int ahead = s0 + warp, page_next = page_of(ahead);  // next step to copy, and its page
+        uint32_t fill = ring;                               // and its place
+        auto issue = [&]() {
             const int page = page_next;
-            page_next = page_of(it + 1);
-            if (it < cnt) {
-                const int t = (s0 + warp + it * kCtxWarps) * kStep;
-                const bool ok = page >= 0 && page < a.c.pages;
-                okbits = (okbits & ~(1u << (it & 31))) | ((uint32_t)ok << (it & 31));
-                if (ok) {
-                    const int64_t row = (int64_t)page * a.c.page_stride + (int64_t)h * a.c.head_stride +
-                                        (t & ((1 << a.c.lpage) - 1));
-                    uint8_t* st = ring + (it % kDepth) * S::kBytes;
-                    const uint8_t* kc = reinterpret_cast<const uint8_t*>(a.c.kcodes) + row * S::kKRow;
+            const uint32_t row16 = (uint32_t)page * page16 + h * head16 + (ahead & in_page);
+            page_next = page_of(ahead + kCtxWarps);
+            okbits <<= 1;
+            if (ahead < s1) {
+                if ((uint32_t)page < (uint32_t)a.c.pages) {
+                    okbits |= 1;
+                    const uint8_t* k = kc + (uint64_t)row16 * (kStep * S::kKRow);
 #pragma unroll
-                    for (int x = 0; x < kStep * S::kKRow / 512; ++x) {
-                        const int c = lane + 32 * x;
-                        // 128-byte rows: chunks of odd rows swapped in pairs, so that eight lanes of a read
-                        // (two rows, every other chunk) meet all banks
-                        const int d = KL == 256 ? c ^ ((c >> 3) & 1) : c;
-                        cp16(st + S::kK + d * 16, kc + c * 16);
-                    }
-                    const uint8_t* vc = reinterpret_cast<const uint8_t*>(a.c.vcodes) + row * (KvBook<VL>::kWords * 4);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int c = lane + 32 * x;
-                        if (c < kStep * KvBook<VL>::kWords / 4)
-                            cp16(st + S::kV + (VL == 16 ? (c >> 2) * S::kVRow + (c & 3) * 16 : c * 16), vc + c * 16);
-                    }
-                    const int c = lane & 15;
-                    if (c < 2 * ng)
-                        cp16(st + (lane < 16 ? S::kKs : S::kVs) + c * 16,
-                             reinterpret_cast<const uint8_t*>((lane < 16 ? a.c.kscales : a.c.vscales) + row * ng) + c * 16);
+                    for (int x = 0; x < kStep * S::kKRow / 512; ++x) cp16(fill + dk + 512 * x, k + 512 * x);
+                    const uint8_t* v = vc + (uint64_t)row16 * (kStep * KvBook<VL>::kWords * 4);
+                    cp16(fill + dv, v);
+                    if (VL == 16 || lane < kStep * KvBook<VL>::kWords / 4 - 32)
+                        cp16(fill + dv + (VL == 16 ? 8 * S::kVRow : 512), v + 512);
+                    if (copies_z) cp16(fill + dz, zc + (uint64_t)row16 * (uint32_t)(kStep * 2 * ng));
                 } else if (lane == 0 && a.err) {
                     atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
+            ahead += kCtxWarps;
+            fill = fill + S::kBytes == ring_end ? ring : fill + S::kBytes;
         };
 
         float o[16][4];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        // running maxima (log2) of rows r and r + 8, their negatives (0 while there is none), and the rows' sums
+        float m0 = -INFINITY, m1 = -INFINITY, b0 = 0.f, b1 = 0.f, l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int it = 0; it < kDepth - 1; ++it) issue(it);
+        for (int it = 0; it < kDepth - 1; ++it) issue();
         // scale places of the lane: keys' dims 32 j and 32 j + 16, values' dims 16 r
         const int gk0 = (32 * j) >> a.c.lgroup, gk1 = (32 * j + 16) >> a.c.lgroup, gv = (16 * r) >> a.c.lgroup;
-        // 3-bit values: dims 16 r .. + 15 begin at code `rem` of word w0 (ten to a word)
-        const int w0 = (16 * r) / 10, rem = (16 * r) % 10;
-        const int sh0 = 3 * rem, sh1 = rem == 0 ? 24 : 3 * (rem - 2);
+        // 3-bit values: dims 16 r .. + 7 begin at code c0 of word w0 (ten to a word), dims 16 r + 8 .. at c1 of w1
+        const int w0 = (16 * r) / 10, c0 = (16 * r) % 10, w1 = (16 * r + 8) / 10, c1 = (16 * r + 8) % 10;
+        const uint32_t k_at = S::kK + r * S::kKRow + (KL == 256 ? 0 : j * 16);
+        const uint32_t kx = KL == 256 ? ((2 * j) ^ (r & 1)) * 16 : 0;  // of the first 16 dims; the other's is ^ 16 (8-bit) or + 8
+        const uint32_t ks0 = S::kKs + (r * ng + gk0) * 2, ks1 = S::kKs + (r * ng + gk1) * 2;
+        const uint32_t vs_at = S::kVs + (2 * j * ng + gv) * 2;
+        const uint32_t v_at = S::kV + 2 * j * S::kVRow + (VL == 8 ? 0 : r * 8);
+        uint32_t st = ring;
 #pragma unroll 1
-        for (int it = 0; it < cnt; ++it) {
-            issue(it + kDepth - 1);
+        for (int step = s0 + warp; step < s1; step += kCtxWarps) {
+            issue();
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
             __syncwarp();
-            if ((okbits >> (it & 31)) & 1) {
-                const uint8_t* st = ring + (it % kDepth) * S::kBytes;
-                const int t0 = (s0 + warp + it * kCtxWarps) * kStep, left = len - t0;  // tokens of the step
-                // ---- scores of tokens r (tile 0) and r + 8 (tile 1)
+            if ((okbits >> (kDepth - 1)) & 1) {
+                const int left = len - step * kStep;  // tokens of the step
+                // ---- products of the rows with tokens r (tile 0) and r + 8 (tile 1)
                 float sc[2][4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int tok = r + 8 * e;
                     sc[e][0] = sc[e][1] = sc[e][2] = sc[e][3] = 0.f;
-                    const uint16_t* ks = reinterpret_cast<const uint16_t*>(st + S::kKs) + tok * ng;
-                    const uint32_t s_lo = ks[gk0] * 0x10001u, s_hi = ks[gk1] * 0x10001u;
+                    const uint32_t s_lo = lds16(st + ks0 + 16 * e * ng) * 0x10001u, s_hi = lds16(st + ks1 + 16 * e * ng) * 0x10001u;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t s2 = half ? s_hi : s_lo;
                         if constexpr (KL == 256) {
-                            const uint4 w4 = *reinterpret_cast<const uint4*>(st + S::kK + tok * 128 +
-                                                                             ((2 * j + half) ^ (r & 1)) * 16);
+                            const uint4 w4 = lds128(st + k_at + 8 * S::kKRow * e + (kx ^ (16 * half)));
                             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t v[4];
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)  // byte 1: the code, byte 0: the lane's bank
-                                    v[c] = *reinterpret_cast<const uint32_t*>(lut + prmt(w[i], lane4, 0x5504u | (c << 4)));
-                                mma_f16(sc[e], qa[4 * half + i], mul2(prmt(v[0], v[1], 0x5410), s2),
-                                        mul2(prmt(v[2], v[3], 0x5410), s2));
-                            }
+                            for (int i = 0; i < 4; ++i)
+                                mma_f16(sc[e], qa[4 * half + i],
+                                        mul2(prmt(table<0>(w[i], lane_k), table<1>(w[i], lane_k), 0x5410), s2),
+                                        mul2(prmt(table<2>(w[i], lane_k), table<3>(w[i], lane_k), 0x5410), s2));
                         } else {
-                            const uint2 w2 = *reinterpret_cast<const uint2*>(st + S::kK + tok * 64 + j * 16 + half * 8);
+                            const uint2 w2 = lds64(st + k_at + 8 * S::kKRow * e + 8 * half);
                             const uint32_t w[2] = {w2.x, w2.y};
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                uint32_t v[4];
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    v[c] = *reinterpret_cast<const uint32_t*>(lut + prmt(w[i], lane4, 0x5504u | (c << 4)));
-                                mma_f16(sc[e], qa[4 * half + 2 * i], mul2(v[0], s2), mul2(v[1], s2));
-                                mma_f16(sc[e], qa[4 * half + 2 * i + 1], mul2(v[2], s2), mul2(v[3], s2));
+                                mma_f16(sc[e], qa[4 * half + 2 * i], mul2(table<0>(w[i], lane_k), s2),
+                                        mul2(table<1>(w[i], lane_k), s2));
+                                mma_f16(sc[e], qa[4 * half + 2 * i + 1], mul2(table<2>(w[i], lane_k), s2),
+                                        mul2(table<3>(w[i], lane_k), s2));
                             }
                         }
                     }
                 }
-                // ---- log2 scores, tokens past the end left out; columns 8 e + 2 j + {0, 1}
+                if (left < kStep) {  // tokens past the end are left out; columns 8 e + 2 j + {0, 1}
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const bool in = 8 * e + 2 * j + (c & 1) < left;
-                        sc[e][c] = in ? sc[e][c] * (c < 2 ? f0 : f1) : -INFINITY;
-                    }
-                const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-                const float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+                        for (int c = 0; c < 4; ++c)
+                            if (8 * e + 2 * j + (c & 1) >= left) sc[e][c] = -INFINITY;
+                }
+                // log2 scores are products times f0 and f1, which are not negative
+                const float x0 = f0 * fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+                const float x1 = f1 * fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
                 // the maximum follows only when a score passes it by kSlack: weights stay below 2^8, well inside fp16
                 if (__any_sync(kFull, x0 > m0 + kSlack || x1 > m1 + kSlack)) {
                     float n0 = x0, n1 = x1;
@@ -417,8 +451,10 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
                     const float g0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0), g1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
                     m0 = n0;
                     m1 = n1;
-                    l0 *= g0;
-                    l1 *= g1;
+                    b0 = m0 == -INFINITY ? 0.f : -m0;
+                    b1 = m1 == -INFINITY ? 0.f : -m1;
+                    l[0] *= g0;
+                    l[2] *= g1;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         o[i][0] *= g0;
@@ -427,36 +463,34 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
                         o[i][3] *= g1;
                     }
                 }
-                const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
                 uint32_t pa[4];  // weights as the A operand: the score fragment is already in its order
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float w00 = fast_exp2(sc[e][0] - b0), w01 = fast_exp2(sc[e][1] - b0);
-                    const float w10 = fast_exp2(sc[e][2] - b1), w11 = fast_exp2(sc[e][3] - b1);
-                    l0 += w00 + w01;
-                    l1 += w10 + w11;
-                    pa[2 * e] = pack_f16(w00, w01);
-                    pa[2 * e + 1] = pack_f16(w10, w11);
+                    pa[2 * e] = pack_f16(fast_exp2(fmaf(sc[e][0], f0, b0)), fast_exp2(fmaf(sc[e][1], f0, b0)));
+                    pa[2 * e + 1] = pack_f16(fast_exp2(fmaf(sc[e][2], f1, b1)), fast_exp2(fmaf(sc[e][3], f1, b1)));
                 }
+                mma_f16(l, pa, 0x3c003c00u, 0x3c003c00u);  // their sums: a product with ones
                 // ---- weighted values: tokens 2 j, 2 j + 1 and 2 j + 8, 2 j + 9, dims 16 r + i in tile i
-                const uint16_t* vs = reinterpret_cast<const uint16_t*>(st + S::kVs);
                 uint32_t s2[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int tok = 8 * e + 2 * j;
-                    const uint32_t sa = tok < left ? vs[tok * ng + gv] : 0u, sb = tok + 1 < left ? vs[(tok + 1) * ng + gv] : 0u;
-                    s2[e] = sa | (sb << 16);
+                    const uint32_t at = st + vs_at + 16 * e * ng;
+                    s2[e] = lds16(at) | (lds16(at + 2 * ng) << 16);
+                }
+                if (left < kStep) {  // a scale past the end may be anything
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        s2[e] &= (8 * e + 2 * j < left ? 0xffffu : 0u) | (8 * e + 2 * j + 1 < left ? 0xffff0000u : 0u);
                 }
                 if constexpr (VL == 8) {
-                    uint32_t bits[2][2][2];  // [pair][token][dims 8 q .. + 7]
+                    uint32_t bits[2][2][2];  // [pair][token][dims 8 q .. + 7]: 24 bits, then whatever follows
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const uint32_t* w = reinterpret_cast<const uint32_t*>(st + S::kV) + (8 * e + 2 * j + x) * 13 + w0;
-                            const uint32_t wa = w[0], wb = w[1], wc = r == 7 ? 0u : w[2];
-                            bits[e][x][0] = (wa >> sh0) | (wb << (30 - sh0));
-                            bits[e][x][1] = rem == 0 ? (wa >> 24) | (wb << 6) : (wb >> sh1) | (wc << (30 - sh1));
+                            const uint32_t at = st + v_at + (8 * e + x) * S::kVRow;
+                            bits[e][x][0] = (lds32(at + 4 * w0) >> (3 * c0)) + lds32(at + 4 * w0 + 4) * (1u << (30 - 3 * c0));
+                            bits[e][x][1] = (lds32(at + 4 * w1) >> (3 * c1)) + lds32(at + 4 * w1 + 4) * (1u << (30 - 3 * c1));
                         }
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
@@ -485,52 +519,48 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
                         for (int i = 0; i < 8; ++i) mma_f16(o[8 * q + i], pa, v[0][i], v[1][i]);
                     }
                 } else {
-                    uint2 w[2][2];
+                    uint32_t w[2][2][2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            w[e][x] = *reinterpret_cast<const uint2*>(st + S::kV + (8 * e + 2 * j + x) * S::kVRow + r * 8);
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) {  // byte y of the 16 dims: dims 2 y and 2 y + 1
+                        for (int x = 0; x < 2; ++x) {
+                            const uint2 y = lds64(st + v_at + (8 * e + x) * S::kVRow);
+                            w[e][x][0] = y.x;
+                            w[e][x][1] = y.y;
+                        }
+                    static_for<0, 8>([&](auto yc) {  // byte y of the 16 dims: dims 2 y and 2 y + 1
+                        constexpr int y = decltype(yc)::value;
                         uint32_t lo[2], hi[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            uint32_t v[2];
-#pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                v[x] = *reinterpret_cast<const uint32_t*>(
-                                    lut + 128 + prmt(y < 4 ? w[e][x].x : w[e][x].y, lane4, 0x5504u | ((y & 3) << 4)));
-                            lo[e] = mul2(prmt(v[0], v[1], 0x5410), s2[e]);
-                            hi[e] = mul2(prmt(v[0], v[1], 0x7632), s2[e]);
+                            const uint32_t va = table<(y & 3)>(w[e][0][y >> 2], lane_v), vb = table<(y & 3)>(w[e][1][y >> 2], lane_v);
+                            lo[e] = mul2(prmt(va, vb, 0x5410), s2[e]);
+                            hi[e] = mul2(prmt(va, vb, 0x7632), s2[e]);
                         }
                         mma_f16(o[2 * y], pa, lo[0], lo[1]);
                         mma_f16(o[2 * y + 1], pa, hi[0], hi[1]);
-                    }
+                    });
                 }
             }
-            __syncwarp();  // the ring slot is free for the copy after next
+            __syncwarp();  // the ring slot is free for the next copy
+            st = st + S::kBytes == ring_end ? ring : st + S::kBytes;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
 
         // ---- join the warps: fragments through shared memory (over the rings)
-        l0 += __shfl_xor_sync(kFull, l0, 1);
-        l0 += __shfl_xor_sync(kFull, l0, 2);
-        l1 += __shfl_xor_sync(kFull, l1, 1);
-        l1 += __shfl_xor_sync(kFull, l1, 2);
-        __syncthreads();
         const int act = min(kCtxWarps, s1 - s0);
-        float* frag = reinterpret_cast<float*>(rings);                 // [warp][64][33]
-        float2* ml = reinterpret_cast<float2*>(frag + kCtxWarps * 64 * kFragPad);  // [warp][16]
+        auto frag = [&](int w) { return reinterpret_cast<float*>(space + region(w)); };                            // [64][33]
+        auto ml = [&](int w) { return reinterpret_cast<float2*>(space + region(w) + 64 * kFragPad * 4); };  // [16]
+        __syncwarp();
         if (warp < act) {
-            float* f = frag + warp * 64 * kFragPad + lane;
+            float* f = frag(warp) + lane;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) f[(4 * i + c) * kFragPad] = o[i][c];
             if (j == 0) {
-                ml[warp * kStep + r] = make_float2(m0, l0);
-                ml[warp * kStep + r + 8] = make_float2(m1, l1);
+                ml(warp)[r] = make_float2(m0, l[0]);
+                ml(warp)[r + 8] = make_float2(m1, l[2]);
             }
         }
         __syncthreads();
@@ -540,13 +570,13 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
             const int row = x >> 7, d = x & 127, i = d & 15, nn = d >> 4;
             const int at = (4 * i + 2 * (row >> 3) + (nn & 1)) * kFragPad + (row & 7) * 4 + (nn >> 1);
             float M = -INFINITY;
-            for (int w = 0; w < act; ++w) M = fmaxf(M, ml[w * kStep + row].x);
+            for (int w = 0; w < act; ++w) M = fmaxf(M, ml(w)[row].x);
             float L = 0.f, acc = 0.f;
             for (int w = 0; w < act; ++w) {
-                const float2 s = ml[w * kStep + row];
+                const float2 s = ml(w)[row];
                 const float g = s.x == -INFINITY ? 1.f : fast_exp2(s.x - M);  // nothing seen: zeros, or NaN scores
                 L = fmaf(g, s.y, L);
-                acc = fmaf(g, frag[w * 64 * kFragPad + at], acc);
+                acc = fmaf(g, frag(w)[at], acc);
             }
             a.part[(slot * kStep + row) * kPD + d] = acc * vscale;
             if (d == 0) a.stat[slot * kStep + row] = make_float2(M, L);
@@ -850,8 +880,18 @@ Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, i
 
 template <int KL, int VL>
 tq_status launch_context(const TreeArgs& a, cudaStream_t st) {
-    if (ensure_smem((const void*)kv_tree_context_kernel<KL, VL>, context_smem<KL, VL>()) != cudaSuccess) return TQ_ERR_CUDA;
-    kv_tree_context_kernel<KL, VL><<<a.ctas, 32 * kCtxWarps, context_smem<KL, VL>(), st>>>(a);
+    constexpr size_t smem = context_smem_end<KL, VL>() - 1024;  // from the start of the dynamic part, wherever it is
+    static const bool fits = [] {  // the system's part and the static variables end below kSmemStart
+        int dev = 0, reserved = 0;
+        cudaFuncAttributes at{};
+        return cudaGetDevice(&dev) == cudaSuccess &&
+               cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) == cudaSuccess &&
+               cudaFuncGetAttributes(&at, (const void*)kv_tree_context_kernel<KL, VL>) == cudaSuccess &&
+               reserved >= 1024 && reserved + at.sharedSizeBytes <= kSmemStart;
+    }();
+    if (!fits) return TQ_ERR_UNSUPPORTED;
+    if (ensure_smem((const void*)kv_tree_context_kernel<KL, VL>, smem) != cudaSuccess) return TQ_ERR_CUDA;
+    kv_tree_context_kernel<KL, VL><<<a.ctas, 32 * kCtxWarps, smem, st>>>(a);
     return launch_status();
 }
 
@@ -891,6 +931,8 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
     const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, std::min(sm_count(), kMaxSms));
     if ((int64_t)n * (Hq / cache->Hkv) > 0x3fffffffll || p.units > 0x3fffffffll || max_len > 0x7fffffffll - kStep)
         return TQ_ERR_UNSUPPORTED;
+    // cache rows by the 16 are 32-bit numbers
+    if ((cache->pages * cache->page_stride + cache->Hkv * cache->head_stride) / 16 > 0xffffffffll) return TQ_ERR_UNSUPPORTED;
     TreeArgs a{};
     a.c = kv_pages_view(cache);
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -910,7 +952,8 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
     a.ratio = Hq / cache->Hkv;
     a.table_stride = table_stride;
     a.ctas = std::max(p.ctas, 1);
-    a.scale2 = scale * kLog2e;
+    // a scale of 0 (all weights equal) as one that no score feels: masked scores are -infinity times a factor
+    a.scale2 = fabsf(scale) < 1e-30f ? 1e-30f : scale * kLog2e;
     a.o = static_cast<__nv_bfloat16*>(o);
     a.part = static_cast<float*>(ws);
     a.stat = reinterpret_cast<float2*>(a.part + (size_t)p.slots * kStep * kPD);
