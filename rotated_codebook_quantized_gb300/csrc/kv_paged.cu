@@ -5,6 +5,8 @@
 // vector is tq_kv_quantize's; a token's row is found through its slot.
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kv_pages.cuh"
 #include "rope.cuh"
@@ -13,7 +15,115 @@ using namespace tq;
 
 namespace {
 
+// Both kernels: four lanes to a (token, kv head), key and value together; a warp takes eight consecutive tokens of a
+// head, so that their cache rows are one run of bytes.  Lane l of four holds elements 32 m + 8 l + i (m < 4, i < 8) of
+// both vectors, the key's in the low and the value's in the high half of a 64-bit pair: the Hadamard butterflies of
+// both are one packed fp32 instruction, strides 1, 2, 4, 32, 64 stay in the lane and 8, 16 are two shuffles; rows are
+// read and written 16 bytes a lane, 64 bytes in a piece.
 constexpr int kWarps = 8;
+constexpr int kVecs = 8;  // tokens of a warp
+constexpr float kInvSqrtD = 0.08838834764831845f;  // 1 / sqrt(128)
+
+using f2 = unsigned long long;  // (key, value) as packed fp32
+TQ_DEVFN f2 pk(float k, float v) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(k), "f"(v));
+    return r;
+}
+TQ_DEVFN float2 un(f2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+TQ_DEVFN f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+TQ_DEVFN f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+TQ_DEVFN f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Unnormalised Walsh-Hadamard transform of both vectors, x[8 m + i]; the strides ascend as in fwht_warp128, so the
+// sums round the same way.
+TQ_DEVFN void fwht_pair(f2 (&x)[32]) {
+    const f2 minus = pk(-1.f, -1.f);
+    auto inside = [&](int h) {  // stride h of x's own index
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (!(e & h)) {
+                const f2 p = x[e], q = x[e + h];
+                x[e] = add2(p, q);
+                x[e + h] = fma2(q, minus, p);
+            }
+    };
+    inside(1);
+    inside(2);
+    inside(4);
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1) {
+        const float sg = (threadIdx.x & m) ? -1.f : 1.f;
+        const f2 sg2 = pk(sg, sg);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const float2 v = un(x[e]);
+            x[e] = fma2(x[e], sg2, pk(__shfl_xor_sync(kFull, v.x, m), __shfl_xor_sync(kFull, v.y, m)));
+        }
+    }
+    inside(8);
+    inside(16);
+}
+
+// The lane's signs, both vectors': +-factor.
+TQ_DEVFN float sign_of(uint2 w, int i, float factor) {
+    return (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3))) < 0 ? -factor : factor;
+}
+
+TQ_DEVFN void load8(const void* p, int64_t at, int dt, float (&y)[8]) {
+    if (dt == TQ_BF16) {
+        const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p) + at);
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[2 * i] = __uint_as_float(v[i] << 16);
+            y[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+        }
+    } else {
+        const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
+        const float4 a = f[0], b = f[1];
+        y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
+    }
+}
+
+TQ_DEVFN void store8(void* p, int64_t at, int dt, const float (&y)[8]) {
+    if (dt == TQ_F32) {
+        float4* f = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + at);
+        f[0] = make_float4(y[0], y[1], y[2], y[3]);
+        f[1] = make_float4(y[4], y[5], y[6], y[7]);
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (dt == TQ_BF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------- write
 
 struct AppendArgs {
     KvPages c;
@@ -25,93 +135,256 @@ struct AppendArgs {
     const uint64_t* steps;
     int lrot, interleaved;  // log2 of the rotary length
     float factor;
+    int heads;  // of a warp's unit
     int dt;
     uint32_t* err;
 };
 
-// One warp per (token, head): K, then V.
-template <int KL, int VL>
-__global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(AppendArgs a) {
-    __shared__ float kt[256], vt[16];
-    __shared__ uint8_t cd[kWarps][kPD];
-    for (int i = threadIdx.x; i < KL - 1; i += blockDim.x) kt[i] = a.c.kthr[i];
-    for (int i = threadIdx.x; i < VL - 1; i += blockDim.x) vt[i] = a.c.vthr[i];
-    __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t vec = (int64_t)blockIdx.x * kWarps + warp;
-    if (vec >= a.T * a.c.Hkv) return;
-    const int64_t t = vec / a.c.Hkv;
-    const int h = (int)(vec - t * a.c.Hkv);
-    const int32_t slot = a.slots[t];
-    if (slot < 0) return;
-    if ((int64_t)slot >= a.c.pages << a.c.lpage) {
-        if (lane == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
-        return;
+// Keys' 255 thresholds through 1024 equal bins over [-4.5, 4.5): bin(x) is the same float expression for thresholds and
+// values, hence monotone, and a Lloyd-Max book's thresholds are further apart than a bin is wide (0.0169 against
+// 0.0088), so code = (thresholds of lower bins) + (the bin's own < u).  Other books, and calls too small to pay for the
+// table, search the thresholds.
+constexpr int kBins = 1024;
+TQ_DEVFN int bin_of(float x) { return min(max(__float2int_rd((x + 4.5f) * (kBins / 9.0f)), 0), kBins - 1); }
+
+TQ_DEVFN int count_below(const float* t, int n, float u) {  // thresholds strictly below u
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (t[mid] < u) lo = mid + 1; else hi = mid;
     }
-    const int64_t row = a.c.row(slot, h);
-    const int group = 1 << a.c.lgroup, lpg = group / 4;
-    for (int which = 0; which < 2; ++which) {
-        const int64_t src = t * (which ? a.vs : a.ks) + (int64_t)h * kPD;
-        float x[4];
+    return lo;
+}
+
+// Rotary positions of the lane's key elements.  Half pairs lie 64, 32 or 16 elements apart: in the lane's own other
+// rows (m + 2, m + 1) or two lanes on.
+struct Turn {
+    float cs[16], sn[16];
+};
+TQ_DEVFN void turn_angles(const AppendArgs& a, int32_t pos, int l, Turn& w) {
+    const int half = 1 << (a.lrot - 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = load_as_float(which ? a.v : a.k, src + lane * 4 + i, a.dt);
-        if (which == 0 && a.steps) {
-            const int rotary = 1 << a.lrot, half = rotary / 2;
-            float y[4];
+    for (int z = 0; z < 16; ++z) {
+        // interleaved: pairs 16 m + 4 l + 0 .. 3 at z = 4 m + ..; half: pairs 32 m + 8 l + i at z = 8 m + i
+        const int pair = a.interleaved ? 16 * (z >> 2) + 4 * l + (z & 3) : (32 * (z >> 3) + 8 * l + (z & 7)) & (half - 1);
+        const bool in = a.interleaved ? pair < half : (z < 8 || a.lrot == 7);
+        float s = 0.f, c = 1.f;
+        if (in) rope_angle(pos, a.steps[pair], s, c);
+        w.sn[z] = s * a.factor;
+        w.cs[z] = c * a.factor;
+    }
+}
+TQ_DEVFN void turn_keys(const AppendArgs& a, const Turn& w, int l, float (&k)[32]) {
+    auto pair = [&](float& x, float& y, int z) {
+        const float p = x * w.cs[z] - y * w.sn[z], q = x * w.sn[z] + y * w.cs[z];
+        x = p;
+        y = q;
+    };
+    if (a.interleaved) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = lane * 4 + i;
-                const float o = a.interleaved ? x[i ^ 1] : __shfl_xor_sync(kFull, x[i], half / 4);
-                const int pair = a.interleaved ? e >> 1 : e & (half - 1);
-                const bool second = a.interleaved ? (i & 1) : (e & half);
-                float sn = 0.f, cs = 1.f;
-                if (e < rotary) {
-                    rope_angle(a.pos[t], a.steps[pair], sn, cs);
-                    sn *= second ? a.factor : -a.factor;
-                    cs *= a.factor;
-                }
-                y[i] = e < rotary ? x[i] * cs + o * sn : x[i];
-            }
+        for (int z = 0; z < 16; ++z)
+            if ((z >> 2) < 1 << (a.lrot - 5)) pair(k[8 * (z >> 2) + 2 * (z & 3)], k[8 * (z >> 2) + 2 * (z & 3) + 1], z);
+    } else if (a.lrot == 7) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = y[i];
-        }
+        for (int z = 0; z < 16; ++z) pair(k[z], k[z + 16], z);
+    } else if (a.lrot == 6) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] *= (float)a.c.signs[lane * 4 + i];
-        fwht_warp128(x);
-        float ss = 0.f;
+        for (int z = 0; z < 8; ++z) pair(k[z], k[z + 8], z);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] *= 0.08838834764831845f;  // 1 / sqrt(128)
-            ss += x[i] * x[i];
-        }
-        for (int m = 1; m < lpg; m <<= 1) ss += __shfl_xor_sync(kFull, ss, m);
-        const float s = sqrtf(ss / (float)group);
-        uint16_t* scales = which ? a.c.vscales : a.c.kscales;
-        if ((lane & (lpg - 1)) == 0)
-            scales[(row << (7 - a.c.lgroup)) + lane / lpg] = __half_as_ushort(__float2half_rn(s));
-        const float* thr = which ? vt : kt;
-        const int n = (which ? VL : KL) - 1;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float u = s > 0.f ? x[i] / s : 0.f;
-            int lo = 0, hi = n;  // thresholds strictly below u
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (thr[mid] < u) lo = mid + 1; else hi = mid;
-            }
-            cd[warp][lane * 4 + i] = (uint8_t)lo;
-        }
-        __syncwarp();
-        const int bits = which ? KvBook<VL>::kBits : KvBook<KL>::kBits, cw = 32 / bits;
-        const int words = which ? KvBook<VL>::kWords : KvBook<KL>::kWords;
-        if (lane < words) {
-            uint32_t w = 0;
-            for (int i = 0; i < cw && lane * cw + i < kPD; ++i) w |= (uint32_t)cd[warp][lane * cw + i] << (bits * i);
-            (which ? a.c.vcodes : a.c.kcodes)[row * words + lane] = w;
+        for (int z = 0; z < 8; ++z) {
+            const float o = __shfl_xor_sync(kFull, k[z], 2);
+            k[z] = l < 2 ? k[z] * w.cs[z] - o * w.sn[z] : o * w.sn[z] + k[z] * w.cs[z];
         }
     }
 }
+
+template <int KL, int VL, bool BINS, bool ROPE>
+__global__ void __launch_bounds__(32 * kWarps, 2) kv_append_kernel(AppendArgs a) {
+    using KB = KvBook<KL>;
+    using VB = KvBook<VL>;
+    __shared__ float kt[256], vt[16];
+    __shared__ float2 bins[BINS ? kBins : 1];  // (thresholds of lower bins, the bin's own or +inf)
+    __shared__ uint16_t kb[BINS ? 256 : 1];
+    __shared__ uint32_t vbits[kWarps][kVecs][17];  // 24-bit pieces of 3-bit codes
+    for (int i = threadIdx.x; i < KL - 1; i += blockDim.x) kt[i] = a.c.kthr[i];
+    for (int i = threadIdx.x; i < VL - 1; i += blockDim.x) vt[i] = a.c.vthr[i];
+    bool fast = false;
+    if constexpr (BINS) {
+        __syncthreads();
+        if (threadIdx.x < KL - 1) kb[threadIdx.x] = (uint16_t)bin_of(kt[threadIdx.x]);
+        __syncthreads();
+        for (int x = threadIdx.x; x < kBins; x += blockDim.x) {
+            int lo = 0, hi = KL - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (kb[mid] < x) lo = mid + 1; else hi = mid;
+            }
+            bins[x] = make_float2(__int_as_float(lo), lo < KL - 1 && kb[lo] == x ? kt[lo] : INFINITY);
+        }
+        fast = __syncthreads_and(threadIdx.x >= KL - 2 || kb[threadIdx.x] < kb[threadIdx.x + 1]);
+    }
+    __syncthreads();
+    float vthr[VL - 1];
+#pragma unroll
+    for (int i = 0; i < VL - 1; ++i) vthr[i] = vt[i];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, vec = lane >> 2, l = lane & 3;
+    const int lg = a.c.lgroup;
+    const float per_group = 1.0f / (float)(1 << lg);
+    const int parts = (a.c.Hkv + a.heads - 1) / a.heads;
+    const int64_t units = (a.T + kVecs - 1) / kVecs * parts;
+    for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < units; unit += (int64_t)gridDim.x * kWarps) {
+        const int64_t tb = unit / parts;
+        const int h0 = (int)(unit - tb * parts) * a.heads, h1 = min(h0 + a.heads, a.c.Hkv);
+        const int64_t t = tb * kVecs + vec;
+        int32_t slot = t < a.T ? a.slots[t] : -1;
+        if ((int64_t)slot >= a.c.pages << a.c.lpage) {
+            if (l == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
+            slot = -1;
+        }
+        Turn w;
+        if (ROPE) turn_angles(a, t < a.T ? a.pos[t] : 0, l, w);
+        if (!__any_sync(kFull, slot >= 0)) continue;
+        for (int h = h0; h < h1; ++h) {
+            f2 x[32];
+            {
+                float k[32], v[32];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    float y[8], z[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = z[i] = 0.f;
+                    if (slot >= 0) {
+                        load8(a.k, t * a.ks + (int64_t)h * kPD + 32 * m + 8 * l, a.dt, y);
+                        load8(a.v, t * a.vs + (int64_t)h * kPD + 32 * m + 8 * l, a.dt, z);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        k[8 * m + i] = y[i];
+                        v[8 * m + i] = z[i];
+                    }
+                }
+                if (ROPE) turn_keys(a, w, l, k);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint2 sg = *reinterpret_cast<const uint2*>(a.c.signs + 32 * m + 8 * l);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float s = sign_of(sg, i, 1.f);
+                        x[8 * m + i] = pk(k[8 * m + i] * s, v[8 * m + i] * s);
+                    }
+                }
+            }
+            fwht_pair(x);
+            const f2 r = pk(kInvSqrtD, kInvSqrtD);
+            f2 ss[4];  // sums of squares of the groups that piece m belongs to
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[8 * m + i] = mul2(x[8 * m + i], r);
+                    ss[m] = i ? fma2(x[8 * m + i], x[8 * m + i], ss[m]) : mul2(x[8 * m], x[8 * m]);
+                }
+                const float2 p = un(ss[m]);
+                ss[m] = add2(ss[m], pk(__shfl_xor_sync(kFull, p.x, 1), __shfl_xor_sync(kFull, p.y, 1)));
+                if (lg > 4) {
+                    const float2 q = un(ss[m]);
+                    ss[m] = add2(ss[m], pk(__shfl_xor_sync(kFull, q.x, 2), __shfl_xor_sync(kFull, q.y, 2)));
+                }
+            }
+            if (lg > 5) {
+                ss[0] = ss[1] = add2(ss[0], ss[1]);
+                ss[2] = ss[3] = add2(ss[2], ss[3]);
+            }
+            if (lg > 6) ss[0] = ss[1] = ss[2] = ss[3] = add2(ss[0], ss[2]);
+            const int64_t row = slot >= 0 ? a.c.row(slot, h) : 0;
+            uint32_t hk[4], hv[4];  // fp16 scales
+            uint32_t vpiece[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float2 q = un(ss[m]);
+                const float sk = sqrtf(q.x * per_group), sv = sqrtf(q.y * per_group);
+                hk[m] = __half_as_ushort(__float2half_rn(sk));
+                hv[m] = __half_as_ushort(__float2half_rn(sv));
+                const f2 inv = pk(sk > 0.f ? 1.0f / sk : 0.f, sv > 0.f ? 1.0f / sv : 0.f);
+                uint32_t kw[2] = {0, 0}, vw = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 u = un(mul2(x[8 * m + i], inv));
+                    uint32_t ck;
+                    if (BINS && fast) {
+                        const float2 e = bins[bin_of(u.x)];
+                        ck = __float_as_uint(e.x) + (e.y < u.x ? 1u : 0u);
+                    } else {
+                        ck = count_below(kt, KL - 1, u.x);
+                    }
+                    kw[KL == 256 ? i >> 2 : 0] |= ck << (KB::kBits * (KL == 256 ? i & 3 : i));
+                    uint32_t cv = 0;  // by halves: the threshold in the middle, then of the half, ...
+                    if constexpr (VL == 8) {
+                        const bool b2 = vthr[3] < u.y;
+                        const bool b1 = (b2 ? vthr[5] : vthr[1]) < u.y;
+                        const bool b0 = (b2 ? (b1 ? vthr[6] : vthr[4]) : (b1 ? vthr[2] : vthr[0])) < u.y;
+                        cv = (b2 ? 4u : 0u) | (b1 ? 2u : 0u) | (b0 ? 1u : 0u);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < VL - 1; ++c) cv += vthr[c] < u.y ? 1u : 0u;
+                    }
+                    vw |= cv << (VB::kBits * i);
+                }
+                vpiece[m] = vw;
+                if (slot >= 0) {
+                    if constexpr (KL == 256)
+                        *reinterpret_cast<uint2*>(a.c.kcodes + row * 32 + 8 * m + 2 * l) = make_uint2(kw[0], kw[1]);
+                    else
+                        a.c.kcodes[row * 16 + 4 * m + l] = kw[0];
+                    if constexpr (VL == 16) a.c.vcodes[row * 16 + 4 * m + l] = vw;
+                }
+            }
+            if constexpr (VL == 8) {  // ten codes to a word: word w takes codes 10 w .. + 9, from pieces 10 w / 8 and the next
+#pragma unroll
+                for (int m = 0; m < 4; ++m) vbits[warp][vec][4 * m + l] = vpiece[m];
+                __syncwarp();
+                if (slot >= 0) {
+                    uint32_t* dst = a.c.vcodes + row * 13;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const int wd = 4 * z + l;
+                        if (wd < 13) {
+                            const int first = 10 * wd, piece = first >> 3, off = 3 * (first & 7);
+                            const uint32_t lo = vbits[warp][vec][piece] >> off;
+                            const uint32_t hi = wd < 12 ? vbits[warp][vec][piece + 1] << (24 - off) : 0u;
+                            dst[wd] = (lo | hi) & 0x3fffffffu;
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            if (slot >= 0) {
+                const int64_t z = row << (7 - lg);
+                if (lg == 5) {
+                    if (l == 0) *reinterpret_cast<uint2*>(a.c.kscales + z) = make_uint2(hk[0] | hk[1] << 16, hk[2] | hk[3] << 16);
+                    if (l == 1) *reinterpret_cast<uint2*>(a.c.vscales + z) = make_uint2(hv[0] | hv[1] << 16, hv[2] | hv[3] << 16);
+                } else if (lg == 4) {
+                    if (!(l & 1))
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            a.c.kscales[z + 2 * m + (l >> 1)] = (uint16_t)hk[m];
+                            a.c.vscales[z + 2 * m + (l >> 1)] = (uint16_t)hv[m];
+                        }
+                } else if (l == 0) {
+                    a.c.kscales[z] = (uint16_t)hk[0];
+                    a.c.vscales[z] = (uint16_t)hv[0];
+                    if (lg == 6) {
+                        a.c.kscales[z + 1] = (uint16_t)hk[2];
+                        a.c.vscales[z + 1] = (uint16_t)hv[2];
+                    }
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- read
 
 struct FetchArgs {
     KvPages c;
@@ -123,46 +396,95 @@ struct FetchArgs {
     uint32_t* err;
 };
 
-// One warp per (token, head): K, then V.
+// Eight codes from bit 0 of a piece; 3-bit pieces span two words.
+template <int LEVELS>
+TQ_DEVFN void piece8(const uint32_t* words, int piece, uint32_t (&w)[2]) {
+    if constexpr (LEVELS == 256) {
+        const uint2 y = *reinterpret_cast<const uint2*>(words + 2 * piece);
+        w[0] = y.x;
+        w[1] = y.y;
+    } else if constexpr (LEVELS == 16) {
+        w[0] = words[piece];
+        w[1] = 0;
+    } else {
+        const int first = (8 * piece) / 10, off = 3 * (8 * piece - 10 * first);
+        const uint32_t lo = words[first] >> off;
+        w[0] = off > 6 ? lo | (words[first + 1] << (30 - off)) : lo;
+        w[1] = 0;
+    }
+}
+
 template <int KL, int VL>
-__global__ void __launch_bounds__(32 * kWarps) kv_fetch_kernel(FetchArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 2) kv_fetch_kernel(FetchArgs a) {
     __shared__ float kl[KL], vl[VL];
     for (int i = threadIdx.x; i < KL; i += blockDim.x) kl[i] = a.c.kcent[i];
     for (int i = threadIdx.x; i < VL; i += blockDim.x) vl[i] = a.c.vcent[i];
     __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t vec = (int64_t)blockIdx.x * kWarps + warp;
-    if (vec >= a.T * a.c.Hkv) return;
-    const int64_t t = vec / a.c.Hkv;
-    const int h = (int)(vec - t * a.c.Hkv);
-    int32_t slot = a.slots[t];
-    if ((int64_t)slot >= a.c.pages << a.c.lpage) {
-        if (lane == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
-        slot = -1;
-    }
-    const int64_t row = slot < 0 ? 0 : a.c.row(slot, h);
-    for (int which = 0; which < 2; ++which) {
-        void* out = which ? a.v : a.k;
-        if (!out) continue;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, vec = lane >> 2, l = lane & 3;
+    const int lg = a.c.lgroup;
+    const int64_t units = (a.T + kVecs - 1) / kVecs * a.c.Hkv;
+    for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < units; unit += (int64_t)gridDim.x * kWarps) {
+        const int64_t tb = unit / a.c.Hkv;
+        const int h = (int)(unit - tb * a.c.Hkv);
+        const int64_t t = tb * kVecs + vec;
+        int32_t slot = t < a.T ? a.slots[t] : -1;
+        if ((int64_t)slot >= a.c.pages << a.c.lpage) {
+            if (l == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
+            slot = -1;
+        }
+        f2 x[32];
         if (slot >= 0) {
-            const int bits = which ? KvBook<VL>::kBits : KvBook<KL>::kBits, cw = 32 / bits;
-            const uint32_t* w = (which ? a.c.vcodes : a.c.kcodes) + row * (which ? KvBook<VL>::kWords : KvBook<KL>::kWords);
-            const uint16_t* sc = (which ? a.c.vscales : a.c.kscales) + (row << (7 - a.c.lgroup));
-            const float s = half_bits_to_float(sc[(lane * 4) >> a.c.lgroup]);
+            const int64_t row = a.c.row(slot, h);
+            const uint32_t* kw = a.c.kcodes + row * KvBook<KL>::kWords;
+            const uint32_t* vw = a.c.vcodes + row * KvBook<VL>::kWords;
+            const int64_t z = row << (7 - lg);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int d = lane * 4 + i;
-                const uint32_t c = (w[d / cw] >> (bits * (d % cw))) & ((1u << bits) - 1u);
-                x[i] = s * (which ? vl : kl)[c];
+            for (int m = 0; m < 4; ++m) {
+                uint32_t ck[2], cv[2];
+                piece8<KL>(kw, 4 * m + l, ck);
+                piece8<VL>(vw, 4 * m + l, cv);
+                const int g = (32 * m + 8 * l) >> lg;
+                const f2 s = pk(half_bits_to_float(a.c.kscales[z + g]), half_bits_to_float(a.c.vscales[z + g]));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t p = KL == 256 ? (ck[i >> 2] >> (8 * (i & 3))) & 255u : (ck[0] >> (4 * i)) & 15u;
+                    const uint32_t q = (cv[0] >> (KvBook<VL>::kBits * i)) & (VL - 1);
+                    x[8 * m + i] = mul2(pk(kl[p % KL], vl[q]), s);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = 0;
+        }
+        fwht_pair(x);
+        if (t < a.T) {
+            const int64_t at = (t * a.c.Hkv + h) * kPD;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint2 sg = *reinterpret_cast<const uint2*>(a.c.signs + 32 * m + 8 * l);
+                float y[8], w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float s = sign_of(sg, i, kInvSqrtD);
+                    const float2 u = un(x[8 * m + i]);
+                    y[i] = u.x * s;
+                    w[i] = u.y * s;
+                }
+                if (a.k) store8(a.k, at + 32 * m + 8 * l, a.dt, y);
+                if (a.v) store8(a.v, at + 32 * m + 8 * l, a.dt, w);
             }
         }
-        fwht_warp128(x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            store_from_float(out, vec * kPD + lane * 4 + i, a.dt,
-                             x[i] * 0.08838834764831845f * (float)a.c.signs[lane * 4 + i]);
     }
+}
+
+int sm_count() {
+    static const int n = [] {
+        int dev = 0, v = 0;
+        cudaGetDevice(&dev);
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+        return std::max(v, 1);
+    }();
+    return n;
 }
 
 // fn<KL, VL>() for the books of a cache.
@@ -209,11 +531,24 @@ extern "C" tq_status tq_kv_append(const tq_kv_pages_t* cache, const void* k, int
     }
     a.dt = dt;
     a.err = err;
-    const int64_t blocks = (T * cache->Hkv + kWarps - 1) / kWarps;
-    if (blocks > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;
+    // A warp's unit: eight tokens of one head; of four heads where rotary angles are shared among them and there are
+    // units enough for every warp of two CTAs an SM.
+    const int64_t blocks8 = (T + kVecs - 1) / kVecs, all = (int64_t)sm_count() * 2 * kWarps;
+    a.heads = rope && blocks8 * ((cache->Hkv + 3) / 4) >= all ? std::min(4, cache->Hkv) : 1;
+    const int64_t units = blocks8 * ((cache->Hkv + a.heads - 1) / a.heads);
+    const unsigned blocks = (unsigned)std::min<int64_t>((units + kWarps - 1) / kWarps, sm_count() * 2);
+    // the bin table costs a CTA about as much as 8 units searched: it is built where a warp has as many
+    const bool bins = cache->kcb.levels == 256 && units * a.heads >= 8 * all;
     cudaStream_t st = as_stream(stream);
     return by_books(cache, [&](auto kl, auto vl) {
-        kv_append_kernel<decltype(kl)::value, decltype(vl)::value><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a);
+        constexpr int KL = decltype(kl)::value, VL = decltype(vl)::value;
+        if (KL == 256 && bins) {
+            if (rope) kv_append_kernel<KL, VL, KL == 256, true><<<blocks, 32 * kWarps, 0, st>>>(a);
+            else kv_append_kernel<KL, VL, KL == 256, false><<<blocks, 32 * kWarps, 0, st>>>(a);
+        } else {
+            if (rope) kv_append_kernel<KL, VL, false, true><<<blocks, 32 * kWarps, 0, st>>>(a);
+            else kv_append_kernel<KL, VL, false, false><<<blocks, 32 * kWarps, 0, st>>>(a);
+        }
         return launch_status();
     });
 }
@@ -233,8 +568,8 @@ extern "C" tq_status tq_kv_fetch(const tq_kv_pages_t* cache, const int32_t* slot
     a.v = v;
     a.dt = dt;
     a.err = err;
-    const int64_t blocks = (T * cache->Hkv + kWarps - 1) / kWarps;
-    if (blocks > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;
+    const int64_t units = (T + kVecs - 1) / kVecs * cache->Hkv;
+    const unsigned blocks = (unsigned)std::min<int64_t>((units + kWarps - 1) / kWarps, sm_count() * 2);
     cudaStream_t st = as_stream(stream);
     return by_books(cache, [&](auto kl, auto vl) {
         kv_fetch_kernel<decltype(kl)::value, decltype(vl)::value><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a);
