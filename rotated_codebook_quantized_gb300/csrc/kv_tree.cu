@@ -14,154 +14,18 @@
 
 #include <algorithm>
 
-#include "common.cuh"
-#include "kv_pages.cuh"
+#include "kv_tree.cuh"
 
 using namespace tq;
+using namespace tq::tree;
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kInvSqrtD = 0.08838834764831845f;  // 1 / sqrt(128)
-constexpr int kStep = 16;                           // tokens of a step, rows of a tile
-constexpr int kCtxWarps = 12;                       // 168 registers a thread: 64 of sums, 32 of queries
-constexpr int kDepth = 3;                           // steps of a warp's ring: two in flight while one is decoded
-constexpr float kSlack = 8.0f;                      // a running maximum may be this far (log2) below the true one
+constexpr int kStep = 16;      // tokens of a step, rows of a tile
+constexpr int kCtxWarps = 12;  // 168 registers a thread: 64 of sums, 32 of queries
+constexpr int kDepth = 3;      // steps of a warp's ring: two in flight while one is decoded
 constexpr int kFinWarps = 8, kDraftWarps = 4;
 constexpr int kFragPad = 33;  // floats of a fragment register over the lanes, padded
-
-struct TreeArgs {
-    KvPages c;
-    const __nv_bfloat16* q;
-    const __nv_bfloat16* kn;
-    const __nv_bfloat16* vn;
-    int64_t qs, ks, vs, max_len;
-    const int32_t* table;
-    const int32_t* lens;
-    const uint64_t* mask;
-    const int32_t* n_tok;
-    int B, n, Hq, ratio, table_stride, ctas;  // ratio: query heads per kv head; ctas: of the context launch
-    float scale2;                             // scale * log2(e)
-    __nv_bfloat16* o;
-    float2* stat;  // [slot][16]: running maximum (log2 units) and sum of a row
-    float* part;   // [slot][16][128]: weighted values, rotated
-    uint32_t* err;
-};
-
-// ---------------------------------------------------------------- the batch's work, counted on the device
-
-TQ_DEVFN int seq_len(const TreeArgs& a, int b) {
-    const int len = a.lens[b];
-    return len < 0 ? 0 : (int)min((int64_t)len, a.max_len);
-}
-TQ_DEVFN int seq_live(const TreeArgs& a, int b) { return a.n_tok ? min(max(a.n_tok[b], 0), a.n) : a.n; }
-TQ_DEVFN int seq_tiles(const TreeArgs& a, int b) { return (seq_live(a, b) * a.ratio + kStep - 1) / kStep; }
-TQ_DEVFN int seq_steps(const TreeArgs& a, int b) { return (seq_len(a, b) + kStep - 1) / kStep; }
-
-struct Work {
-    long long steps;  // steps of the sequences before this one
-    int units;        // (kv head, tile) units of the sequences before this one
-};
-
-// Steps and units of the sequences before b, and of all (one warp).
-TQ_DEVFN void count_work(const TreeArgs& a, int b, Work& before, long long& total) {
-    const int lane = threadIdx.x & 31;
-    long long s = 0, all = 0;
-    int u = 0;
-    for (int i = lane; i < a.B; i += 32) {
-        const int units = seq_tiles(a, i) * a.c.Hkv;
-        const long long w = (long long)units * seq_steps(a, i);
-        all += w;
-        if (i < b) {
-            s += w;
-            u += units;
-        }
-    }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) {
-        s += __shfl_xor_sync(kFull, s, m);
-        all += __shfl_xor_sync(kFull, all, m);
-        u += __shfl_xor_sync(kFull, u, m);
-    }
-    before = {s, u};
-    total = all;
-}
-
-// Steps of one CTA's run: an equal share, and no fewer than one for each of its warps.
-TQ_DEVFN long long steps_per_cta(const TreeArgs& a, long long total) {
-    return max((total + a.ctas - 1) / a.ctas, (long long)kCtxWarps);
-}
-
-// ---------------------------------------------------------------- fragments
-
-TQ_DEVFN uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
-    uint32_t d;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(s));
-    return d;
-}
-TQ_DEVFN uint32_t mul2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-// D[16, 8] += A[16, 16] B[16, 8], fp32 sums.
-TQ_DEVFN void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-TQ_DEVFN void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-TQ_DEVFN uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-TQ_DEVFN float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-TQ_DEVFN void cp16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-TQ_DEVFN uint32_t lds32(uint32_t at) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
-    return v;
-}
-TQ_DEVFN uint32_t lds16(uint32_t at) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-    return v;
-}
-TQ_DEVFN uint2 lds64(uint32_t at) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-    return v;
-}
-TQ_DEVFN uint4 lds128(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-    return v;
-}
-// The lane's entry of a table of 256-byte rows: the row is byte `c` of w (asm without volatile: the table
-// does not change after it is built, so the compiler may order these reads as it likes).
-template <int C>
-TQ_DEVFN uint32_t table(uint32_t w, uint32_t lane_base) {
-    uint32_t v;
-    asm("{\n .reg .b32 a;\n prmt.b32 a, %1, %2, %3;\n ld.shared.u32 %0, [a];\n}\n"
-        : "=r"(v)
-        : "r"(w), "r"(lane_base), "n"(0x6504 | (C << 4)));
-    return v;
-}
-// 2^-e just above x's magnitude, as an exponent: 0 for 0, infinities and NaN.
-TQ_DEVFN int exponent_above(float x) {
-    const int e = (__float_as_int(x) >> 23) & 255;
-    return e == 0 || e == 255 ? 0 : e - 126;
-}
 
 // One step of a ring: 16 tokens' codes and scales.
 template <int KL, int VL>
@@ -205,42 +69,13 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
     pdl_trigger();
     if (warp == 0) {
-        // where this CTA's run begins: the last sequence with at most P0 steps before it
         Work w;
         long long total;
         count_work(a, 0, w, total);
-        const long long P0 = blockIdx.x * steps_per_cta(a, total);
-        long long base = 0;
-        int units = 0, b = 0;
-        if (P0 < total) {
-            for (int b0 = 0; b0 < a.B; b0 += 32) {
-                const int i = b0 + lane;
-                const int u = i < a.B ? seq_tiles(a, i) * a.c.Hkv : 0;
-                long long s = i < a.B ? (long long)u * seq_steps(a, i) : 0, incl = s;
-                int ui = u;
-#pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const long long x = __shfl_up_sync(kFull, incl, m);
-                    const int y = __shfl_up_sync(kFull, ui, m);
-                    if (lane >= m) {
-                        incl += x;
-                        ui += y;
-                    }
-                }
-                const unsigned hit = __ballot_sync(kFull, base + incl > P0);
-                if (hit) {
-                    const int src = __ffs(hit) - 1;
-                    base += __shfl_sync(kFull, incl - s, src);
-                    units += __shfl_sync(kFull, ui - u, src);
-                    b = b0 + src;
-                    break;
-                }
-                base += __shfl_sync(kFull, incl, 31);
-                units += __shfl_sync(kFull, ui, 31);
-            }
-        }
+        int b;
+        find_run(a, blockIdx.x * steps_per_cta(a, total), w, b);
         if (lane == 0) {
-            s_before = {base, units};
+            s_before = w;
             s_total = total;
             s_b = b;
         }
@@ -775,8 +610,9 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
 
     // Partial results of this tile: runs first .. last, each at slot run + unit.  Warps share a row where rows are few.
     const long long per = steps_per_cta(a, s_total);
-    const int steps = seq_steps(a, b), unit = s_before.units + h * seq_tiles(a, b) + tile;
-    const long long at = s_before.steps + (long long)(h * seq_tiles(a, b) + tile) * steps;
+    const int wide = tile * kStep / a.trows, row_at = tile * kStep - wide * a.trows;  // the context's tile, and the first row in it
+    const int steps = seq_steps(a, b), unit = s_before.units + h * seq_tiles(a, b) + wide;
+    const long long at = s_before.steps + (long long)(h * seq_tiles(a, b) + wide) * steps;
     const int first = used > 0 && steps ? (int)(at / per) : 0;
     const int count = used > 0 && steps ? (int)((at + steps - 1) / per) - first + 1 : 0;
     int share = 1;
@@ -786,11 +622,11 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
         float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
         if (row < used) {
             const int64_t slot0 = (int64_t)first + unit;
-            for (int x = warp % share; x < count; x += share) M = fmaxf(M, a.stat[(slot0 + x) * kStep + row].x);
+            for (int x = warp % share; x < count; x += share) M = fmaxf(M, a.stat[(slot0 + x) * a.trows + row_at + row].x);
 #pragma unroll 4
             for (int x = warp % share; x < count; x += share) {
-                const float2 s = a.stat[(slot0 + x) * kStep + row];
-                const float4 y = *reinterpret_cast<const float4*>(a.part + ((slot0 + x) * kStep + row) * kPD + lane * 4);
+                const float2 s = a.stat[(slot0 + x) * a.trows + row_at + row];
+                const float4 y = *reinterpret_cast<const float4*>(a.part + ((slot0 + x) * a.trows + row_at + row) * kPD + lane * 4);
                 const float g = s.x == -INFINITY ? 1.f : exp2f(s.x - M);
                 L = fmaf(g, s.y, L);
                 v[0] = fmaf(g, y.x, v[0]);
@@ -862,19 +698,23 @@ int sm_count() {
 }
 
 struct Plan {
-    int64_t tiles, units, slots;  // tiles of 16 rows, (sequence, kv head, tile) units, partial results at most
-    int ctas;
+    int64_t tiles, slots;  // output tiles of 16 rows, partial results at most
+    int ctas, trows, stoks, least;
 };
 
-// Workspace of a call.  Runs (CTAs) and units both ascend along the work, so run + unit numbers every partial result once.
+// Context launch and workspace of a call.  Runs (CTAs) and units both ascend along the work, so run + unit numbers every
+// partial result once.  Up to 16 rows to a kv head go to the kernel above, more to the one that decodes a step once for
+// 128 or 256 rows.
 Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, int sms) {
     Plan p{};
-    p.tiles = ((int64_t)n * (Hq / Hkv) + kStep - 1) / kStep;
-    p.units = p.tiles * Hkv * B;
-    const int64_t steps = (max_len + kStep - 1) / kStep;
-    const int64_t runs = (p.units * steps + kCtxWarps - 1) / kCtxWarps;
-    p.ctas = (int)std::min<int64_t>(sms, runs);
-    p.slots = p.ctas ? p.units + p.ctas : 0;
+    const int64_t rows = (int64_t)n * (Hq / Hkv);
+    p.trows = rows <= kStep ? kStep : (rows <= 128 ? 128 : 256);
+    p.stoks = p.trows == kStep ? kStep : 64;
+    p.least = p.trows == kStep ? kCtxWarps : 1;
+    p.tiles = (rows + kStep - 1) / kStep;
+    const int64_t units = (rows + p.trows - 1) / p.trows * Hkv * B, steps = (max_len + p.stoks - 1) / p.stoks;
+    p.ctas = (int)std::min<int64_t>(sms, (units * steps + p.least - 1) / p.least);
+    p.slots = p.ctas ? units + p.ctas : 0;
     return p;
 }
 
@@ -903,7 +743,7 @@ extern "C" size_t tq_kv_attend_tree_workspace_bytes(const tq_kv_pages_t* cache, 
                                                     int64_t max_len) {
     if (kv_pages_check(cache, false) != TQ_OK || B <= 0 || n <= 0 || Hq <= 0 || Hq % cache->Hkv || max_len < 0) return 0;
     const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, kMaxSms);
-    return 16 + (size_t)p.slots * kStep * (kPD * sizeof(float) + sizeof(float2));
+    return 16 + (size_t)p.slots * p.trows * (kPD * sizeof(float) + sizeof(float2));
 }
 
 extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q, int64_t q_stride, tq_dtype dt,
@@ -929,10 +769,10 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
         return TQ_ERR_INVALID;
     if (ws_bytes < tq_kv_attend_tree_workspace_bytes(cache, B, n, Hq, max_len)) return TQ_ERR_INVALID;
     const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, std::min(sm_count(), kMaxSms));
-    if ((int64_t)n * (Hq / cache->Hkv) > 0x3fffffffll || p.units > 0x3fffffffll || max_len > 0x7fffffffll - kStep)
+    if ((int64_t)n * (Hq / cache->Hkv) > 0x3fffffffll || p.tiles * B * cache->Hkv > 0x3fffffffll || max_len > 0x7fffffffll - kStep)
         return TQ_ERR_UNSUPPORTED;
-    // cache rows by the 16 are 32-bit numbers
-    if ((cache->pages * cache->page_stride + cache->Hkv * cache->head_stride) / 16 > 0xffffffffll) return TQ_ERR_UNSUPPORTED;
+    // cache rows by the 8 are 32-bit numbers
+    if ((cache->pages * cache->page_stride + cache->Hkv * cache->head_stride) / 8 > 0xffffffffll) return TQ_ERR_UNSUPPORTED;
     TreeArgs a{};
     a.c = kv_pages_view(cache);
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -952,20 +792,25 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
     a.ratio = Hq / cache->Hkv;
     a.table_stride = table_stride;
     a.ctas = std::max(p.ctas, 1);
+    a.trows = p.trows;
+    a.stoks = p.stoks;
+    a.least = p.least;
+    a.wait_cycles = wait_budget();
     // a scale of 0 (all weights equal) as one that no score feels: masked scores are -infinity times a factor
     a.scale2 = fabsf(scale) < 1e-30f ? 1e-30f : scale * kLog2e;
     a.o = static_cast<__nv_bfloat16*>(o);
     a.part = static_cast<float*>(ws);
-    a.stat = reinterpret_cast<float2*>(a.part + (size_t)p.slots * kStep * kPD);
+    a.stat = reinterpret_cast<float2*>(a.part + (size_t)p.slots * p.trows * kPD);
     a.err = err;
     cudaStream_t st = as_stream(stream);
     if (p.ctas) {
         tq_status s;
-        if (cache->kcb.levels == 256) s = cache->vcb.levels == 8 ? launch_context<256, 8>(a, st) : launch_context<256, 16>(a, st);
+        if (p.trows != kStep) s = launch_wide(cache->kcb.levels, cache->vcb.levels, a, st);
+        else if (cache->kcb.levels == 256) s = cache->vcb.levels == 8 ? launch_context<256, 8>(a, st) : launch_context<256, 16>(a, st);
         else s = cache->vcb.levels == 8 ? launch_context<16, 8>(a, st) : launch_context<16, 16>(a, st);
         if (s != TQ_OK) return s;
-        return launch_pdl(kv_tree_finish_kernel, dim3((unsigned)p.units), dim3(32 * kFinWarps), 0, st, a, (int)p.tiles);
+        return launch_pdl(kv_tree_finish_kernel, dim3((unsigned)(p.tiles * cache->Hkv * B)), dim3(32 * kFinWarps), 0, st, a, (int)p.tiles);
     }
-    kv_tree_finish_kernel<<<(unsigned)p.units, 32 * kFinWarps, 0, st>>>(a, (int)p.tiles);
+    kv_tree_finish_kernel<<<(unsigned)(p.tiles * cache->Hkv * B), 32 * kFinWarps, 0, st>>>(a, (int)p.tiles);
     return launch_status();
 }
