@@ -62,37 +62,20 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
     auto region = [&](int w) {  // of a warp
         return w < kLowWarps ? kRingsLow + w * warp_region<KL, VL>() : kTableEnd + (w - kLowWarps) * warp_region<KL, VL>();
     };
-    __shared__ Work s_before;
-    __shared__ long long s_total;
-    __shared__ int s_b;
+    __shared__ Run s_run;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
     pdl_trigger();
     if (warp == 0) {
-        Work w;
-        long long total;
-        count_work(a, 0, w, total);
-        int b;
-        find_run(a, blockIdx.x * steps_per_cta(a, total), w, b);
-        if (lane == 0) {
-            s_before = w;
-            s_total = total;
-            s_b = b;
-        }
+        const Run run = find_run(a, blockIdx.x);
+        if (lane == 0) s_run = run;
     }
     // The books as fp16 over a power of two just above their largest centroid, a copy for each lane
     // (bank = lane), so a decoded value over 2^e is at most its group's scale and never overflows fp16.
-    // Row c: the key centroid of code c (8-bit), or the centroids of the two 4-bit codes of byte c; the
-    // same pair for 4-bit values in the upper half of the row.
     const int ek = exponent_above(fmaxf(fabsf(a.c.kcent[0]), fabsf(a.c.kcent[KL - 1])));
     const int ev = exponent_above(fmaxf(fabsf(a.c.vcent[0]), fabsf(a.c.vcent[VL - 1])));
     const float kd = exp2f((float)-ek), vd = exp2f((float)-ev);
-    for (int c = warp; c < 256; c += kCtxWarps) {
-        uint32_t* row = reinterpret_cast<uint32_t*>(space + kTable + c * 256);
-        row[lane] = KL == 256 ? pack_f16(a.c.kcent[c % KL] * kd, 0.f)
-                              : pack_f16(a.c.kcent[(c & 15) % KL] * kd, a.c.kcent[(c >> 4) % KL] * kd);
-        if (VL == 16) row[32 + lane] = pack_f16(a.c.vcent[(c & 15) % VL] * vd, a.c.vcent[(c >> 4) % VL] * vd);
-    }
+    build_table<KL, VL>(a.c, space + kTable, kd, vd, warp, kCtxWarps);
     // An 8-level value book lives in four registers: low and high bytes of its fp16 centroids.
     uint32_t tl[2] = {0, 0}, th[2] = {0, 0};
     if (VL == 8) {
@@ -105,12 +88,7 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
     }
     __syncthreads();
 
-    const long long total = s_total, per = steps_per_cta(a, total);
-    long long p = blockIdx.x * per;
-    const long long pend = min(p + per, total);
-    int b = s_b;
-    long long base = s_before.steps;
-    int ubase = s_before.units;
+    Walk walk(s_run);
     const int ng = kPD >> a.c.lgroup;
     const uint32_t ring = region(warp), ring_end = ring + kDepth * S::kBytes;
     // bytes 0 .. 2 of a table address beside the code: lane * 4 in byte 0, the table's 64 K in byte 2
@@ -128,26 +106,15 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
     const uint32_t dz = (lane < 16 ? S::kKs : S::kVs) + (lane & 15) * 16;
     const bool copies_z = (lane & 15) < 2 * ng;
 
-    while (p < pend) {
-        int steps = seq_steps(a, b), tiles = seq_tiles(a, b);
-        while (p >= base + (long long)steps * tiles * a.c.Hkv) {  // into the next sequence that has any
-            base += (long long)steps * tiles * a.c.Hkv;
-            ubase += tiles * a.c.Hkv;
-            ++b;
-            steps = seq_steps(a, b);
-            tiles = seq_tiles(a, b);
-        }
-        const int unit = (int)((p - base) / steps);
-        const int s0 = (int)(p - base - (long long)unit * steps);
-        const int s1 = (int)min((long long)steps, s0 + (pend - p));
-        const int h = unit / tiles, tile = unit - h * tiles;
-        const int len = seq_len(a, b), rows = min(kStep, seq_live(a, b) * a.ratio - tile * kStep);
+    Stretch x;
+    while (walk.next(a, x)) {
+        const int b = x.b, h = x.h, tile = x.tile, s0 = x.s0, s1 = x.s1, len = x.len, rows = x.rows;
 
         // queries of the tile: rotated, over a power of two of their own, fp16
         for (int row = warp; row < kStep; row += kCtxWarps) {
             float v[4] = {0.f, 0.f, 0.f, 0.f};
             if (row < rows) {
-                const int x = tile * kStep + row, i = x / a.ratio, g = x - i * a.ratio;
+                const int y = tile * kStep + row, i = y / a.ratio, g = y - i * a.ratio;
                 const uint2 raw = *reinterpret_cast<const uint2*>(a.q + ((int64_t)b * a.n + i) * a.qs +
                                                                   (int64_t)(h * a.ratio + g) * kPD + lane * 4);
                 const uint32_t sg = *reinterpret_cast<const uint32_t*>(a.c.signs + lane * 4);
@@ -399,10 +366,10 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
             }
         }
         __syncthreads();
-        const int64_t slot = (int64_t)blockIdx.x + ubase + unit;
+        const int64_t slot = (int64_t)blockIdx.x + x.unit;
         const float vscale = exp2f((float)ev);
-        for (int x = threadIdx.x; x < rows * kPD; x += 32 * kCtxWarps) {
-            const int row = x >> 7, d = x & 127, i = d & 15, nn = d >> 4;
+        for (int e = threadIdx.x; e < rows * kPD; e += 32 * kCtxWarps) {
+            const int row = e >> 7, d = e & 127, i = d & 15, nn = d >> 4;
             const int at = (4 * i + 2 * (row >> 3) + (nn & 1)) * kFragPad + (row & 7) * 4 + (nn >> 1);
             float M = -INFINITY;
             for (int w = 0; w < act; ++w) M = fmaxf(M, ml(w)[row].x);
@@ -417,7 +384,6 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
             if (d == 0) a.stat[slot * kStep + row] = make_float2(M, L);
         }
         __syncthreads();  // the rings and the queries are free
-        p += s1 - s0;
     }
 }
 
@@ -438,7 +404,7 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
     __shared__ __align__(16) float joined[kFinWarps][kPD];
     __shared__ float2 jml[kFinWarps];
     __shared__ Work s_before;
-    __shared__ long long s_total;
+    __shared__ int s_total;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
     const int tile = blockIdx.x % tiles_max, bh = blockIdx.x / tiles_max, h = bh % a.c.Hkv, b = bh / a.c.Hkv;
     const int live = seq_live(a, b), all = a.n * a.ratio;
@@ -598,7 +564,7 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
             if (a.lens[i] < 0 || a.lens[i] > a.max_len) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
     if (warp == kFinWarps - 1) {
         Work w;
-        long long total;
+        int total;
         count_work(a, b, w, total);
         if (lane == 0) {
             s_before = w;
@@ -609,12 +575,12 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
     pdl_wait();  // the context's partial results
 
     // Partial results of this tile: runs first .. last, each at slot run + unit.  Warps share a row where rows are few.
-    const long long per = steps_per_cta(a, s_total);
+    const int per = steps_per_cta(a, s_total);
     const int wide = tile * kStep / a.trows, row_at = tile * kStep - wide * a.trows;  // the context's tile, and the first row in it
     const int steps = seq_steps(a, b), unit = s_before.units + h * seq_tiles(a, b) + wide;
-    const long long at = s_before.steps + (long long)(h * seq_tiles(a, b) + wide) * steps;
-    const int first = used > 0 && steps ? (int)(at / per) : 0;
-    const int count = used > 0 && steps ? (int)((at + steps - 1) / per) - first + 1 : 0;
+    const int at = s_before.steps + (h * seq_tiles(a, b) + wide) * steps;
+    const int first = used > 0 && steps ? at / per : 0;
+    const int count = used > 0 && steps ? (at + steps - 1) / per - first + 1 : 0;
     int share = 1;
     while (share * 2 * rows <= kFinWarps) share *= 2;  // warps of a row
     for (int row0 = 0; row0 < rows; row0 += kFinWarps / share) {
@@ -698,7 +664,7 @@ int sm_count() {
 }
 
 struct Plan {
-    int64_t tiles, slots;  // output tiles of 16 rows, partial results at most
+    int64_t tiles, slots, steps;  // output tiles of 16 rows, partial results at most, steps at most
     int ctas, trows, stoks, least;
 };
 
@@ -713,6 +679,7 @@ Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, i
     p.least = p.trows == kStep ? kCtxWarps : 1;
     p.tiles = (rows + kStep - 1) / kStep;
     const int64_t units = (rows + p.trows - 1) / p.trows * Hkv * B, steps = (max_len + p.stoks - 1) / p.stoks;
+    p.steps = units * steps;
     p.ctas = (int)std::min<int64_t>(sms, (units * steps + p.least - 1) / p.least);
     p.slots = p.ctas ? units + p.ctas : 0;
     return p;
@@ -769,7 +736,7 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
         return TQ_ERR_INVALID;
     if (ws_bytes < tq_kv_attend_tree_workspace_bytes(cache, B, n, Hq, max_len)) return TQ_ERR_INVALID;
     const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, std::min(sm_count(), kMaxSms));
-    if ((int64_t)n * (Hq / cache->Hkv) > 0x3fffffffll || p.tiles * B * cache->Hkv > 0x3fffffffll || max_len > 0x7fffffffll - kStep)
+    if ((int64_t)n * (Hq / cache->Hkv) > 0x3fffffffll || p.tiles * B * cache->Hkv > 0x3fffffffll || p.steps > 0x3fffffffll || max_len > 0x7fffffffll - 64)
         return TQ_ERR_UNSUPPORTED;
     // cache rows by the 8 are 32-bit numbers
     if ((cache->pages * cache->page_stride + cache->Hkv * cache->head_stride) / 8 > 0xffffffffll) return TQ_ERR_UNSUPPORTED;

@@ -45,72 +45,107 @@ TQ_DEVFN int seq_live(const TreeArgs& a, int b) { return a.n_tok ? min(max(a.n_t
 TQ_DEVFN int seq_tiles(const TreeArgs& a, int b) { return (seq_live(a, b) * a.ratio + a.trows - 1) / a.trows; }
 TQ_DEVFN int seq_steps(const TreeArgs& a, int b) { return (seq_len(a, b) + a.stoks - 1) / a.stoks; }
 
+// Counts of steps and of units fit 31 bits: the host checks their bound.
 struct Work {
-    long long steps;  // steps of the sequences before this one
-    int units;        // (kv head, tile) units of the sequences before this one
+    int steps, units;  // steps, and (kv head, tile) units, of the sequences before one
 };
 
-// Steps and units of the sequences before b, and of all (one warp).
-TQ_DEVFN void count_work(const TreeArgs& a, int b, Work& before, long long& total) {
+// Steps and units of the sequences before b, and the steps of all (one warp).
+TQ_DEVFN void count_work(const TreeArgs& a, int b, Work& before, int& total) {
     const int lane = threadIdx.x & 31;
-    long long s = 0, all = 0;
-    int u = 0;
+    int s = 0, all = 0, u = 0;
     for (int i = lane; i < a.B; i += 32) {
-        const int units = seq_tiles(a, i) * a.c.Hkv;
-        const long long w = (long long)units * seq_steps(a, i);
+        const int units = seq_tiles(a, i) * a.c.Hkv, w = units * seq_steps(a, i);
         all += w;
         if (i < b) {
             s += w;
             u += units;
         }
     }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) {
-        s += __shfl_xor_sync(kFull, s, m);
-        all += __shfl_xor_sync(kFull, all, m);
-        u += __shfl_xor_sync(kFull, u, m);
-    }
-    before = {s, u};
-    total = all;
+    before = {__reduce_add_sync(kFull, s), __reduce_add_sync(kFull, u)};
+    total = __reduce_add_sync(kFull, all);
 }
 
 // Steps of one CTA's run: an equal share, and no fewer than `least`.
-TQ_DEVFN long long steps_per_cta(const TreeArgs& a, long long total) {
-    return max((total + a.ctas - 1) / a.ctas, (long long)a.least);
-}
+TQ_DEVFN int steps_per_cta(const TreeArgs& a, int total) { return max((total + a.ctas - 1) / a.ctas, a.least); }
 
-// Where the run that begins at step P0 starts: the last sequence with at most P0 steps before it (one warp).
-TQ_DEVFN void find_run(const TreeArgs& a, long long P0, Work& before, int& b) {
+// The run of CTA `run`: its first step `at`, the last sequence b with at most so many steps before it, what lies before b,
+// the steps of a run and of all (one warp).
+struct Run {
+    int at, b, per, total;
+    Work before;
+};
+TQ_DEVFN Run find_run(const TreeArgs& a, int run) {
     const int lane = threadIdx.x & 31;
-    before = {0, 0};
-    b = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
+    Run r{};
+    int units = 0, steps = 0;  // of sequence b0 + lane
+    auto read = [&](int b0) {
         const int i = b0 + lane;
-        const int u = i < a.B ? seq_tiles(a, i) * a.c.Hkv : 0;
-        const long long s = i < a.B ? (long long)u * seq_steps(a, i) : 0;
-        long long incl = s;
-        int ui = u;
+        units = i < a.B ? seq_tiles(a, i) * a.c.Hkv : 0;
+        steps = i < a.B ? units * seq_steps(a, i) : 0;
+    };
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        read(b0);
+        r.total += __reduce_add_sync(kFull, steps);
+    }
+    r.per = steps_per_cta(a, r.total);
+    r.at = run * r.per;  // at most the total and a run more
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        if (a.B > 32) read(b0);
+        int s = steps, u = units;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const long long x = __shfl_up_sync(kFull, incl, m);
-            const int y = __shfl_up_sync(kFull, ui, m);
+            const int x = __shfl_up_sync(kFull, s, m), y = __shfl_up_sync(kFull, u, m);
             if (lane >= m) {
-                incl += x;
-                ui += y;
+                s += x;
+                u += y;
             }
         }
-        const unsigned hit = __ballot_sync(kFull, before.steps + incl > P0);
+        const unsigned hit = __ballot_sync(kFull, r.before.steps + s > r.at);
         if (hit) {
             const int src = __ffs(hit) - 1;
-            before.steps += __shfl_sync(kFull, incl - s, src);
-            before.units += __shfl_sync(kFull, ui - u, src);
-            b = b0 + src;
-            return;
+            r.before.steps += __shfl_sync(kFull, s - steps, src);
+            r.before.units += __shfl_sync(kFull, u - units, src);
+            r.b = b0 + src;
+            break;
         }
-        before.steps += __shfl_sync(kFull, incl, 31);
-        before.units += __shfl_sync(kFull, ui, 31);
+        r.before.steps += __shfl_sync(kFull, s, 31);
+        r.before.units += __shfl_sync(kFull, u, 31);
     }
+    return r;
 }
+
+// A stretch of a run within one (sequence, kv head, tile): steps s0 .. s1 - 1 of it.
+struct Stretch {
+    int b, h, tile, unit, s0, s1, len, rows;  // unit: numbered over the batch; rows in use
+};
+struct Walk {
+    int p, end, b;
+    Work before;
+    TQ_DEVFN explicit Walk(const Run& r) : p(r.at), end(min(r.at + r.per, r.total)), b(r.b), before(r.before) {}
+    TQ_DEVFN bool next(const TreeArgs& a, Stretch& x) {
+        if (p >= end) return false;
+        int steps = seq_steps(a, b), tiles = seq_tiles(a, b);
+        while (p >= before.steps + steps * tiles * a.c.Hkv) {  // into the next sequence that has any
+            before.steps += steps * tiles * a.c.Hkv;
+            before.units += tiles * a.c.Hkv;
+            ++b;
+            steps = seq_steps(a, b);
+            tiles = seq_tiles(a, b);
+        }
+        const int unit = (p - before.steps) / steps;
+        x.b = b;
+        x.h = unit / tiles;
+        x.tile = unit - x.h * tiles;
+        x.unit = before.units + unit;
+        x.s0 = p - before.steps - unit * steps;
+        x.s1 = min(steps, x.s0 + (end - p));
+        x.len = seq_len(a, b);
+        x.rows = min(a.trows, seq_live(a, b) * a.ratio - x.tile * a.trows);
+        p += x.s1 - x.s0;
+        return true;
+    }
+};
 
 // ---------------------------------------------------------------- fragments
 
@@ -139,32 +174,77 @@ TQ_DEVFN uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+using f2 = unsigned long long;  // two packed fp32
+TQ_DEVFN f2 pk(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+TQ_DEVFN float2 un(f2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+TQ_DEVFN f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+TQ_DEVFN f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 TQ_DEVFN float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The decode table at shared address TABLE: row c of 256 bytes holds, a copy for each lane (bank = lane), the fp16 centroid
+// of 8-bit key code c, or the centroids of the two 4-bit key codes of byte c, and in its upper half the pair of two 4-bit
+// value codes, all over powers of two (kd, vd).  Written by all of the CTA's warps.
+template <int KL, int VL>
+TQ_DEVFN void build_table(const KvPages& c, uint8_t* table, float kd, float vd, int warp, int warps) {
+    const int lane = threadIdx.x & 31;
+    const float k16 = KL == 16 ? c.kcent[lane & 15] * kd : 0.f, v16 = VL == 16 ? c.vcent[lane & 15] * vd : 0.f;
+    const int per = (256 + warps - 1) / warps, first = warp * per;  // rows of this warp: at most 32
+    const float own = KL == 256 && first + lane < 256 ? c.kcent[first + lane] * kd : 0.f;
+    for (int i = 0; i < per && first + i < 256; ++i) {
+        const int row = first + i;
+        uint32_t* to = reinterpret_cast<uint32_t*>(table + row * 256) + lane;
+        to[0] = KL == 256 ? pack_f16(__shfl_sync(kFull, own, i), 0.f)
+                          : pack_f16(__shfl_sync(kFull, k16, row & 15), __shfl_sync(kFull, k16, row >> 4));
+        if (VL == 16) to[32] = pack_f16(__shfl_sync(kFull, v16, row & 15), __shfl_sync(kFull, v16, row >> 4));
+    }
+}
 TQ_DEVFN void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// Shared memory at a 32-bit address and an offset known to the compiler.
+template <int OFF = 0>
 TQ_DEVFN uint32_t lds32(uint32_t at) {
     uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    asm volatile("ld.shared.u32 %0, [%1+%2];" : "=r"(v) : "r"(at), "n"(OFF));
     return v;
 }
+template <int OFF = 0>
 TQ_DEVFN uint32_t lds16(uint32_t at) {
     uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+    asm volatile("ld.shared.u16 %0, [%1+%2];" : "=h"(v) : "r"(at), "n"(OFF));
     return v;
 }
+template <int OFF = 0>
 TQ_DEVFN uint2 lds64(uint32_t at) {
     uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2+%3];" : "=r"(v.x), "=r"(v.y) : "r"(at), "n"(OFF));
     return v;
 }
+template <int OFF = 0>
 TQ_DEVFN uint4 lds128(uint32_t at) {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4+%5];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at), "n"(OFF));
     return v;
 }
 // The lane's entry of a table of 256-byte rows: the row is byte `c` of w (asm without volatile: the table

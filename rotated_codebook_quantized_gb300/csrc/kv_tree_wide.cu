@@ -5,10 +5,13 @@
 //   scores   S[128 x 64]   = Q (TMEM, fp16) . K^T (shared)          8 MMAs of K = 16
 //   weights  P = exp2(S f - m), fp16, written over S in TMEM        one thread to a row
 //   values   O[128 x 128] += P (TMEM) . V (shared)                  4 MMAs of K = 16
-// Roles: four softmax warps to a tile, eight decoder warps (8 tokens of a step each, fed by their own cp.async rings), one
-// thread issuing MMAs.  Operands from TMEM leave the shared-memory bandwidth to the decoders' table reads and stores and to
-// the tensor cores' reads of K and V.  A row's running maximum follows only when a score passes it by 2^kSlack, so O is
-// seldom rescaled.  Every wait on an mbarrier is bounded; on expiry the CTA sets TQ_DEVERR_TIMEOUT, drains and frees TMEM.
+// Two streams of four softmax warps each, with scores and sums of their own, so that one stream's exponentials run beside
+// the other's products: the two tiles (T = 2), or the even and the odd steps of one tile (T = 1), joined at the end of the
+// run.  Decoder warps take units of 8 tokens in turn, each fed by a cp.async ring of its own; a thread to a stream issues its
+// MMAs (an issue costs its thread about 50 cycles: one thread for both streams held them up).
+// Operands from TMEM leave the shared-memory bandwidth to the decoders' table reads and stores and to the tensor cores'
+// reads of K and V.  A row's running maximum follows only when a score passes it by 2^kSlack, so O is seldom rescaled.
+// Every wait on an mbarrier is bounded; on expiry the CTA sets TQ_DEVERR_TIMEOUT, drains and frees TMEM.
 #include <math.h>
 
 #include "kv_tree.cuh"
@@ -19,8 +22,8 @@ using namespace tq::tree;
 namespace {
 
 constexpr int kTok = 64;       // tokens of a step
-constexpr int kUnit = 8;       // of a decoder warp
-constexpr int kDec = kTok / kUnit;
+constexpr int kUnit = 8;       // of a unit, which one decoder warp decodes
+constexpr int kUnits = kTok / kUnit;
 constexpr int kStages = 3;     // decoded steps
 constexpr int kDepth = 3;      // units of a decoder's ring: two in flight while one is decoded
 constexpr uint32_t kTile = kTok * kPD * 2;  // bytes of a step's keys, or values
@@ -30,7 +33,8 @@ constexpr uint32_t kHalf = kTile / 2;       // of 64 of their dims (one 128-byte
 // rings and barriers lie below it, the decoded steps above.
 constexpr uint32_t kTable = 65536, kSteps = 131072, kEnd = kSteps + kStages * 2 * kTile;
 constexpr uint32_t kStart = 1024 + 512;  // the system's first KB, then the static variables
-constexpr uint32_t kFactors = kStart, kRings = kFactors + 256 * 4;
+constexpr uint32_t kSigns = kStart, kOdd = kSigns + kPD * 4, kRings = kOdd + 2 * 128 * 4;
+constexpr int kDec = 10;  // decoder warps
 static_assert(kEnd <= 232448, "fits an SM");
 
 template <int KL, int VL>
@@ -83,281 +87,231 @@ TQ_DEVFN void tc_st32(uint32_t at, const uint32_t* v) {
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " TQ_L32 ";" ::TQ_I8(0), TQ_I8(8), TQ_I8(16), TQ_I8(24), "r"(at)
         : "memory");
 }
+TQ_DEVFN void tc_ld8(uint32_t at, uint32_t* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : TQ_O8(0) : "r"(at) : "memory");
+}
+TQ_DEVFN void tc_st8(uint32_t at, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::TQ_I8(0), "r"(at) : "memory");
+}
 #undef TQ_O8
 #undef TQ_I8
 #undef TQ_L32
 TQ_DEVFN void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 TQ_DEVFN void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// One lane of the (converged) warp.  The compiler knows that a single thread passes, so that what it guards (MMA issue, whose
+// operands are uniform registers) is straight code and not a loop over lanes.
+TQ_DEVFN bool elected() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+template <int OFF>
 TQ_DEVFN void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+    asm volatile("st.shared.v4.b32 [%0+%5], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d), "n"(OFF)
+                 : "memory");
 }
 
-template <int T>
-constexpr int kThreads = 32 * (4 * T + kDec + 1);
+constexpr int kSoft = 8, kMma = kSoft + kDec, kWarps = kMma + 2;
+
+// The queries of a tile, a thread to a row: rotated by the cache's rotation, over a power of two of their own, as fp16 pairs in
+// the row's 64 TMEM columns at `to` (where `write` is set).  The transform of 128 is two of 64, of the sum and of the
+// difference of the row's halves; element i is packed with element i + 32.  Returns the power's exponent: the largest
+// element before the rotation bounds the sums after it by 2^7.
+TQ_DEVFN int turn_queries(const __nv_bfloat16* q, const float* signs, uint32_t to, float sgn, bool in, bool write) {
+    const uint4* src = reinterpret_cast<const uint4*>(q);
+    float top = 0.f;
+    if (in) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const uint4 w = __ldg(src + c);
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
+        }
+    }
+    const int e = exponent_above(top) + 7;
+    if (!write) return e;
+    const float d = sgn * exp2f((float)-e);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        const float sg = half ? -d : d;
+        f2 x[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // elements 8 c .. + 7 and 32 + 8 c .. + 7, and the same 64 on
+            float y[2][8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint4 lo = in ? __ldg(src + c + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 hi = in ? __ldg(src + 8 + c + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    const float a = __uint_as_float(z & 1 ? l[z >> 1] & 0xffff0000u : l[z >> 1] << 16);
+                    const float b = __uint_as_float(z & 1 ? h[z >> 1] & 0xffff0000u : h[z >> 1] << 16);
+                    const int at = 8 * c + 32 * k + z;
+                    y[k][z] = fmaf(b * sg, signs[64 + at], a * d * signs[at]);
+                }
+            }
+#pragma unroll
+            for (int z = 0; z < 8; ++z) x[8 * c + z] = pk(y[0][z], y[1][z]);
+        }
+        const f2 minus = pk(-1.f, -1.f);
+#pragma unroll
+        for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+            for (int z = 0; z < 32; ++z)
+                if (!(z & h)) {
+                    const f2 a = x[z], b = x[z + h];
+                    x[z] = add2(a, b);
+                    x[z + h] = fma2(b, minus, a);
+                }
+        uint32_t w[32];
+#pragma unroll
+        for (int z = 0; z < 16; ++z) {
+            const float2 a = un(x[2 * z]), b = un(x[2 * z + 1]);
+            w[z] = pack_f16(a.x + a.y, b.x + b.y);
+            w[16 + z] = pack_f16(a.x - a.y, b.x - b.y);
+        }
+        tc_st32(to + 32 * half, w);
+    }
+    return e;
+}
 
 template <int KL, int VL, int T>
-__global__ void __launch_bounds__(kThreads<T>, 1) kv_tree_wide_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a) {
     using U = Unit<KL, VL>;
-    constexpr int kSoft = 4 * T, kMma = kSoft + kDec, kRows = 128 * T;
-    // TMEM columns: T = 1: sums, queries, two score buffers; T = 2: sums, queries, scores of each tile
-    constexpr uint32_t kO = 0, kQ = 128 * T, kS = kQ + 64 * T;
+    constexpr int kRows = 128 * T, D = kDec;
+    // TMEM columns: sums and scores of each stream, queries of each tile
+    constexpr uint32_t kO = 0, kS = 256, kQ = 384;
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* const space = smem - (uint32_t)__cvta_generic_to_shared(smem);  // shared address 0
-    float* factors = reinterpret_cast<float*>(space + kFactors);            // [kRows] from a row's products to log2 scores
-    // S and P alternate between two places: of the step's parity (T = 1), or of the tile (T = 2)
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], s_ready[2], p_ready[2], o_done[2], drain;
-    __shared__ __align__(8) uint8_t valid[kStages][kDec];  // tokens of each unit of a decoded step, a bit each
+    float* const signs = reinterpret_cast<float*>(space + kSigns);          // [128] of the rotation
+    float* const odd = reinterpret_cast<float*>(space + kOdd);              // [2][128] maxima and sums of the odd steps (T = 1)
+    // full / empty: of a decoded step's place.  Of a stream: scores, weights, values written; queries written, and read for the
+    // last time.  Odd steps' statistics ready, and the sums they go with read (T = 1).
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], s_ready[2], p_ready[2], o_done[2], q_ready[2], q_free[2],
+        odd_ready, odd_free, drain;
+    __shared__ __align__(8) uint8_t valid[kStages][kUnits];  // tokens of each unit of a decoded step, a bit each
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_word, s_b;
-    __shared__ Work s_before;
-    __shared__ long long s_total;
+    __shared__ int abort_word;
+    __shared__ Run s_run;
     volatile int* abort_flag = &abort_word;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;  // (the warp: known to be uniform)
     pdl_trigger();
     if (warp == kMma) {
         if (lane == 0) {
             abort_word = 0;
             for (int s = 0; s < kStages; ++s) {
-                mbar_init(full + s, 32 * kDec);
-                mbar_init(empty + s, 1);
+                mbar_init(full + s, 32 * kUnits);
+                mbar_init(empty + s, T);
             }
             for (int s = 0; s < 2; ++s) {
                 mbar_init(s_ready + s, 1);
                 mbar_init(p_ready + s, 128);
                 mbar_init(o_done + s, 1);
+                mbar_init(q_ready + s, 128);
+                mbar_init(q_free + s, 3 - T);
             }
-            mbar_init(&drain, 1);
+            mbar_init(&odd_ready, 128);
+            mbar_init(&odd_free, 128);
+            mbar_init(&drain, 2);
             fence_mbar_init();
         }
         __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (warp == kMma + 1) {
+        const Run run = find_run(a, blockIdx.x);
+        if (lane == 0) s_run = run;
+    } else if (tid < kPD) {
+        signs[tid] = (float)a.c.signs[tid];
     }
-    if (warp == 0) {
-        Work w;
-        long long total;
-        count_work(a, 0, w, total);
-        int b;
-        find_run(a, blockIdx.x * steps_per_cta(a, total), w, b);
-        if (lane == 0) {
-            s_before = w;
-            s_total = total;
-            s_b = b;
-        }
-    }
-    // The decode table, as in the 16-row kernel: row c of 256 bytes holds, a copy for each lane, the fp16 centroid of key
-    // code c (or of both 4-bit codes of byte c) over a power of two, and in its upper half the pair of two 4-bit values.
     const int ek = exponent_above(fmaxf(fabsf(a.c.kcent[0]), fabsf(a.c.kcent[KL - 1])));
     const int ev = exponent_above(fmaxf(fabsf(a.c.vcent[0]), fabsf(a.c.vcent[VL - 1])));
-    const float kd = exp2f((float)-ek), vd = exp2f((float)-ev);
-    for (int c = warp; c < 256; c += kMma + 1) {
-        uint32_t* row = reinterpret_cast<uint32_t*>(space + kTable + c * 256);
-        row[lane] = KL == 256 ? pack_f16(a.c.kcent[c % KL] * kd, 0.f)
-                              : pack_f16(a.c.kcent[(c & 15) % KL] * kd, a.c.kcent[(c >> 4) % KL] * kd);
-        if (VL == 16) row[32 + lane] = pack_f16(a.c.vcent[(c & 15) % VL] * vd, a.c.vcent[(c >> 4) % VL] * vd);
-    }
-    uint32_t tl[2] = {0, 0}, th[2] = {0, 0};  // low and high bytes of an 8-level value book
-    if (VL == 8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t h = __half_as_ushort(__float2half_rn(a.c.vcent[i % VL] * vd));
-            tl[i >> 2] |= (h & 255u) << (8 * (i & 3));
-            th[i >> 2] |= (h >> 8) << (8 * (i & 3));
-        }
-    }
+    const float vd = exp2f((float)-ev);
+    if (warp < kMma) build_table<KL, VL>(a.c, space + kTable, exp2f((float)-ek), vd, warp, kMma);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    Walk walk(s_run);
+    Stretch x;
+    uint32_t g = 0, seg = 0;  // steps and stretches of this CTA so far: the phases of every barrier
+    // Each role walks the CTA's stretches on its own; the decoders run ahead into the next one.
 
-    const long long total = s_total, per = steps_per_cta(a, total);
-    long long p = blockIdx.x * per;
-    const long long pend = min(p + per, total);
-    int b = s_b;
-    long long base = s_before.steps;
-    int ubase = s_before.units;
-    uint32_t g = 0;  // steps of this CTA so far: the phase of every barrier
-    const int ng = kPD >> a.c.lgroup;
-
-    // decoder state that outlives a segment
-    const int d = warp - kSoft;
-    const uint32_t ring = kRings + (d > 0 ? d : 0) * kDepth * U::kBytes, ring_end = ring + kDepth * U::kBytes;
-
-    while (p < pend) {
-        int steps = seq_steps(a, b), tiles = seq_tiles(a, b);
-        while (p >= base + (long long)steps * tiles * a.c.Hkv) {  // into the next sequence that has any
-            base += (long long)steps * tiles * a.c.Hkv;
-            ubase += tiles * a.c.Hkv;
-            ++b;
-            steps = seq_steps(a, b);
-            tiles = seq_tiles(a, b);
-        }
-        const int unit = (int)((p - base) / steps);
-        const int s0 = (int)(p - base - (long long)unit * steps);
-        const int s1 = (int)min((long long)steps, s0 + (pend - p));
-        const int h = unit / tiles, tile = unit - h * tiles;
-        const int len = seq_len(a, b), rows = min(kRows, seq_live(a, b) * a.ratio - tile * kRows);
-
-        // ---- decoders: the first copies are under way while the queries are turned
-        const int32_t* tab = a.table + (int64_t)b * a.table_stride;
-        auto page_of = [&](int st) {
-            const int t = st * kTok + d * kUnit;
-            return st < s1 && t < len ? __ldg(tab + (t >> a.c.lpage)) : -1;
-        };
-        int ahead = s0, page_next = -1;
-        uint32_t fill = ring, counts = 0;  // four bits a step: valid tokens of the unit
-        auto issue = [&]() {
-            const int page = page_next, t = ahead * kTok + d * kUnit;
-            page_next = page_of(ahead + 1);
-            counts <<= 4;
-            if (ahead < s1 && t < len) {
-                if ((uint32_t)page < (uint32_t)a.c.pages) {
-                    counts |= (uint32_t)min(len - t, kUnit);
-                    const uint32_t row8 = (uint32_t)page * (uint32_t)(a.c.page_stride >> 3) +
-                                          (uint32_t)h * (uint32_t)(a.c.head_stride >> 3) + ((t & ((1 << a.c.lpage) - 1)) >> 3);
-                    const uint8_t* k = reinterpret_cast<const uint8_t*>(a.c.kcodes) + (uint64_t)row8 * (kUnit * U::kKRow) + lane * 16;
-                    cp16(fill + U::kK + lane * 16, k);
-                    if (KL == 256) cp16(fill + U::kK + lane * 16 + 512, k + 512);
-                    if (lane < kUnit * (int)U::kVRow / 16)
-                        cp16(fill + U::kV + lane * 16,
-                             reinterpret_cast<const uint8_t*>(a.c.vcodes) + (uint64_t)row8 * (kUnit * U::kVRow) + lane * 16);
-                    if ((lane & 7) < ng && lane < 16)
-                        cp16(fill + (lane < 8 ? U::kKs : U::kVs) + (lane & 7) * 16,
-                             reinterpret_cast<const uint8_t*>(lane < 8 ? a.c.kscales : a.c.vscales) +
-                                 (uint64_t)row8 * (uint32_t)(kUnit * 2 * ng) + (lane & 7) * 16);
-                } else if (lane == 0 && a.err) {
-                    atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            ++ahead;
-            fill = fill + U::kBytes == ring_end ? ring : fill + U::kBytes;
-        };
-        if (d >= 0 && d < kDec) {
-            page_next = page_of(s0);
-#pragma unroll
-            for (int i = 0; i < kDepth - 1; ++i) issue();
-        }
-
-        // ---- queries: rotated, over a power of two of their own, fp16, through the decoded steps' memory into TMEM
-        if (warp != kMma) {
-#pragma unroll 2
-            for (int row = warp; row < kRows; row += kMma) {
-                float v[4] = {0.f, 0.f, 0.f, 0.f};
-                if (row < rows) {
-                    const int x = tile * kRows + row, i = x / a.ratio, gq = x - i * a.ratio;
-                    const uint2 raw = *reinterpret_cast<const uint2*>(a.q + ((int64_t)b * a.n + i) * a.qs +
-                                                                      (int64_t)(h * a.ratio + gq) * kPD + lane * 4);
-                    const uint32_t sg = *reinterpret_cast<const uint32_t*>(a.c.signs + lane * 4);
-                    v[0] = __uint_as_float(raw.x << 16) * (float)(int8_t)sg;
-                    v[1] = __uint_as_float(raw.x & 0xffff0000u) * (float)(int8_t)(sg >> 8);
-                    v[2] = __uint_as_float(raw.y << 16) * (float)(int8_t)(sg >> 16);
-                    v[3] = __uint_as_float(raw.y & 0xffff0000u) * (float)(int8_t)(sg >> 24);
-                    fwht_warp128(v);
-                }
-                float mx = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-                for (int m = 16; m; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, m));
-                const int e = exponent_above(mx);
-                const float dn = a.scale2 < 0.f ? -exp2f((float)-e) : exp2f((float)-e);  // the factor below is not negative
-                // 16-byte pieces of a row are swapped by its number: the reader is a thread to a row
-                *reinterpret_cast<uint2*>(space + kSteps + row * 256 + (((lane >> 1) ^ (row & 7)) << 4) + (lane & 1) * 8) =
-                    make_uint2(pack_f16(v[0] * dn, v[1] * dn), pack_f16(v[2] * dn, v[3] * dn));
-                if (lane == 0) factors[row] = exp2f((float)(e + ek)) * (kInvSqrtD * fabsf(a.scale2));
-            }
-        }
-        __syncthreads();
-        const int row = warp * 32 + lane;  // softmax threads: of the CTA's rows
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's TMEM lanes
-        const uint32_t col_o = tmem + kO + (warp >> 2) * 128 + lanes;
-        float f = 0.f;
-        if (warp < kSoft) {
-            f = factors[row];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t w[32];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 x = lds128(kSteps + row * 256 + (((8 * half + c) ^ (row & 7)) << 4));
-                    w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
-                }
-                tc_st32(tmem + kQ + (warp >> 2) * 64 + 32 * half + lanes, w);
-            }
-            tc_wait_st();
-        }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-
-        if (warp == kMma) {
-            // -------------------------------------------------------- MMA issue
-            if (lane == 0) {
-                auto scores = [&](uint32_t i, int t) {  // of the CTA's step i, tile t
-                    const uint32_t at = kSteps + (i % kStages) * 2 * kTile, to = tmem + kS + 64 * (T == 1 ? i & 1 : t);
+    if (warp >= kMma) {
+        // ------------------------------------------------------------ MMA issue, of one stream
+        const int t = warp - kMma;
+        if (elected()) {
+            uint32_t done = 0;  // steps of this stream so far
+            const uint32_t to_s = tmem + kS + 64 * t, to_o = tmem + kO + 128 * t, from_q = tmem + kQ + (T == 1 ? 0 : 64 * t);
+            bool ok = true;
+            while (ok && walk.next(a, x)) {
+                const uint32_t ge = g + (x.s1 - x.s0), first = g + (T == 1 ? t : 0);
+                ok = mbar_wait(q_ready + (T == 1 ? 0 : t), seg & 1, abort_flag, a.wait_cycles);
+                for (uint32_t i = first; i < ge && ok; i += 3 - T) {
+                    const uint32_t stage = i % kStages;
+                    // the scores go where the weights of the step before were read from
+                    ok = mbar_wait(full + stage, (i / kStages) & 1, abort_flag, a.wait_cycles) &&
+                         (i == first || mbar_wait(o_done + t, (done - 1) & 1, abort_flag, a.wait_cycles));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dk = desc(kSteps, 16) + stage * (2 * kTile / 16), dv = desc(kSteps + kTile, kHalf) + stage * (2 * kTile / 16);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        tc_mma_ts(to, tmem + kQ + 64 * t + 8 * k, desc(at + (k >> 2) * kHalf, 16) + 2 * (k & 3), idesc(kTok, 0), k != 0);
-                    tc_commit(s_ready + (T == 1 ? i & 1 : t));
-                };
-                auto values = [&](uint32_t i, int t, bool first) {
-                    const uint32_t at = kSteps + (i % kStages) * 2 * kTile + kTile, from = tmem + kS + 64 * (T == 1 ? i & 1 : t);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_ts(tmem + kO + 128 * t, from + 8 * k, desc(at + 2048 * k, kHalf), idesc(kPD, 1), !first || k != 0);
-                };
-                auto wait_full = [&](uint32_t i) {
-                    const bool ok = mbar_wait(full + i % kStages, (i / kStages) & 1, abort_flag, a.wait_cycles);
+                        tc_mma_ts(to_s, from_q + 8 * k, dk + ((k >> 2) * (kHalf / 16) + 2 * (k & 3)), idesc(kTok, 0), k != 0);
+                    tc_commit(s_ready + t);
+                    ok = mbar_wait(p_ready + t, done & 1, abort_flag, a.wait_cycles);
+                    if (!ok) break;
                     tc_fence_after();
-                    return ok;
-                };
-                const uint32_t ge = g + (s1 - s0);
-                bool ok = wait_full(g);
-                if (ok)
-                    for (int t = 0; t < T; ++t) scores(g, t);
-                for (uint32_t i = g; i < ge && ok; ++i) {
-                    if (T == 1 && i + 1 < ge) {
-                        // the other score buffer still held the weights of step i - 1
-                        ok = wait_full(i + 1) && (i == g || mbar_wait(o_done, (i - 1) & 1, abort_flag, a.wait_cycles));
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(i + 1, 0);
-                    }
-                    for (int t = 0; t < T; ++t) {
-                        ok = mbar_wait(p_ready + (T == 1 ? i & 1 : t), T == 1 ? (i >> 1) & 1 : i & 1, abort_flag, a.wait_cycles);
-                        if (!ok) break;
-                        tc_fence_after();
-                        values(i, t, i == g);
-                        tc_commit(o_done + t);
-                        if (t == T - 1) tc_commit(empty + i % kStages);
-                        if (T == 2 && i + 1 < ge) {
-                            // the scores go where the weights were read from
-                            ok = (t || wait_full(i + 1)) && mbar_wait(o_done + t, i & 1, abort_flag, a.wait_cycles);
-                            if (!ok) break;
-                            tc_fence_after();
-                            scores(i + 1, t);
-                        }
-                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tc_mma_ts(to_o, to_s + 8 * k, dv + 128 * k, idesc(kPD, 1), i != first || k != 0);
+                    tc_commit(o_done + t);
+                    tc_commit(empty + stage);
+                    ++done;
                 }
+                mbar_arrive(q_free + (T == 1 ? 0 : t));
+                g = ge;
+                ++seg;
             }
-            __syncwarp();
-        } else if (warp < kSoft) {
-            // -------------------------------------------------------- softmax: a thread to a row
-            const int t = warp >> 2;
-            const bool idle = (warp & 3) * 32 + t * 128 >= rows;  // no row of this warp is in use
+            tc_commit(&drain);  // completes when every MMA issued above has finished
+        }
+        __syncwarp();
+    } else if (warp < kSoft) {
+        // ------------------------------------------------------------ softmax: a thread to a row
+        const int stream = warp >> 2, row = (T == 1 ? 0 : stream * 128) + (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's TMEM lanes
+        const uint32_t col_o = tmem + kO + stream * 128 + lanes, at = tmem + kS + 64 * stream + lanes;
+        uint32_t done = 0;  // steps of this stream so far
+        bool ok = true;
+        while (walk.next(a, x)) {
+            const uint32_t first = g + (T == 1 ? stream : 0), ge = g + (x.s1 - x.s0);
+            const bool idle = row - lane >= x.rows;  // no row of this warp is in use
+            const bool writer = T == 2 || stream == 0;
+            if (writer && seg) ok = __all_sync(kFull, mbar_wait(q_free + (T == 1 ? 0 : stream), (seg - 1) & 1, abort_flag, a.wait_cycles));
+            if (!ok) break;
+            float f = 0.f;  // from a row's products to log2 scores
+            if (!idle) {
+                const int y = x.tile * kRows + row, i = y / a.ratio;
+                const __nv_bfloat16* q = a.q + ((int64_t)x.b * a.n + i) * a.qs + (int64_t)(x.h * a.ratio + y - i * a.ratio) * kPD;
+                const int e = turn_queries(q, signs, tmem + kQ + (T == 1 ? 0 : 64 * stream) + lanes, a.scale2 < 0.f ? -1.f : 1.f, row < x.rows, writer);
+                f = exp2f((float)(e + ek)) * (kInvSqrtD * fabsf(a.scale2));  // not negative: a scale's sign goes to the queries
+                if (writer) tc_wait_st();
+            }
+            if (writer) {
+                tc_fence_before();
+                mbar_arrive(q_ready + (T == 1 ? 0 : stream));
+            }
             float m = -INFINITY, l = 0.f, bias = 0.f;
-            bool ok = true;
-            for (uint32_t i = g; i < g + (s1 - s0) && ok; ++i) {
-                const int buf = T == 1 ? i & 1 : t;
-                const uint32_t at = tmem + kS + 64 * buf + lanes;
+            for (uint32_t i = first; i < ge; i += 3 - T) {
                 // (the decoders' barrier has long completed; waiting on it too orders their `valid` before the read)
-                ok = mbar_wait(s_ready + buf, T == 1 ? (i >> 1) & 1 : i & 1, abort_flag, a.wait_cycles) &&
+                ok = mbar_wait(s_ready + stream, done & 1, abort_flag, a.wait_cycles) &&
                      mbar_wait(full + i % kStages, (i / kStages) & 1, abort_flag, a.wait_cycles);
-                if (!__all_sync(kFull, ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
                 tc_fence_after();
                 if (!idle) {
                     uint32_t s[64];
@@ -374,119 +328,231 @@ __global__ void __launch_bounds__(kThreads<T>, 1) kv_tree_wide_kernel(TreeArgs a
 #pragma unroll
                     for (int c = 0; c < 4; ++c) x[c] = __uint_as_float(s[c]);
 #pragma unroll
-                    for (int c = 4; c < 64; ++c) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
+                    for (int c = 4; c < 60; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[e] = fmaxf(fmaxf(x[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + e + 4]));
+#pragma unroll
+                    for (int c = 60; c < 64; ++c) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
                     const float top = f * fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                     if (__any_sync(kFull, top > m + kSlack)) {
                         const float n = fmaxf(m, top), r = m == -INFINITY ? 0.f : fast_exp2(m - n);
                         m = n;
                         bias = m == -INFINITY ? 0.f : -m;
                         l *= r;
-                        if (i != g) {  // the sums so far, once the last product has written them
-                            ok = mbar_wait(o_done + t, (i - 1) & 1, abort_flag, a.wait_cycles);
-                            if (!__all_sync(kFull, ok)) {
-                                ok = false;
-                                break;
-                            }
+                        if (i != first) {  // the sums so far, once the last product has written them
+                            ok = __all_sync(kFull, mbar_wait(o_done + stream, (done - 1) & 1, abort_flag, a.wait_cycles));
+                            if (!ok) break;
                             tc_fence_after();
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t o[32];
-                                tc_ld32(col_o + 32 * c, o);
+#pragma unroll 1
+                            for (int c = 0; c < 16; ++c) {
+                                uint32_t o[8];
+                                tc_ld8(col_o + 8 * c, o);
                                 tc_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
-                                tc_st32(col_o + 32 * c, o);
+                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+                                tc_st8(col_o + 8 * c, o);
                             }
                         }
                     }
-                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t w[32];
+                    const f2 ff = pk(f, f), bb = pk(bias, bias);
+                    f2 ls[2] = {0, 0};
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float u = fast_exp2(fmaf(__uint_as_float(s[2 * c]), f, bias));
-                        const float v = fast_exp2(fmaf(__uint_as_float(s[2 * c + 1]), f, bias));
-                        ls[c & 3] += u + v;
-                        w[c] = pack_f16(u, v);
+                    for (int c = 0; c < 32; ++c) {  // the weights take the scores' registers
+                        const float2 e = un(fma2(pk(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), ff, bb));
+                        const float u = fast_exp2(e.x), v = fast_exp2(e.y);
+                        ls[c & 1] = add2(ls[c & 1], pk(u, v));
+                        s[c] = pack_f16(u, v);
                     }
-                    l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-                    tc_st32(at, w);
+                    const float2 sum = un(add2(ls[0], ls[1]));
+                    l += sum.x + sum.y;
+                    tc_st32(at, s);
                     tc_wait_st();
                 }
                 tc_fence_before();
-                mbar_arrive(p_ready + buf);
+                mbar_arrive(p_ready + stream);
+                ++done;
             }
-            // ---- the run's partial result of this tile
-            if (ok) ok = mbar_wait(o_done + t, (g + (s1 - s0) - 1) & 1, abort_flag, a.wait_cycles);
-            if (__all_sync(kFull, ok) && !idle) {
+            if (!ok) break;
+            // ---- the stretch's partial result
+            if (first < ge) {  // (the odd steps may be none)
+                ok = __all_sync(kFull, mbar_wait(o_done + stream, (done - 1) & 1, abort_flag, a.wait_cycles));
+                if (!ok) break;
                 tc_fence_after();
-                const int64_t at = ((int64_t)blockIdx.x + ubase + unit) * kRows + row;
-                const float vscale = exp2f((float)ev);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tc_ld32(col_o + 32 * c, o);
-                    tc_wait_ld();
-                    if (row < rows) {
-                        float4* to = reinterpret_cast<float4*>(a.part + at * kPD + 32 * c);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            to[e] = make_float4(__uint_as_float(o[4 * e]) * vscale, __uint_as_float(o[4 * e + 1]) * vscale,
-                                                __uint_as_float(o[4 * e + 2]) * vscale, __uint_as_float(o[4 * e + 3]) * vscale);
-                    }
-                }
-                if (row < rows) a.stat[at] = make_float2(m, l);
-                tc_fence_before();
             }
-        } else {
-            // -------------------------------------------------------- decoders
+            float m1 = -INFINITY, l1 = 0.f;
+            if (T == 1) {  // the even steps' warps add the odd steps' sums, which lie in the same TMEM lanes
+                if (stream == 1) {
+                    odd[row] = m;
+                    odd[128 + row] = l;
+                    tc_fence_before();
+                    mbar_arrive(&odd_ready);
+                    ok = __all_sync(kFull, mbar_wait(&odd_free, seg & 1, abort_flag, a.wait_cycles));
+                } else {
+                    ok = __all_sync(kFull, mbar_wait(&odd_ready, seg & 1, abort_flag, a.wait_cycles));
+                    tc_fence_after();
+                    m1 = odd[row];
+                    l1 = odd[128 + row];
+                }
+                if (!ok) break;
+            }
+            if (writer) {
+                if (!idle) {
+                    const bool two = T == 1 && ge - g > 1;
+                    const float n = two ? fmaxf(m, m1) : m;
+                    // weight 1 for the joint maximum's own (also where both saw nothing); a NaN sum stays one
+                    const float w0 = m == n ? 1.f : fast_exp2(m - n), w1 = m1 == n ? 1.f : fast_exp2(m1 - n);
+                    const int64_t to = ((int64_t)blockIdx.x + x.unit) * kRows + row;
+                    const float vscale = exp2f((float)ev);
+#pragma unroll 1
+                    for (int c = 0; c < 16; ++c) {
+                        uint32_t o[8], o1[8];
+                        tc_ld8(col_o + 8 * c, o);
+                        if (two) tc_ld8(col_o + 128 + 8 * c, o1);
+                        tc_wait_ld();
+                        float z[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            z[k] = __uint_as_float(o[k]) * (w0 * vscale);
+                            if (two) z[k] = fmaf(__uint_as_float(o1[k]), w1 * vscale, z[k]);
+                        }
+                        if (row < x.rows) {
+                            float4* out = reinterpret_cast<float4*>(a.part + to * kPD + 8 * c);
+                            out[0] = make_float4(z[0], z[1], z[2], z[3]);
+                            out[1] = make_float4(z[4], z[5], z[6], z[7]);
+                        }
+                    }
+                    if (row < x.rows) a.stat[to] = make_float2(n, two ? l * w0 + l1 * w1 : l);
+                }
+                tc_fence_before();
+                if (T == 1) mbar_arrive(&odd_free);
+            }
+            g = ge;
+            ++seg;
+        }
+    } else {
+        // ------------------------------------------------------------ decoders: warp d takes units d, d + D, ... of a stretch
+        const int d = warp - kSoft, ng = kPD >> a.c.lgroup;
+        uint32_t tl[2] = {0, 0}, th[2] = {0, 0};  // low and high bytes of an 8-level value book
+        if (VL == 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t h = __half_as_ushort(__float2half_rn(a.c.vcent[i % VL] * vd));
+                tl[i >> 2] |= (h & 255u) << (8 * (i & 3));
+                th[i >> 2] |= (h >> 8) << (8 * (i & 3));
+            }
+        }
+        const uint32_t ring = kRings + d * kDepth * U::kBytes, ring_end = ring + kDepth * U::kBytes;
+        // (cache rows by the 8: 32-bit numbers)
+        const uint32_t page8 = (uint32_t)(a.c.page_stride >> 3), head8 = (uint32_t)(a.c.head_stride >> 3);
+        const uint32_t in_page = (1u << (a.c.lpage - 3)) - 1;
+        const uint8_t* kc = reinterpret_cast<const uint8_t*>(a.c.kcodes) + lane * 16;
+        const uint8_t* vc = reinterpret_cast<const uint8_t*>(a.c.vcodes) + lane * 16;
+        const uint8_t* zc = reinterpret_cast<const uint8_t*>(lane < 8 ? a.c.kscales : a.c.vscales) + (lane & 7) * 16;
+        const uint32_t z_at = (lane < 8 ? U::kKs : U::kVs) + (lane & 7) * 16;
+        const bool copies_z = (lane & 7) < ng && lane < 16, copies_v = lane < kUnit * (int)U::kVRow / 16;
+        bool ok = true;
+        while (ok && walk.next(a, x)) {
+            const int s0 = x.s0, s1 = x.s1, len = x.len, h = x.h;
+            const int32_t* tab = a.table + (int64_t)x.b * a.table_stride;
+        const int u0 = s0 * kUnits, u1 = min(s1 * kUnits, (len + kUnit - 1) / kUnit);  // units that hold tokens
+        auto page_of = [&](int u) { return u < u1 ? __ldg(tab + (u >> (a.c.lpage - 3))) : 0; };
+        int ahead = u0 + d, page_next = 0;
+        uint32_t fill = ring, counts = 0;  // four bits a unit: its valid tokens
+        auto issue = [&]() {
+            const int page = page_next, u = ahead;
+            ahead += D;
+            page_next = page_of(ahead);
+            counts <<= 4;
+            if (u < u1) {
+                if ((uint32_t)page < (uint32_t)a.c.pages) {
+                    counts |= (uint32_t)min(len - u * kUnit, kUnit);
+                    const uint64_t row8 = (uint32_t)page * page8 + (uint32_t)h * head8 + (u & in_page);
+                    const uint8_t* k = kc + row8 * (kUnit * U::kKRow);
+                    cp16(fill + U::kK + lane * 16, k);
+                    if (KL == 256) cp16(fill + U::kK + lane * 16 + 512, k + 512);
+                    if (copies_v) cp16(fill + U::kV + lane * 16, vc + row8 * (kUnit * U::kVRow));
+                    if (copies_z) cp16(fill + z_at, zc + row8 * (uint32_t)(kUnit * 2 * ng));
+                } else if (lane == 0 && a.err) {
+                    atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            fill = fill + U::kBytes == ring_end ? ring : fill + U::kBytes;
+        };
+
+            page_next = page_of(ahead);
+#pragma unroll
+            for (int i = 0; i < kDepth - 1; ++i) issue();
             const int c = lane & 15, hi = lane >> 4;  // 8 dims of tokens hi, hi + 2, ...
             const uint32_t lane_k = lane * 4 | 0x100, lane_v = lane_k + 128;
             const uint32_t k_at = U::kK + hi * U::kKRow + c * (KL == 256 ? 8 : 4);
-            const uint32_t ks_at = U::kKs + (hi * ng + ((8 * c) >> a.c.lgroup)) * 2, vs_at = ks_at + 128;
+            const uint32_t ks_at = U::kKs + (hi * ng + ((8 * c) >> a.c.lgroup)) * 2;  // the value's 128 on
             // 3-bit values: 8 codes from code `from` of word w0, ten to a word
             const int w0 = (8 * c) / 10, from = (8 * c) % 10;
             const uint32_t v_at = U::kV + hi * U::kVRow + (VL == 8 ? w0 * 4 : c * 4);
             const uint32_t shr = 3 * from, mulr = 1u << (30 - 3 * from);
             // in a decoded step: 64 dims to a half, a 128-byte row to a token, its 16-byte pieces swapped by the token
-            const uint32_t to = kSteps + (c >> 3) * kHalf + (d * kUnit + hi) * 128, piece = ((c & 7) ^ hi) * 16;
+            const uint32_t to = kSteps + (c >> 3) * kHalf + hi * 128 + ((c & 7) ^ hi) * 16;
             uint32_t at = ring;
-            bool ok = true;
-            for (uint32_t i = g; i < g + (s1 - s0) && ok; ++i) {
+            // the unit's step, as a place among the decoded ones and the phase of its barriers
+            uint32_t stage = (g + d / kUnits) % kStages, phase = (g + d / kUnits) / kStages & 1;
+            for (int u = u0 + d; u < s1 * kUnits; u += D) {
                 issue();
                 asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
                 __syncwarp();
-                ok = mbar_wait(empty + i % kStages, ((i / kStages) & 1) ^ 1, abort_flag, a.wait_cycles);
-                if (!__all_sync(kFull, ok)) {
-                    ok = false;
-                    break;
-                }
                 const uint32_t count = (counts >> (4 * (kDepth - 1))) & 15u;
-                const uint32_t dst = to + (i % kStages) * 2 * kTile;
-#pragma unroll
-                for (int q = 0; q < kUnit / 2; ++q) {  // keys of tokens 2 q + hi
-                    uint32_t s = lds16(at + ks_at + 4 * q * ng) * 0x10001u;
-                    if (count < kUnit && 2 * q + hi >= (int)count) s = 0;  // what lies past the end may be anything
+                if (count < kUnit) {  // what lies past the end may be anything: its scales are taken as zeros
+                    for (uint32_t x = count * ng + lane; x < kUnit * ng; x += 32) {
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + U::kKs + 2 * x), "h"((uint16_t)0) : "memory");
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + U::kVs + 2 * x), "h"((uint16_t)0) : "memory");
+                    }
+                    __syncwarp();
+                }
+                constexpr int N = kUnit / 2;  // passes of two tokens
+                uint32_t ks[N], vs[N], kw[N][2], vw[N];
+                const uint32_t at_k = at + k_at, at_v = at + v_at;
+                static_for<0, N>([&](auto qc) {
+                    constexpr int q = decltype(qc)::value;
+                    ks[q] = lds16(at + ks_at + 4 * q * ng);
+                    vs[q] = lds16<128>(at + ks_at + 4 * q * ng);
+                    if constexpr (KL == 256) {
+                        const uint2 x = lds64<2 * q * U::kKRow>(at_k);
+                        kw[q][0] = x.x;
+                        kw[q][1] = x.y;
+                    } else {
+                        kw[q][0] = lds32<2 * q * U::kKRow>(at_k);
+                    }
+                    if constexpr (VL == 8)
+                        vw[q] = (lds32<2 * q * U::kVRow>(at_v) >> shr) + lds32<2 * q * U::kVRow + 4>(at_v) * mulr;
+                    else
+                        vw[q] = lds32<2 * q * U::kVRow>(at_v);
+                });
+                ok = __all_sync(kFull, mbar_wait(empty + stage, phase ^ 1, abort_flag, a.wait_cycles));
+                if (!ok) break;
+                const uint32_t dst = to + (u & (kUnits - 1)) * (kUnit * 128) + stage * 2 * kTile;
+                static_for<0, N>([&](auto qc) {  // keys of tokens 2 q + hi
+                    constexpr int q = decltype(qc)::value;
+                    const uint32_t s = ks[q] * 0x10001u;
                     uint32_t w[4];
                     if constexpr (KL == 256) {
-                        const uint2 x = lds64(at + k_at + 2 * q * U::kKRow);
-                        w[0] = prmt(table<0>(x.x, lane_k), table<1>(x.x, lane_k), 0x5410);
-                        w[1] = prmt(table<2>(x.x, lane_k), table<3>(x.x, lane_k), 0x5410);
-                        w[2] = prmt(table<0>(x.y, lane_k), table<1>(x.y, lane_k), 0x5410);
-                        w[3] = prmt(table<2>(x.y, lane_k), table<3>(x.y, lane_k), 0x5410);
+                        const uint32_t x = kw[q][0], y = kw[q][1];
+                        w[0] = prmt(table<0>(x, lane_k), table<1>(x, lane_k), 0x5410);
+                        w[1] = prmt(table<2>(x, lane_k), table<3>(x, lane_k), 0x5410);
+                        w[2] = prmt(table<0>(y, lane_k), table<1>(y, lane_k), 0x5410);
+                        w[3] = prmt(table<2>(y, lane_k), table<3>(y, lane_k), 0x5410);
                     } else {
-                        const uint32_t x = lds32(at + k_at + 2 * q * U::kKRow);
+                        const uint32_t x = kw[q][0];
                         w[0] = table<0>(x, lane_k), w[1] = table<1>(x, lane_k);
                         w[2] = table<2>(x, lane_k), w[3] = table<3>(x, lane_k);
                     }
-                    sts128(dst + 256 * q + (piece ^ (32 * q)), mul2(w[0], s), mul2(w[1], s), mul2(w[2], s), mul2(w[3], s));
-                }
-#pragma unroll
-                for (int q = 0; q < kUnit / 2; ++q) {  // values
-                    uint32_t s = lds16(at + vs_at + 4 * q * ng) * 0x10001u;
-                    if (count < kUnit && 2 * q + hi >= (int)count) s = 0;
+                    sts128<256 * q>(dst ^ (32 * q), mul2(w[0], s), mul2(w[1], s), mul2(w[2], s), mul2(w[3], s));
+                });
+                static_for<0, N>([&](auto qc) {  // values
+                    constexpr int q = decltype(qc)::value;
+                    const uint32_t s = vs[q] * 0x10001u, x = vw[q];
                     uint32_t w[4];
                     if constexpr (VL == 8) {
-                        const uint32_t x = (lds32(at + v_at + 2 * q * U::kVRow) >> shr) + lds32(at + v_at + 2 * q * U::kVRow + 4) * mulr;
                         const uint32_t y = (x & 0x0000ffffu) | ((x << 4) & 0xffff0000u);          // 12 bits to 16
                         const uint32_t z = (y & 0x00ff00ffu) | ((y << 2) & 0xff00ff00u);          // 6 to 8
                         const uint32_t sel = ((z & 0x0f0f0f0fu) | ((z << 1) & 0xf0f0f0f0u)) & 0x77777777u;  // 3 to 4: byte selectors
@@ -497,28 +563,26 @@ __global__ void __launch_bounds__(kThreads<T>, 1) kv_tree_wide_kernel(TreeArgs a
                             w[2 * e + 1] = prmt(lo, hb, 0x7362);
                         }
                     } else {
-                        const uint32_t x = lds32(at + v_at + 2 * q * U::kVRow);
                         w[0] = table<0>(x, lane_v), w[1] = table<1>(x, lane_v);
                         w[2] = table<2>(x, lane_v), w[3] = table<3>(x, lane_v);
                     }
-                    sts128(dst + kTile + 256 * q + (piece ^ (32 * q)), mul2(w[0], s), mul2(w[1], s), mul2(w[2], s), mul2(w[3], s));
-                }
-                if (lane == 0) valid[i % kStages][d] = (uint8_t)((1u << count) - 1u);
+                    sts128<kTile + 256 * q>(dst ^ (32 * q), mul2(w[0], s), mul2(w[1], s), mul2(w[2], s), mul2(w[3], s));
+                });
+                if (lane == 0) valid[stage][u & (kUnits - 1)] = (uint8_t)((1u << count) - 1u);
                 fence_async_smem();
-                mbar_arrive(full + i % kStages);
+                mbar_arrive(full + stage);
                 __syncwarp();  // the ring's place is free for the next copy
                 at = at + U::kBytes == ring_end ? ring : at + U::kBytes;
+                stage += (u + D) / kUnits - u / kUnits;  // the next unit is 1 or 2 steps on
+                if (stage >= kStages) stage -= kStages, phase ^= 1;
             }
+
             asm volatile("cp.async.wait_group 0;" ::: "memory");
+            g += s1 - s0;
         }
-        __syncthreads();
-        if (*abort_flag) break;
-        g += s1 - s0;
-        p += s1 - s0;
     }
 
-    if (warp == kMma && lane == 0) {
-        tc_commit(&drain);  // completes when every MMA issued above has finished
+    if (warp >= kMma && elected()) {
         if (!mbar_wait_drain(&drain, 0)) *abort_flag = 1;
     }
     tc_fence_before();
@@ -543,7 +607,7 @@ tq_status launch(const TreeArgs& a, cudaStream_t st) {
     }();
     if (!fits) return TQ_ERR_UNSUPPORTED;
     if (ensure_smem((const void*)kv_tree_wide_kernel<KL, VL, T>, smem) != cudaSuccess) return TQ_ERR_CUDA;
-    kv_tree_wide_kernel<KL, VL, T><<<a.ctas, kThreads<T>, smem, st>>>(a);
+    kv_tree_wide_kernel<KL, VL, T><<<a.ctas, 32 * kWarps, smem, st>>>(a);
     return launch_status();
 }
 
