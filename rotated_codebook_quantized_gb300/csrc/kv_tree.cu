@@ -664,7 +664,7 @@ int sm_count() {
 }
 
 struct Plan {
-    int64_t tiles, slots, steps;  // output tiles of 16 rows, partial results at most, steps at most
+    int64_t tiles, slots, steps, turned;  // output tiles of 16 rows; partial results, steps, rows of turned queries at most
     int ctas, trows, stoks, least;
 };
 
@@ -682,6 +682,7 @@ Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, i
     p.steps = units * steps;
     p.ctas = (int)std::min<int64_t>(sms, (units * steps + p.least - 1) / p.least);
     p.slots = p.ctas ? units + p.ctas : 0;
+    p.turned = p.ctas && p.trows != kStep ? units * p.trows : 0;
     return p;
 }
 
@@ -710,7 +711,7 @@ extern "C" size_t tq_kv_attend_tree_workspace_bytes(const tq_kv_pages_t* cache, 
                                                     int64_t max_len) {
     if (kv_pages_check(cache, false) != TQ_OK || B <= 0 || n <= 0 || Hq <= 0 || Hq % cache->Hkv || max_len < 0) return 0;
     const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, kMaxSms);
-    return 16 + (size_t)p.slots * p.trows * (kPD * sizeof(float) + sizeof(float2));
+    return 16 + (size_t)p.slots * p.trows * (kPD * sizeof(float) + sizeof(float2)) + (size_t)p.turned * (kPD * 2 + 4);
 }
 
 extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q, int64_t q_stride, tq_dtype dt,
@@ -768,6 +769,8 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
     a.o = static_cast<__nv_bfloat16*>(o);
     a.part = static_cast<float*>(ws);
     a.stat = reinterpret_cast<float2*>(a.part + (size_t)p.slots * p.trows * kPD);
+    a.turned = reinterpret_cast<uint4*>(a.stat + (size_t)p.slots * p.trows);
+    a.power = reinterpret_cast<int32_t*>(a.turned + (size_t)p.turned * 16);
     a.err = err;
     cudaStream_t st = as_stream(stream);
     if (p.ctas) {

@@ -29,6 +29,8 @@ struct TreeArgs {
     __nv_bfloat16* o;
     float2* stat;  // [slot][trows]: running maximum (log2 units) and sum of a row
     float* part;   // [slot][trows][128]: weighted values, rotated
+    uint4* turned;   // more than 16 rows: rotated queries [unit][16 pieces][trows] and their exponents
+    int32_t* power;  // [unit][trows]
     uint32_t* err;
     long long wait_cycles;  // budget of each bounded wait
 };

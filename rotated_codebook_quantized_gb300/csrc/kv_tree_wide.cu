@@ -1,14 +1,16 @@
 // The cached context of tq_kv_attend_tree for more than 16 query rows to a kv head, on the 5th-generation tensor cores.
 //
-// A persistent CTA takes a run of 64-token steps.  Each step is decoded once into shared memory, as fp16 keys (K-major)
-// and values (MN-major, so that neither needs a transpose), for one or two tiles of 128 query rows:
-//   scores   S[128 x 64]   = Q (TMEM, fp16) . K^T (shared)          8 MMAs of K = 16
+// kv_tree_turn_kernel rotates the query rows once.  Then a persistent CTA takes a run of 64-token steps.  Each step is decoded
+// once into shared memory, as fp16 keys (K-major) and values (MN-major, so that neither needs a transpose), for one or two
+// tiles of 128 query rows; a tile's rows meet it by the half step of 32 tokens:
+//   scores   S[128 x 32]   = Q (TMEM, fp16) . K^T (shared)          8 MMAs of K = 16
 //   weights  P = exp2(S f - m), fp16, written over S in TMEM        one thread to a row
-//   values   O[128 x 128] += P (TMEM) . V (shared)                  4 MMAs of K = 16
-// Two streams of four softmax warps each, with scores and sums of their own, so that one stream's exponentials run beside
-// the other's products: the two tiles (T = 2), or the even and the odd steps of one tile (T = 1), joined at the end of the
-// run.  Decoder warps take units of 8 tokens in turn, each fed by a cp.async ring of its own; a thread to a stream issues its
-// MMAs (an issue costs its thread about 50 cycles: one thread for both streams held them up).
+//   values   O[128 x 128] += P (TMEM) . V (shared)                  2 MMAs of K = 16
+// Two streams of four softmax warps each, with scores and sums of their own: the two tiles (T = 2), or the even and the odd
+// steps of one tile (T = 1), joined at the end of the run.  A stream's scores alternate between two places, so that its
+// exponentials run beside its products (whole steps in one place measured 1.9 times as long: the tensor cores and the softmax
+// waited for one another).  Decoder warps take units of 8 tokens in turn, each fed by a cp.async ring of its own; a thread to
+// a stream issues its MMAs (an issue costs its thread about 30 cycles).
 // Operands from TMEM leave the shared-memory bandwidth to the decoders' table reads and stores and to the tensor cores'
 // reads of K and V.  A row's running maximum follows only when a score passes it by 2^kSlack, so O is seldom rescaled.
 // Every wait on an mbarrier is bounded; on expiry the CTA sets TQ_DEVERR_TIMEOUT, drains and frees TMEM.
@@ -25,7 +27,8 @@ constexpr int kTok = 64;       // tokens of a step
 constexpr int kUnit = 8;       // of a unit, which one decoder warp decodes
 constexpr int kUnits = kTok / kUnit;
 constexpr int kStages = 3;     // decoded steps
-constexpr int kDepth = 3;      // units of a decoder's ring: two in flight while one is decoded
+constexpr int kDepth = 2;      // units of a decoder's ring: one in flight while one is decoded
+constexpr int kPart = 32;      // tokens of a half step
 constexpr uint32_t kTile = kTok * kPD * 2;  // bytes of a step's keys, or values
 constexpr uint32_t kHalf = kTile / 2;       // of 64 of their dims (one 128-byte swizzled row a token)
 
@@ -33,8 +36,8 @@ constexpr uint32_t kHalf = kTile / 2;       // of 64 of their dims (one 128-byte
 // rings and barriers lie below it, the decoded steps above.
 constexpr uint32_t kTable = 65536, kSteps = 131072, kEnd = kSteps + kStages * 2 * kTile;
 constexpr uint32_t kStart = 1024 + 512;  // the system's first KB, then the static variables
-constexpr uint32_t kSigns = kStart, kOdd = kSigns + kPD * 4, kRings = kOdd + 2 * 128 * 4;
-constexpr int kDec = 10;  // decoder warps
+constexpr uint32_t kOdd = kStart, kRings = kOdd + 2 * 128 * 4;
+constexpr int kDec = 14;  // decoder warps
 static_assert(kEnd <= 232448, "fits an SM");
 
 template <int KL, int VL>
@@ -93,6 +96,13 @@ TQ_DEVFN void tc_ld8(uint32_t at, uint32_t* v) {
 TQ_DEVFN void tc_st8(uint32_t at, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::TQ_I8(0), "r"(at) : "memory");
 }
+TQ_DEVFN void tc_st16(uint32_t at, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::TQ_I8(
+            0),
+        TQ_I8(8), "r"(at)
+        : "memory");
+}
 #undef TQ_O8
 #undef TQ_I8
 #undef TQ_L32
@@ -111,86 +121,57 @@ TQ_DEVFN void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d
                  : "memory");
 }
 
-constexpr int kSoft = 8, kMma = kSoft + kDec, kWarps = kMma + 2;
+constexpr int kSoft = 8, kMma = kSoft + kDec, kWarps = kMma + 2;  // 24 warps: 80 registers a thread
 
-// The queries of a tile, a thread to a row: rotated by the cache's rotation, over a power of two of their own, as fp16 pairs in
-// the row's 64 TMEM columns at `to` (where `write` is set).  The transform of 128 is two of 64, of the sum and of the
-// difference of the row's halves; element i is packed with element i + 32.  Returns the power's exponent: the largest
-// element before the rotation bounds the sums after it by 2^7.
-TQ_DEVFN int turn_queries(const __nv_bfloat16* q, const float* signs, uint32_t to, float sgn, bool in, bool write) {
-    const uint4* src = reinterpret_cast<const uint4*>(q);
-    float top = 0.f;
-    if (in) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            const uint4 w = __ldg(src + c);
-            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
-        }
-    }
-    const int e = exponent_above(top) + 7;
-    if (!write) return e;
-    const float d = sgn * exp2f((float)-e);
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-        const float sg = half ? -d : d;
-        f2 x[32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {  // elements 8 c .. + 7 and 32 + 8 c .. + 7, and the same 64 on
-            float y[2][8];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint4 lo = in ? __ldg(src + c + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
-                const uint4 hi = in ? __ldg(src + 8 + c + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                    const float a = __uint_as_float(z & 1 ? l[z >> 1] & 0xffff0000u : l[z >> 1] << 16);
-                    const float b = __uint_as_float(z & 1 ? h[z >> 1] & 0xffff0000u : h[z >> 1] << 16);
-                    const int at = 8 * c + 32 * k + z;
-                    y[k][z] = fmaf(b * sg, signs[64 + at], a * d * signs[at]);
-                }
-            }
-#pragma unroll
-            for (int z = 0; z < 8; ++z) x[8 * c + z] = pk(y[0][z], y[1][z]);
-        }
-        const f2 minus = pk(-1.f, -1.f);
-#pragma unroll
-        for (int h = 1; h < 32; h <<= 1)
-#pragma unroll
-            for (int z = 0; z < 32; ++z)
-                if (!(z & h)) {
-                    const f2 a = x[z], b = x[z + h];
-                    x[z] = add2(a, b);
-                    x[z + h] = fma2(b, minus, a);
-                }
-        uint32_t w[32];
-#pragma unroll
-        for (int z = 0; z < 16; ++z) {
-            const float2 a = un(x[2 * z]), b = un(x[2 * z + 1]);
-            w[z] = pack_f16(a.x + a.y, b.x + b.y);
-            w[16 + z] = pack_f16(a.x - a.y, b.x - b.y);
-        }
-        tc_st32(to + 32 * half, w);
-    }
-    return e;
+// The queries, rotated, over a power of two of their own, fp16: a warp to a row.  Of a tile of `trows` rows the 16-byte pieces
+// [16][trows] lie together, a thread of the next kernel reading its row's; the power's exponent beside them.
+__global__ void __launch_bounds__(256) kv_tree_turn_kernel(TreeArgs a, int tiles) {
+    pdl_trigger();
+    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (at >= (int64_t)a.B * a.n * a.Hq) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t token = at / a.Hq;
+    const int hq = (int)(at - token * a.Hq), b = (int)(token / a.n), i = (int)(token - (int64_t)b * a.n);
+    if (i >= seq_live(a, b)) return;
+    const int h = hq / a.ratio, y = i * a.ratio + hq - h * a.ratio, tile = y / a.trows, row = y - tile * a.trows;
+    const uint2 raw = *reinterpret_cast<const uint2*>(a.q + token * a.qs + (int64_t)hq * kPD + lane * 4);
+    const uint32_t sg = *reinterpret_cast<const uint32_t*>(a.c.signs + lane * 4);
+    float v[4] = {__uint_as_float(raw.x << 16) * (float)(int8_t)sg, __uint_as_float(raw.x & 0xffff0000u) * (float)(int8_t)(sg >> 8),
+                  __uint_as_float(raw.y << 16) * (float)(int8_t)(sg >> 16),
+                  __uint_as_float(raw.y & 0xffff0000u) * (float)(int8_t)(sg >> 24)};
+    fwht_warp128(v);
+    // magnitudes order as their bits
+    const float top = __uint_as_float(__reduce_max_sync(
+        kFull, max(max(__float_as_uint(fabsf(v[0])), __float_as_uint(fabsf(v[1]))),
+                   max(__float_as_uint(fabsf(v[2])), __float_as_uint(fabsf(v[3]))))));
+    const int e = exponent_above(top);
+    const float d = a.scale2 < 0.f ? -exp2f((float)-e) : exp2f((float)-e);  // a negative scale's sign goes here
+    const int64_t unit = ((int64_t)b * a.c.Hkv + h) * tiles + tile;
+    uint8_t* to = reinterpret_cast<uint8_t*>(a.turned) + ((unit * 16 + (lane >> 1)) * a.trows + row) * 16 + (lane & 1) * 8;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_f16(v[0] * d, v[1] * d), pack_f16(v[2] * d, v[3] * d));
+    if (lane == 0) a.power[unit * a.trows + row] = e;
+}
+
+// A 16-byte asynchronous copy, where `on`.
+template <int OFF>
+TQ_DEVFN void cp16_if(uint32_t dst, const void* src, bool on) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n @p cp.async.cg.shared.global [%0+%3], [%1], 16;\n}\n" ::"r"(dst), "l"(src),
+                 "r"((int)on), "n"(OFF)
+                 : "memory");
 }
 
 template <int KL, int VL, int T>
-__global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a, int tiles) {
     using U = Unit<KL, VL>;
     constexpr int kRows = 128 * T, D = kDec;
     // TMEM columns: sums and scores of each stream, queries of each tile
     constexpr uint32_t kO = 0, kS = 256, kQ = 384;
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* const space = smem - (uint32_t)__cvta_generic_to_shared(smem);  // shared address 0
-    float* const signs = reinterpret_cast<float*>(space + kSigns);          // [128] of the rotation
     float* const odd = reinterpret_cast<float*>(space + kOdd);              // [2][128] maxima and sums of the odd steps (T = 1)
-    // full / empty: of a decoded step's place.  Of a stream: scores, weights, values written; queries written, and read for the
-    // last time.  Odd steps' statistics ready, and the sums they go with read (T = 1).
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], s_ready[2], p_ready[2], o_done[2], q_ready[2], q_free[2],
+    // full / empty: of a decoded step's place.  Of a stream's half step: scores, weights, values written.  Of a stream: queries
+    // written, and read for the last time.  Odd steps' statistics ready, and the sums they go with read (T = 1).
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], s_ready[2][2], p_ready[2][2], o_done[2][2], q_ready[2], q_free[2],
         odd_ready, odd_free, drain;
     __shared__ __align__(8) uint8_t valid[kStages][kUnits];  // tokens of each unit of a decoded step, a bit each
     __shared__ uint32_t tmem_slot;
@@ -208,9 +189,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                 mbar_init(empty + s, T);
             }
             for (int s = 0; s < 2; ++s) {
-                mbar_init(s_ready + s, 1);
-                mbar_init(p_ready + s, 128);
-                mbar_init(o_done + s, 1);
+                for (int e = 0; e < 2; ++e) {
+                    mbar_init(&s_ready[s][e], 1);
+                    mbar_init(&p_ready[s][e], 128);
+                    mbar_init(&o_done[s][e], 1);
+                }
                 mbar_init(q_ready + s, 128);
                 mbar_init(q_free + s, 3 - T);
             }
@@ -226,8 +209,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
     } else if (warp == kMma + 1) {
         const Run run = find_run(a, blockIdx.x);
         if (lane == 0) s_run = run;
-    } else if (tid < kPD) {
-        signs[tid] = (float)a.c.signs[tid];
     }
     const int ek = exponent_above(fmaxf(fabsf(a.c.kcent[0]), fabsf(a.c.kcent[KL - 1])));
     const int ev = exponent_above(fmaxf(fabsf(a.c.vcent[0]), fabsf(a.c.vcent[VL - 1])));
@@ -252,25 +233,37 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             while (ok && walk.next(a, x)) {
                 const uint32_t ge = g + (x.s1 - x.s0), first = g + (T == 1 ? t : 0);
                 ok = mbar_wait(q_ready + (T == 1 ? 0 : t), seg & 1, abort_flag, a.wait_cycles);
-                for (uint32_t i = first; i < ge && ok; i += 3 - T) {
+                // scores of half e of step i, the stream's n-th: they go where the weights of its step before were read from
+                auto scores = [&](uint32_t i, int e, uint32_t n) {
                     const uint32_t stage = i % kStages;
-                    // the scores go where the weights of the step before were read from
-                    ok = mbar_wait(full + stage, (i / kStages) & 1, abort_flag, a.wait_cycles) &&
-                         (i == first || mbar_wait(o_done + t, (done - 1) & 1, abort_flag, a.wait_cycles));
-                    if (!ok) break;
+                    if ((e == 0 && !mbar_wait(full + stage, (i / kStages) & 1, abort_flag, a.wait_cycles)) ||
+                        (i != first && !mbar_wait(&o_done[t][e], (n - 1) & 1, abort_flag, a.wait_cycles)))
+                        return false;
                     tc_fence_after();
-                    const uint64_t dk = desc(kSteps, 16) + stage * (2 * kTile / 16), dv = desc(kSteps + kTile, kHalf) + stage * (2 * kTile / 16);
+                    const uint64_t dk = desc(kSteps, 16) + stage * (2 * kTile / 16) + e * (kPart * 128 / 16);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        tc_mma_ts(to_s, from_q + 8 * k, dk + ((k >> 2) * (kHalf / 16) + 2 * (k & 3)), idesc(kTok, 0), k != 0);
-                    tc_commit(s_ready + t);
-                    ok = mbar_wait(p_ready + t, done & 1, abort_flag, a.wait_cycles);
-                    if (!ok) break;
-                    tc_fence_after();
+                        tc_mma_ts(to_s + kPart * e, from_q + 8 * k, dk + ((k >> 2) * (kHalf / 16) + 2 * (k & 3)), idesc(kPart, 0), k != 0);
+                    tc_commit(&s_ready[t][e]);
+                    return true;
+                };
+                if (ok && first < ge) ok = scores(first, 0, done);
+                for (uint32_t i = first; i < ge && ok; i += 3 - T) {
+                    const uint32_t stage = i % kStages;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tc_mma_ts(to_o, to_s + 8 * k, dv + 128 * k, idesc(kPD, 1), i != first || k != 0);
-                    tc_commit(o_done + t);
-                    tc_commit(empty + stage);
+                    for (int e = 0; e < 2; ++e) {
+                        if (e == 0) ok = scores(i, 1, done);
+                        else if (i + (3 - T) < ge) ok = scores(i + (3 - T), 0, done + 1);
+                        if (ok) ok = mbar_wait(&p_ready[t][e], done & 1, abort_flag, a.wait_cycles);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t dv = desc(kSteps + kTile, kHalf) + stage * (2 * kTile / 16) + e * (kPart * 128 / 16);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            tc_mma_ts(to_o, to_s + kPart * e + 8 * k, dv + 128 * k, idesc(kPD, 1), i != first || e != 0 || k != 0);
+                        tc_commit(&o_done[t][e]);
+                        if (e == 1) tc_commit(empty + stage);
+                    }
                     ++done;
                 }
                 mbar_arrive(q_free + (T == 1 ? 0 : t));
@@ -293,13 +286,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             const bool writer = T == 2 || stream == 0;
             if (writer && seg) ok = __all_sync(kFull, mbar_wait(q_free + (T == 1 ? 0 : stream), (seg - 1) & 1, abort_flag, a.wait_cycles));
             if (!ok) break;
-            float f = 0.f;  // from a row's products to log2 scores
+            float f = 0.f;  // from a row's products to log2 scores: not negative
+            if (seg == 0) pdl_wait();  // the turned queries
             if (!idle) {
-                const int y = x.tile * kRows + row, i = y / a.ratio;
-                const __nv_bfloat16* q = a.q + ((int64_t)x.b * a.n + i) * a.qs + (int64_t)(x.h * a.ratio + y - i * a.ratio) * kPD;
-                const int e = turn_queries(q, signs, tmem + kQ + (T == 1 ? 0 : 64 * stream) + lanes, a.scale2 < 0.f ? -1.f : 1.f, row < x.rows, writer);
-                f = exp2f((float)(e + ek)) * (kInvSqrtD * fabsf(a.scale2));  // not negative: a scale's sign goes to the queries
-                if (writer) tc_wait_st();
+                const int64_t unit = ((int64_t)x.b * a.c.Hkv + x.h) * tiles + x.tile;
+                const bool in = row < x.rows;
+                if (writer) {
+                    const uint4* src = a.turned + unit * 16 * kRows + row;
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint4 v = in ? src[(8 * half + c) * kRows] : make_uint4(0u, 0u, 0u, 0u);
+                            w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+                        }
+                        tc_st32(tmem + kQ + (T == 1 ? 0 : 64 * stream) + 32 * half + lanes, w);
+                    }
+                    tc_wait_st();
+                }
+                f = exp2f((float)((in ? a.power[unit * kRows + row] : 0) + ek)) * (kInvSqrtD * fabsf(a.scale2));
             }
             if (writer) {
                 tc_fence_before();
@@ -307,76 +313,79 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             }
             float m = -INFINITY, l = 0.f, bias = 0.f;
             for (uint32_t i = first; i < ge; i += 3 - T) {
-                // (the decoders' barrier has long completed; waiting on it too orders their `valid` before the read)
-                ok = mbar_wait(s_ready + stream, done & 1, abort_flag, a.wait_cycles) &&
-                     mbar_wait(full + i % kStages, (i / kStages) & 1, abort_flag, a.wait_cycles);
-                ok = __all_sync(kFull, ok);
-                if (!ok) break;
-                tc_fence_after();
-                if (!idle) {
-                    uint32_t s[64];
-                    tc_ld32(at, s);
-                    tc_ld32(at + 32, s + 32);
-                    tc_wait_ld();
-                    const unsigned long long in = *reinterpret_cast<const unsigned long long*>(valid[i % kStages]);
-                    if (in != ~0ull) {  // tokens past the end, or of a bad page
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (!((in >> c) & 1)) s[c] = __float_as_uint(-INFINITY);
-                    }
-                    float x[4];
+                for (int e = 0; e < 2; ++e) {
+                    // (the decoders' barrier has long completed; waiting on it too orders their `valid` before the read)
+                    ok = mbar_wait(&s_ready[stream][e], done & 1, abort_flag, a.wait_cycles) &&
+                         (e || mbar_wait(full + i % kStages, (i / kStages) & 1, abort_flag, a.wait_cycles));
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (!idle) {
+                        uint32_t s[32];
+                        tc_ld32(at + kPart * e, s);
+                        const uint32_t in = *reinterpret_cast<const uint32_t*>(&valid[i % kStages][4 * e]);
+                        tc_wait_ld();
+                        if (in != ~0u) {  // tokens past the end, or of a bad page
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) x[c] = __uint_as_float(s[c]);
+                            for (int c = 0; c < 32; ++c)
+                                if (!((in >> c) & 1)) s[c] = __float_as_uint(-INFINITY);
+                        }
+                        float x4[4];
 #pragma unroll
-                    for (int c = 4; c < 60; c += 8)
+                        for (int c = 0; c < 4; ++c) x4[c] = __uint_as_float(s[c]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[e] = fmaxf(fmaxf(x[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + e + 4]));
+                        for (int c = 4; c < 28; c += 8)
 #pragma unroll
-                    for (int c = 60; c < 64; ++c) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
-                    const float top = f * fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-                    if (__any_sync(kFull, top > m + kSlack)) {
-                        const float n = fmaxf(m, top), r = m == -INFINITY ? 0.f : fast_exp2(m - n);
-                        m = n;
-                        bias = m == -INFINITY ? 0.f : -m;
-                        l *= r;
-                        if (i != first) {  // the sums so far, once the last product has written them
-                            ok = __all_sync(kFull, mbar_wait(o_done + stream, (done - 1) & 1, abort_flag, a.wait_cycles));
-                            if (!ok) break;
-                            tc_fence_after();
+                            for (int z = 0; z < 4; ++z)
+                                x4[z] = fmaxf(fmaxf(x4[z], __uint_as_float(s[c + z])), __uint_as_float(s[c + z + 4]));
+#pragma unroll
+                        for (int c = 28; c < 32; ++c) x4[c & 3] = fmaxf(x4[c & 3], __uint_as_float(s[c]));
+                        const float top = f * fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
+                        if (__any_sync(kFull, top > m + kSlack)) {
+                            const float n = fmaxf(m, top), r = m == -INFINITY ? 0.f : fast_exp2(m - n);
+                            m = n;
+                            bias = m == -INFINITY ? 0.f : -m;
+                            l *= r;
+                            if (e || i != first) {  // the sums so far, once the last product has written them
+                                ok = __all_sync(kFull, mbar_wait(&o_done[stream][e ^ 1], (done - (e ^ 1)) & 1, abort_flag, a.wait_cycles));
+                                if (!ok) break;
+                                tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < 16; ++c) {
-                                uint32_t o[8];
-                                tc_ld8(col_o + 8 * c, o);
-                                tc_wait_ld();
+                                for (int c = 0; c < 16; ++c) {
+                                    uint32_t o[8];
+                                    tc_ld8(col_o + 8 * c, o);
+                                    tc_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
-                                tc_st8(col_o + 8 * c, o);
+                                    for (int z = 0; z < 8; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * r);
+                                    tc_st8(col_o + 8 * c, o);
+                                }
                             }
                         }
-                    }
-                    const f2 ff = pk(f, f), bb = pk(bias, bias);
-                    f2 ls[2] = {0, 0};
+                        const f2 ff = pk(f, f), bb = pk(bias, bias);
+                        f2 ls[2] = {0, 0};
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {  // the weights take the scores' registers
-                        const float2 e = un(fma2(pk(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), ff, bb));
-                        const float u = fast_exp2(e.x), v = fast_exp2(e.y);
-                        ls[c & 1] = add2(ls[c & 1], pk(u, v));
-                        s[c] = pack_f16(u, v);
+                        for (int c = 0; c < 16; ++c) {  // the weights take the scores' registers
+                            const float2 y = un(fma2(pk(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), ff, bb));
+                            const float u = fast_exp2(y.x), v = fast_exp2(y.y);
+                            ls[c & 1] = add2(ls[c & 1], pk(u, v));
+                            s[c] = pack_f16(u, v);
+                        }
+                        const float2 sum = un(add2(ls[0], ls[1]));
+                        l += sum.x + sum.y;
+                        tc_st16(at + kPart * e, s);
+                        tc_wait_st();
                     }
-                    const float2 sum = un(add2(ls[0], ls[1]));
-                    l += sum.x + sum.y;
-                    tc_st32(at, s);
-                    tc_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&p_ready[stream][e]);
                 }
-                tc_fence_before();
-                mbar_arrive(p_ready + stream);
+                if (!ok) break;
                 ++done;
             }
             if (!ok) break;
             // ---- the stretch's partial result
             if (first < ge) {  // (the odd steps may be none)
-                ok = __all_sync(kFull, mbar_wait(o_done + stream, (done - 1) & 1, abort_flag, a.wait_cycles));
+                ok = __all_sync(kFull, mbar_wait(&o_done[stream][1], (done - 1) & 1, abort_flag, a.wait_cycles));
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -463,24 +472,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             const int page = page_next, u = ahead;
             ahead += D;
             page_next = page_of(ahead);
-            counts <<= 4;
-            if (u < u1) {
-                if ((uint32_t)page < (uint32_t)a.c.pages) {
-                    counts |= (uint32_t)min(len - u * kUnit, kUnit);
-                    const uint64_t row8 = (uint32_t)page * page8 + (uint32_t)h * head8 + (u & in_page);
-                    const uint8_t* k = kc + row8 * (kUnit * U::kKRow);
-                    cp16(fill + U::kK + lane * 16, k);
-                    if (KL == 256) cp16(fill + U::kK + lane * 16 + 512, k + 512);
-                    if (copies_v) cp16(fill + U::kV + lane * 16, vc + row8 * (kUnit * U::kVRow));
-                    if (copies_z) cp16(fill + z_at, zc + row8 * (uint32_t)(kUnit * 2 * ng));
-                } else if (lane == 0 && a.err) {
-                    atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
-                }
-            }
+            const bool in = u < u1, good = in && (uint32_t)page < (uint32_t)a.c.pages;
+            counts = counts << 4 | (good ? (uint32_t)min(len - u * kUnit, kUnit) : 0u);
+            const uint64_t row8 = (uint32_t)page * page8 + (uint32_t)h * head8 + (u & in_page);
+            const uint8_t* k = kc + row8 * (kUnit * U::kKRow);
+            cp16_if<U::kK>(fill + lane * 16, k, good);
+            if (KL == 256) cp16_if<U::kK + 512>(fill + lane * 16, k + 512, good);
+            cp16_if<U::kV>(fill + lane * 16, vc + row8 * (kUnit * U::kVRow), good && copies_v);
+            cp16_if<0>(fill + z_at, zc + row8 * (uint32_t)(kUnit * 2 * ng), good && copies_z);
             asm volatile("cp.async.commit_group;" ::: "memory");
+            if (in && !good && lane == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
             fill = fill + U::kBytes == ring_end ? ring : fill + U::kBytes;
         };
-
             page_next = page_of(ahead);
 #pragma unroll
             for (int i = 0; i < kDepth - 1; ++i) issue();
@@ -607,8 +610,12 @@ tq_status launch(const TreeArgs& a, cudaStream_t st) {
     }();
     if (!fits) return TQ_ERR_UNSUPPORTED;
     if (ensure_smem((const void*)kv_tree_wide_kernel<KL, VL, T>, smem) != cudaSuccess) return TQ_ERR_CUDA;
-    kv_tree_wide_kernel<KL, VL, T><<<a.ctas, 32 * kWarps, smem, st>>>(a);
-    return launch_status();
+    const int tiles = (a.n * a.ratio + a.trows - 1) / a.trows;
+    kv_tree_turn_kernel<<<(unsigned)(((int64_t)a.B * a.n * a.Hq + 7) / 8), 256, 0, st>>>(a, tiles);
+    const tq_status s = launch_status();
+    if (s != TQ_OK) return s;
+    // its prologue and first copies run beside the turn, which began after everything before it on the stream had ended
+    return launch_pdl(kv_tree_wide_kernel<KL, VL, T>, dim3((unsigned)a.ctas), dim3(32 * kWarps), smem, st, a, tiles);
 }
 
 template <int T>
