@@ -252,8 +252,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                     const uint32_t stage = i % kStages;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        // the next half's scores first, so that they are there when the softmax is done with this half; but a
+                        // step that is not decoded yet is not waited for (its place may be this step's to free)
+                        const uint32_t on = i + (3 - T);
+                        const bool next = e == 1 && on < ge, early = next && mbar_peek(full + on % kStages, (on / kStages) & 1);
                         if (e == 0) ok = scores(i, 1, done);
-                        else if (i + (3 - T) < ge) ok = scores(i + (3 - T), 0, done + 1);
+                        else if (early) ok = scores(on, 0, done + 1);
                         if (ok) ok = mbar_wait(&p_ready[t][e], done & 1, abort_flag, a.wait_cycles);
                         if (!ok) break;
                         tc_fence_after();
@@ -263,6 +267,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                             tc_mma_ts(to_o, to_s + kPart * e + 8 * k, dv + 128 * k, idesc(kPD, 1), i != first || e != 0 || k != 0);
                         tc_commit(&o_done[t][e]);
                         if (e == 1) tc_commit(empty + stage);
+                        if (next && !early) ok = scores(on, 0, done + 1);
                     }
                     ++done;
                 }
