@@ -168,10 +168,16 @@ def _check(status: int, what: str):
 
 # ---------------------------------------------------------------- torch marshalling
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -182,9 +188,14 @@ def _stream():
     return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
 
 
+_dtype_codes = {}
+
+
 def _dt(t) -> int:
-    torch = _torch()
-    return {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}[t.dtype]
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16})
+    return _dtype_codes[t.dtype]
 
 
 def _torch_dtype(code: int):
@@ -605,9 +616,14 @@ class Rope:
         self.steps = steps.to(device).contiguous()
         self.factor = 1.0 if factor is None else float(factor)
 
+        self._c = tq_rope_t(self.dim, self.rotary, TQ_ROPE_INTERLEAVED if layout == "interleaved" else TQ_ROPE_HALF,
+                            self.factor, self.steps.data_ptr())
+
     def c(self) -> tq_rope_t:
-        return tq_rope_t(self.dim, self.rotary, TQ_ROPE_INTERLEAVED if self.layout == "interleaved" else TQ_ROPE_HALF,
-                         self.factor, self.steps.data_ptr())
+        return self._c
+
+    def ref(self):
+        return ctypes.byref(self._c)
 
 
 def rope_steps(rotary: int, base: float = 10000.0, scaling: dict | None = None):
@@ -626,55 +642,69 @@ def rope_steps(rotary: int, base: float = 10000.0, scaling: dict | None = None):
     return steps, float(factor.value)
 
 
+# A decode step's calls last about as long on the GPU as their arguments take to check, so the calls below keep their
+# Python short: plain integers for pointers, one shape and one stride query a tensor, descriptors kept with their handles.
+
+def _raw_stream(t) -> int:
+    """torch's current stream on the tensor's device, as a number."""
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _heads(x, name, dim):
     """(tokens, heads, token stride) of x [..., heads, dim] whose heads lie one after another."""
-    if not x.is_cuda or x.dim() < 3 or x.shape[-1] != dim:
+    shape = x.shape
+    nd = len(shape)
+    if not x.is_cuda or nd < 3 or shape[-1] != dim:
         raise ValueError(f"{name} must be a CUDA tensor [..., heads, {dim}]")
-    lead, stride = x.shape[:-2], x.stride()
-    if x.numel() and (stride[-1] != 1 or (x.shape[-2] > 1 and stride[-2] != dim)):
-        raise ValueError(f"{name}'s heads must lie one after another")
+    stride, heads = x.stride(), shape[-2]
     tokens, step = 1, None
-    for size, st in zip(reversed(lead), reversed(stride[:-2])):
+    for i in range(nd - 3, -1, -1):
+        size = shape[i]
         if size == 1:
             continue
+        if size == 0:
+            return 0, heads, heads * dim
         if step is None:
-            step = st
-        elif st != step * tokens:
+            step = stride[i]
+        elif stride[i] != step * tokens:
             raise ValueError(f"{name}'s tokens must lie at one stride")
         tokens *= size
-    return (0 if 0 in lead else tokens), x.shape[-2], (x.shape[-2] * dim if step is None else step)
+    if heads and (stride[-1] != 1 or (heads > 1 and stride[-2] != dim)):
+        raise ValueError(f"{name}'s heads must lie one after another")
+    return tokens, heads, (heads * dim if step is None else step)
 
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} must be on {ref.device}")
-
-
-def _ints(t, name, count, dtype=None):
-    torch = _torch()
-    if not t.is_cuda or t.dtype != (dtype or torch.int32) or not t.is_contiguous() or t.numel() != count:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {count} {dtype or torch.int32}")
-    return t
+def _ints(t, name, count, device, dtype=None):
+    """The address of a contiguous integer tensor of `count` entries (int32 unless told otherwise)."""
+    if dtype is None:
+        dtype = _torch().int32
+    if t.dtype is not dtype or t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {count} {dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the same device as the others")
+    return t.data_ptr()
 
 
 def rope(q, positions, r: Rope, k=None, inverse: bool = False, inplace: bool = False):
     """Rotary positions of q [..., Hq, dim] and, in the same launch, k [..., Hkv, dim] (views of a fused
     projection are fine); positions: int32 with one entry per token.  Returns q's result, or (q's, k's)."""
-    torch = _torch()
-    T, hq, qs = _heads(q, "q", r.dim)
-    _ints(positions, "positions", T)
-    _same_device(q, positions=positions, k=k, steps=r.steps)
-    yq, yqs = (q, qs) if inplace else (torch.empty(q.shape, dtype=q.dtype, device=q.device), hq * r.dim)
-    yk, hk, ks, yks = None, 0, 0, 0
-    if k is not None:
-        Tk, hk, ks = _heads(k, "k", r.dim)
-        if Tk != T or k.dtype != q.dtype:
-            raise ValueError("k must have q's tokens and dtype")
-        yk, yks = (k, ks) if inplace else (torch.empty(k.shape, dtype=k.dtype, device=k.device), hk * r.dim)
-    c = r.c()
-    _check(load().tq_rope(ctypes.byref(c), _ptr(positions), T, _dt(q), int(inverse), _ptr(q), qs, hq, _ptr(yq), yqs,
-                          _ptr(k), ks, hk, _ptr(yk), yks, _stream()), "tq_rope")
+    dim, dev = r.dim, q.get_device()
+    T, hq, qs = _heads(q, "q", dim)
+    pos = _ints(positions, "positions", T, dev)
+    if r.steps.get_device() != dev:
+        raise ValueError("the rotary frequencies must be on q's device")
+    yq, yqs = (q, qs) if inplace else (q.new_empty(q.shape), hq * dim)
+    if k is None:
+        kp = ks = hk = yp = yks = 0
+        yk = None
+    else:
+        Tk, hk, ks = _heads(k, "k", dim)
+        if Tk != T or k.dtype is not q.dtype or k.get_device() != dev:
+            raise ValueError("k must have q's tokens, dtype and device")
+        yk, yks = (k, ks) if inplace else (k.new_empty(k.shape), hk * dim)
+        kp, yp = k.data_ptr(), yk.data_ptr()
+    _check(load().tq_rope(r.ref(), pos, T, _dt(q), int(inverse), q.data_ptr(), qs, hq, yq.data_ptr(), yqs, kp, ks, hk, yp,
+                          yks, _raw_stream(q)), "tq_rope")
     return yq if k is None else (yq, yk)
 
 
@@ -721,9 +751,31 @@ class PagedKVCache:
         return self
 
     def c(self) -> tq_kv_pages_t:
-        return tq_kv_pages_t(self.kcodes.data_ptr(), self.kscales.data_ptr(), self.vcodes.data_ptr(),
-                             self.vscales.data_ptr(), self.heads, self.dim, self.group, self.page, self.pages,
-                             self.page_stride, self.head_stride, self.kcb.c(), self.vcb.c(), self.rot.c())
+        c = tq_kv_pages_t(self.kcodes.data_ptr(), self.kscales.data_ptr(), self.vcodes.data_ptr(),
+                          self.vscales.data_ptr(), self.heads, self.dim, self.group, self.page, self.pages,
+                          self.page_stride, self.head_stride, self.kcb.c(), self.vcb.c(), self.rot.c())
+        self._kept = (self.kcodes, self.kscales, self.vcodes, self.vscales, self.kcb, self.vcb, self.rot)
+        self._c, self._sizes = c, {}
+        return c
+
+    def ref(self):
+        """The descriptor, made again when a tensor or book of the cache was replaced."""
+        k = self.__dict__.get("_kept")
+        if k is None or not (k[0] is self.kcodes and k[1] is self.kscales and k[2] is self.vcodes and k[3] is self.vscales
+                             and k[4] is self.kcb and k[5] is self.vcb and k[6] is self.rot):
+            self.c()
+        return ctypes.byref(self._c)
+
+    def tree_bytes(self, B, n, hq, max_len) -> int:
+        """Workspace of kv_attend_tree at these sizes."""
+        key = (B, n, hq, max_len)
+        ref = self.ref()
+        nb = self._sizes.get(key)
+        if nb is None:
+            if len(self._sizes) > 4096:
+                self._sizes.clear()
+            nb = self._sizes[key] = int(load().tq_kv_attend_tree_workspace_bytes(ref, B, n, hq, max_len))
+        return nb
 
 
 def kv_append(cache: PagedKVCache, k, v, slots, rope: Rope | None = None, positions=None, err=None):
@@ -732,31 +784,31 @@ def kv_append(cache: PagedKVCache, k, v, slots, rope: Rope | None = None, positi
     With ``rope`` and ``positions`` the keys get their rotary positions on the way."""
     T, h, ks = _heads(k, "k", cache.dim)
     Tv, hv, vs = _heads(v, "v", cache.dim)
-    if (T, h) != (Tv, hv) or h != cache.heads or k.dtype != v.dtype:
-        raise ValueError("k and v must have the same tokens, the cache's heads and one dtype")
-    _ints(slots, "slots", T)
+    dev = k.get_device()
+    if T != Tv or h != hv or h != cache.heads or k.dtype is not v.dtype or v.get_device() != dev:
+        raise ValueError("k and v must have the same tokens, the cache's heads, one dtype and one device")
+    if cache.kcodes.get_device() != dev:
+        raise ValueError("the cache must be on the tokens' device")
+    at = _ints(slots, "slots", T, dev)
+    turn, pos = None, 0
     if rope is not None:
         if positions is None:
             raise ValueError("rope needs positions")
-        _ints(positions, "positions", T)
-    _same_device(k, v=v, slots=slots, positions=positions, cache=cache.kcodes)
-    c, r = cache.c(), rope.c() if rope is not None else None
-    _check(load().tq_kv_append(ctypes.byref(c), _ptr(k), ks, _ptr(v), vs, _dt(k), T, _ptr(slots),
-                               ctypes.byref(r) if r is not None else None, _ptr(positions), _ptr(err), _stream()),
-           "tq_kv_append")
+        if rope.steps.get_device() != dev:
+            raise ValueError("the rotary frequencies must be on the tokens' device")
+        turn, pos = rope.ref(), _ints(positions, "positions", T, dev)
+    _check(load().tq_kv_append(cache.ref(), k.data_ptr(), ks, v.data_ptr(), vs, _dt(k), T, at, turn, pos,
+                               0 if err is None else err.data_ptr(), _raw_stream(k)), "tq_kv_append")
 
 
 def kv_fetch(cache: PagedKVCache, slots, out_dtype=None, err=None):
     """The tokens of ``slots`` (int32 [T]) as (k, v) [T, heads, dim], bf16 unless told otherwise; a negative slot is zeros."""
-    torch = _torch()
-    T = slots.numel()
-    _ints(slots, "slots", T)
-    _same_device(slots, cache=cache.kcodes)
-    k = torch.empty((T, cache.heads, cache.dim), dtype=out_dtype or torch.bfloat16, device=slots.device)
-    v = torch.empty_like(k)
-    c = cache.c()
-    _check(load().tq_kv_fetch(ctypes.byref(c), _ptr(slots), T, _ptr(k), _ptr(v), _dt(k), _ptr(err), _stream()),
-           "tq_kv_fetch")
+    T, dev = slots.numel(), cache.kcodes.get_device()
+    at = _ints(slots, "slots", T, dev)
+    k = cache.kcodes.new_empty((T, cache.heads, cache.dim), dtype=out_dtype or _torch().bfloat16)
+    v = k.new_empty(k.shape)
+    _check(load().tq_kv_fetch(cache.ref(), at, T, k.data_ptr(), v.data_ptr(), _dt(k), 0 if err is None else err.data_ptr(),
+                              _raw_stream(slots)), "tq_kv_fetch")
     return k, v
 
 
@@ -768,37 +820,37 @@ def kv_attend_tree(cache: PagedKVCache, q, table, lens, k_new=None, v_new=None, 
     the host knows (default: what the table can hold).  k_new, v_new: the drafts' own keys and values
     [B, n, heads, dim] (bf16); mask: int64 [B, n, ceil(n/64)], bit j of row i set where draft i sees draft j
     (None: a chain, j <= i); n_tok: int32 [B] drafts in use.  Returns [B, n, Hq, dim] bf16."""
-    torch = _torch()
     if q.dim() != 4:
         raise ValueError("q must be [B, n, heads, dim]")
+    dim, dev = cache.dim, q.get_device()
+    _, hq, qs = _heads(q, "q", dim)
     B, n = q.shape[:2]
-    _, hq, qs = _heads(q, "q", cache.dim)
     if table.dim() != 2 or table.shape[0] != B:
         raise ValueError(f"table must be [{B}, pages]")
-    _ints(table, "table", table.numel())
-    _ints(lens, "lens", B)
-    ks = vs = 0
+    wide = table.shape[1]
+    tp, lp = _ints(table, "table", B * wide, dev), _ints(lens, "lens", B, dev)
+    kp = vp = ks = vs = 0
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
     if k_new is not None:
-        for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-            if tuple(t.shape) != (B, n, cache.heads, cache.dim) or t.dtype != q.dtype:
-                raise ValueError(f"{name} must be [{B}, {n}, {cache.heads}, {cache.dim}] of q's dtype")
-        ks, vs = _heads(k_new, "k_new", cache.dim)[2], _heads(v_new, "v_new", cache.dim)[2]
-    if mask is not None:
-        _ints(mask, "mask", B * n * (-(-n // 64)), torch.int64)
-    if n_tok is not None:
-        _ints(n_tok, "n_tok", B)
-    _same_device(q, table=table, lens=lens, k_new=k_new, v_new=v_new, mask=mask, n_tok=n_tok, cache=cache.kcodes)
-    max_len = table.shape[1] * cache.page if max_len is None else int(max_len)
-    o = torch.empty((B, n, hq, cache.dim), dtype=torch.bfloat16, device=q.device)
-    c = cache.c()
-    nb = int(load().tq_kv_attend_tree_workspace_bytes(ctypes.byref(c), B, n, hq, max_len))
-    ws = _workspace(nb, q.device, ws)
-    _check(load().tq_kv_attend_tree(ctypes.byref(c), _ptr(q), qs, _dt(q), B, n, hq, _ptr(table), table.shape[1],
-                                    _ptr(lens), max_len, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(mask), _ptr(n_tok),
-                                    cache.dim ** -0.5 if scale is None else scale, _ptr(o), _ptr(ws), nb, _ptr(err),
-                                    _stream()), "tq_kv_attend_tree")
+        want = (B, n, cache.heads, dim)
+        if k_new.shape != want or v_new.shape != want or k_new.dtype is not q.dtype or v_new.dtype is not q.dtype:
+            raise ValueError(f"k_new and v_new must be {list(want)} of q's dtype")
+        if k_new.get_device() != dev or v_new.get_device() != dev:
+            raise ValueError("k_new and v_new must be on q's device")
+        kp, ks, vp, vs = k_new.data_ptr(), _heads(k_new, "k_new", dim)[2], v_new.data_ptr(), _heads(v_new, "v_new", dim)[2]
+    if cache.kcodes.get_device() != dev:
+        raise ValueError("the cache must be on q's device")
+    mp = 0 if mask is None else _ints(mask, "mask", B * n * (-(-n // 64)), dev, _torch().int64)
+    np_ = 0 if n_tok is None else _ints(n_tok, "n_tok", B, dev)
+    max_len = wide * cache.page if max_len is None else int(max_len)
+    o = q.new_empty((B, n, hq, dim), dtype=_torch().bfloat16)
+    nb = cache.tree_bytes(B, n, hq, max_len)
+    if ws is None or ws.numel() * ws.element_size() < nb:
+        ws = q.new_empty(nb, dtype=_torch().uint8)
+    _check(load().tq_kv_attend_tree(cache.ref(), q.data_ptr(), qs, _dt(q), B, n, hq, tp, wide, lp, max_len, kp, ks, vp, vs, mp,
+                                    np_, dim ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr(), nb,
+                                    0 if err is None else err.data_ptr(), _raw_stream(q)), "tq_kv_attend_tree")
     return o
 
 
