@@ -643,7 +643,8 @@ def rope_steps(rotary: int, base: float = 10000.0, scaling: dict | None = None):
 
 
 # A decode step's calls last about as long on the GPU as their arguments take to check, so the calls below keep their
-# Python short: plain integers for pointers, one shape and one stride query a tensor, descriptors kept with their handles.
+# Python short: plain integers for pointers, one shape and one stride query a tensor, descriptors kept with their handles,
+# torch.empty (1.6 us; new_empty takes 3.6).
 
 def _raw_stream(t) -> int:
     """torch's current stream on the tensor's device, as a number."""
@@ -693,7 +694,7 @@ def rope(q, positions, r: Rope, k=None, inverse: bool = False, inplace: bool = F
     pos = _ints(positions, "positions", T, dev)
     if r.steps.get_device() != dev:
         raise ValueError("the rotary frequencies must be on q's device")
-    yq, yqs = (q, qs) if inplace else (q.new_empty(q.shape), hq * dim)
+    yq, yqs = (q, qs) if inplace else (_torch().empty(q.shape, dtype=q.dtype, device=q.device), hq * dim)
     if k is None:
         kp = ks = hk = yp = yks = 0
         yk = None
@@ -701,7 +702,7 @@ def rope(q, positions, r: Rope, k=None, inverse: bool = False, inplace: bool = F
         Tk, hk, ks = _heads(k, "k", dim)
         if Tk != T or k.dtype is not q.dtype or k.get_device() != dev:
             raise ValueError("k must have q's tokens, dtype and device")
-        yk, yks = (k, ks) if inplace else (k.new_empty(k.shape), hk * dim)
+        yk, yks = (k, ks) if inplace else (_torch().empty(k.shape, dtype=k.dtype, device=k.device), hk * dim)
         kp, yp = k.data_ptr(), yk.data_ptr()
     _check(load().tq_rope(r.ref(), pos, T, _dt(q), int(inverse), q.data_ptr(), qs, hq, yq.data_ptr(), yqs, kp, ks, hk, yp,
                           yks, _raw_stream(q)), "tq_rope")
@@ -805,8 +806,9 @@ def kv_fetch(cache: PagedKVCache, slots, out_dtype=None, err=None):
     """The tokens of ``slots`` (int32 [T]) as (k, v) [T, heads, dim], bf16 unless told otherwise; a negative slot is zeros."""
     T, dev = slots.numel(), cache.kcodes.get_device()
     at = _ints(slots, "slots", T, dev)
-    k = cache.kcodes.new_empty((T, cache.heads, cache.dim), dtype=out_dtype or _torch().bfloat16)
-    v = k.new_empty(k.shape)
+    torch = _torch()
+    shape, dtype, device = (T, cache.heads, cache.dim), out_dtype or torch.bfloat16, slots.device
+    k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
     _check(load().tq_kv_fetch(cache.ref(), at, T, k.data_ptr(), v.data_ptr(), _dt(k), 0 if err is None else err.data_ptr(),
                               _raw_stream(slots)), "tq_kv_fetch")
     return k, v
@@ -824,7 +826,7 @@ def kv_attend_tree(cache: PagedKVCache, q, table, lens, k_new=None, v_new=None, 
         raise ValueError("q must be [B, n, heads, dim]")
     dim, dev = cache.dim, q.get_device()
     _, hq, qs = _heads(q, "q", dim)
-    B, n = q.shape[:2]
+    B, n, _, _ = q.shape
     if table.dim() != 2 or table.shape[0] != B:
         raise ValueError(f"table must be [{B}, pages]")
     wide = table.shape[1]
@@ -844,10 +846,11 @@ def kv_attend_tree(cache: PagedKVCache, q, table, lens, k_new=None, v_new=None, 
     mp = 0 if mask is None else _ints(mask, "mask", B * n * (-(-n // 64)), dev, _torch().int64)
     np_ = 0 if n_tok is None else _ints(n_tok, "n_tok", B, dev)
     max_len = wide * cache.page if max_len is None else int(max_len)
-    o = q.new_empty((B, n, hq, dim), dtype=_torch().bfloat16)
+    torch, device = _torch(), q.device
+    o = torch.empty((B, n, hq, dim), dtype=torch.bfloat16, device=device)
     nb = cache.tree_bytes(B, n, hq, max_len)
     if ws is None or ws.numel() * ws.element_size() < nb:
-        ws = q.new_empty(nb, dtype=_torch().uint8)
+        ws = torch.empty(nb, dtype=torch.uint8, device=device)
     _check(load().tq_kv_attend_tree(cache.ref(), q.data_ptr(), qs, _dt(q), B, n, hq, tp, wide, lp, max_len, kp, ks, vp, vs, mp,
                                     np_, dim ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr(), nb,
                                     0 if err is None else err.data_ptr(), _raw_stream(q)), "tq_kv_attend_tree")
