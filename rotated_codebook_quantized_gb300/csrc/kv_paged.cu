@@ -86,9 +86,11 @@ TQ_DEVFN float sign_of(uint2 w, int i, float factor) {
     return (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3))) < 0 ? -factor : factor;
 }
 
-TQ_DEVFN void load8(const void* p, int64_t at, int dt, float (&y)[8]) {
-    if (dt == TQ_BF16) {
-        const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p) + at);
+// Eight elements from 16 (bf16) or 32 (f32) bytes of shared memory.
+template <bool BF16>
+TQ_DEVFN void load8(const uint8_t* p, float (&y)[8]) {
+    if constexpr (BF16) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
         const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -96,8 +98,7 @@ TQ_DEVFN void load8(const void* p, int64_t at, int dt, float (&y)[8]) {
             y[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
         }
     } else {
-        const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
-        const float4 a = f[0], b = f[1];
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 128);
         y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
     }
 }
@@ -140,12 +141,53 @@ struct AppendArgs {
     uint32_t* err;
 };
 
-// Keys' 255 thresholds through 1024 equal bins over [-4.5, 4.5): bin(x) is the same float expression for thresholds and
-// values, hence monotone, and a Lloyd-Max book's thresholds are further apart than a bin is wide (0.0169 against
-// 0.0088), so code = (thresholds of lower bins) + (the bin's own < u).  Other books, and calls too small to pay for the
-// table, search the thresholds.
-constexpr int kBins = 1024;
-TQ_DEVFN int bin_of(float x) { return min(max(__float2int_rd((x + 4.5f) * (kBins / 9.0f)), 0), kBins - 1); }
+// A value's code, the number of thresholds strictly below it, through equal bins over [-4.5, 4.5] (what lies outside goes to
+// the end bins): bin_of is the same float expression for thresholds and values, hence monotone, so code = (thresholds of
+// lower bins) + (the bin's own < u) wherever a bin holds one threshold at most.  A Lloyd-Max book's are further apart than
+// its bins are wide (keys: 0.0169 against 0.0088; values: 0.258 against 0.143); other books search their thresholds.
+// Entries are (thresholds of lower bins, the bin's own or +infinity); kReps copies lie interleaved, a lane reading copy
+// lane % kReps, which keeps the lanes of a read from the same banks.
+template <int N, int REPS>
+struct Bins {
+    static constexpr int kN = N, kReps = REPS;
+    float2 at[N * REPS];
+};
+using KeyBins = Bins<1024, 2>;
+using ValueBins = Bins<64, 16>;
+// The bin of x as the low bits of a float's: 2^23 + bin.  NaN goes to bin 0.
+template <int N>
+TQ_DEVFN uint32_t bin_bits(float x) {
+    return __float_as_uint(fmaf(__saturatef(fmaf(x, 1.0f / 9.0f, 0.5f)), (float)(N - 1), 8388608.0f));
+}
+// Fills a table from its book (all threads of the CTA); false if two thresholds share a bin.  bin: scratch of a book's size.
+template <class B>
+TQ_DEVFN bool fill_bins(B& t, const float* thr, int n, uint16_t* bin) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) bin[i] = (uint16_t)(bin_bits<B::kN>(thr[i]) & 0xffffu);
+    __syncthreads();
+    for (int x = threadIdx.x; x < B::kN; x += blockDim.x) {
+        int lo = 0, hi = n;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (bin[mid] < x) lo = mid + 1; else hi = mid;
+        }
+        const float2 e = make_float2(__int_as_float(lo), lo < n && bin[lo] == x ? thr[lo] : INFINITY);
+        for (int r = 0; r < B::kReps; ++r) t.at[x * B::kReps + r] = e;
+    }
+    bool apart = true;
+    for (int i = threadIdx.x; i + 1 < n; i += blockDim.x) apart = apart && bin[i] < bin[i + 1];
+    return __syncthreads_and(apart);
+}
+// The code of u, looked up: `own` is the lane's copy of entry 0.
+template <class B>
+TQ_DEVFN uint32_t bin_code(uint32_t own, float u) {
+    float2 e;
+    // bits * (bytes of an entry's copies) wraps to the entry's offset: 2^23's exponent bits leave at the top
+    const uint32_t at = own + (bin_bits<B::kN>(u) - 0x4b000000u) * (uint32_t)(sizeof(float2) * B::kReps);
+    asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(e.x), "=f"(e.y) : "r"(at));
+    uint32_t below;  // all ones where the bin's own threshold is below u
+    asm("set.lt.u32.f32 %0, %1, %2;" : "=r"(below) : "f"(e.y), "f"(u));
+    return __float_as_uint(e.x) - below;
+}
 
 TQ_DEVFN int count_below(const float* t, int n, float u) {  // thresholds strictly below u
     int lo = 0, hi = n;
@@ -199,81 +241,114 @@ TQ_DEVFN void turn_keys(const AppendArgs& a, const Turn& w, int l, float (&k)[32
     }
 }
 
-template <int KL, int VL, bool BINS, bool ROPE>
+// Persistent warps; a unit is eight tokens of one head (of four heads where rotary angles are shared among them).  The next
+// head's or unit's vectors are copied to the warp's own shared memory while the present ones are encoded.
+//
+// Bound by instruction issue and the shared-memory pipe (table reads, shuffles): see the measured table in the design notes.
+template <int KL, int VL, bool BF16, bool ROPE>
 __global__ void __launch_bounds__(32 * kWarps, 2) kv_append_kernel(AppendArgs a) {
     using KB = KvBook<KL>;
     using VB = KvBook<VL>;
+    constexpr int kPiece = BF16 ? 16 : 32, kVec = 16 * kPiece;  // bytes of eight elements, of a vector
+    extern __shared__ __align__(16) uint8_t smem[];
+    KeyBins& kbins = *reinterpret_cast<KeyBins*>(smem);
+    ValueBins& vbins = *reinterpret_cast<ValueBins*>(smem + (KL == 256 ? sizeof(KeyBins) : sizeof(ValueBins)));
+    // 4-bit keys take a small table too
+    ValueBins& k4bins = *reinterpret_cast<ValueBins*>(smem);
+    f2* const signs = reinterpret_cast<f2*>(reinterpret_cast<uint8_t*>(&vbins) + sizeof(ValueBins));  // [4][34] of a lane's 32
+    uint8_t* const stage = reinterpret_cast<uint8_t*>(signs + 4 * 34) + (threadIdx.x >> 5) * (2 * kVecs * kVec);  // K, then V
     __shared__ float kt[256], vt[16];
-    __shared__ float2 bins[BINS ? kBins : 1];  // (thresholds of lower bins, the bin's own or +inf)
-    __shared__ uint16_t kb[BINS ? 256 : 1];
+    __shared__ uint16_t scratch[256];
     __shared__ uint32_t vbits[kWarps][kVecs][17];  // 24-bit pieces of 3-bit codes
     for (int i = threadIdx.x; i < KL - 1; i += blockDim.x) kt[i] = a.c.kthr[i];
     for (int i = threadIdx.x; i < VL - 1; i += blockDim.x) vt[i] = a.c.vthr[i];
-    bool fast = false;
-    if constexpr (BINS) {
-        __syncthreads();
-        if (threadIdx.x < KL - 1) kb[threadIdx.x] = (uint16_t)bin_of(kt[threadIdx.x]);
-        __syncthreads();
-        for (int x = threadIdx.x; x < kBins; x += blockDim.x) {
-            int lo = 0, hi = KL - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (kb[mid] < x) lo = mid + 1; else hi = mid;
-            }
-            bins[x] = make_float2(__int_as_float(lo), lo < KL - 1 && kb[lo] == x ? kt[lo] : INFINITY);
-        }
-        fast = __syncthreads_and(threadIdx.x >= KL - 2 || kb[threadIdx.x] < kb[threadIdx.x + 1]);
+    if (threadIdx.x < kPD) {  // element 32 m + 8 l + i of lane l
+        const int m = threadIdx.x >> 5, q = (threadIdx.x >> 3) & 3, i = threadIdx.x & 7;
+        const float s = (float)a.c.signs[threadIdx.x];
+        signs[q * 34 + 8 * m + i] = pk(s, s);
     }
     __syncthreads();
-    float vthr[VL - 1];
-#pragma unroll
-    for (int i = 0; i < VL - 1; ++i) vthr[i] = vt[i];
+    bool fast;
+    if constexpr (KL == 256) fast = fill_bins(kbins, kt, KL - 1, scratch);
+    else fast = fill_bins(k4bins, kt, KL - 1, scratch);
+    __syncthreads();
+    fast = fill_bins(vbins, vt, VL - 1, scratch) && fast;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, vec = lane >> 2, l = lane & 3;
     const int lg = a.c.lgroup;
     const float per_group = 1.0f / (float)(1 << lg);
     const int parts = (a.c.Hkv + a.heads - 1) / a.heads;
-    const int64_t units = (a.T + kVecs - 1) / kVecs * parts;
-    for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < units; unit += (int64_t)gridDim.x * kWarps) {
+    const int64_t units = (a.T + kVecs - 1) / kVecs * parts, stride = (int64_t)gridDim.x * kWarps;
+    const uint32_t kown = (uint32_t)__cvta_generic_to_shared(smem) + (KL == 256 ? (lane % KeyBins::kReps) : (lane % ValueBins::kReps)) * 8;
+    const uint32_t vown = (uint32_t)__cvta_generic_to_shared(&vbins) + (lane % ValueBins::kReps) * 8;
+    // The lane's pieces of its vector.  bf16: 64 bytes of four lanes to a piece number, those of odd vectors swapped by pairs,
+    // so that eight lanes of a read (two vectors) meet all banks.  f32: the two halves of a piece 128 bytes apart.
+    auto piece_at = [&](int m) {
+        return stage + vec * kVec + (BF16 ? (m ^ (vec & 1)) * 64 : (m >> 1) * 256 + ((m ^ vec) & 1) * 64) + l * 16;
+    };
+    auto copy = [&](int64_t t, int h, bool on) {  // token t's key and value of head h
+        if (on) {
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(which ? a.v : a.k) +
+                                     (t * (which ? a.vs : a.ks) + (int64_t)h * kPD + 8 * l) * (kPiece / 8);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(piece_at(m) + which * kVecs * kVec);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + m * 4 * kPiece) : "memory");
+                    if (!BF16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 128), "l"(src + m * 4 * kPiece + 16)
+                                     : "memory");
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto slot_of = [&](int64_t unit) {  // of the lane's token; -1 where there is nothing to write
+        const int64_t t = unit / parts * kVecs + vec;
+        return unit < units && t < a.T ? a.slots[t] : -1;
+    };
+    const int64_t all = a.c.pages << a.c.lpage;
+    int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
+    int32_t slot_next = slot_of(unit);
+    copy(unit / parts * kVecs + vec, (int)(unit % parts) * a.heads, slot_next >= 0 && slot_next < all);
+    for (; unit < units; unit += stride) {
         const int64_t tb = unit / parts;
         const int h0 = (int)(unit - tb * parts) * a.heads, h1 = min(h0 + a.heads, a.c.Hkv);
         const int64_t t = tb * kVecs + vec;
-        int32_t slot = t < a.T ? a.slots[t] : -1;
-        if ((int64_t)slot >= a.c.pages << a.c.lpage) {
+        int32_t slot = slot_next;
+        slot_next = slot_of(unit + stride);
+        if (slot >= all) {
             if (l == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
             slot = -1;
         }
         Turn w;
         if (ROPE) turn_angles(a, t < a.T ? a.pos[t] : 0, l, w);
-        if (!__any_sync(kFull, slot >= 0)) continue;
         for (int h = h0; h < h1; ++h) {
             f2 x[32];
             {
                 float k[32], v[32];
+                asm volatile("cp.async.wait_group 0;" ::: "memory");  // the lane reads what it copied itself
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     float y[8], z[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = z[i] = 0.f;
-                    if (slot >= 0) {
-                        load8(a.k, t * a.ks + (int64_t)h * kPD + 32 * m + 8 * l, a.dt, y);
-                        load8(a.v, t * a.vs + (int64_t)h * kPD + 32 * m + 8 * l, a.dt, z);
-                    }
+                    load8<BF16>(piece_at(m), y);
+                    load8<BF16>(piece_at(m) + kVecs * kVec, z);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         k[8 * m + i] = y[i];
                         v[8 * m + i] = z[i];
                     }
                 }
+                // the next head's, or the next unit's first
+                if (h + 1 < h1) {
+                    copy(t, h + 1, slot >= 0);
+                } else {
+                    const int64_t on = unit + stride;
+                    copy(on / parts * kVecs + vec, (int)(on % parts) * a.heads, slot_next >= 0 && slot_next < all);
+                }
                 if (ROPE) turn_keys(a, w, l, k);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const uint2 sg = *reinterpret_cast<const uint2*>(a.c.signs + 32 * m + 8 * l);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float s = sign_of(sg, i, 1.f);
-                        x[8 * m + i] = pk(k[8 * m + i] * s, v[8 * m + i] * s);
-                    }
-                }
+                for (int e = 0; e < 32; ++e) x[e] = mul2(pk(k[e], v[e]), signs[l * 34 + e]);
             }
             fwht_pair(x);
             const f2 r = pk(kInvSqrtD, kInvSqrtD);
@@ -311,25 +386,16 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv_append_kernel(AppendArgs a)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float2 u = un(mul2(x[8 * m + i], inv));
-                    uint32_t ck;
-                    if (BINS && fast) {
-                        const float2 e = bins[bin_of(u.x)];
-                        ck = __float_as_uint(e.x) + (e.y < u.x ? 1u : 0u);
+                    uint32_t ck, cv;
+                    if (fast) {
+                        ck = bin_code<std::conditional_t<KL == 256, KeyBins, ValueBins>>(kown, u.x);
+                        cv = bin_code<ValueBins>(vown, u.y);
                     } else {
                         ck = count_below(kt, KL - 1, u.x);
+                        cv = count_below(vt, VL - 1, u.y);
                     }
-                    kw[KL == 256 ? i >> 2 : 0] |= ck << (KB::kBits * (KL == 256 ? i & 3 : i));
-                    uint32_t cv = 0;  // by halves: the threshold in the middle, then of the half, ...
-                    if constexpr (VL == 8) {
-                        const bool b2 = vthr[3] < u.y;
-                        const bool b1 = (b2 ? vthr[5] : vthr[1]) < u.y;
-                        const bool b0 = (b2 ? (b1 ? vthr[6] : vthr[4]) : (b1 ? vthr[2] : vthr[0])) < u.y;
-                        cv = (b2 ? 4u : 0u) | (b1 ? 2u : 0u) | (b0 ? 1u : 0u);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < VL - 1; ++c) cv += vthr[c] < u.y ? 1u : 0u;
-                    }
-                    vw |= cv << (VB::kBits * i);
+                    kw[KL == 256 ? i >> 2 : 0] += ck * (1u << (KB::kBits * (KL == 256 ? i & 3 : i)));
+                    vw += cv * (1u << (VB::kBits * i));
                 }
                 vpiece[m] = vw;
                 if (slot >= 0) {
@@ -381,6 +447,93 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv_append_kernel(AppendArgs a)
                 }
             }
         }
+    }
+}
+
+// Calls of few vectors, where latency counts: a warp to a key or value vector, four elements a lane, the thresholds
+// searched.  Every load that does not wait for another is under way before the first is needed.
+template <int KL, int VL>
+__global__ void __launch_bounds__(32 * kWarps) kv_append_small_kernel(AppendArgs a) {
+    __shared__ float thr[2][256];
+    __shared__ uint8_t cd[kWarps][kPD];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t job = (int64_t)blockIdx.x * kWarps + warp, vec = job >> 1;
+    const int which = (int)(job & 1);
+    const bool on = vec < a.T * a.c.Hkv;
+    const int64_t t = vec / a.c.Hkv;
+    const int h = (int)(vec - t * a.c.Hkv);
+    int32_t slot = -1, pos = 0;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t sg = 0;
+    if (on) {
+        slot = a.slots[t];
+        const int64_t src = t * (which ? a.vs : a.ks) + (int64_t)h * kPD + lane * 4;
+        if (a.dt == TQ_BF16) {
+            const uint2 r = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(which ? a.v : a.k) + src);
+            x[0] = __uint_as_float(r.x << 16), x[1] = __uint_as_float(r.x & 0xffff0000u);
+            x[2] = __uint_as_float(r.y << 16), x[3] = __uint_as_float(r.y & 0xffff0000u);
+        } else {
+            const float4 r = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(which ? a.v : a.k) + src);
+            x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w;
+        }
+        sg = *reinterpret_cast<const uint32_t*>(a.c.signs + lane * 4);
+        if (a.steps && which == 0) pos = a.pos[t];
+    }
+    if (threadIdx.x < KL - 1) thr[0][threadIdx.x] = a.c.kthr[threadIdx.x];
+    if (threadIdx.x < VL - 1) thr[1][threadIdx.x] = a.c.vthr[threadIdx.x];
+    __syncthreads();
+    if (slot < 0) return;
+    if ((int64_t)slot >= a.c.pages << a.c.lpage) {
+        if (lane == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
+        return;
+    }
+    if (a.steps && which == 0) {
+        const int rotary = 1 << a.lrot, half = rotary / 2;
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = lane * 4 + i;
+            const float o = a.interleaved ? x[i ^ 1] : __shfl_xor_sync(kFull, x[i], half / 4);
+            const int pair = a.interleaved ? e >> 1 : e & (half - 1);
+            const bool second = a.interleaved ? (i & 1) : (e & half);
+            float sn = 0.f, cs = 1.f;
+            if (e < rotary) {
+                rope_angle(pos, a.steps[pair], sn, cs);
+                sn *= second ? a.factor : -a.factor;
+                cs *= a.factor;
+            }
+            y[i] = e < rotary ? x[i] * cs + o * sn : x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = y[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] *= (float)(int8_t)(sg >> (8 * i));
+    fwht_warp128(x);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[i] *= kInvSqrtD;
+        ss += x[i] * x[i];
+    }
+    const int group = 1 << a.c.lgroup, lpg = group / 4;
+    for (int m = 1; m < lpg; m <<= 1) ss += __shfl_xor_sync(kFull, ss, m);
+    const float s = sqrtf(ss / (float)group), inv = s > 0.f ? 1.0f / s : 0.f;
+    const int64_t row = a.c.row(slot, h);
+    if ((lane & (lpg - 1)) == 0)
+        (which ? a.c.vscales : a.c.kscales)[(row << (7 - a.c.lgroup)) + lane / lpg] = __half_as_ushort(__float2half_rn(s));
+    const int n = (which ? VL : KL) - 1;
+    const int bits = which ? KvBook<VL>::kBits : KvBook<KL>::kBits, cw = 32 / bits;
+    uint32_t c4 = 0;  // the lane's four codes
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c4 |= (uint32_t)count_below(thr[which], n, x[i] * inv) << (8 * i);
+    reinterpret_cast<uint32_t*>(cd[warp])[lane] = c4;
+    __syncwarp();
+    const int words = which ? KvBook<VL>::kWords : KvBook<KL>::kWords;
+    if (lane < words) {
+        uint32_t w = 0;
+        for (int i = 0; i < cw && lane * cw + i < kPD; ++i) w |= (uint32_t)cd[warp][lane * cw + i] << (bits * i);
+        (which ? a.c.vcodes : a.c.kcodes)[row * words + lane] = w;
     }
 }
 
@@ -531,25 +684,33 @@ extern "C" tq_status tq_kv_append(const tq_kv_pages_t* cache, const void* k, int
     }
     a.dt = dt;
     a.err = err;
+    cudaStream_t st = as_stream(stream);
+    // Up to 8192 vectors a warp to each (1 token of 8 heads: 5 us, against 18 for the persistent kernel and its tables);
+    // past that the persistent kernel (524288 vectors: 0.48 ns each, against 1.7).
+    if (T * cache->Hkv <= 8192) {
+        const unsigned blocks = (unsigned)((T * cache->Hkv * 2 + kWarps - 1) / kWarps);
+        return by_books(cache, [&](auto kl, auto vl) {
+            kv_append_small_kernel<decltype(kl)::value, decltype(vl)::value><<<blocks, 32 * kWarps, 0, st>>>(a);
+            return launch_status();
+        });
+    }
     // A warp's unit: eight tokens of one head; of four heads where rotary angles are shared among them and there are
     // units enough for every warp of two CTAs an SM.
     const int64_t blocks8 = (T + kVecs - 1) / kVecs, all = (int64_t)sm_count() * 2 * kWarps;
     a.heads = rope && blocks8 * ((cache->Hkv + 3) / 4) >= all ? std::min(4, cache->Hkv) : 1;
     const int64_t units = blocks8 * ((cache->Hkv + a.heads - 1) / a.heads);
     const unsigned blocks = (unsigned)std::min<int64_t>((units + kWarps - 1) / kWarps, sm_count() * 2);
-    // the bin table costs a CTA about as much as 8 units searched: it is built where a warp has as many
-    const bool bins = cache->kcb.levels == 256 && units * a.heads >= 8 * all;
-    cudaStream_t st = as_stream(stream);
     return by_books(cache, [&](auto kl, auto vl) {
         constexpr int KL = decltype(kl)::value, VL = decltype(vl)::value;
-        if (KL == 256 && bins) {
-            if (rope) kv_append_kernel<KL, VL, KL == 256, true><<<blocks, 32 * kWarps, 0, st>>>(a);
-            else kv_append_kernel<KL, VL, KL == 256, false><<<blocks, 32 * kWarps, 0, st>>>(a);
-        } else {
-            if (rope) kv_append_kernel<KL, VL, false, true><<<blocks, 32 * kWarps, 0, st>>>(a);
-            else kv_append_kernel<KL, VL, false, false><<<blocks, 32 * kWarps, 0, st>>>(a);
-        }
-        return launch_status();
+        auto launch = [&](auto kernel, size_t vector) {
+            const size_t smem = (KL == 256 ? sizeof(KeyBins) : sizeof(ValueBins)) + sizeof(ValueBins) + 4 * 34 * sizeof(f2) +
+                                kWarps * 2 * kVecs * vector;
+            if (ensure_smem((const void*)kernel, smem) != cudaSuccess) return TQ_ERR_CUDA;
+            kernel<<<blocks, 32 * kWarps, smem, st>>>(a);
+            return launch_status();
+        };
+        if (dt == TQ_BF16) return rope ? launch(kv_append_kernel<KL, VL, true, true>, 256) : launch(kv_append_kernel<KL, VL, true, false>, 256);
+        return rope ? launch(kv_append_kernel<KL, VL, false, true>, 512) : launch(kv_append_kernel<KL, VL, false, false>, 512);
     });
 }
 
