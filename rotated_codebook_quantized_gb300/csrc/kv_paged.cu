@@ -152,7 +152,7 @@ struct Bins {
     static constexpr int kN = N, kReps = REPS;
     float2 at[N * REPS];
 };
-using KeyBins = Bins<1024, 2>;
+using KeyBins = Bins<1024, 4>;
 using ValueBins = Bins<64, 16>;
 // The bin of x as the low bits of a float's: 2^23 + bin.  NaN goes to bin 0.
 template <int N>
@@ -374,36 +374,41 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv_append_kernel(AppendArgs a)
             if (lg > 6) ss[0] = ss[1] = ss[2] = ss[3] = add2(ss[0], ss[2]);
             const int64_t row = slot >= 0 ? a.c.row(slot, h) : 0;
             uint32_t hk[4], hv[4];  // fp16 scales
-            uint32_t vpiece[4];
+            uint32_t vpiece[4], kpiece[4][KL == 256 ? 2 : 1];
+            auto encode = [&](auto fast_c) {
+                constexpr bool FAST = decltype(fast_c)::value;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float2 q = un(ss[m]);
-                const float sk = sqrtf(q.x * per_group), sv = sqrtf(q.y * per_group);
-                hk[m] = __half_as_ushort(__float2half_rn(sk));
-                hv[m] = __half_as_ushort(__float2half_rn(sv));
-                const f2 inv = pk(sk > 0.f ? 1.0f / sk : 0.f, sv > 0.f ? 1.0f / sv : 0.f);
-                uint32_t kw[2] = {0, 0}, vw = 0;
+                for (int m = 0; m < 4; ++m) {
+                    const float2 q = un(ss[m]);
+                    const float sk = sqrtf(q.x * per_group), sv = sqrtf(q.y * per_group);
+                    hk[m] = __half_as_ushort(__float2half_rn(sk));
+                    hv[m] = __half_as_ushort(__float2half_rn(sv));
+                    const f2 inv = pk(sk > 0.f ? 1.0f / sk : 0.f, sv > 0.f ? 1.0f / sv : 0.f);
+                    uint32_t kw[2] = {0, 0}, vw = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 u = un(mul2(x[8 * m + i], inv));
-                    uint32_t ck, cv;
-                    if (fast) {
-                        ck = bin_code<std::conditional_t<KL == 256, KeyBins, ValueBins>>(kown, u.x);
-                        cv = bin_code<ValueBins>(vown, u.y);
-                    } else {
-                        ck = count_below(kt, KL - 1, u.x);
-                        cv = count_below(vt, VL - 1, u.y);
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 u = un(mul2(x[8 * m + i], inv));
+                        const uint32_t ck = FAST ? bin_code<std::conditional_t<KL == 256, KeyBins, ValueBins>>(kown, u.x)
+                                                 : (uint32_t)count_below(kt, KL - 1, u.x);
+                        const uint32_t cv = FAST ? bin_code<ValueBins>(vown, u.y) : (uint32_t)count_below(vt, VL - 1, u.y);
+                        kw[KL == 256 ? i >> 2 : 0] += ck * (1u << (KB::kBits * (KL == 256 ? i & 3 : i)));
+                        vw += cv * (1u << (VB::kBits * i));
                     }
-                    kw[KL == 256 ? i >> 2 : 0] += ck * (1u << (KB::kBits * (KL == 256 ? i & 3 : i)));
-                    vw += cv * (1u << (VB::kBits * i));
+                    kpiece[m][0] = kw[0];
+                    if constexpr (KL == 256) kpiece[m][1] = kw[1];
+                    vpiece[m] = vw;
                 }
-                vpiece[m] = vw;
-                if (slot >= 0) {
+            };
+            if (fast) encode(std::true_type{});
+            else encode(std::false_type{});
+            if (slot >= 0) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
                     if constexpr (KL == 256)
-                        *reinterpret_cast<uint2*>(a.c.kcodes + row * 32 + 8 * m + 2 * l) = make_uint2(kw[0], kw[1]);
+                        *reinterpret_cast<uint2*>(a.c.kcodes + row * 32 + 8 * m + 2 * l) = make_uint2(kpiece[m][0], kpiece[m][1]);
                     else
-                        a.c.kcodes[row * 16 + 4 * m + l] = kw[0];
-                    if constexpr (VL == 16) a.c.vcodes[row * 16 + 4 * m + l] = vw;
+                        a.c.kcodes[row * 16 + 4 * m + l] = kpiece[m][0];
+                    if constexpr (VL == 16) a.c.vcodes[row * 16 + 4 * m + l] = vpiece[m];
                 }
             }
             if constexpr (VL == 8) {  // ten codes to a word: word w takes codes 10 w .. + 9, from pieces 10 w / 8 and the next
