@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv_append_kernel(AppendArgs a)
     const int lg = a.c.lgroup;
     const float per_group = 1.0f / (float)(1 << lg);
     const int parts = (a.c.Hkv + a.heads - 1) / a.heads;
-    const int64_t units = (a.T + kVecs - 1) / kVecs * parts, stride = (int64_t)gridDim.x * kWarps;
+    // units are 32-bit numbers (the host sees to it): their division is a few instructions
+    const uint32_t units = (uint32_t)((a.T + kVecs - 1) / kVecs) * parts, stride = gridDim.x * kWarps;
     const uint32_t kown = (uint32_t)__cvta_generic_to_shared(smem) + (KL == 256 ? (lane % KeyBins::kReps) : (lane % ValueBins::kReps)) * 8;
     const uint32_t vown = (uint32_t)__cvta_generic_to_shared(&vbins) + (lane % ValueBins::kReps) * 8;
     // The lane's pieces of its vector.  bf16: 64 bytes of four lanes to a piece number, those of odd vectors swapped by pairs,
@@ -303,20 +304,25 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv_append_kernel(AppendArgs a)
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto slot_of = [&](int64_t unit) {  // of the lane's token; -1 where there is nothing to write
-        const int64_t t = unit / parts * kVecs + vec;
-        return unit < units && t < a.T ? a.slots[t] : -1;
-    };
     const int64_t all = a.c.pages << a.c.lpage;
-    int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
-    int32_t slot_next = slot_of(unit);
-    copy(unit / parts * kVecs + vec, (int)(unit % parts) * a.heads, slot_next >= 0 && slot_next < all);
+    uint32_t unit = blockIdx.x * kWarps + warp;
+    int64_t t = 0, t_next = 0;  // the lane's token of the unit, and of the next one; their slots (-1: nothing to write)
+    int h0 = 0, h0_next = 0;
+    int32_t slot = -1, slot_next = -1;
+    auto look = [&](uint32_t u) {
+        const uint32_t tb = u / (uint32_t)parts;
+        t_next = (int64_t)tb * kVecs + vec;
+        h0_next = (int)(u - tb * (uint32_t)parts) * a.heads;
+        slot_next = u < units && t_next < a.T ? a.slots[t_next] : -1;
+    };
+    look(unit);
+    copy(t_next, h0_next, slot_next >= 0 && slot_next < all);
     for (; unit < units; unit += stride) {
-        const int64_t tb = unit / parts;
-        const int h0 = (int)(unit - tb * parts) * a.heads, h1 = min(h0 + a.heads, a.c.Hkv);
-        const int64_t t = tb * kVecs + vec;
-        int32_t slot = slot_next;
-        slot_next = slot_of(unit + stride);
+        t = t_next;
+        h0 = h0_next;
+        slot = slot_next;
+        look(unit + stride);
+        const int h1 = min(h0 + a.heads, a.c.Hkv);
         if (slot >= all) {
             if (l == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
             slot = -1;
@@ -340,12 +346,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv_append_kernel(AppendArgs a)
                     }
                 }
                 // the next head's, or the next unit's first
-                if (h + 1 < h1) {
-                    copy(t, h + 1, slot >= 0);
-                } else {
-                    const int64_t on = unit + stride;
-                    copy(on / parts * kVecs + vec, (int)(on % parts) * a.heads, slot_next >= 0 && slot_next < all);
-                }
+                if (h + 1 < h1) copy(t, h + 1, slot >= 0);
+                else copy(t_next, h0_next, slot_next >= 0 && slot_next < all);
                 if (ROPE) turn_keys(a, w, l, k);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = mul2(pk(k[e], v[e]), signs[l * 34 + e]);
@@ -572,21 +574,36 @@ TQ_DEVFN void piece8(const uint32_t* words, int piece, uint32_t (&w)[2]) {
     }
 }
 
-template <int KL, int VL>
+// REPS copies of the 8-bit keys' book, interleaved: 32 give every lane a bank of its own (one wavefront a read, against about
+// 3.4), 1 costs a small call less to fill.  Bound by the shared-memory pipe (table reads, shuffles) and by latency.
+template <int KL, int VL, int REPS>
 __global__ void __launch_bounds__(32 * kWarps, 2) kv_fetch_kernel(FetchArgs a) {
-    __shared__ float kl[KL], vl[VL];
-    for (int i = threadIdx.x; i < KL; i += blockDim.x) kl[i] = a.c.kcent[i];
+    __shared__ float kl[KL * REPS], vl[VL];
+    for (int i = threadIdx.x; i < KL * REPS; i += blockDim.x) kl[i] = a.c.kcent[i / REPS];
     for (int i = threadIdx.x; i < VL; i += blockDim.x) vl[i] = a.c.vcent[i];
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, vec = lane >> 2, l = lane & 3;
     const int lg = a.c.lgroup;
-    const int64_t units = (a.T + kVecs - 1) / kVecs * a.c.Hkv;
-    for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < units; unit += (int64_t)gridDim.x * kWarps) {
-        const int64_t tb = unit / a.c.Hkv;
-        const int h = (int)(unit - tb * a.c.Hkv);
-        const int64_t t = tb * kVecs + vec;
-        int32_t slot = t < a.T ? a.slots[t] : -1;
-        if ((int64_t)slot >= a.c.pages << a.c.lpage) {
+    const float* const own = kl + lane % REPS;
+    const uint32_t units = (uint32_t)((a.T + kVecs - 1) / kVecs) * a.c.Hkv, stride = gridDim.x * kWarps;  // 32-bit numbers
+    const int64_t all = a.c.pages << a.c.lpage;
+    uint32_t unit = blockIdx.x * kWarps + warp;
+    int64_t t_next = 0;
+    int h_next = 0;
+    int32_t slot_next = -1;
+    auto look = [&](uint32_t u) {  // the lane's token of a unit, and its slot (-1: none)
+        const uint32_t tb = u / (uint32_t)a.c.Hkv;
+        t_next = (int64_t)tb * kVecs + vec;
+        h_next = (int)(u - tb * (uint32_t)a.c.Hkv);
+        slot_next = u < units && t_next < a.T ? a.slots[t_next] : -1;
+    };
+    look(unit);
+    for (; unit < units; unit += stride) {
+        const int64_t t = t_next;
+        const int h = h_next;
+        int32_t slot = slot_next;
+        look(unit + stride);
+        if (slot >= all) {
             if (l == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
             slot = -1;
         }
@@ -607,12 +624,19 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv_fetch_kernel(FetchArgs a) {
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t p = KL == 256 ? (ck[i >> 2] >> (8 * (i & 3))) & 255u : (ck[0] >> (4 * i)) & 15u;
                     const uint32_t q = (cv[0] >> (KvBook<VL>::kBits * i)) & (VL - 1);
-                    x[8 * m + i] = mul2(pk(kl[p % KL], vl[q]), s);
+                    x[8 * m + i] = mul2(pk(own[(p % KL) * REPS], vl[q]), s);
                 }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = 0;
+        }
+        if (slot_next >= 0 && slot_next < all) {  // the next unit's rows on their way to L1 beside the transform: a lane to an array
+            const int64_t row = a.c.row(slot_next, h_next);
+            const void* p = l == 0 ? (const void*)(a.c.kcodes + row * KvBook<KL>::kWords)
+                                   : (l == 1 ? (const void*)(a.c.vcodes + row * KvBook<VL>::kWords)
+                                             : (const void*)((l == 2 ? a.c.kscales : a.c.vscales) + (row << (7 - lg))));
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
         }
         fwht_pair(x);
         if (t < a.T) {
@@ -704,6 +728,7 @@ extern "C" tq_status tq_kv_append(const tq_kv_pages_t* cache, const void* k, int
     const int64_t blocks8 = (T + kVecs - 1) / kVecs, all = (int64_t)sm_count() * 2 * kWarps;
     a.heads = rope && blocks8 * ((cache->Hkv + 3) / 4) >= all ? std::min(4, cache->Hkv) : 1;
     const int64_t units = blocks8 * ((cache->Hkv + a.heads - 1) / a.heads);
+    if (units > 0x3fffffffll) return TQ_ERR_UNSUPPORTED;
     const unsigned blocks = (unsigned)std::min<int64_t>((units + kWarps - 1) / kWarps, sm_count() * 2);
     return by_books(cache, [&](auto kl, auto vl) {
         constexpr int KL = decltype(kl)::value, VL = decltype(vl)::value;
@@ -735,10 +760,16 @@ extern "C" tq_status tq_kv_fetch(const tq_kv_pages_t* cache, const int32_t* slot
     a.dt = dt;
     a.err = err;
     const int64_t units = (T + kVecs - 1) / kVecs * cache->Hkv;
+    if (units > 0x3fffffffll) return TQ_ERR_UNSUPPORTED;
     const unsigned blocks = (unsigned)std::min<int64_t>((units + kWarps - 1) / kWarps, sm_count() * 2);
     cudaStream_t st = as_stream(stream);
     return by_books(cache, [&](auto kl, auto vl) {
-        kv_fetch_kernel<decltype(kl)::value, decltype(vl)::value><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a);
+        constexpr int KL = decltype(kl)::value, VL = decltype(vl)::value;
+        // 32 copies of a 256-entry book where a warp has eight units or more to read through them
+        if (KL == 256 && units >= (int64_t)sm_count() * 2 * kWarps * 8)
+            kv_fetch_kernel<KL, VL, KL == 256 ? 32 : 1><<<blocks, 32 * kWarps, 0, st>>>(a);
+        else
+            kv_fetch_kernel<KL, VL, 1><<<blocks, 32 * kWarps, 0, st>>>(a);
         return launch_status();
     });
 }
