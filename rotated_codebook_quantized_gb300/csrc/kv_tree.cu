@@ -675,8 +675,8 @@ Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, i
     Plan p{};
     const int64_t rows = (int64_t)n * (Hq / Hkv);
     p.trows = rows <= kStep ? kStep : (rows <= 128 ? 128 : 256);
-    p.stoks = p.trows == kStep ? kStep : 64;
-    p.least = p.trows == kStep ? kCtxWarps : 1;
+    p.stoks = p.trows == kStep ? kStep : 32;
+    p.least = p.trows == kStep ? kCtxWarps : 2;
     p.tiles = (rows + kStep - 1) / kStep;
     const int64_t units = (rows + p.trows - 1) / p.trows * Hkv * B, steps = (max_len + p.stoks - 1) / p.stoks;
     p.steps = units * steps;

@@ -1,16 +1,16 @@
 // The cached context of tq_kv_attend_tree for more than 16 query rows to a kv head, on the 5th-generation tensor cores.
 //
-// kv_tree_turn_kernel rotates the query rows once.  Then a persistent CTA takes a run of 64-token steps.  Each step is decoded
+// kv_tree_turn_kernel rotates the query rows once.  Then a persistent CTA takes a run of 32-token steps.  Each step is decoded
 // once into shared memory, as fp16 keys (K-major) and values (MN-major, so that neither needs a transpose), for one or two
-// tiles of 128 query rows; a tile's rows meet it by the half step of 32 tokens:
+// tiles of 128 query rows:
 //   scores   S[128 x 32]   = Q (TMEM, fp16) . K^T (shared)          8 MMAs of K = 16
 //   weights  P = exp2(S f - m), fp16, written over S in TMEM        one thread to a row
 //   values   O[128 x 128] += P (TMEM) . V (shared)                  2 MMAs of K = 16
 // Two streams of four softmax warps each, with scores and sums of their own: the two tiles (T = 2), or the even and the odd
 // steps of one tile (T = 1), joined at the end of the run.  A stream's scores alternate between two places, so that its
-// exponentials run beside its products (whole steps in one place measured 1.9 times as long: the tensor cores and the softmax
-// waited for one another).  Decoder warps take units of 8 tokens in turn, each fed by a cp.async ring of its own; a thread to
-// a stream issues its MMAs (an issue costs its thread about 30 cycles).
+// exponentials run beside its products (one place: 1.9 times as long, the tensor cores and the softmax waiting for one
+// another).  Decoder warps take units of 8 tokens in turn, each fed by a cp.async ring of its own; a thread to a stream issues
+// its MMAs (an issue costs its thread about 30 cycles).
 // Operands from TMEM leave the shared-memory bandwidth to the decoders' table reads and stores and to the tensor cores'
 // reads of K and V.  A row's running maximum follows only when a score passes it by 2^kSlack, so O is seldom rescaled.
 // Every wait on an mbarrier is bounded; on expiry the CTA sets TQ_DEVERR_TIMEOUT, drains and frees TMEM.
@@ -23,12 +23,11 @@ using namespace tq::tree;
 
 namespace {
 
-constexpr int kTok = 64;       // tokens of a step
+constexpr int kTok = 32;       // tokens of a step
 constexpr int kUnit = 8;       // of a unit, which one decoder warp decodes
 constexpr int kUnits = kTok / kUnit;
-constexpr int kStages = 3;     // decoded steps
+constexpr int kStages = 6;     // decoded steps
 constexpr int kDepth = 2;      // units of a decoder's ring: one in flight while one is decoded
-constexpr int kPart = 32;      // tokens of a half step
 constexpr uint32_t kTile = kTok * kPD * 2;  // bytes of a step's keys, or values
 constexpr uint32_t kHalf = kTile / 2;       // of 64 of their dims (one 128-byte swizzled row a token)
 
@@ -37,7 +36,11 @@ constexpr uint32_t kHalf = kTile / 2;       // of 64 of their dims (one 128-byte
 constexpr uint32_t kTable = 65536, kSteps = 131072, kEnd = kSteps + kStages * 2 * kTile;
 constexpr uint32_t kStart = 1024 + 512;  // the system's first KB, then the static variables
 constexpr uint32_t kOdd = kStart, kRings = kOdd + 2 * 128 * 4;
-constexpr int kDec = 14;  // decoder warps
+// Decoder warps.  A warp's units lie kDec / kUnits steps apart, a divisor of kStages: it comes to the same places of decoded
+// steps in every round, and so knows a place's phase (a place's barrier tells only odd from even phases; a warp that left a
+// round of a place out could take a phase two back for the one it waits for, as the two streams free places out of order).
+constexpr int kDec = 12;
+static_assert(kDec % kUnits == 0 && kStages % (kDec / kUnits) == 0, "every place in every round");
 static_assert(kEnd <= 232448, "fits an SM");
 
 template <int KL, int VL>
@@ -121,7 +124,7 @@ TQ_DEVFN void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d
                  : "memory");
 }
 
-constexpr int kSoft = 8, kMma = kSoft + kDec, kWarps = kMma + 2;  // 24 warps: 80 registers a thread
+constexpr int kSoft = 8, kMma = kSoft + kDec, kWarps = kMma + 2;  // 22 warps: 80 registers a thread
 
 // The queries, rotated, over a power of two of their own, fp16: a warp to a row.  Of a tile of `trows` rows the 16-byte pieces
 // [16][trows] lie together, a thread of the next kernel reading its row's; the power's exponent beside them.
@@ -169,8 +172,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* const space = smem - (uint32_t)__cvta_generic_to_shared(smem);  // shared address 0
     float* const odd = reinterpret_cast<float*>(space + kOdd);              // [2][128] maxima and sums of the odd steps (T = 1)
-    // full / empty: of a decoded step's place.  Of a stream's half step: scores, weights, values written.  Of a stream: queries
-    // written, and read for the last time.  Odd steps' statistics ready, and the sums they go with read (T = 1).
+    // full / empty: of a decoded step's place.  Of a place of a stream's scores: scores, weights, values written.  Of a stream:
+    // queries written, and read for the last time.  Odd steps' statistics ready, and the sums they go with read (T = 1).
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], s_ready[2][2], p_ready[2][2], o_done[2][2], q_ready[2], q_free[2],
         odd_ready, odd_free, drain;
     __shared__ __align__(8) uint8_t valid[kStages][kUnits];  // tokens of each unit of a decoded step, a bit each
@@ -233,43 +236,37 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             while (ok && walk.next(a, x)) {
                 const uint32_t ge = g + (x.s1 - x.s0), first = g + (T == 1 ? t : 0);
                 ok = mbar_wait(q_ready + (T == 1 ? 0 : t), seg & 1, abort_flag, a.wait_cycles);
-                // scores of half e of step i, the stream's n-th: they go where the weights of its step before were read from
-                auto scores = [&](uint32_t i, int e, uint32_t n) {
-                    const uint32_t stage = i % kStages;
-                    if ((e == 0 && !mbar_wait(full + stage, (i / kStages) & 1, abort_flag, a.wait_cycles)) ||
-                        (i != first && !mbar_wait(&o_done[t][e], (n - 1) & 1, abort_flag, a.wait_cycles)))
+                // Scores of the CTA's step i, the stream's n-th, where the weights of its n-2nd were read from.
+                auto scores = [&](uint32_t i, uint32_t n) {
+                    const uint32_t stage = i % kStages, e = n & 1;
+                    if (!mbar_wait(full + stage, (i / kStages) & 1, abort_flag, a.wait_cycles) ||
+                        (n >= 2 && !mbar_wait(&o_done[t][e], ((n - 2) >> 1) & 1, abort_flag, a.wait_cycles)))
                         return false;
                     tc_fence_after();
-                    const uint64_t dk = desc(kSteps, 16) + stage * (2 * kTile / 16) + e * (kPart * 128 / 16);
+                    const uint64_t dk = desc(kSteps, 16) + stage * (2 * kTile / 16);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        tc_mma_ts(to_s + kPart * e, from_q + 8 * k, dk + ((k >> 2) * (kHalf / 16) + 2 * (k & 3)), idesc(kPart, 0), k != 0);
+                        tc_mma_ts(to_s + kTok * e, from_q + 8 * k, dk + ((k >> 2) * (kHalf / 16) + 2 * (k & 3)), idesc(kTok, 0), k != 0);
                     tc_commit(&s_ready[t][e]);
                     return true;
                 };
-                if (ok && first < ge) ok = scores(first, 0, done);
-                for (uint32_t i = first; i < ge && ok; i += 3 - T) {
-                    const uint32_t stage = i % kStages;
+                if (ok && first < ge) ok = scores(first, done);
+                for (uint32_t i = first; i < ge && ok; i += 3 - T, ++done) {
+                    // the next scores first, so that they are there when the softmax is done with these; but a step that is
+                    // not decoded yet is not waited for (its place may be this step's to free)
+                    const uint32_t on = i + (3 - T), stage = i % kStages, e = done & 1;
+                    const bool next = on < ge, early = next && mbar_peek(full + on % kStages, (on / kStages) & 1);
+                    if (early) ok = scores(on, done + 1);
+                    if (ok) ok = mbar_wait(&p_ready[t][e], (done >> 1) & 1, abort_flag, a.wait_cycles);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dv = desc(kSteps + kTile, kHalf) + stage * (2 * kTile / 16);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // the next half's scores first, so that they are there when the softmax is done with this half; but a
-                        // step that is not decoded yet is not waited for (its place may be this step's to free)
-                        const uint32_t on = i + (3 - T);
-                        const bool next = e == 1 && on < ge, early = next && mbar_peek(full + on % kStages, (on / kStages) & 1);
-                        if (e == 0) ok = scores(i, 1, done);
-                        else if (early) ok = scores(on, 0, done + 1);
-                        if (ok) ok = mbar_wait(&p_ready[t][e], done & 1, abort_flag, a.wait_cycles);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t dv = desc(kSteps + kTile, kHalf) + stage * (2 * kTile / 16) + e * (kPart * 128 / 16);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            tc_mma_ts(to_o, to_s + kPart * e + 8 * k, dv + 128 * k, idesc(kPD, 1), i != first || e != 0 || k != 0);
-                        tc_commit(&o_done[t][e]);
-                        if (e == 1) tc_commit(empty + stage);
-                        if (next && !early) ok = scores(on, 0, done + 1);
-                    }
-                    ++done;
+                    for (int k = 0; k < kTok / 16; ++k)
+                        tc_mma_ts(to_o, to_s + kTok * e + 8 * k, dv + 128 * k, idesc(kPD, 1), i != first || k != 0);
+                    tc_commit(&o_done[t][e]);
+                    tc_commit(empty + stage);
+                    if (next && !early) ok = scores(on, done + 1);
                 }
                 mbar_arrive(q_free + (T == 1 ? 0 : t));
                 g = ge;
@@ -318,18 +315,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             }
             float m = -INFINITY, l = 0.f, bias = 0.f;
             for (uint32_t i = first; i < ge; i += 3 - T) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                const uint32_t e = done & 1;
+                {
                     // (the decoders' barrier has long completed; waiting on it too orders their `valid` before the read)
-                    ok = mbar_wait(&s_ready[stream][e], done & 1, abort_flag, a.wait_cycles) &&
-                         (e || mbar_wait(full + i % kStages, (i / kStages) & 1, abort_flag, a.wait_cycles));
+                    ok = mbar_wait(&s_ready[stream][e], (done >> 1) & 1, abort_flag, a.wait_cycles) &&
+                         mbar_wait(full + i % kStages, (i / kStages) & 1, abort_flag, a.wait_cycles);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
                     tc_fence_after();
                     if (!idle) {
                         uint32_t s[32];
-                        tc_ld32(at + kPart * e, s);
-                        const uint32_t in = *reinterpret_cast<const uint32_t*>(&valid[i % kStages][4 * e]);
+                        tc_ld32(at + kTok * e, s);
+                        const uint32_t in = *reinterpret_cast<const uint32_t*>(valid[i % kStages]);
                         tc_wait_ld();
                         if (in != ~0u) {  // tokens past the end, or of a bad page
 #pragma unroll
@@ -352,8 +349,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                             m = n;
                             bias = m == -INFINITY ? 0.f : -m;
                             l *= r;
-                            if (e || i != first) {  // the sums so far, once the last product has written them
-                                ok = __all_sync(kFull, mbar_wait(&o_done[stream][e ^ 1], (done - (e ^ 1)) & 1, abort_flag, a.wait_cycles));
+                            if (i != first) {  // the sums so far, once the last product has written them
+                                ok = __all_sync(kFull, mbar_wait(&o_done[stream][e ^ 1], ((done - 1) >> 1) & 1, abort_flag, a.wait_cycles));
                                 if (!ok) break;
                                 tc_fence_after();
 #pragma unroll 1
@@ -378,7 +375,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                         }
                         const float2 sum = un(add2(ls[0], ls[1]));
                         l += sum.x + sum.y;
-                        tc_st16(at + kPart * e, s);
+                        tc_st16(at + kTok * e, s);
                         tc_wait_st();
                     }
                     tc_fence_before();
@@ -390,7 +387,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             if (!ok) break;
             // ---- the stretch's partial result
             if (first < ge) {  // (the odd steps may be none)
-                ok = __all_sync(kFull, mbar_wait(&o_done[stream][1], (done - 1) & 1, abort_flag, a.wait_cycles));
+                ok = __all_sync(kFull, mbar_wait(&o_done[stream][(done - 1) & 1], ((done - 1) >> 1) & 1, abort_flag, a.wait_cycles));
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -581,7 +578,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                 mbar_arrive(full + stage);
                 __syncwarp();  // the ring's place is free for the next copy
                 at = at + U::kBytes == ring_end ? ring : at + U::kBytes;
-                stage += (u + D) / kUnits - u / kUnits;  // the next unit is 1 or 2 steps on
+                stage += D / kUnits;
                 if (stage >= kStages) stage -= kStages, phase ^= 1;
             }
 

@@ -691,3 +691,28 @@ def test_serving_step_end_to_end(lib):
         lib.kv_append(c, k, v, slot)
         lens += taken.sum(-1).int()
     assert bool((lens > 3).all())
+
+
+@pytest.mark.parametrize("n,Hq,H", [(1, 4, 8), (16, 32, 8), (30, 8, 2), (64, 32, 8), (70, 4, 1)])
+def test_tree_long_runs_repeat_and_report_nothing(lib, n, Hq, H):
+    """Runs of many steps through every kernel form, ten times on fresh queries: no wait runs out, and a repeat is the same."""
+    Hq = max(Hq, H)
+    g = _rng(17, n)
+    context, page = 20011, 64
+    pages = -(-context // page)
+    c = lib.PagedKVCache(pages, page, H, D, 32, lib.Codebook(256), lib.Codebook(8), lib.Rotation(D, D, seed=77))
+    slots = torch.arange(context, dtype=torch.int32, device="cuda")
+    lib.kv_append(c, *(torch.randn((context, H, D), device="cuda", dtype=torch.bfloat16) for _ in range(2)), slots)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k, v = lib.kv_fetch(c, slots, out_dtype=torch.float32)
+    for _ in range(10):
+        q, kn, vn = (_dev(g.normal(size=(1, n, h, D)), torch.bfloat16) for h in (Hq, H, H))
+        out = [lib.kv_attend_tree(c, q, table, _dev([context], torch.int32), k_new=kn, v_new=vn, err=err) for _ in range(2)]
+        assert lib.check_error(err) == 0
+        assert torch.equal(*out)
+        # rounding of the fp32 sums is far below the tolerance
+        kk, vv = (torch.cat([a, b[0].float()]).repeat_interleave(Hq // H, 1).transpose(0, 1) for a, b in ((k, kn), (v, vn)))
+        s = q[0].float().transpose(0, 1) @ kk.transpose(1, 2) * D ** -0.5
+        s[:, :, context:].masked_fill_(~torch.tril(torch.ones((n, n), dtype=torch.bool, device="cuda")), float("-inf"))
+        assert helpers.rel_l2(_f64(out[0][0]), _f64((torch.softmax(s, -1) @ vv).transpose(0, 1))) < ATTEND

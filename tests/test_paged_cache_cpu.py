@@ -134,3 +134,51 @@ def test_tree_refusals(lib):
         assert bad == tq.TQ_ERR_INVALID
     assert call(dt=tq.TQ_F32) == tq.TQ_ERR_UNSUPPORTED and call(dt=tq.TQ_F16) == tq.TQ_ERR_UNSUPPORTED
     assert call(B=0, q=None) == tq.TQ_OK and call(n=0, q=None) == tq.TQ_OK
+
+
+@pytest.mark.parametrize("streams_share_steps", [False, True])
+def test_wide_kernel_places_are_never_taken_early(streams_share_steps):
+    """The hand-over of decoded steps in csrc/kv_tree_wide.cu, played with its own constants and every order of the roles
+    that a slow stream allows: decoder warps wait for a place by its barrier's parity, the two streams free places out of
+    order (each takes every other step) or together (each takes all).  No unit may be written before its place is free,
+    and no step be read before it is whole."""
+    import os
+    import random
+    import re
+
+    src = open(os.path.join(os.path.dirname(tq.__file__), "csrc", "kv_tree_wide.cu")).read()
+    const = lambda n: int(re.search(rf"constexpr int {n} = (\d+);", src).group(1))  # noqa: E731
+    decoders, places = const("kDec"), const("kStages")
+    per_step = const("kTok") // const("kUnit")
+    steps, need = 40, 2 if streams_share_steps else 1
+    for seed in range(40):
+        rnd = random.Random(seed)
+        freed, frees, wrote, whole = [0] * places, [0] * places, [0] * places, [0] * places
+        unit, at = list(range(decoders)), [0, 0] if streams_share_steps else [0, 1]
+        while min(at) < steps:
+            moves = []
+            for d in range(decoders):
+                step, k = unit[d] // per_step % places, unit[d] // per_step // places
+                if unit[d] < steps * per_step and freed[step] % 2 != (k - 1) % 2:
+                    moves.append(("write", d))
+            for s in range(2):
+                if at[s] < steps and whole[at[s] % places] % 2 != at[s] // places % 2:
+                    moves.append(("read", s))
+            assert moves, "every role waits"
+            kind, who = rnd.choice(moves)
+            if kind == "read" and who == seed % 2 and len(moves) > 1 and rnd.random() < 0.95:
+                continue  # one stream is slow
+            if kind == "write":
+                place, k = unit[who] // per_step % places, unit[who] // per_step // places
+                assert freed[place] == k, "a place was written before it was free"
+                unit[who] += decoders
+                wrote[place] += 1
+                if wrote[place] == per_step:
+                    wrote[place], whole[place] = 0, whole[place] + 1
+            else:
+                place = at[who] % places
+                assert whole[place] == at[who] // places + 1, "a step was read before it was whole"
+                at[who] += 1 if streams_share_steps else 2
+                frees[place] += 1
+                if frees[place] == need:
+                    frees[place], freed[place] = 0, freed[place] + 1
