@@ -389,27 +389,29 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
 
 // ---------------------------------------------------------------- drafted tokens, join, output
 
-// Whether draft i of sequence b sees draft t.
-TQ_DEVFN bool sees(const TreeArgs& a, int b, int i, int t, int live) {
-    if (t >= live) return false;
-    if (!a.mask) return t <= i;
-    return (a.mask[((int64_t)b * a.n + i) * ((a.n + 63) >> 6) + (t >> 6)] >> (t & 63)) & 1;
+// Which of the drafts t0 .. t0 + 15 draft i of sequence b sees (t0 a multiple of 16, i < n): bit by bit.
+TQ_DEVFN uint32_t sees(const TreeArgs& a, int b, int i, int t0, int live) {
+    const uint32_t in = live - t0 >= kStep ? 0xffffu : (1u << max(live - t0, 0)) - 1u;
+    if (!a.mask) return in & (i - t0 >= kStep - 1 ? 0xffffu : (1u << max(i - t0 + 1, 0)) - 1u);
+    return in & (uint32_t)(a.mask[((int64_t)b * a.n + i) * ((a.n + 63) >> 6) + (t0 >> 6)] >> (t0 & 63));
 }
 
 // One CTA per (sequence, kv head, tile of 16 rows).  The drafted tokens come as they are: bf16 queries, keys
 // and values on the tensor cores, exact but for the weights, which are split in two bf16 halves.
-__global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs a, int tiles_max) {
+__global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs a, int tiles_max, int parts) {
     __shared__ float frag[kDraftWarps][64][kFragPad];
     __shared__ float2 ml[kDraftWarps][kStep];
     __shared__ __align__(16) float joined[kFinWarps][kPD];
     __shared__ float2 jml[kFinWarps];
-    __shared__ Work s_before;
-    __shared__ int s_total;
+    __shared__ Count s_before, s_all;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
-    const int tile = blockIdx.x % tiles_max, bh = blockIdx.x / tiles_max, h = bh % a.c.Hkv, b = bh / a.c.Hkv;
+    const int part = blockIdx.x % parts, tb = blockIdx.x / parts;  // of a tile's rows; parts: 1, 2 or 4
+    const int tile = tb % tiles_max, bh = tb / tiles_max, h = bh % a.c.Hkv, b = bh / a.c.Hkv;
     const int live = seq_live(a, b), all = a.n * a.ratio;
-    const int rows = min(kStep, all - tile * kStep);           // rows of the output
-    const int used = min(rows, live * a.ratio - tile * kStep);  // of which in use (may be none)
+    const int row0 = part * (kStep / parts);
+    const int rows = min(kStep / parts, all - tile * kStep - row0);  // rows of the output, from row0 of the tile
+    if (rows <= 0) return;
+    const int used = min(rows, live * a.ratio - tile * kStep - row0);  // of which in use (may be none)
     // A operand rows r and r + 8 of the tile
     const int x0 = tile * kStep + r, x1 = x0 + 8;
     const int i0 = x0 / a.ratio, i1 = x1 / a.ratio;
@@ -436,6 +438,20 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
 #pragma unroll 1
         for (int st = warp; st < dsteps; st += kDraftWarps) {
             const int t0 = st * kStep;
+            // everything that the step reads is under way before the first of it is used
+            const uint32_t see[2] = {sees(a, b, min(i0, a.n - 1), t0, live), sees(a, b, min(i1, a.n - 1), t0, live)};
+            uint4 vraw[2][2][2];  // values of tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9, dims 16 r .. + 15
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int t = t0 + 8 * e + 2 * j + y;
+                        vraw[z][e][y] = t < live ? reinterpret_cast<const uint4*>(a.vn + ((int64_t)b * a.n + t) * a.vs +
+                                                                                  (int64_t)h * kPD + 16 * r)[z]
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+                    }
             float sc[2][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -454,8 +470,7 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int t = t0 + 8 * e + 2 * j + (c & 1);
-                    sc[e][c] = sees(a, b, min(c < 2 ? i0 : i1, a.n - 1), t, live) ? sc[e][c] * a.scale2 : -INFINITY;
+                    sc[e][c] = (see[c >> 1] >> (8 * e + 2 * j + (c & 1))) & 1 ? sc[e][c] * a.scale2 : -INFINITY;
                     x[c >> 1] = fmaxf(x[c >> 1], sc[e][c]);
                 }
 #pragma unroll
@@ -491,8 +506,8 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
                     ph[2 * e + y] = *reinterpret_cast<const uint32_t*>(&hi);
                     pl[2 * e + y] = *reinterpret_cast<const uint32_t*>(&lo);
                 }
-            // values of tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9, dims 16 r .. + 15; what is not finite is taken
-            // out (0 times it would reach rows that do not see it) and added below to those that do
+            // values that are not finite are taken out (0 times them would reach rows that do not see them) and added below
+            // to the rows that do
             uint32_t bad = 0;
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
@@ -501,10 +516,7 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const int t = t0 + 8 * e + 2 * j + y;
-                        const uint4 v = t < live ? reinterpret_cast<const uint4*>(a.vn + ((int64_t)b * a.n + t) * a.vs +
-                                                                                  (int64_t)h * kPD + 16 * r)[z]
-                                                 : make_uint4(0u, 0u, 0u, 0u);
+                        const uint4 v = vraw[z][e][y];
                         w[e][y][0] = v.x, w[e][y][1] = v.y, w[e][y][2] = v.z, w[e][y][3] = v.w;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -530,7 +542,7 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
                     const float w0 = __shfl_sync(kFull, sc[col >> 3][col & 1], from);
                     const float w1 = __shfl_sync(kFull, sc[col >> 3][2 + (col & 1)], from);
                     if (t < live) {
-                        const bool see0 = sees(a, b, min(i0, a.n - 1), t, live), see1 = sees(a, b, min(i1, a.n - 1), t, live);
+                        const bool see0 = (see[0] >> col) & 1, see1 = (see[1] >> col) & 1;
                         const __nv_bfloat16* v = a.vn + ((int64_t)b * a.n + t) * a.vs + (int64_t)h * kPD;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -563,93 +575,141 @@ __global__ void __launch_bounds__(32 * kFinWarps) kv_tree_finish_kernel(TreeArgs
         for (int i = threadIdx.x; i < a.B; i += 32 * kFinWarps)
             if (a.lens[i] < 0 || a.lens[i] > a.max_len) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
     if (warp == kFinWarps - 1) {
-        Work w;
-        int total;
-        count_work(a, b, w, total);
+        Count before, total;
+        count_work(a, b, before, total);
         if (lane == 0) {
-            s_before = w;
-            s_total = total;
+            s_before = before;
+            s_all = total;
         }
     }
-    __syncthreads();
-    pdl_wait();  // the context's partial results
-
-    // Partial results of this tile: runs first .. last, each at slot run + unit.  Warps share a row where rows are few.
-    const int per = steps_per_cta(a, s_total);
-    const int wide = tile * kStep / a.trows, row_at = tile * kStep - wide * a.trows;  // the context's tile, and the first row in it
-    const int steps = seq_steps(a, b), unit = s_before.units + h * seq_tiles(a, b) + wide;
-    const int at = s_before.steps + (h * seq_tiles(a, b) + wide) * steps;
-    const int first = used > 0 && steps ? at / per : 0;
-    const int count = used > 0 && steps ? (at + steps - 1) / per - first + 1 : 0;
+    const uint32_t sg = *reinterpret_cast<const uint32_t*>(a.c.signs + lane * 4);
     int share = 1;
     while (share * 2 * rows <= kFinWarps) share *= 2;  // warps of a row
-    for (int row0 = 0; row0 < rows; row0 += kFinWarps / share) {
-        const int row = row0 + warp / share;
-        float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (row < used) {
-            const int64_t slot0 = (int64_t)first + unit;
-            for (int x = warp % share; x < count; x += share) M = fmaxf(M, a.stat[(slot0 + x) * a.trows + row_at + row].x);
-#pragma unroll 4
-            for (int x = warp % share; x < count; x += share) {
-                const float2 s = a.stat[(slot0 + x) * a.trows + row_at + row];
-                const float4 y = *reinterpret_cast<const float4*>(a.part + ((slot0 + x) * a.trows + row_at + row) * kPD + lane * 4);
-                const float g = s.x == -INFINITY ? 1.f : exp2f(s.x - M);
-                L = fmaf(g, s.y, L);
-                v[0] = fmaf(g, y.x, v[0]);
-                v[1] = fmaf(g, y.y, v[1]);
-                v[2] = fmaf(g, y.z, v[2]);
-                v[3] = fmaf(g, y.w, v[3]);
-            }
-        }
-        if (share > 1) {
-            __syncthreads();  // the last round's reads
-            *reinterpret_cast<float4*>(&joined[warp][lane * 4]) = make_float4(v[0], v[1], v[2], v[3]);
-            if (lane == 0) jml[warp] = make_float2(M, L);
-            __syncthreads();
-            if (warp % share == 0) {
-                float N = -INFINITY;
-                for (int x = 0; x < share; ++x) N = fmaxf(N, jml[warp + x].x);
-                M = N;
-                L = v[0] = v[1] = v[2] = v[3] = 0.f;
-                for (int x = 0; x < share; ++x) {
-                    const float2 s = jml[warp + x];
-                    const float4 y = *reinterpret_cast<const float4*>(&joined[warp + x][lane * 4]);
-                    const float g = s.x == -INFINITY ? 1.f : exp2f(s.x - N);
-                    L = fmaf(g, s.y, L);
-                    v[0] = fmaf(g, y.x, v[0]);
-                    v[1] = fmaf(g, y.y, v[1]);
-                    v[2] = fmaf(g, y.z, v[2]);
-                    v[3] = fmaf(g, y.w, v[3]);
-                }
-            }
-        }
-        if (row < rows && warp % share == 0) {
-            float N = M;
-            for (int w = 0; w < dact; ++w) N = fmaxf(N, ml[w][row].x);
-            const float g = M == -INFINITY ? 1.f : exp2f(M - N);
-            fwht_warp128(v);
-            L *= g;
+    // A warp's rows: one of up to 8, or two (row and row + 8), whose reads go together.
+    constexpr int kRowsOf = kStep / kFinWarps;
+    auto row_of = [&](int k) { return warp / share + kFinWarps * k; };
+    __syncthreads();
+    // the drafts' results of the rows, joined while the context is under way
+    float dm[kRowsOf], dl[kRowsOf], dv[kRowsOf][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] *= g * kInvSqrtD * (float)a.c.signs[lane * 4 + e];
+    for (int k = 0; k < kRowsOf; ++k) {
+        const int row = row0 + row_of(k);
+        dm[k] = -INFINITY;
+        dl[k] = dv[k][0] = dv[k][1] = dv[k][2] = dv[k][3] = 0.f;
+        if (row_of(k) < used)
             for (int w = 0; w < dact; ++w) {
-                const float2 s = ml[w][row];
-                const float f = s.x == -INFINITY ? 1.f : exp2f(s.x - N);
-                L = fmaf(f, s.y, L);
+                const float2 st = ml[w][row];
+                const float N = fmaxf(dm[k], st.x), g = dm[k] == -INFINITY ? 1.f : exp2f(dm[k] - N);
+                const float f = st.x == -INFINITY ? 1.f : exp2f(st.x - N);  // nothing seen: zeros, or NaN sums
+                dm[k] = N;
+                dl[k] = fmaf(f, st.y, dl[k] * g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int d = lane * 4 + e, i = d & 15, nn = d >> 4;
-                    v[e] = fmaf(f, frag[w][4 * i + 2 * (row >> 3) + (nn & 1)][(row & 7) * 4 + (nn >> 1)], v[e]);
+                    dv[k][e] = fmaf(f, frag[w][4 * i + 2 * (row >> 3) + (nn & 1)][(row & 7) * 4 + (nn >> 1)], dv[k][e] * g);
                 }
             }
-            // no weight at all: zeros.  A NaN sum stays NaN.
-            const float inv = L == 0.f || row >= used ? 0.f : 1.0f / L;
-            const int x = tile * kStep + row, i = x / a.ratio;
-            __nv_bfloat162 y[2];
-            y[0] = row >= used ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(v[0] * inv, v[1] * inv);
-            y[1] = row >= used ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(v[2] * inv, v[3] * inv);
-            *reinterpret_cast<uint2*>(a.o + (((int64_t)b * a.n + i) * a.Hq + h * a.ratio + x - i * a.ratio) * kPD + lane * 4) =
-                make_uint2(*reinterpret_cast<uint32_t*>(&y[0]), *reinterpret_cast<uint32_t*>(&y[1]));
+    }
+    pdl_wait();  // the context's partial results
+
+    // Partial results of this tile: runs first .. last, each at slot run + unit.  Warps share a row where rows are few.
+    const int pad = tile_pad(a, s_all.steps), per = places_per_cta(a, s_all.steps + s_all.busy * pad);
+    const int wide = tile * kStep / a.trows, row_at = tile * kStep + row0 - wide * a.trows;  // the context's tile, and the first row in it
+    const int steps = seq_steps(a, b), of_seq = h * seq_tiles(a, b) + wide, unit = s_before.units + of_seq;
+    const int at = s_before.steps + s_before.busy * pad + of_seq * (steps + pad) + pad;  // its first step's place
+    const int first = used > 0 && steps ? at / per : 0;
+    const int count = used > 0 && steps ? (at + steps - 1) / per - first + 1 : 0;
+    // A lane reads a partial result's statistics, then all of them walk the weighted values.
+    float M[kRowsOf], L[kRowsOf], v[kRowsOf][4];
+    const int mine = (count - warp % share + share - 1) / share;  // partial results of this warp
+    const int64_t slot0 = (int64_t)first + unit + warp % share;
+#pragma unroll
+    for (int k = 0; k < kRowsOf; ++k) {
+        M[k] = -INFINITY;
+        L[k] = v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.f;
+    }
+    for (int x0 = 0; x0 < mine; x0 += 32) {
+        float w[kRowsOf];
+#pragma unroll
+        for (int k = 0; k < kRowsOf; ++k) {
+            const bool in = row_of(k) < used && x0 + lane < mine;
+            const float2 st = in ? a.stat[(slot0 + (int64_t)(x0 + lane) * share) * a.trows + row_at + row_of(k)] : make_float2(-INFINITY, 0.f);
+            float top = fmaxf(M[k], st.x);
+#pragma unroll
+            for (int m = 16; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, m));
+            const float g = M[k] == -INFINITY ? 1.f : exp2f(M[k] - top);  // nothing so far: zeros, or NaN sums
+            w[k] = st.x == -INFINITY ? 1.f : exp2f(st.x - top);
+            float l = w[k] * st.y;
+#pragma unroll
+            for (int m = 16; m; m >>= 1) l += __shfl_xor_sync(kFull, l, m);
+            M[k] = top;
+            L[k] = fmaf(L[k], g, l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[k][e] *= g;
         }
+        const int n = min(32, mine - x0);
+        constexpr int kBatch = 8;  // reads under way together: each takes about a thousand cycles
+        for (int x1 = 0; x1 < n; x1 += kBatch) {
+            float4 y[kBatch][kRowsOf];
+#pragma unroll
+            for (int z = 0; z < kBatch; ++z) {
+                const float* src = a.part + ((slot0 + (int64_t)(x0 + min(x1 + z, n - 1)) * share) * a.trows + row_at) * kPD + lane * 4;
+#pragma unroll
+                for (int k = 0; k < kRowsOf; ++k)
+                    y[z][k] = row_of(k) < used ? *reinterpret_cast<const float4*>(src + row_of(k) * kPD) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int z = 0; z < kBatch; ++z)
+                if (x1 + z < n) {
+#pragma unroll
+                    for (int k = 0; k < kRowsOf; ++k) {
+                        const float g = __shfl_sync(kFull, w[k], x1 + z);
+                        v[k][0] = fmaf(g, y[z][k].x, v[k][0]);
+                        v[k][1] = fmaf(g, y[z][k].y, v[k][1]);
+                        v[k][2] = fmaf(g, y[z][k].z, v[k][2]);
+                        v[k][3] = fmaf(g, y[z][k].w, v[k][3]);
+                    }
+                }
+        }
+    }
+    if (share > 1) {  // the warps of a row (rows of at most half as many as warps: one to a warp)
+        *reinterpret_cast<float4*>(&joined[warp][lane * 4]) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+        if (lane == 0) jml[warp] = make_float2(M[0], L[0]);
+        __syncthreads();
+        if (warp % share) return;
+        float N = -INFINITY;
+        for (int x = 0; x < share; ++x) N = fmaxf(N, jml[warp + x].x);
+        M[0] = N;
+        L[0] = v[0][0] = v[0][1] = v[0][2] = v[0][3] = 0.f;
+        for (int x = 0; x < share; ++x) {
+            const float2 st = jml[warp + x];
+            const float4 y = *reinterpret_cast<const float4*>(&joined[warp + x][lane * 4]);
+            const float g = st.x == -INFINITY ? 1.f : exp2f(st.x - N);
+            L[0] = fmaf(g, st.y, L[0]);
+            v[0][0] = fmaf(g, y.x, v[0][0]);
+            v[0][1] = fmaf(g, y.y, v[0][1]);
+            v[0][2] = fmaf(g, y.z, v[0][2]);
+            v[0][3] = fmaf(g, y.w, v[0][3]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsOf; ++k) {
+        const int row = row_of(k);
+        if (row >= rows) continue;
+        const float N = fmaxf(M[k], dm[k]);
+        const float g = M[k] == -INFINITY ? 1.f : exp2f(M[k] - N), f = dm[k] == -INFINITY ? 1.f : exp2f(dm[k] - N);
+        fwht_warp128(v[k]);
+        L[k] = fmaf(f, dl[k], L[k] * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = fmaf(f, dv[k][e], v[k][e] * (g * kInvSqrtD * (float)(int8_t)(sg >> (8 * e))));
+        // no weight at all: zeros.  A NaN sum stays NaN.
+        const float inv = L[k] == 0.f ? 0.f : 1.0f / L[k];
+        const int x = tile * kStep + row0 + row, i = x / a.ratio;
+        __nv_bfloat162 y[2];
+        y[0] = row >= used ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(v[k][0] * inv, v[k][1] * inv);
+        y[1] = row >= used ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(v[k][2] * inv, v[k][3] * inv);
+        *reinterpret_cast<uint2*>(a.o + (((int64_t)b * a.n + i) * a.Hq + h * a.ratio + x - i * a.ratio) * kPD + lane * 4) =
+            make_uint2(*reinterpret_cast<uint32_t*>(&y[0]), *reinterpret_cast<uint32_t*>(&y[1]));
     }
 }
 
@@ -665,7 +725,7 @@ int sm_count() {
 
 struct Plan {
     int64_t tiles, slots, steps, turned;  // output tiles of 16 rows; partial results, steps, rows of turned queries at most
-    int ctas, trows, stoks, least;
+    int ctas, trows, stoks, least, pad;
 };
 
 // Context launch and workspace of a call.  Runs (CTAs) and units both ascend along the work, so run + unit numbers every
@@ -677,8 +737,10 @@ Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, i
     p.trows = rows <= kStep ? kStep : (rows <= 128 ? 128 : 256);
     p.stoks = p.trows == kStep ? kStep : 32;
     p.least = p.trows == kStep ? kCtxWarps : 2;
+    // measured, beginning another tile within a run: about 4 us (16 rows, 128 rows) and 10 us (256 rows)
+    p.pad = p.trows == kStep ? 2 * kCtxWarps : (p.trows == 128 ? 8 : 14);
     p.tiles = (rows + kStep - 1) / kStep;
-    const int64_t units = (rows + p.trows - 1) / p.trows * Hkv * B, steps = (max_len + p.stoks - 1) / p.stoks;
+    const int64_t units = (rows + p.trows - 1) / p.trows * Hkv * B, steps = max_len ? (max_len + p.stoks - 1) / p.stoks + p.pad : 0;
     p.steps = units * steps;
     p.ctas = (int)std::min<int64_t>(sms, (units * steps + p.least - 1) / p.least);
     p.slots = p.ctas ? units + p.ctas : 0;
@@ -711,7 +773,7 @@ extern "C" size_t tq_kv_attend_tree_workspace_bytes(const tq_kv_pages_t* cache, 
                                                     int64_t max_len) {
     if (kv_pages_check(cache, false) != TQ_OK || B <= 0 || n <= 0 || Hq <= 0 || Hq % cache->Hkv || max_len < 0) return 0;
     const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, kMaxSms);
-    return 16 + (size_t)p.slots * p.trows * (kPD * sizeof(float) + sizeof(float2)) + (size_t)p.turned * (kPD * 2 + 4);
+    return 32 + (size_t)p.slots * p.trows * (kPD * sizeof(float) + sizeof(float2)) + (size_t)p.turned * (kPD * 2 + 4);
 }
 
 extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q, int64_t q_stride, tq_dtype dt,
@@ -763,15 +825,20 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
     a.trows = p.trows;
     a.stoks = p.stoks;
     a.least = p.least;
+    a.pad = p.pad;
     a.wait_cycles = wait_budget();
     // a scale of 0 (all weights equal) as one that no score feels: masked scores are -infinity times a factor
     a.scale2 = fabsf(scale) < 1e-30f ? 1e-30f : scale * kLog2e;
     a.o = static_cast<__nv_bfloat16*>(o);
-    a.part = static_cast<float*>(ws);
+    a.part = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));  // 32-byte stores
     a.stat = reinterpret_cast<float2*>(a.part + (size_t)p.slots * p.trows * kPD);
     a.turned = reinterpret_cast<uint4*>(a.stat + (size_t)p.slots * p.trows);
     a.power = reinterpret_cast<int32_t*>(a.turned + (size_t)p.turned * 16);
     a.err = err;
+    // A tile's rows go to up to four CTAs of the last launch where there are SMs for them: reading the partial results is
+    // bound by each SM's share of the L2 (32 tiles of 20 partial results: 32 CTAs 11 us, 128 CTAs see the design notes).
+    const int64_t all_tiles = p.tiles * cache->Hkv * B;
+    const int parts = all_tiles * 4 <= sm_count() ? 4 : (all_tiles * 2 <= sm_count() ? 2 : 1);
     cudaStream_t st = as_stream(stream);
     if (p.ctas) {
         tq_status s;
@@ -779,8 +846,8 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
         else if (cache->kcb.levels == 256) s = cache->vcb.levels == 8 ? launch_context<256, 8>(a, st) : launch_context<256, 16>(a, st);
         else s = cache->vcb.levels == 8 ? launch_context<16, 8>(a, st) : launch_context<16, 16>(a, st);
         if (s != TQ_OK) return s;
-        return launch_pdl(kv_tree_finish_kernel, dim3((unsigned)(p.tiles * cache->Hkv * B)), dim3(32 * kFinWarps), 0, st, a, (int)p.tiles);
+        return launch_pdl(kv_tree_finish_kernel, dim3((unsigned)(p.tiles * cache->Hkv * B * parts)), dim3(32 * kFinWarps), 0, st, a, (int)p.tiles, parts);
     }
-    kv_tree_finish_kernel<<<(unsigned)(p.tiles * cache->Hkv * B), 32 * kFinWarps, 0, st>>>(a, (int)p.tiles);
+    kv_tree_finish_kernel<<<(unsigned)(p.tiles * cache->Hkv * B * parts), 32 * kFinWarps, 0, st>>>(a, (int)p.tiles, parts);
     return launch_status();
 }

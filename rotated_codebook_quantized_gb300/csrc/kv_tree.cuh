@@ -24,7 +24,8 @@ struct TreeArgs {
     const uint64_t* mask;
     const int32_t* n_tok;
     int B, n, Hq, ratio, table_stride;  // ratio: query heads per kv head
-    int ctas, trows, stoks, least;      // context launch: CTAs, query rows of a tile, tokens of a step, fewest steps of a run
+    // context launch: CTAs, query rows of a tile, tokens of a step, fewest steps of a run, steps that beginning a tile weighs
+    int ctas, trows, stoks, least, pad;
     float scale2;                       // scale * log2(e)
     __nv_bfloat16* o;
     float2* stat;  // [slot][trows]: running maximum (log2 units) and sum of a row
@@ -47,35 +48,40 @@ TQ_DEVFN int seq_live(const TreeArgs& a, int b) { return a.n_tok ? min(max(a.n_t
 TQ_DEVFN int seq_tiles(const TreeArgs& a, int b) { return (seq_live(a, b) * a.ratio + a.trows - 1) / a.trows; }
 TQ_DEVFN int seq_steps(const TreeArgs& a, int b) { return (seq_len(a, b) + a.stoks - 1) / a.stoks; }
 
-// Counts of steps and of units fit 31 bits: the host checks their bound.
-struct Work {
-    int steps, units;  // steps, and (kv head, tile) units, of the sequences before one
-};
+// A run is a stretch of an axis on which every tile of a sequence that has steps takes `pad` places, then one for each step: so
+// that a run which begins another tile on its way has fewer steps to do.  Where runs are short (there are few steps for the
+// CTAs), the pad is at most a quarter of a run's steps.  Counts fit 31 bits: the host checks their bound.
+TQ_DEVFN int tile_pad(const TreeArgs& a, int steps) { return min(a.pad, steps / (4 * a.ctas)); }
 
-// Steps and units of the sequences before b, and the steps of all (one warp).
-TQ_DEVFN void count_work(const TreeArgs& a, int b, Work& before, int& total) {
+// Places of one CTA's run: an equal share, and no fewer than `least`.
+TQ_DEVFN int places_per_cta(const TreeArgs& a, int total) { return max((total + a.ctas - 1) / a.ctas, a.least); }
+
+// Over the batch, and over the sequences before b (one warp): steps, units ((kv head, tile) pairs), and units that have steps.
+struct Count {
+    int steps, units, busy;
+};
+TQ_DEVFN void count_work(const TreeArgs& a, int b, Count& before, Count& all) {
     const int lane = threadIdx.x & 31;
-    int s = 0, all = 0, u = 0;
+    Count p{}, q{};
     for (int i = lane; i < a.B; i += 32) {
-        const int units = seq_tiles(a, i) * a.c.Hkv, w = units * seq_steps(a, i);
-        all += w;
+        const int units = seq_tiles(a, i) * a.c.Hkv, steps = seq_steps(a, i);
+        q.steps += units * steps;
+        q.units += units;
+        q.busy += steps ? units : 0;
         if (i < b) {
-            s += w;
-            u += units;
+            p.steps += units * steps;
+            p.units += units;
+            p.busy += steps ? units : 0;
         }
     }
-    before = {__reduce_add_sync(kFull, s), __reduce_add_sync(kFull, u)};
-    total = __reduce_add_sync(kFull, all);
+    before = {__reduce_add_sync(kFull, p.steps), __reduce_add_sync(kFull, p.units), __reduce_add_sync(kFull, p.busy)};
+    all = {__reduce_add_sync(kFull, q.steps), __reduce_add_sync(kFull, q.units), __reduce_add_sync(kFull, q.busy)};
 }
 
-// Steps of one CTA's run: an equal share, and no fewer than `least`.
-TQ_DEVFN int steps_per_cta(const TreeArgs& a, int total) { return max((total + a.ctas - 1) / a.ctas, a.least); }
-
-// The run of CTA `run`: its first step `at`, the last sequence b with at most so many steps before it, what lies before b,
-// the steps of a run and of all (one warp).
+// The run of CTA `run`: its first place `at`, places of a run and of all, the pad, and the last sequence b with at most `at`
+// places before it, with the places and units before b (one warp).
 struct Run {
-    int at, b, per, total;
-    Work before;
+    int at, per, total, pad, b, places, units;
 };
 TQ_DEVFN Run find_run(const TreeArgs& a, int run) {
     const int lane = threadIdx.x & 31;
@@ -84,17 +90,22 @@ TQ_DEVFN Run find_run(const TreeArgs& a, int run) {
     auto read = [&](int b0) {
         const int i = b0 + lane;
         units = i < a.B ? seq_tiles(a, i) * a.c.Hkv : 0;
-        steps = i < a.B ? units * seq_steps(a, i) : 0;
+        steps = i < a.B ? seq_steps(a, i) : 0;
     };
+    int all = 0, busy = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
         read(b0);
-        r.total += __reduce_add_sync(kFull, steps);
+        all += __reduce_add_sync(kFull, units * steps);
+        busy += __reduce_add_sync(kFull, steps ? units : 0);
     }
-    r.per = steps_per_cta(a, r.total);
+    r.pad = tile_pad(a, all);
+    r.total = all + busy * r.pad;
+    r.per = places_per_cta(a, r.total);
     r.at = run * r.per;  // at most the total and a run more
     for (int b0 = 0; b0 < a.B; b0 += 32) {
         if (a.B > 32) read(b0);
-        int s = steps, u = units;
+        const int own = steps ? units * (steps + r.pad) : 0;
+        int s = own, u = units;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const int x = __shfl_up_sync(kFull, s, m), y = __shfl_up_sync(kFull, u, m);
@@ -103,16 +114,16 @@ TQ_DEVFN Run find_run(const TreeArgs& a, int run) {
                 u += y;
             }
         }
-        const unsigned hit = __ballot_sync(kFull, r.before.steps + s > r.at);
+        const unsigned hit = __ballot_sync(kFull, r.places + s > r.at);
         if (hit) {
             const int src = __ffs(hit) - 1;
-            r.before.steps += __shfl_sync(kFull, s - steps, src);
-            r.before.units += __shfl_sync(kFull, u - units, src);
+            r.places += __shfl_sync(kFull, s - own, src);
+            r.units += __shfl_sync(kFull, u - units, src);
             r.b = b0 + src;
             break;
         }
-        r.before.steps += __shfl_sync(kFull, s, 31);
-        r.before.units += __shfl_sync(kFull, u, 31);
+        r.places += __shfl_sync(kFull, s, 31);
+        r.units += __shfl_sync(kFull, u, 31);
     }
     return r;
 }
@@ -122,30 +133,35 @@ struct Stretch {
     int b, h, tile, unit, s0, s1, len, rows;  // unit: numbered over the batch; rows in use
 };
 struct Walk {
-    int p, end, b;
-    Work before;
-    TQ_DEVFN explicit Walk(const Run& r) : p(r.at), end(min(r.at + r.per, r.total)), b(r.b), before(r.before) {}
+    int p, end, pad, b, places, units;  // places and units before sequence b
+    TQ_DEVFN explicit Walk(const Run& r)
+        : p(r.at), end(min(r.at + r.per, r.total)), pad(r.pad), b(r.b), places(r.places), units(r.units) {}
     TQ_DEVFN bool next(const TreeArgs& a, Stretch& x) {
-        if (p >= end) return false;
-        int steps = seq_steps(a, b), tiles = seq_tiles(a, b);
-        while (p >= before.steps + steps * tiles * a.c.Hkv) {  // into the next sequence that has any
-            before.steps += steps * tiles * a.c.Hkv;
-            before.units += tiles * a.c.Hkv;
-            ++b;
-            steps = seq_steps(a, b);
-            tiles = seq_tiles(a, b);
+        while (p < end) {
+            int steps = seq_steps(a, b), tiles = seq_tiles(a, b), own = steps ? steps + pad : 0;
+            while (p >= places + own * tiles * a.c.Hkv) {  // into the next sequence that has any
+                places += own * tiles * a.c.Hkv;
+                units += tiles * a.c.Hkv;
+                ++b;
+                steps = seq_steps(a, b);
+                tiles = seq_tiles(a, b);
+                own = steps ? steps + pad : 0;
+            }
+            const int unit = (p - places) / own, at = p - places - unit * own;
+            const int to = min(own, at + (end - p));
+            p += to - at;
+            if (to <= pad) continue;  // no step of this tile
+            x.b = b;
+            x.h = unit / tiles;
+            x.tile = unit - x.h * tiles;
+            x.unit = units + unit;
+            x.s0 = max(at - pad, 0);
+            x.s1 = to - pad;
+            x.len = seq_len(a, b);
+            x.rows = min(a.trows, seq_live(a, b) * a.ratio - x.tile * a.trows);
+            return true;
         }
-        const int unit = (p - before.steps) / steps;
-        x.b = b;
-        x.h = unit / tiles;
-        x.tile = unit - x.h * tiles;
-        x.unit = before.units + unit;
-        x.s0 = p - before.steps - unit * steps;
-        x.s1 = min(steps, x.s0 + (end - p));
-        x.len = seq_len(a, b);
-        x.rows = min(a.trows, seq_live(a, b) * a.ratio - x.tile * a.trows);
-        p += x.s1 - x.s0;
-        return true;
+        return false;
     }
 };
 

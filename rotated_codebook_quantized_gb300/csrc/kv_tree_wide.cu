@@ -155,6 +155,11 @@ __global__ void __launch_bounds__(256) kv_tree_turn_kernel(TreeArgs a, int tiles
     if (lane == 0) a.power[unit * a.trows + row] = e;
 }
 
+TQ_DEVFN void stg256(float* p, const float* v) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                 "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
 // A 16-byte asynchronous copy, where `on`.
 template <int OFF>
 TQ_DEVFN void cp16_if(uint32_t dst, const void* src, bool on) {
@@ -317,17 +322,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             for (uint32_t i = first; i < ge; i += 3 - T) {
                 const uint32_t e = done & 1;
                 {
-                    // (the decoders' barrier has long completed; waiting on it too orders their `valid` before the read)
-                    ok = mbar_wait(&s_ready[stream][e], (done >> 1) & 1, abort_flag, a.wait_cycles) &&
-                         mbar_wait(full + i % kStages, (i / kStages) & 1, abort_flag, a.wait_cycles);
-                    ok = __all_sync(kFull, ok);
+                    // (the decoders' barrier has long completed; waiting on it too, beside the load, orders `valid` before its read)
+                    ok = __all_sync(kFull, mbar_wait(&s_ready[stream][e], (done >> 1) & 1, abort_flag, a.wait_cycles));
                     if (!ok) break;
                     tc_fence_after();
                     if (!idle) {
                         uint32_t s[32];
                         tc_ld32(at + kTok * e, s);
+                        ok = __all_sync(kFull, mbar_wait(full + i % kStages, (i / kStages) & 1, abort_flag, a.wait_cycles));
                         const uint32_t in = *reinterpret_cast<const uint32_t*>(valid[i % kStages]);
                         tc_wait_ld();
+                        if (!ok) break;
                         if (in != ~0u) {  // tokens past the end, or of a bad page
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
@@ -416,21 +421,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                     const int64_t to = ((int64_t)blockIdx.x + x.unit) * kRows + row;
                     const float vscale = exp2f((float)ev);
 #pragma unroll 1
-                    for (int c = 0; c < 16; ++c) {
-                        uint32_t o[8], o1[8];
-                        tc_ld8(col_o + 8 * c, o);
-                        if (two) tc_ld8(col_o + 128 + 8 * c, o1);
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o[16], o1[16];
+                        tc_ld8(col_o + 16 * c, o);
+                        tc_ld8(col_o + 16 * c + 8, o + 8);
+                        if (two) {
+                            tc_ld8(col_o + 128 + 16 * c, o1);
+                            tc_ld8(col_o + 136 + 16 * c, o1 + 8);
+                        }
                         tc_wait_ld();
-                        float z[8];
+                        float z[16];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
+                        for (int k = 0; k < 16; ++k) {
                             z[k] = __uint_as_float(o[k]) * (w0 * vscale);
                             if (two) z[k] = fmaf(__uint_as_float(o1[k]), w1 * vscale, z[k]);
                         }
-                        if (row < x.rows) {
-                            float4* out = reinterpret_cast<float4*>(a.part + to * kPD + 8 * c);
-                            out[0] = make_float4(z[0], z[1], z[2], z[3]);
-                            out[1] = make_float4(z[4], z[5], z[6], z[7]);
+                        if (row < x.rows) {  // whole 32-byte sectors
+                            float* out = a.part + to * kPD + 16 * c;
+                            stg256(out, z);
+                            stg256(out + 8, z + 8);
                         }
                     }
                     if (row < x.rows) a.stat[to] = make_float2(n, two ? l * w0 + l1 * w1 : l);
