@@ -469,7 +469,7 @@ tq_status tq_rope(const tq_rope_t* rope, const int32_t* positions, int64_t token
  * head_stride = capacity.
  * D: 128.  page: 16, 32, 64, 128 or 256.  kcb.levels: 16 or 256, vcb.levels: 8 or
  * 16.  group: 16, 32, 64 or 128.  Strides: multiples of 16 rows.  The four arrays
- * start 16-byte aligned. */
+ * and the rotation's signs start 16-byte aligned. */
 typedef struct tq_kv_pages_t {
     uint32_t* kcodes;
     uint16_t* kscales;

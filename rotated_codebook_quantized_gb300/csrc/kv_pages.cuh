@@ -36,7 +36,7 @@ inline tq_status kv_pages_check(const tq_kv_pages_t* c, bool write) {
     if (c->pages * c->page > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;  // slots are int32
     if (c->page_stride < c->page || c->head_stride < c->page || c->page_stride % 16 || c->head_stride % 16)
         return TQ_ERR_INVALID;
-    if (!c->rot.signs || c->rot.dim != kPD || c->rot.block != kPD) return TQ_ERR_INVALID;
+    if (!c->rot.signs || !aligned(c->rot.signs, 16) || c->rot.dim != kPD || c->rot.block != kPD) return TQ_ERR_INVALID;
     if (!c->kcb.centroids || !c->vcb.centroids || (write && (!c->kcb.thresholds || !c->vcb.thresholds)))
         return TQ_ERR_INVALID;
     if (!host_codes_per_word(c->kcb.levels) || !host_codes_per_word(c->vcb.levels)) return TQ_ERR_INVALID;

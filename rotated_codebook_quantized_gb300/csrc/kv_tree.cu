@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
     pdl_trigger();
-    if (warp == 0) {
+    if (warp == kCtxWarps - 1) {  // beside the others, which build the table
         const Run run = find_run(a, blockIdx.x);
         if (lane == 0) s_run = run;
     }
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
     const int ek = exponent_above(fmaxf(fabsf(a.c.kcent[0]), fabsf(a.c.kcent[KL - 1])));
     const int ev = exponent_above(fmaxf(fabsf(a.c.vcent[0]), fabsf(a.c.vcent[VL - 1])));
     const float kd = exp2f((float)-ek), vd = exp2f((float)-ev);
-    build_table<KL, VL>(a.c, space + kTable, kd, vd, warp, kCtxWarps);
+    if (warp < kCtxWarps - 1) build_table<KL, VL>(a.c, space + kTable, kd, vd, warp, kCtxWarps - 1);
     // An 8-level value book lives in four registers: low and high bytes of its fp16 centroids.
     uint32_t tl[2] = {0, 0}, th[2] = {0, 0};
     if (VL == 8) {
@@ -109,6 +109,39 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
     Stretch x;
     while (walk.next(a, x)) {
         const int b = x.b, h = x.h, tile = x.tile, s0 = x.s0, s1 = x.s1, len = x.len, rows = x.rows;
+
+        // the first copies are under way while the queries are turned
+        const int32_t* tab = a.table + (int64_t)b * a.table_stride;
+        uint32_t okbits = 0;
+        auto page_of = [&](int st) { return st < s1 ? __ldg(tab + (st >> (a.c.lpage - 4))) : 0; };
+        int ahead = s0 + warp, page_next = page_of(ahead);  // next step to copy, and its page
+        uint32_t fill = ring;                               // and its place
+        auto issue = [&]() {
+            const int page = page_next;
+            const uint32_t row16 = (uint32_t)page * page16 + h * head16 + (ahead & in_page);
+            page_next = page_of(ahead + kCtxWarps);
+            okbits <<= 1;
+            if (ahead < s1) {
+                if ((uint32_t)page < (uint32_t)a.c.pages) {
+                    okbits |= 1;
+                    const uint8_t* k = kc + (uint64_t)row16 * (kStep * S::kKRow);
+#pragma unroll
+                    for (int x = 0; x < kStep * S::kKRow / 512; ++x) cp16(fill + dk + 512 * x, k + 512 * x);
+                    const uint8_t* v = vc + (uint64_t)row16 * (kStep * KvBook<VL>::kWords * 4);
+                    cp16(fill + dv, v);
+                    if (VL == 16 || lane < kStep * KvBook<VL>::kWords / 4 - 32)
+                        cp16(fill + dv + (VL == 16 ? 8 * S::kVRow : 512), v + 512);
+                    if (copies_z) cp16(fill + dz, zc + (uint64_t)row16 * (uint32_t)(kStep * 2 * ng));
+                } else if (lane == 0 && a.err) {
+                    atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            ahead += kCtxWarps;
+            fill = fill + S::kBytes == ring_end ? ring : fill + S::kBytes;
+        };
+#pragma unroll
+        for (int it = 0; it < kDepth - 1; ++it) issue();
 
         // queries of the tile: rotated, over a power of two of their own, fp16
         for (int row = warp; row < kStep; row += kCtxWarps) {
@@ -146,43 +179,11 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
         }
         const float f0 = qf[r], f1 = qf[r + 8];
 
-        const int32_t* tab = a.table + (int64_t)b * a.table_stride;
-        uint32_t okbits = 0;
-        auto page_of = [&](int st) { return st < s1 ? __ldg(tab + (st >> (a.c.lpage - 4))) : 0; };
-        int ahead = s0 + warp, page_next = page_of(ahead);  // next step to copy, and its page
-        uint32_t fill = ring;                               // and its place
-        auto issue = [&]() {
-            const int page = page_next;
-            const uint32_t row16 = (uint32_t)page * page16 + h * head16 + (ahead & in_page);
-            page_next = page_of(ahead + kCtxWarps);
-            okbits <<= 1;
-            if (ahead < s1) {
-                if ((uint32_t)page < (uint32_t)a.c.pages) {
-                    okbits |= 1;
-                    const uint8_t* k = kc + (uint64_t)row16 * (kStep * S::kKRow);
-#pragma unroll
-                    for (int x = 0; x < kStep * S::kKRow / 512; ++x) cp16(fill + dk + 512 * x, k + 512 * x);
-                    const uint8_t* v = vc + (uint64_t)row16 * (kStep * KvBook<VL>::kWords * 4);
-                    cp16(fill + dv, v);
-                    if (VL == 16 || lane < kStep * KvBook<VL>::kWords / 4 - 32)
-                        cp16(fill + dv + (VL == 16 ? 8 * S::kVRow : 512), v + 512);
-                    if (copies_z) cp16(fill + dz, zc + (uint64_t)row16 * (uint32_t)(kStep * 2 * ng));
-                } else if (lane == 0 && a.err) {
-                    atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            ahead += kCtxWarps;
-            fill = fill + S::kBytes == ring_end ? ring : fill + S::kBytes;
-        };
-
         float o[16][4];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         // running maxima (log2) of rows r and r + 8, their negatives (0 while there is none), and the rows' sums
         float m0 = -INFINITY, m1 = -INFINITY, b0 = 0.f, b1 = 0.f, l[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int it = 0; it < kDepth - 1; ++it) issue();
         // scale places of the lane: keys' dims 32 j and 32 j + 16, values' dims 16 r
         const int gk0 = (32 * j) >> a.c.lgroup, gk1 = (32 * j + 16) >> a.c.lgroup, gv = (16 * r) >> a.c.lgroup;
         // 3-bit values: dims 16 r .. + 7 begin at code c0 of word w0 (ten to a word), dims 16 r + 8 .. at c1 of w1
@@ -736,7 +737,7 @@ Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, i
     const int64_t rows = (int64_t)n * (Hq / Hkv);
     p.trows = rows <= kStep ? kStep : (rows <= 128 ? 128 : 256);
     p.stoks = p.trows == kStep ? kStep : 32;
-    p.least = p.trows == kStep ? kCtxWarps : 2;
+    p.least = p.trows == kStep ? 4 : 2;
     // measured, beginning another tile within a run: about 4 us (16 rows, 128 rows) and 10 us (256 rows)
     p.pad = p.trows == kStep ? 2 * kCtxWarps : (p.trows == 128 ? 8 : 14);
     p.tiles = (rows + kStep - 1) / kStep;
@@ -746,6 +747,11 @@ Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, i
     p.slots = p.ctas ? units + p.ctas : 0;
     p.turned = p.ctas && p.trows != kStep ? units * p.trows : 0;
     return p;
+}
+
+// Scratch of a plan: partial results and their statistics, turned queries and their exponents, and 32 bytes of alignment.
+size_t plan_bytes(const Plan& p) {
+    return 32 + (size_t)p.slots * p.trows * (kPD * sizeof(float) + sizeof(float2)) + (size_t)p.turned * (kPD * 2 + 4);
 }
 
 template <int KL, int VL>
@@ -772,8 +778,7 @@ constexpr int kMaxSms = 256;  // bound on the SMs that the workspace is sized fo
 extern "C" size_t tq_kv_attend_tree_workspace_bytes(const tq_kv_pages_t* cache, int32_t B, int32_t n, int32_t Hq,
                                                     int64_t max_len) {
     if (kv_pages_check(cache, false) != TQ_OK || B <= 0 || n <= 0 || Hq <= 0 || Hq % cache->Hkv || max_len < 0) return 0;
-    const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, kMaxSms);
-    return 32 + (size_t)p.slots * p.trows * (kPD * sizeof(float) + sizeof(float2)) + (size_t)p.turned * (kPD * 2 + 4);
+    return plan_bytes(make_plan(cache->Hkv, B, n, Hq, max_len, kMaxSms));
 }
 
 extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q, int64_t q_stride, tq_dtype dt,
@@ -798,7 +803,9 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
         !aligned(mask, 8))
         return TQ_ERR_INVALID;
     if (ws_bytes < tq_kv_attend_tree_workspace_bytes(cache, B, n, Hq, max_len)) return TQ_ERR_INVALID;
+    // (the size above is for the most SMs; a plan for fewer takes no more, and is held to it)
     const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, std::min(sm_count(), kMaxSms));
+    if (ws_bytes < plan_bytes(p)) return TQ_ERR_INVALID;
     if ((int64_t)n * (Hq / cache->Hkv) > 0x3fffffffll || p.tiles * B * cache->Hkv > 0x3fffffffll || p.steps > 0x3fffffffll || max_len > 0x7fffffffll - 64)
         return TQ_ERR_UNSUPPORTED;
     // cache rows by the 8 are 32-bit numbers

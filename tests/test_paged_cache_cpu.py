@@ -80,7 +80,7 @@ def _pages(kl=256, vl=8, page=64, group=32, D=128, Hkv=8, pages=10, ps=512, hs=6
 
 BAD_POOLS = [(dict(D=64), 2), (dict(group=48), 1), (dict(page=8), 1), (dict(page=48), 1), (dict(page=512), 1), (dict(kl=8), 2),
              (dict(vl=256), 2), (dict(kl=5), 1), (dict(Hkv=0), 1), (dict(pages=-1), 1), (dict(ps=500), 1), (dict(hs=32), 1),
-             (dict(ptr=0x1008), 1), (dict(ptr=0), 1), (dict(signs=0), 1), (dict(block=64), 1), (dict(pages=1 << 26), 2)]
+             (dict(ptr=0x1008), 1), (dict(ptr=0), 1), (dict(signs=0), 1), (dict(signs=0x1004), 1), (dict(block=64), 1), (dict(pages=1 << 26), 2)]
 
 
 @pytest.mark.parametrize("change,status", BAD_POOLS)
