@@ -518,7 +518,9 @@ tq_status tq_kv_fetch(const tq_kv_pages_t* cache, const int32_t* slots, int64_t 
  * left out.  Entries of table past a sequence's pages are not read.
  * o: device bf16 [B][n][Hq][D].  Cached keys, values and their weights are fp16
  * tensor-core operands; scores, softmax statistics and sums are fp32.  ws: 16-byte
- * aligned device scratch of tq_kv_attend_tree_workspace_bytes(...) bytes. */
+ * aligned device scratch of tq_kv_attend_tree_workspace_bytes(...) bytes; calls that
+ * may run at the same time must not share it.  A bounded wait that ran out (more than
+ * 16 rows, n*Hq/Hkv, to a kv head) sets TQ_DEVERR_TIMEOUT; o is then incomplete. */
 tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q, int64_t q_stride, tq_dtype dt, int32_t B,
                             int32_t n, int32_t Hq, const int32_t* table, int32_t table_stride, const int32_t* lens,
                             int64_t max_len, const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
@@ -682,7 +684,7 @@ tq_status tq_expert_cache_stats(const tq_expert_cache* cache, int64_t* hits, int
 tq_status tq_check_error(uint32_t* err, uint32_t* bits, void* stream);
 
 /* Test hook for the bounded waits of the tensor-core kernels (tq_gather_qmm,
- * tq_qmv_tc) and of the three-level tensor-copy matvec (the ternary kernel of
+ * tq_qmv_tc, tq_kv_attend_tree for more than 16 rows to a kv head) and of the three-level tensor-copy matvec (the ternary kernel of
  * calls without scratch, of groups other than 16 and of the fused input
  * stages): every wait of a pipeline role on another (an mbarrier phase)
  * gives up after `cycles` SM clock cycles, raises TQ_DEVERR_TIMEOUT in the

@@ -716,3 +716,20 @@ def test_tree_long_runs_repeat_and_report_nothing(lib, n, Hq, H):
         s = q[0].float().transpose(0, 1) @ kk.transpose(1, 2) * D ** -0.5
         s[:, :, context:].masked_fill_(~torch.tril(torch.ones((n, n), dtype=torch.bool, device="cuda")), float("-inf"))
         assert helpers.rel_l2(_f64(out[0][0]), _f64((torch.softmax(s, -1) @ vv).transpose(0, 1))) < ATTEND
+
+
+@pytest.mark.parametrize("n", [8, 64])
+def test_tree_wait_budget(lib, n):
+    """With no budget the bounded waits give up, the call reports it, and the next call is as before."""
+    g, c, table, dlens, ctx, q, kn, vn = _setup(lib, (18, n), [3000], n, 16, 4, 64)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    before = lib.kv_attend_tree(c, q, table, dlens, k_new=kn, v_new=vn, err=err)
+    assert lib.check_error(err) == 0
+    lib.set_wait_budget(0)
+    try:
+        lib.kv_attend_tree(c, q, table, dlens, k_new=kn, v_new=vn, err=err)
+        assert lib.check_error(err) == lib.TQ_DEVERR_TIMEOUT
+    finally:
+        lib.set_wait_budget(-1)
+    assert torch.equal(before, lib.kv_attend_tree(c, q, table, dlens, k_new=kn, v_new=vn, err=err))
+    assert lib.check_error(err) == 0
