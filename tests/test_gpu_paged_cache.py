@@ -733,3 +733,15 @@ def test_tree_wait_budget(lib, n):
         lib.set_wait_budget(-1)
     assert torch.equal(before, lib.kv_attend_tree(c, q, table, dlens, k_new=kn, v_new=vn, err=err))
     assert lib.check_error(err) == 0
+
+
+def test_example_of_drafted_decoding(lib):
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "drafted_decode.py")
+    spec = importlib.util.spec_from_file_location("drafted_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    worst, bits = example.main()
+    assert bits == 0 and worst < ATTEND
