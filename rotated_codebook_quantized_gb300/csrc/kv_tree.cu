@@ -4,12 +4,16 @@
 // mask, over the drafted tokens.  As in tq_kv_attend the rotation moves off the cache:
 // q . k = (R q) . (R k), and sum_t p_t v_t = R^T sum_t p_t (R v_t), one de-rotation per row.
 //
-// Two launches.  kv_tree_context_kernel: the cached tokens.  The work is cut into steps of
-// 16 tokens of one (sequence, kv head, tile of 16 query rows); one persistent CTA per SM
-// takes an equal run of the steps of the whole batch, whatever the sequences' lengths, and
-// leaves a partial result (maximum, sum, weighted values of 16 rows) wherever its run
-// crosses into another tile.  kv_tree_finish_kernel: the drafted tokens, then the join of a
-// tile's partial results, the de-rotation and the output.
+// Up to 16 query rows to a kv head, two launches.  kv_tree_context_kernel: the cached tokens.  The work is cut into
+// steps of 16 tokens of one (sequence, kv head, tile of query rows); one persistent CTA per SM takes an equal run of the
+// steps of the whole batch, whatever the sequences' lengths, and leaves a partial result (maximum, sum, weighted values
+// of the rows) wherever its run crosses into another tile.  kv_tree_finish_kernel: the drafted tokens, then the join of a
+// tile's partial results, the de-rotation and the output.  More rows: kv_tree_wide.cu's two kernels take the place of the
+// first.  One row over a few thousand tokens would be as fast there (100 tokens of one sequence: 12.7 us against 13.8),
+// over 65536 it takes 63 us against 44.
+//
+// The context kernel is bound by instruction issue: a lane decodes 128 codes of a step by a table read or two byte
+// permutes each (131072 tokens of 8 heads: 3.1 TB/s of codes and scales, 47 % of the copy rate).
 #include <math.h>
 
 #include <algorithm>
@@ -22,8 +26,17 @@ using namespace tq::tree;
 namespace {
 
 constexpr int kStep = 16;      // tokens of a step, rows of a tile
-constexpr int kCtxWarps = 12;  // 168 registers a thread: 64 of sums, 32 of queries
-constexpr int kDepth = 3;      // steps of a warp's ring: two in flight while one is decoded
+// The context kernel for tiles of up to ROWS query rows: warps, and steps of a warp's ring (all but one in flight).
+// Up to 8 rows the keys and values are the A operands of the products and the rows the 8 columns of B, which halves
+// the products and the registers of sums and lets 16 warps stay (32 heads on 8, one token over 131072: 67 us, the
+// other form 82; over 100: 13.8 and 15.8).
+template <int ROWS>
+struct Ctx {
+    static constexpr int kWarps = ROWS == 8 ? 16 : 12;  // 128 registers a thread; 168, of which 64 of sums and 32 of queries
+    static constexpr int kDepth = ROWS == 8 ? 2 : 3;
+    static constexpr int kLowWarps = ROWS == 8 ? 7 : 5;  // whose rings lie below the decode table
+    static constexpr int kSums = 4 * ROWS;               // registers of sums
+};
 constexpr int kFinWarps = 8, kDraftWarps = 4;
 constexpr int kFragPad = 33;  // floats of a fragment register over the lanes, padded
 
@@ -36,31 +49,39 @@ struct Stage {
 };
 // Shared memory of the context kernel.  The decode table (256 rows of 256 bytes) starts at shared address
 // 64 K, so that one byte permute builds the address of an entry (64 K + code * 256 + lane * 4); the rings of
-// the first kLowWarps warps lie below it, the others above.
+// some warps lie below it, the others above.
 constexpr uint32_t kTable = 65536, kTableEnd = 131072;
-constexpr int kLowWarps = 5;
 constexpr uint32_t kSmemStart = 1024 + 512;  // of the space below: the system's first KB, then the static variables
 constexpr uint32_t kQueries = kSmemStart, kFactors = kQueries + kStep * kPD * 2, kRingsLow = kFactors + kStep * 4;
-template <int KL, int VL>
+template <int KL, int VL, int ROWS>
 constexpr uint32_t warp_region() {  // a warp's ring, and its fragments of the join over it
-    const uint32_t ring = kDepth * Stage<KL, VL>::kBytes, join = 64 * kFragPad * 4 + kStep * 8;
+    const uint32_t ring = Ctx<ROWS>::kDepth * Stage<KL, VL>::kBytes, join = Ctx<ROWS>::kSums * kFragPad * 4 + ROWS * 8;
     return ((ring > join ? ring : join) + 127) / 128 * 128;
 }
-template <int KL, int VL>
+template <int KL, int VL, int ROWS>
 constexpr uint32_t context_smem_end() {
-    static_assert(kRingsLow % 16 == 0 && kRingsLow + kLowWarps * warp_region<KL, VL>() <= kTable, "rings below the table");
-    return kTableEnd + (kCtxWarps - kLowWarps) * warp_region<KL, VL>();
+    static_assert(kRingsLow % 16 == 0 && kRingsLow + Ctx<ROWS>::kLowWarps * warp_region<KL, VL, ROWS>() <= kTable, "rings below the table");
+    return kTableEnd + (Ctx<ROWS>::kWarps - Ctx<ROWS>::kLowWarps) * warp_region<KL, VL, ROWS>();
 }
 
-template <int KL, int VL>
-__global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(TreeArgs a) {
+// An 8 x 8 matrix of 16-bit elements, a fragment register, transposed.
+TQ_DEVFN uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int KL, int VL, int ROWS>
+__global__ void __launch_bounds__(32 * Ctx<ROWS>::kWarps, 1) kv_tree_context_kernel(TreeArgs a) {
     using S = Stage<KL, VL>;
+    constexpr int kCtxWarps = Ctx<ROWS>::kWarps, kDepth = Ctx<ROWS>::kDepth, kLowWarps = Ctx<ROWS>::kLowWarps;
+    constexpr bool kFew = ROWS == 8;
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* const space = smem - (uint32_t)__cvta_generic_to_shared(smem);  // shared address 0
     __half* qh = reinterpret_cast<__half*>(space + kQueries);  // [16][128] rotated queries
     float* qf = reinterpret_cast<float*>(space + kFactors);    // [16] factor from a row's products to log2 scores
     auto region = [&](int w) {  // of a warp
-        return w < kLowWarps ? kRingsLow + w * warp_region<KL, VL>() : kTableEnd + (w - kLowWarps) * warp_region<KL, VL>();
+        return w < kLowWarps ? kRingsLow + w * warp_region<KL, VL, ROWS>() : kTableEnd + (w - kLowWarps) * warp_region<KL, VL, ROWS>();
     };
     __shared__ Run s_run;
 
@@ -144,7 +165,7 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
         for (int it = 0; it < kDepth - 1; ++it) issue();
 
         // queries of the tile: rotated, over a power of two of their own, fp16
-        for (int row = warp; row < kStep; row += kCtxWarps) {
+        for (int row = warp; row < ROWS; row += kCtxWarps) {
             float v[4] = {0.f, 0.f, 0.f, 0.f};
             if (row < rows) {
                 const int y = tile * kStep + row, i = y / a.ratio, g = y - i * a.ratio;
@@ -167,22 +188,25 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
             if (lane == 0) qf[row] = exp2f((float)(e + ek)) * (kInvSqrtD * fabsf(a.scale2));
         }
         __syncthreads();
-        // A operand of product step s: the lane's rows r and r + 8, dims 32 j + 4 s .. + 3.  Any order
+        // Operand of product step s: the lane's row r (A: and r + 8), dims 32 j + 4 s .. + 3.  Any order
         // of the dims will do as long as the keys' follows it; this one gives a lane whole words of a key.
-        uint32_t qa[8][4];
+        uint32_t qa[8][4];  // up to 8 rows: B, two registers
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint4 lo = *reinterpret_cast<const uint4*>(qh + r * kPD + 32 * j + 8 * i);
-            const uint4 hi = *reinterpret_cast<const uint4*>(qh + (r + 8) * kPD + 32 * j + 8 * i);
             qa[2 * i][0] = lo.x, qa[2 * i][2] = lo.y, qa[2 * i + 1][0] = lo.z, qa[2 * i + 1][2] = lo.w;
+            if (kFew) continue;
+            const uint4 hi = *reinterpret_cast<const uint4*>(qh + (r + 8) * kPD + 32 * j + 8 * i);
             qa[2 * i][1] = hi.x, qa[2 * i][3] = hi.y, qa[2 * i + 1][1] = hi.z, qa[2 * i + 1][3] = hi.w;
         }
-        const float f0 = qf[r], f1 = qf[r + 8];
+        // the lane's two rows: of scores and sums they are r and r + 8, or 2 j and 2 j + 1
+        const float f0 = qf[kFew ? 2 * j : r], f1 = qf[kFew ? 2 * j + 1 : r + 8];
 
-        float o[16][4];
+        constexpr int kTiles = kFew ? 8 : 16;
+        float o[kTiles][4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        // running maxima (log2) of rows r and r + 8, their negatives (0 while there is none), and the rows' sums
+        for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        // the two rows' running maxima (log2), their negatives (0 while there is none), and sums
         float m0 = -INFINITY, m1 = -INFINITY, b0 = 0.f, b1 = 0.f, l[4] = {0.f, 0.f, 0.f, 0.f};
         // scale places of the lane: keys' dims 32 j and 32 j + 16, values' dims 16 r
         const int gk0 = (32 * j) >> a.c.lgroup, gk1 = (32 * j + 16) >> a.c.lgroup, gv = (16 * r) >> a.c.lgroup;
@@ -201,51 +225,77 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
             __syncwarp();
             if ((okbits >> (kDepth - 1)) & 1) {
                 const int left = len - step * kStep;  // tokens of the step
-                // ---- products of the rows with tokens r (tile 0) and r + 8 (tile 1)
+                // ---- products of the rows with tokens r (e = 0) and r + 8 (e = 1).  Up to 8 rows: the keys are the A operand, so
+                // that one product takes the place of two.
                 float sc[2][4];
 #pragma unroll
+                for (int e = 0; e < 2; ++e) sc[e][0] = sc[e][1] = sc[e][2] = sc[e][3] = 0.f;
+                uint32_t ks2[2][2];
+#pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    sc[e][0] = sc[e][1] = sc[e][2] = sc[e][3] = 0.f;
-                    const uint32_t s_lo = lds16(st + ks0 + 16 * e * ng) * 0x10001u, s_hi = lds16(st + ks1 + 16 * e * ng) * 0x10001u;
+                    ks2[e][0] = lds16(st + ks0 + 16 * e * ng) * 0x10001u;
+                    ks2[e][1] = lds16(st + ks1 + 16 * e * ng) * 0x10001u;
+                }
+                auto key = [&](int e, int half, uint32_t (&k)[4][2]) {  // 16 dims of a token: four steps' operands
+                    const uint32_t s2 = ks2[e][half];
+                    if constexpr (KL == 256) {
+                        const uint4 w4 = lds128(st + k_at + 8 * S::kKRow * e + (kx ^ (16 * half)));
+                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t s2 = half ? s_hi : s_lo;
-                        if constexpr (KL == 256) {
-                            const uint4 w4 = lds128(st + k_at + 8 * S::kKRow * e + (kx ^ (16 * half)));
-                            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                        for (int i = 0; i < 4; ++i) {
+                            k[i][0] = mul2(prmt(table<0>(w[i], lane_k), table<1>(w[i], lane_k), 0x5410), s2);
+                            k[i][1] = mul2(prmt(table<2>(w[i], lane_k), table<3>(w[i], lane_k), 0x5410), s2);
+                        }
+                    } else {
+                        const uint2 w2 = lds64(st + k_at + 8 * S::kKRow * e + 8 * half);
+                        const uint32_t w[2] = {w2.x, w2.y};
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma_f16(sc[e], qa[4 * half + i],
-                                        mul2(prmt(table<0>(w[i], lane_k), table<1>(w[i], lane_k), 0x5410), s2),
-                                        mul2(prmt(table<2>(w[i], lane_k), table<3>(w[i], lane_k), 0x5410), s2));
-                        } else {
-                            const uint2 w2 = lds64(st + k_at + 8 * S::kKRow * e + 8 * half);
-                            const uint32_t w[2] = {w2.x, w2.y};
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                mma_f16(sc[e], qa[4 * half + 2 * i], mul2(table<0>(w[i], lane_k), s2),
-                                        mul2(table<1>(w[i], lane_k), s2));
-                                mma_f16(sc[e], qa[4 * half + 2 * i + 1], mul2(table<2>(w[i], lane_k), s2),
-                                        mul2(table<3>(w[i], lane_k), s2));
-                            }
+                        for (int i = 0; i < 2; ++i) {
+                            k[2 * i][0] = mul2(table<0>(w[i], lane_k), s2);
+                            k[2 * i][1] = mul2(table<1>(w[i], lane_k), s2);
+                            k[2 * i + 1][0] = mul2(table<2>(w[i], lane_k), s2);
+                            k[2 * i + 1][1] = mul2(table<3>(w[i], lane_k), s2);
                         }
                     }
-                }
-                if (left < kStep) {  // tokens past the end are left out; columns 8 e + 2 j + {0, 1}
+                };
+                if constexpr (kFew) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t k[2][4][2];
+                        key(0, half, k[0]);
+                        key(1, half, k[1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t ka[4] = {k[0][i][0], k[1][i][0], k[0][i][1], k[1][i][1]};
+                            mma_f16(sc[0], ka, qa[4 * half + i][0], qa[4 * half + i][2]);
+                        }
+                    }
+                } else {
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t k[4][2];
+                            key(e, half, k);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mma_f16(sc[e], qa[4 * half + i], k[i][0], k[i][1]);
+                        }
+                }
+                if (left < kStep) {  // tokens past the end are left out: rows r and r + 8, or columns 8 e + 2 j + {0, 1}
+#pragma unroll
+                    for (int e = 0; e < (kFew ? 1 : 2); ++e)
+#pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            if (8 * e + 2 * j + (c & 1) >= left) sc[e][c] = -INFINITY;
+                            if ((kFew ? r + 8 * (c >> 1) : 8 * e + 2 * j + (c & 1)) >= left) sc[e][c] = -INFINITY;
                 }
                 // log2 scores are products times f0 and f1, which are not negative
-                const float x0 = f0 * fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-                const float x1 = f1 * fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+                const float x0 = f0 * (kFew ? fmaxf(sc[0][0], sc[0][2]) : fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])));
+                const float x1 = f1 * (kFew ? fmaxf(sc[0][1], sc[0][3]) : fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])));
                 // the maximum follows only when a score passes it by kSlack: weights stay below 2^8, well inside fp16
                 if (__any_sync(kFull, x0 > m0 + kSlack || x1 > m1 + kSlack)) {
                     float n0 = x0, n1 = x1;
 #pragma unroll
-                    for (int m = 1; m < 4; m <<= 1) {
+                    for (int m = kFew ? 4 : 1; m < (kFew ? 32 : 4); m <<= 1) {
                         n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, m));
                         n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, m));
                     }
@@ -257,22 +307,41 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
                     b0 = m0 == -INFINITY ? 0.f : -m0;
                     b1 = m1 == -INFINITY ? 0.f : -m1;
                     l[0] *= g0;
-                    l[2] *= g1;
+                    l[kFew ? 1 : 2] *= g1;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < kTiles; ++i) {
                         o[i][0] *= g0;
-                        o[i][1] *= g0;
-                        o[i][2] *= g1;
+                        o[i][1] *= kFew ? g1 : g0;
+                        o[i][2] *= kFew ? g0 : g1;
                         o[i][3] *= g1;
                     }
                 }
                 uint32_t pa[4];  // weights as the A operand: the score fragment is already in its order
+                uint32_t pb[2];  // or as B, which takes a transpose
+                if constexpr (kFew) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    pa[2 * e] = pack_f16(fast_exp2(fmaf(sc[e][0], f0, b0)), fast_exp2(fmaf(sc[e][1], f0, b0)));
-                    pa[2 * e + 1] = pack_f16(fast_exp2(fmaf(sc[e][2], f1, b1)), fast_exp2(fmaf(sc[e][3], f1, b1)));
+                    for (int e = 0; e < 2; ++e)
+                        pb[e] = transpose8(pack_f16(fast_exp2(fmaf(sc[0][2 * e], f0, b0)), fast_exp2(fmaf(sc[0][2 * e + 1], f1, b1))));
+                    const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+                    mma_f16(l, ones, pb[0], pb[1]);  // their sums: a product with ones
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        pa[2 * e] = pack_f16(fast_exp2(fmaf(sc[e][0], f0, b0)), fast_exp2(fmaf(sc[e][1], f0, b0)));
+                        pa[2 * e + 1] = pack_f16(fast_exp2(fmaf(sc[e][2], f1, b1)), fast_exp2(fmaf(sc[e][3], f1, b1)));
+                    }
+                    mma_f16(l, pa, 0x3c003c00u, 0x3c003c00u);  // their sums: a product with ones
                 }
-                mma_f16(l, pa, 0x3c003c00u, 0x3c003c00u);  // their sums: a product with ones
+                // dims 16 r + i and 16 r + i + 1 of tokens 2 j, 2 j + 1 (lo, hi [0]) and 2 j + 8, 2 j + 9 ([1])
+                auto weigh = [&](int i, const uint32_t (&lo)[2], const uint32_t (&hi)[2]) {
+                    if constexpr (kFew) {
+                        const uint32_t va[4] = {lo[0], hi[0], lo[1], hi[1]};
+                        mma_f16(o[i / 2], va, pb[0], pb[1]);
+                    } else {
+                        mma_f16(o[i], pa, lo[0], lo[1]);
+                        mma_f16(o[i + 1], pa, hi[0], hi[1]);
+                    }
+                };
                 // ---- weighted values: tokens 2 j, 2 j + 1 and 2 j + 8, 2 j + 9, dims 16 r + i in tile i
                 uint32_t s2[2];
 #pragma unroll
@@ -297,7 +366,7 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
                         }
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        uint32_t v[2][8];
+                        uint32_t v[8][2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             uint32_t u[2];
@@ -314,12 +383,12 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
                             for (int y = 0; y < 4; ++y) {
                                 const uint32_t sel = (y & 1 ? od0 : ev0) >> (16 * (y >> 1));
                                 const uint32_t lo = prmt(tl[0], tl[1], sel), hi = prmt(th[0], th[1], sel);
-                                v[e][4 * (y >> 1) + (y & 1)] = mul2(prmt(lo, hi, 0x5140), s2[e]);
-                                v[e][4 * (y >> 1) + (y & 1) + 2] = mul2(prmt(lo, hi, 0x7362), s2[e]);
+                                v[4 * (y >> 1) + (y & 1)][e] = mul2(prmt(lo, hi, 0x5140), s2[e]);
+                                v[4 * (y >> 1) + (y & 1) + 2][e] = mul2(prmt(lo, hi, 0x7362), s2[e]);
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) mma_f16(o[8 * q + i], pa, v[0][i], v[1][i]);
+                        for (int i = 0; i < 8; i += 2) weigh(8 * q + i, v[i], v[i + 1]);
                     }
                 } else {
                     uint32_t w[2][2][2];
@@ -340,8 +409,7 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
                             lo[e] = mul2(prmt(va, vb, 0x5410), s2[e]);
                             hi[e] = mul2(prmt(va, vb, 0x7632), s2[e]);
                         }
-                        mma_f16(o[2 * y], pa, lo[0], lo[1]);
-                        mma_f16(o[2 * y + 1], pa, hi[0], hi[1]);
+                        weigh(2 * y, lo, hi);
                     });
                 }
             }
@@ -352,18 +420,18 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
 
         // ---- join the warps: fragments through shared memory (over the rings)
         const int act = min(kCtxWarps, s1 - s0);
-        auto frag = [&](int w) { return reinterpret_cast<float*>(space + region(w)); };                            // [64][33]
-        auto ml = [&](int w) { return reinterpret_cast<float2*>(space + region(w) + 64 * kFragPad * 4); };  // [16]
+        auto frag = [&](int w) { return reinterpret_cast<float*>(space + region(w)); };                              // [kSums][33]
+        auto ml = [&](int w) { return reinterpret_cast<float2*>(space + region(w) + Ctx<ROWS>::kSums * kFragPad * 4); };  // [ROWS]
         __syncwarp();
         if (warp < act) {
             float* f = frag(warp) + lane;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < kTiles; ++i)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) f[(4 * i + c) * kFragPad] = o[i][c];
-            if (j == 0) {
-                ml(warp)[r] = make_float2(m0, l[0]);
-                ml(warp)[r + 8] = make_float2(m1, l[2]);
+            if ((kFew ? r : j) == 0) {
+                ml(warp)[kFew ? 2 * j : r] = make_float2(m0, l[0]);
+                ml(warp)[kFew ? 2 * j + 1 : r + 8] = make_float2(m1, l[kFew ? 1 : 2]);
             }
         }
         __syncthreads();
@@ -371,7 +439,8 @@ __global__ void __launch_bounds__(32 * kCtxWarps, 1) kv_tree_context_kernel(Tree
         const float vscale = exp2f((float)ev);
         for (int e = threadIdx.x; e < rows * kPD; e += 32 * kCtxWarps) {
             const int row = e >> 7, d = e & 127, i = d & 15, nn = d >> 4;
-            const int at = (4 * i + 2 * (row >> 3) + (nn & 1)) * kFragPad + (row & 7) * 4 + (nn >> 1);
+            const int at = kFew ? (4 * (i >> 1) + 2 * (i & 1) + (row & 1)) * kFragPad + nn * 4 + (row >> 1)
+                                : (4 * i + 2 * (row >> 3) + (nn & 1)) * kFragPad + (row & 7) * 4 + (nn >> 1);
             float M = -INFINITY;
             for (int w = 0; w < act; ++w) M = fmaxf(M, ml(w)[row].x);
             float L = 0.f, acc = 0.f;
@@ -739,7 +808,7 @@ Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, i
     p.stoks = p.trows == kStep ? kStep : 32;
     p.least = p.trows == kStep ? 4 : 2;
     // measured, beginning another tile within a run: about 4 us (16 rows, 128 rows) and 10 us (256 rows)
-    p.pad = p.trows == kStep ? 2 * kCtxWarps : (p.trows == 128 ? 8 : 14);
+    p.pad = p.trows == kStep ? 24 : (p.trows == 128 ? 8 : 14);
     p.tiles = (rows + kStep - 1) / kStep;
     const int64_t units = (rows + p.trows - 1) / p.trows * Hkv * B, steps = max_len ? (max_len + p.stoks - 1) / p.stoks + p.pad : 0;
     p.steps = units * steps;
@@ -754,21 +823,28 @@ size_t plan_bytes(const Plan& p) {
     return 32 + (size_t)p.slots * p.trows * (kPD * sizeof(float) + sizeof(float2)) + (size_t)p.turned * (kPD * 2 + 4);
 }
 
-template <int KL, int VL>
+template <int KL, int VL, int ROWS>
 tq_status launch_context(const TreeArgs& a, cudaStream_t st) {
-    constexpr size_t smem = context_smem_end<KL, VL>() - 1024;  // from the start of the dynamic part, wherever it is
+    constexpr size_t smem = context_smem_end<KL, VL, ROWS>() - 1024;  // from the start of the dynamic part, wherever it is
     static const bool fits = [] {  // the system's part and the static variables end below kSmemStart
         int dev = 0, reserved = 0;
         cudaFuncAttributes at{};
         return cudaGetDevice(&dev) == cudaSuccess &&
                cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) == cudaSuccess &&
-               cudaFuncGetAttributes(&at, (const void*)kv_tree_context_kernel<KL, VL>) == cudaSuccess &&
+               cudaFuncGetAttributes(&at, (const void*)kv_tree_context_kernel<KL, VL, ROWS>) == cudaSuccess &&
                reserved >= 1024 && reserved + at.sharedSizeBytes <= kSmemStart;
     }();
     if (!fits) return TQ_ERR_UNSUPPORTED;
-    if (ensure_smem((const void*)kv_tree_context_kernel<KL, VL>, smem) != cudaSuccess) return TQ_ERR_CUDA;
-    kv_tree_context_kernel<KL, VL><<<a.ctas, 32 * kCtxWarps, smem, st>>>(a);
+    if (ensure_smem((const void*)kv_tree_context_kernel<KL, VL, ROWS>, smem) != cudaSuccess) return TQ_ERR_CUDA;
+    kv_tree_context_kernel<KL, VL, ROWS><<<a.ctas, 32 * Ctx<ROWS>::kWarps, smem, st>>>(a);
     return launch_status();
+}
+
+template <int ROWS>
+tq_status launch_books(const tq_kv_pages_t* cache, const TreeArgs& a, cudaStream_t st) {
+    if (cache->kcb.levels == 256)
+        return cache->vcb.levels == 8 ? launch_context<256, 8, ROWS>(a, st) : launch_context<256, 16, ROWS>(a, st);
+    return cache->vcb.levels == 8 ? launch_context<16, 8, ROWS>(a, st) : launch_context<16, 16, ROWS>(a, st);
 }
 
 constexpr int kMaxSms = 256;  // bound on the SMs that the workspace is sized for
@@ -850,8 +926,7 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
     if (p.ctas) {
         tq_status s;
         if (p.trows != kStep) s = launch_wide(cache->kcb.levels, cache->vcb.levels, a, st);
-        else if (cache->kcb.levels == 256) s = cache->vcb.levels == 8 ? launch_context<256, 8>(a, st) : launch_context<256, 16>(a, st);
-        else s = cache->vcb.levels == 8 ? launch_context<16, 8>(a, st) : launch_context<16, 16>(a, st);
+        else s = n * a.ratio <= 8 ? launch_books<8>(cache, a, st) : launch_books<16>(cache, a, st);
         if (s != TQ_OK) return s;
         return launch_pdl(kv_tree_finish_kernel, dim3((unsigned)(p.tiles * cache->Hkv * B * parts)), dim3(32 * kFinWarps), 0, st, a, (int)p.tiles, parts);
     }

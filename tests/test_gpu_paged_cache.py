@@ -483,7 +483,7 @@ def test_tree_over_the_context_alone(lib):
     _check(got, _attend(_f64(q), ctx, None, None, None, None))
     assert bool((got[1] == 0).all())
     rot = lib.Rotation(D, D, seed=77)
-    kv = lib.KVCache(3072 // 3 * 2, 8, D, 32, lib.Codebook(256), lib.Codebook(8), rot)
+    kv = lib.KVCache(2048, 8, D, 32, lib.Codebook(256), lib.Codebook(8), rot)
     lib.kv_quantize(kv, *(_dev(_heavy(g, 1999, 8), torch.bfloat16) for _ in range(2)))
     q1 = _dev(g.normal(size=(1, 1, 32, D)), torch.bfloat16)
     pages = lib.PagedKVCache.of(kv)
