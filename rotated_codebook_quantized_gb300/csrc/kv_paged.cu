@@ -574,17 +574,16 @@ TQ_DEVFN void piece8(const uint32_t* words, int piece, uint32_t (&w)[2]) {
     }
 }
 
-// REPS copies of the 8-bit keys' book, interleaved: 32 give every lane a bank of its own (one wavefront a read, against about
-// 3.4), 1 costs a small call less to fill.  Bound by the shared-memory pipe (table reads, shuffles) and by latency.
-template <int KL, int VL, int REPS>
+// The key book in shared memory once (a copy for each lane, without bank conflicts, took as long: 118 us both).  Bound by
+// instruction issue and latency at 16 warps an SM: 65536 tokens of 8 heads 118 us, 3.1 TB/s, 47 % of the copy rate.
+template <int KL, int VL>
 __global__ void __launch_bounds__(32 * kWarps, 2) kv_fetch_kernel(FetchArgs a) {
-    __shared__ float kl[KL * REPS], vl[VL];
-    for (int i = threadIdx.x; i < KL * REPS; i += blockDim.x) kl[i] = a.c.kcent[i / REPS];
+    __shared__ float kl[KL], vl[VL];
+    for (int i = threadIdx.x; i < KL; i += blockDim.x) kl[i] = a.c.kcent[i];
     for (int i = threadIdx.x; i < VL; i += blockDim.x) vl[i] = a.c.vcent[i];
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, vec = lane >> 2, l = lane & 3;
     const int lg = a.c.lgroup;
-    const float* const own = kl + lane % REPS;
     const uint32_t units = (uint32_t)((a.T + kVecs - 1) / kVecs) * a.c.Hkv, stride = gridDim.x * kWarps;  // 32-bit numbers
     const int64_t all = a.c.pages << a.c.lpage;
     uint32_t unit = blockIdx.x * kWarps + warp;
@@ -624,7 +623,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv_fetch_kernel(FetchArgs a) {
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t p = KL == 256 ? (ck[i >> 2] >> (8 * (i & 3))) & 255u : (ck[0] >> (4 * i)) & 15u;
                     const uint32_t q = (cv[0] >> (KvBook<VL>::kBits * i)) & (VL - 1);
-                    x[8 * m + i] = mul2(pk(own[(p % KL) * REPS], vl[q]), s);
+                    x[8 * m + i] = mul2(pk(kl[p % KL], vl[q]), s);
                 }
             }
         } else {
@@ -714,9 +713,9 @@ extern "C" tq_status tq_kv_append(const tq_kv_pages_t* cache, const void* k, int
     a.dt = dt;
     a.err = err;
     cudaStream_t st = as_stream(stream);
-    // Up to 8192 vectors a warp to each (1 token of 8 heads: 5 us, against 18 for the persistent kernel and its tables);
-    // past that the persistent kernel (524288 vectors: 0.48 ns each, against 1.7).
-    if (T * cache->Hkv <= 8192) {
+    // Up to 4096 (token, head) pairs a warp to each vector (8 pairs: 3.8 us, against 9.2 for the persistent kernel and its
+    // tables; 4096: 7.7 and 8.5); past that the persistent kernel (8192: 8.6 us against 13.0; 524288: 150 against 647).
+    if (T * cache->Hkv <= 4096) {
         const unsigned blocks = (unsigned)((T * cache->Hkv * 2 + kWarps - 1) / kWarps);
         return by_books(cache, [&](auto kl, auto vl) {
             kv_append_small_kernel<decltype(kl)::value, decltype(vl)::value><<<blocks, 32 * kWarps, 0, st>>>(a);
@@ -765,11 +764,7 @@ extern "C" tq_status tq_kv_fetch(const tq_kv_pages_t* cache, const int32_t* slot
     cudaStream_t st = as_stream(stream);
     return by_books(cache, [&](auto kl, auto vl) {
         constexpr int KL = decltype(kl)::value, VL = decltype(vl)::value;
-        // 32 copies of a 256-entry book where a warp has eight units or more to read through them
-        if (KL == 256 && units >= (int64_t)sm_count() * 2 * kWarps * 8)
-            kv_fetch_kernel<KL, VL, KL == 256 ? 32 : 1><<<blocks, 32 * kWarps, 0, st>>>(a);
-        else
-            kv_fetch_kernel<KL, VL, 1><<<blocks, 32 * kWarps, 0, st>>>(a);
+        kv_fetch_kernel<KL, VL><<<blocks, 32 * kWarps, 0, st>>>(a);
         return launch_status();
     });
 }
