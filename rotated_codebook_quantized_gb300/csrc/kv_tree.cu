@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(32 * Ctx<ROWS>::kWarps, 1) kv_tree_context_ker
             const float d = a.scale2 < 0.f ? -exp2f((float)-e) : exp2f((float)-e);  // a factor below is not negative
             *reinterpret_cast<uint2*>(qh + row * kPD + lane * 4) =
                 make_uint2(pack_f16(v[0] * d, v[1] * d), pack_f16(v[2] * d, v[3] * d));
-            if (lane == 0) qf[row] = exp2f((float)(e + ek)) * (kInvSqrtD * fabsf(a.scale2));
+            if (lane == 0) qf[row] = score_factor(e + ek, a.scale2);
         }
         __syncthreads();
         // Operand of product step s: the lane's row r (A: and r + 8), dims 32 j + 4 s .. + 3.  Any order

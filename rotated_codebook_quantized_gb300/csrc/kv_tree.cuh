@@ -281,5 +281,9 @@ TQ_DEVFN int exponent_above(float x) {
     return e == 0 || e == 255 ? 0 : e - 126;
 }
 
+// From a row's products, of operands over 2^e together, to log2 scores.  Never 0, so that a masked score, -infinity times it, is
+// no NaN; products are below 2^24, so a score that the bound changes stays below 2^-98.
+TQ_DEVFN float score_factor(int e, float scale2) { return fmaxf(exp2f((float)e) * (kInvSqrtD * fabsf(scale2)), 1e-37f); }
+
 }  // namespace tree
 }  // namespace tq

@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                     }
                     tc_wait_st();
                 }
-                f = exp2f((float)((in ? a.power[unit * kRows + row] : 0) + ek)) * (kInvSqrtD * fabsf(a.scale2));
+                f = score_factor((in ? a.power[unit * kRows + row] : 0) + ek, a.scale2);
             }
             if (writer) {
                 tc_fence_before();

@@ -126,6 +126,23 @@ def test_rope_inverse_is_the_transpose(lib, layout):
     assert float((lib.rope(fx, pos, r, inverse=True) - x).abs().max()) < 8e-7 * 8
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rope_gradient_against_differences(lib, layout):
+    """L(x) = <rope(x), y> is linear: its differences in each of 24 directions are <direction, inverse(y)>, whatever the step."""
+    g = _rng(21)
+    T, H = 5, 3
+    x, y = (_dev(g.normal(size=(T, H, D)), torch.float32) for _ in range(2))
+    pos = _dev(g.integers(0, 100000, T), torch.int32)
+    r = lib.Rope(D, 64, layout=layout, scaling={"kind": "parts", "factor": 16.0, "original": 8192})
+    grad = lib.rope(y, pos, r, inverse=True)
+    for _ in range(24):
+        d = _dev(g.normal(size=(T, H, D)), torch.float32)
+        up, down = (float((lib.rope(z, pos, r).double() * y.double()).sum()) for z in (x + d, x - d))
+        # six fp32 roundings of 2^-24 a result, of sums of |x| + |d| over the norm of y; x + d itself another two
+        assert abs((up - down) / 2 - float((d.double() * grad.double()).sum())) <= 8 * 2 ** -24 * r.factor * float(
+            (x.double().abs() + d.double().abs()).norm() * y.double().norm())
+
+
 @pytest.mark.parametrize("scaling", [None, {"kind": "linear", "factor": 4.0}, {"kind": "base", "factor": 8.0},
                                      {"kind": "parts", "factor": 16.0, "original": 8192},
                                      {"kind": "parts", "factor": 4.0, "original": 4096, "slow_turns": 2.0, "fast_turns": 20.0}])
@@ -563,6 +580,40 @@ def test_tree_flat_and_sharp_scores(lib, factor):
     else:
         # a score of deviation 150 is off by about 2^-11 sqrt(2/3) 150 = 0.06: weights of near ties move by that much
         assert helpers.rel_l2(_f64(got), ref) < 0.1
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05])
+@pytest.mark.parametrize("n,Hq,H", [(1, 4, 1), (2, 4, 1), (3, 4, 1), (33, 4, 1), (70, 4, 1)])
+def test_tree_scales_of_zero_and_below(lib, scale, n, Hq, H):
+    """All weights equal, and the order of the scores turned round; also past the end of a step and where nothing is cached."""
+    lens = [75, 0, 16]
+    g, c, table, dlens, ctx, q, kn, vn = _setup(lib, (22, n), lens, n, Hq, H, 32)
+    see = _tree(g, 3, n)
+    got = lib.kv_attend_tree(c, q, table, dlens, k_new=kn, v_new=vn, mask=_dev(_pack_mask(see)), scale=scale)
+    _check(got, _attend(_f64(q), ctx, _f64(kn), _f64(vn), see, None, scale))
+
+
+@pytest.mark.parametrize("n,Hq,H", [(1, 4, 1), (3, 4, 1), (33, 4, 1), (70, 4, 1)])
+def test_tree_scores_that_vanish(lib, n, Hq, H):
+    """The smallest queries times a small scale: all weights equal, and what lies past a context's end stays out."""
+    g, c, table, dlens, ctx, q, kn, vn = _setup(lib, (24, n), [75], n, Hq, H, 32)
+    see = _tree(g, 1, n)
+    q = (q.float() * 2.0 ** -125).bfloat16()
+    got = lib.kv_attend_tree(c, q, table, dlens, k_new=kn, v_new=vn, mask=_dev(_pack_mask(see)), scale=1e-9)
+    _check(got, _attend(_f64(q), ctx, _f64(kn), _f64(vn), see, None, 1e-9))
+
+
+@pytest.mark.parametrize("n,Hq,H", [(1, 8, 1), (2, 4, 1), (1, 16, 1), (5, 4, 1), (20, 8, 1)])
+def test_tree_a_bad_query_stays_in_its_row_of_each_form(lib, n, Hq, H):
+    g, c, table, dlens, ctx, q, kn, vn = _setup(lib, (23, n, Hq), [333, 40], n, Hq, H, 32)
+    clean = lib.kv_attend_tree(c, q, table, dlens, k_new=kn, v_new=vn)
+    for bad in (float("nan"), float("inf")):
+        b = q.clone()
+        b[0, n - 1, 3, 5] = bad
+        got = lib.kv_attend_tree(c, b, table, dlens, k_new=kn, v_new=vn)
+        assert bool(torch.isnan(got[0, n - 1, 3]).all())
+        got[0, n - 1, 3] = clean[0, n - 1, 3]
+        assert torch.equal(got, clean)
 
 
 @pytest.mark.parametrize("size", [3e-4, 3e3])
