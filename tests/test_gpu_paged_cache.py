@@ -294,6 +294,85 @@ def test_append_turns_keys_on_the_way(lib, layout, rotary, dtype):
     assert torch.equal(_rows(plain.vcodes, slots, page), _rows(c.vcodes, slots, page))  # values do not turn
 
 
+def _compare_written(c, x, codes, scales, levels, thr, slots, group, tie=None):
+    """Codes and scales of tokens x (64 bits) against the definition; tie: the bar on a mismatched u, if not the helpers' own."""
+    T, H = x.shape[:2]
+    y = x.reshape(T * H, D) @ o.rotation_matrix(_signs(), D).T
+    u, rms = helpers.oracle_u(y, group)
+    oc, os16 = o.encode_rotated(y, group, thr)
+    words = helpers.u32(_rows(codes, slots, c.page)).reshape(T * H, -1)
+    if tie is None:
+        helpers.compare_codes(words, o.pack(oc, levels), levels, D, u, thr)
+        helpers.compare_scales(helpers.f16_from_bits(_rows(scales, slots, c.page)).reshape(T * H, -1), os16, rms)
+        return
+    gc = o.unpack(words, levels, D)
+    for i, j in np.argwhere(gc != oc):
+        assert abs(int(gc[i, j]) - int(oc[i, j])) == 1
+        assert abs(u[i, j] - thr[min(gc[i, j], oc[i, j])]) <= tie * max(1.0, abs(u[i, j]))
+
+
+# more (token, head) pairs than the calls above, which another kernel takes: whole tables, eight tokens to a warp
+@pytest.mark.parametrize("kl,vl", BOOKS)
+@pytest.mark.parametrize("group", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("close", [False, True])
+def test_append_of_many_tokens(lib, kl, vl, group, dtype, close):
+    """close: books whose thresholds lie a quarter as far apart, several to a bin of the lookup."""
+    if close and (group, dtype) not in ((32, "bfloat16"), (128, "float32")):
+        pytest.skip("the search does not depend on them")
+    g = _rng(25, group, kl, vl)
+    T, H, page = 605, 7, 64
+    pages = -(-T // page) + 2
+    c = _cache(lib, pages, page, H, group, kl, vl)
+    thrs = []
+    for name, levels in (("kcb", kl), ("vcb", vl)):
+        cent, thr = o.lloyd_max_gaussian(levels)
+        if close:
+            cent, thr = np.float32(cent * 0.25).astype(np.float64), np.float32(thr * 0.25).astype(np.float64)
+            for t, v in ((getattr(c, name).centroids, cent), (getattr(c, name).thresholds, thr)):
+                t.copy_(_dev(v, torch.float32))
+        thrs.append(thr)
+    slots, _ = _slots(g, T, page, pages)
+    slots[[5, 300]] = -1  # skipped
+    kv = _dev(np.concatenate([_heavy(g, T, H), _heavy(g, T, H)], 1), torch.float32).to(getattr(torch, dtype))
+    kv[T // 2, 0] = 0  # an all-zero vector
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lib.kv_append(c, kv[:, :H], kv[:, H:], _dev(slots), err=err)
+    assert lib.check_error(err) == 0
+    kept = slots >= 0
+    for x, codes, scales, levels, thr in ((kv[:, :H], c.kcodes, c.kscales, kl, thrs[0]), (kv[:, H:], c.vcodes, c.vscales, vl, thrs[1])):
+        _compare_written(c, _f64(x)[kept], codes, scales, levels, thr, slots[kept], group)
+    untouched = np.setdiff1d(np.arange(pages * page), slots)
+    assert bool((_rows(c.kcodes, untouched, page) == -1).all()) and bool((_rows(c.vscales, untouched, page) == 0x7C00).all())
+    slots[7] = pages * page  # outside the pool
+    lib.kv_append(c, kv[:, :H], kv[:, H:], _dev(slots), err=err)
+    assert lib.check_error(err) == lib.TQ_DEVERR_BAD_PAGE
+    assert bool((_rows(c.kcodes, untouched, page) == -1).all())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("rotary", [32, 64, 128])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T,H", [(841, 5), (9800, 5)])  # one head to a warp, and four (and the fifth)
+def test_append_turns_keys_of_many_tokens(lib, layout, rotary, dtype, T, H):
+    g = _rng(26, rotary, T)
+    page = 64
+    pages = -(-T // page)
+    c, plain = (_cache(lib, pages, page, H, 32, 256, 8) for _ in range(2))
+    slots, _ = _slots(g, T, page, pages)
+    k, v = (_dev(_heavy(g, T, H), torch.float32).to(getattr(torch, dtype)) for _ in range(2))
+    pos = g.integers(0, 131072, T)
+    scaling = {"kind": "parts", "factor": 4.0, "original": 4096}
+    r = lib.Rope(D, rotary, layout=layout, scaling=scaling)
+    lib.kv_append(c, k, v, _dev(slots), rope=r, positions=_dev(pos, torch.int32))
+    lib.kv_append(plain, k, v, _dev(slots))
+    assert torch.equal(_rows(plain.vcodes, slots, page), _rows(c.vcodes, slots, page))  # values do not turn
+    at = g.permutation(T)[:800]  # of which the definition is computed
+    w, _ = _freq(rotary, scaling=scaling)
+    y = _turn(_f64(k)[at], pos[at], w, rotary, layout, r.factor)
+    _compare_written(c, y, c.kcodes, c.kscales, 256, o.lloyd_max_gaussian(256)[1], slots[at], 32, tie=4e-6)
+
+
 def test_append_equals_the_contiguous_cache(lib):
     """The same tokens through kv_quantize and through pages over the same storage, but for counted ties."""
     g = _rng(7)
