@@ -40,9 +40,10 @@ constexpr uint32_t kHalf = kTile / 2;       // of 64 of their dims (one 128-byte
 constexpr uint32_t kTable = 65536, kSteps = 131072, kEnd = kSteps + kStages * 2 * kTile;
 constexpr uint32_t kStart = 1024 + 512;  // the system's first KB, then the static variables
 constexpr uint32_t kOdd = kStart, kRings = kOdd + 2 * 128 * 4;
-// Decoder warps.  A warp's units lie kDec / kUnits steps apart, a divisor of kStages: it comes to the same places of decoded
-// steps in every round, and so knows a place's phase (a place's barrier tells only odd from even phases; a warp that left a
-// round of a place out could take a phase two back for the one it waits for, as the two streams free places out of order).
+// Decoder warps.  Units go to them in turn over all of a CTA's steps, whatever stretches these belong to: a warp's units lie
+// kDec / kUnits steps apart, a divisor of kStages, so it comes to the same places of decoded steps in every round and knows a
+// place's phase.  (A place's barrier tells only odd from even phases: a warp that left a round of a place out could take a phase
+// two back for the one it waits for, as other warps run ahead and the two streams free places out of order.)
 constexpr int kDec = 12;
 static_assert(kDec % kUnits == 0 && kStages % (kDec / kUnits) == 0, "every place in every round");
 static_assert(kEnd <= 232448, "fits an SM");
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             ++seg;
         }
     } else {
-        // ------------------------------------------------------------ decoders: warp d takes units d, d + D, ... of a stretch
+        // ------------------------------------------------------------ decoders: warp d takes units d, d + D, ... of the CTA's steps
         const int d = warp - kSoft, ng = kPD >> a.c.lgroup;
         uint32_t tl[2] = {0, 0}, th[2] = {0, 0};  // low and high bytes of an 8-level value book
         if (VL == 8) {
@@ -481,7 +482,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             const int32_t* tab = a.table + (int64_t)x.b * a.table_stride;
         const int u0 = s0 * kUnits, u1 = min(s1 * kUnits, (len + kUnit - 1) / kUnit);  // units that hold tokens
         auto page_of = [&](int u) { return u < u1 ? __ldg(tab + (u >> (a.c.lpage - 3))) : 0; };
-        int ahead = u0 + d, page_next = 0;
+        // its first unit here: the first step of the CTA's count that is this warp's
+        const int mine = (d + kDec - kUnits * (int)(g % (kDec / kUnits))) % kDec;
+        int ahead = u0 + mine, page_next = 0;
         uint32_t fill = ring, counts = 0;  // four bits a unit: its valid tokens
         auto issue = [&]() {
             const int page = page_next, u = ahead;
@@ -514,8 +517,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             const uint32_t to = kSteps + (c >> 3) * kHalf + hi * 128 + ((c & 7) ^ hi) * 16;
             uint32_t at = ring;
             // the unit's step, as a place among the decoded ones and the phase of its barriers
-            uint32_t stage = (g + d / kUnits) % kStages, phase = (g + d / kUnits) / kStages & 1;
-            for (int u = u0 + d; u < s1 * kUnits; u += D) {
+            uint32_t stage = (g + mine / kUnits) % kStages, phase = (g + mine / kUnits) / kStages & 1;
+            for (int u = u0 + mine; u < s1 * kUnits; u += D) {
                 issue();
                 asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
                 __syncwarp();
