@@ -455,6 +455,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
             g = ge;
             ++seg;
         }
+        // A CTA without work waits too: this grid must not end before the turn, or what comes after the call could meet it still
+        // reading the queries and writing the workspace.
+        if (seg == 0) pdl_wait();
     } else {
         // ------------------------------------------------------------ decoders: warp d takes units d, d + D, ... of the CTA's steps
         const int d = warp - kSoft, ng = kPD >> a.c.lgroup;

@@ -88,3 +88,24 @@ def test_hundreds_of_ragged_contexts(lib, pool, n):
                              mask=base._dev(base._pack_mask(see)), err=err)
     assert lib.check_error(err) == 0
     base._check(got, _definition(pool, lens, table, see, q, kn, vn))
+
+
+@pytest.mark.parametrize("n", [8, 64])
+def test_nothing_of_a_call_is_left_running(lib, n):
+    """No sequence holds a token: the workspace is the caller's again when the call's last launch is done."""
+    g = base._rng(103, n)
+    B, Hq = 512 // n, 4 * H
+    c = base._cache(lib, 4, PAGE, H, 32, 256, 8)
+    table, lens = torch.zeros((B, 4), dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    q, kn, vn = (base._dev(g.normal(size=(B, n, h, D)), torch.bfloat16) for h in (Hq, H, H))
+    ws = torch.empty(c.tree_bytes(B, n, Hq, 256), dtype=torch.uint8, device="cuda")
+    ref = lib.kv_attend_tree(c, q, table, lens, k_new=kn, v_new=vn)
+    base._check(ref, base._attend(base._f64(q), [(np.zeros((0, H, D)),) * 2] * B, base._f64(kn), base._f64(vn),
+                                  np.broadcast_to(np.tril(np.ones((n, n), bool)), (B, n, n)), None))
+    for _ in range(20):
+        got = lib.kv_attend_tree(c, q, table, lens, ws=ws)
+        ws.fill_(0x5A)
+        torch.cuda.synchronize()
+        assert bool((ws == 0x5A).all())
+        assert not bool(got.any())
+        assert torch.equal(ref, lib.kv_attend_tree(c, q, table, lens, k_new=kn, v_new=vn, ws=ws))
