@@ -616,14 +616,16 @@ class Rope:
         self.steps = steps.to(device).contiguous()
         self.factor = 1.0 if factor is None else float(factor)
 
-        self._c = tq_rope_t(self.dim, self.rotary, TQ_ROPE_INTERLEAVED if layout == "interleaved" else TQ_ROPE_HALF,
-                            self.factor, self.steps.data_ptr())
-
     def c(self) -> tq_rope_t:
-        return self._c
+        """The descriptor of what the handle holds now."""
+        steps = self.steps
+        if steps.dtype is not _torch().int64 or steps.numel() != self.rotary // 2 or not steps.is_contiguous():
+            raise ValueError(f"steps must be contiguous int64 [{self.rotary // 2}]")
+        return tq_rope_t(self.dim, self.rotary, TQ_ROPE_INTERLEAVED if self.layout == "interleaved" else TQ_ROPE_HALF,
+                         self.factor, steps.data_ptr())
 
     def ref(self):
-        return ctypes.byref(self._c)
+        return ctypes.byref(self.c())
 
 
 def rope_steps(rotary: int, base: float = 10000.0, scaling: dict | None = None):
@@ -643,8 +645,8 @@ def rope_steps(rotary: int, base: float = 10000.0, scaling: dict | None = None):
 
 
 # A decode step's calls last about as long on the GPU as their arguments take to check, so the calls below keep their
-# Python short: plain integers for pointers, one shape and one stride query a tensor, descriptors kept with their handles,
-# torch.empty (1.6 us; new_empty takes 3.6).
+# Python short: plain integers for pointers, one shape and one stride query a tensor, a cache's descriptor kept while all that it
+# is made of stays the same, torch.empty (1.6 us; new_empty takes 3.6).
 
 def _raw_stream(t) -> int:
     """torch's current stream on the tensor's device, as a number."""
@@ -752,30 +754,57 @@ class PagedKVCache:
         return self
 
     def c(self) -> tq_kv_pages_t:
-        c = tq_kv_pages_t(self.kcodes.data_ptr(), self.kscales.data_ptr(), self.vcodes.data_ptr(),
-                          self.vscales.data_ptr(), self.heads, self.dim, self.group, self.page, self.pages,
-                          self.page_stride, self.head_stride, self.kcb.c(), self.vcb.c(), self.rot.c())
-        self._kept = (self.kcodes, self.kscales, self.vcodes, self.vscales, self.kcb, self.vcb, self.rot)
-        self._c, self._sizes = c, {}
-        return c
+        """The descriptor of what the handle holds now."""
+        torch, dev = _torch(), self.kcodes.get_device()
+        kcb, vcb, rot, rows = self.kcb, self.vcb, self.rot, self.pages * self.page * self.heads
+        if (self.pages - 1) * self.page_stride + (self.heads - 1) * self.head_stride + self.page > rows and self.pages > 0:
+            raise ValueError("the cache's strides pass the end of its arrays")
+        for name, width, size in (("kcodes", row_words(kcb.levels, self.dim), 4), ("kscales", self.dim // self.group, 2),
+                                  ("vcodes", row_words(vcb.levels, self.dim), 4), ("vscales", self.dim // self.group, 2)):
+            t = getattr(self, name)
+            if t.numel() != rows * width or t.element_size() != size or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous: {rows} rows of {width} {8 * size}-bit words")
+        for t, least, dtype in ((kcb.centroids, kcb.levels, torch.float32), (kcb.thresholds, kcb.levels - 1, torch.float32),
+                                (vcb.centroids, vcb.levels, torch.float32), (vcb.thresholds, vcb.levels - 1, torch.float32),
+                                (rot.signs, rot.dim, torch.int8)):
+            if t.numel() < least or t.dtype is not dtype or not t.is_contiguous():
+                raise ValueError("a book or the rotation's signs are too short, of another type or not contiguous")
+        for t in (self.kcodes, self.kscales, self.vcodes, self.vscales, kcb.centroids, kcb.thresholds, vcb.centroids, vcb.thresholds,
+                  rot.signs):
+            if not t.is_cuda or t.get_device() != dev:
+                raise ValueError("a cache's arrays, books and rotation must be on one CUDA device")
+        return tq_kv_pages_t(self.kcodes.data_ptr(), self.kscales.data_ptr(), self.vcodes.data_ptr(),
+                             self.vscales.data_ptr(), self.heads, self.dim, self.group, self.page, self.pages,
+                             self.page_stride, self.head_stride, kcb.c(), vcb.c(), rot.c())
+
+    _kept = None
+
+    def _now(self):
+        """(key, descriptor, workspace sizes, tensors): the key is all that the descriptor is made of, compared on every call."""
+        kcb, vcb, rot = self.kcb, self.vcb, self.rot
+        t = (self.kcodes, self.kscales, self.vcodes, self.vscales, kcb.centroids, kcb.thresholds, vcb.centroids, vcb.thresholds,
+             rot.signs)
+        # a tensor may be another object at the same address (a view of other strides) or the same object at another
+        key = (*map(id, t), *[x.data_ptr() for x in t], kcb.levels, vcb.levels, rot.dim, rot.block, self.pages, self.page,
+               self.heads, self.dim, self.group, self.page_stride, self.head_stride)
+        kept = self._kept
+        if kept is None or kept[0] != key:
+            # in one piece: another thread finds the old or the new; the tensors are held, so that no id comes back
+            kept = self._kept = (key, self.c(), {}, t)
+        return kept
 
     def ref(self):
-        """The descriptor, made again when a tensor or book of the cache was replaced."""
-        k = self.__dict__.get("_kept")
-        if k is None or not (k[0] is self.kcodes and k[1] is self.kscales and k[2] is self.vcodes and k[3] is self.vscales
-                             and k[4] is self.kcb and k[5] is self.vcb and k[6] is self.rot):
-            self.c()
-        return ctypes.byref(self._c)
+        return ctypes.byref(self._now()[1])
 
     def tree_bytes(self, B, n, hq, max_len) -> int:
         """Workspace of kv_attend_tree at these sizes."""
+        _, c, sizes, _ = self._now()
         key = (B, n, hq, max_len)
-        ref = self.ref()
-        nb = self._sizes.get(key)
+        nb = sizes.get(key)
         if nb is None:
-            if len(self._sizes) > 4096:
-                self._sizes.clear()
-            nb = self._sizes[key] = int(load().tq_kv_attend_tree_workspace_bytes(ref, B, n, hq, max_len))
+            if len(sizes) > 4096:
+                sizes.clear()
+            nb = sizes[key] = int(load().tq_kv_attend_tree_workspace_bytes(ctypes.byref(c), B, n, hq, max_len))
         return nb
 
 

@@ -875,3 +875,126 @@ def test_example_of_drafted_decoding(lib):
     spec.loader.exec_module(example)
     worst, bits = example.main()
     assert bits == 0 and worst < ATTEND
+
+
+# ---------------------------------------------------------------- handles whose tensors are replaced
+
+def test_rope_handle_follows_its_tensors(lib):
+    """Frequencies and factor assigned later, or moved under the same tensor, are those of the next call."""
+    g = _rng(30)
+    x = _dev(g.normal(size=(9, 3, D)), torch.float32)
+    pos = _dev(g.integers(0, 5000, 9), torch.int32)
+    r, other = lib.Rope(D), lib.Rope(D, base=500000.0, scaling={"kind": "linear", "factor": 4.0})
+    r.steps = other.steps
+    assert torch.equal(lib.rope(x, pos, r), lib.rope(x, pos, other))
+    r.factor = other.factor = 1.5
+    assert torch.equal(lib.rope(x, pos, r), lib.rope(x, pos, lib.Rope(D, steps=other.steps, factor=1.5)))
+    own = lib.Rope(D)
+    r = lib.Rope(D, steps=torch.zeros_like(own.steps))
+    r.steps.set_(own.steps.clone())  # the same tensor object, other memory
+    assert torch.equal(lib.rope(x, pos, r), lib.rope(x, pos, own))
+    r.rotary, r.layout, r.steps = 64, "interleaved", lib.Rope(64).steps
+    assert torch.equal(lib.rope(x, pos, r), lib.rope(x, pos, lib.Rope(D, 64, layout="interleaved")))
+    r.steps = own.steps  # 64 frequencies for 32 pairs
+    with pytest.raises(ValueError):
+        lib.rope(x, pos, r)
+
+
+def _step(lib, c, g):
+    """A write, a read and an attention over what was written."""
+    k, v = (_dev(g.normal(size=(40, c.heads, D)), torch.bfloat16) for _ in range(2))
+    slots = torch.arange(40, dtype=torch.int32, device="cuda")
+    lib.kv_append(c, k, v, slots)
+    q = _dev(g.normal(size=(1, 2, 2 * c.heads, D)), torch.bfloat16)
+    table = torch.arange(c.pages, dtype=torch.int32, device="cuda")[None]
+    return (*lib.kv_fetch(c, slots, out_dtype=torch.float32), lib.kv_attend_tree(c, q, table, _dev([40], torch.int32)))
+
+
+@pytest.mark.parametrize("change", ["arrays", "moved arrays", "books", "tensors of the books", "signs", "pages", "order"])
+def test_cache_handle_follows_its_tensors(lib, change):
+    c = _cache(lib, 4, 16, 2, 32, 256, 8, poison=False)
+    _step(lib, c, _rng(31))
+    old = [t.clone() for t in (c.kcodes, c.kscales, c.vcodes, c.vscales)]
+    fresh = lambda **kw: lib.PagedKVCache(kw.get("pages", c.pages), 16, 2, D, 32, kw.get("kcb", c.kcb), kw.get("vcb", c.vcb),  # noqa: E731
+                                          kw.get("rot", c.rot))
+    wide = lambda n: lib.Codebook(n, centroids=lib.codebook(n)[0] * 1.25, thresholds=lib.codebook(n)[1] * 1.25)  # noqa: E731
+    want = fresh()
+    kept = [c.kcodes, c.kscales, c.vcodes, c.vscales]
+    if change == "arrays":
+        c.kcodes, c.kscales, c.vcodes, c.vscales = (torch.zeros_like(t) for t in kept)
+    elif change == "moved arrays":
+        for t in kept:
+            t.set_(torch.zeros_like(t))
+    elif change == "books":
+        c.kcb, c.vcb = wide(256), wide(8)
+        want = fresh(kcb=c.kcb, vcb=c.vcb)
+    elif change == "tensors of the books":
+        a, b = wide(256), wide(8)
+        c.kcb.centroids, c.kcb.thresholds, c.vcb.centroids, c.vcb.thresholds = a.centroids, a.thresholds, b.centroids, b.thresholds
+        want = fresh(kcb=wide(256), vcb=wide(8))
+    elif change == "signs":
+        other = lib.Rotation(D, D, seed=78)
+        c.rot.signs = other.signs
+        want = fresh(rot=other)
+    elif change == "pages":
+        c.kcodes, c.kscales, c.vcodes, c.vscales = (torch.zeros((7, *t.shape[1:]), dtype=t.dtype, device="cuda") for t in kept)
+        c.pages = 7
+        want = fresh(pages=7)
+    else:  # heads first: one sequence's contiguous rows
+        c.kcodes, c.kscales, c.vcodes, c.vscales = (torch.zeros((2, 64, t.shape[-1]), dtype=t.dtype, device="cuda") for t in kept)
+        c.page_stride, c.head_stride = 16, 64
+    for x, y in zip(_step(lib, c, _rng(32)), _step(lib, want, _rng(32))):
+        assert torch.equal(x, y)
+    if change == "arrays":  # and what was replaced is left alone
+        for x, y in zip(kept, old):
+            assert torch.equal(x, y)
+    assert c.tree_bytes(1, 40, 4, 64) == want.tree_bytes(1, 40, 4, 64)
+
+
+def test_cache_handle_refuses_tensors_that_do_not_fit(lib):
+    slots = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for name, value in (("kcodes", lambda t: t[:2].clone()), ("vscales", lambda t: t.float()), ("kscales", lambda t: t.cpu()),
+                        ("vcodes", lambda t: t.transpose(0, 1)), ("pages", lambda n: n + 1), ("head_stride", lambda n: 4 * n),
+                        ("kcb", lambda b: lib.Codebook(16)), ("vcb", lambda b: lib.Codebook(8, device="cpu")),
+                        ("rot", lambda r: lib.Rotation(D, D, seed=1, device="cpu"))):
+        c = _cache(lib, 4, 16, 2, 32, 256, 8)
+        lib.kv_fetch(c, slots)
+        setattr(c, name, value(getattr(c, name)))
+        with pytest.raises(ValueError):
+            lib.kv_fetch(c, slots)
+    c = _cache(lib, 4, 16, 2, 32, 256, 8)
+    for short in (c.kcb.centroids[:200], c.kcb.centroids.double()):
+        c.kcb.centroids = short
+        with pytest.raises(ValueError):
+            lib.kv_fetch(c, slots)
+    with pytest.raises(ValueError):  # everything on the host
+        lib.kv_fetch(lib.PagedKVCache(4, 16, 2, D, 32, lib.Codebook(256, device="cpu"), lib.Codebook(8, device="cpu"),
+                                      lib.Rotation(D, D, seed=1, device="cpu"), device="cpu"), slots.cpu())
+
+
+def test_cache_handle_is_made_by_two_threads_at_once(lib):
+    import sys
+    import threading
+
+    kcb, vcb, rot = lib.Codebook(256), lib.Codebook(8), lib.Rotation(D, D, seed=77)
+    wrong, interval = [], sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        for _ in range(100):
+            c = lib.PagedKVCache(4, 16, 2, D, 32, kcb, vcb, rot)
+
+            def use():
+                try:
+                    if c.tree_bytes(1, 2, 4, 64) <= 0 or c._now()[1].kcodes != c.kcodes.data_ptr():
+                        wrong.append("another descriptor")
+                except Exception as e:  # noqa: BLE001
+                    wrong.append(e)
+
+            threads = [threading.Thread(target=use) for _ in range(4)]
+            for t in threads:
+                t.start()
+            for t in threads:
+                t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    assert not wrong
