@@ -649,8 +649,20 @@ def rope_steps(rotary: int, base: float = 10000.0, scaling: dict | None = None):
 # is made of stays the same, torch.empty (1.6 us; new_empty takes 3.6).
 
 def _raw_stream(t) -> int:
-    """torch's current stream on the tensor's device, as a number."""
-    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+    """torch's current stream on the tensor's device, as a number.  Launches go to the current device, so it has to be that one."""
+    torch, device = _torch(), t.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {device}, the current device is {torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _word(err, device) -> int:
+    """The address of a device error word (None: none)."""
+    if err is None:
+        return 0
+    if err.get_device() != device or err.element_size() != 4 or err.is_floating_point() or err.numel() < 1:
+        raise ValueError("err must hold a 32-bit integer on the same device as the others")
+    return err.data_ptr()
 
 
 def _heads(x, name, dim):
@@ -828,7 +840,7 @@ def kv_append(cache: PagedKVCache, k, v, slots, rope: Rope | None = None, positi
             raise ValueError("the rotary frequencies must be on the tokens' device")
         turn, pos = rope.ref(), _ints(positions, "positions", T, dev)
     _check(load().tq_kv_append(cache.ref(), k.data_ptr(), ks, v.data_ptr(), vs, _dt(k), T, at, turn, pos,
-                               0 if err is None else err.data_ptr(), _raw_stream(k)), "tq_kv_append")
+                               _word(err, dev), _raw_stream(k)), "tq_kv_append")
 
 
 def kv_fetch(cache: PagedKVCache, slots, out_dtype=None, err=None):
@@ -838,7 +850,7 @@ def kv_fetch(cache: PagedKVCache, slots, out_dtype=None, err=None):
     torch = _torch()
     shape, dtype, device = (T, cache.heads, cache.dim), out_dtype or torch.bfloat16, slots.device
     k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
-    _check(load().tq_kv_fetch(cache.ref(), at, T, k.data_ptr(), v.data_ptr(), _dt(k), 0 if err is None else err.data_ptr(),
+    _check(load().tq_kv_fetch(cache.ref(), at, T, k.data_ptr(), v.data_ptr(), _dt(k), _word(err, dev),
                               _raw_stream(slots)), "tq_kv_fetch")
     return k, v
 
@@ -878,11 +890,13 @@ def kv_attend_tree(cache: PagedKVCache, q, table, lens, k_new=None, v_new=None, 
     torch, device = _torch(), q.device
     o = torch.empty((B, n, hq, dim), dtype=torch.bfloat16, device=device)
     nb = cache.tree_bytes(B, n, hq, max_len)
+    if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError("ws must be contiguous, on q's device")
     if ws is None or ws.numel() * ws.element_size() < nb:
         ws = torch.empty(nb, dtype=torch.uint8, device=device)
     _check(load().tq_kv_attend_tree(cache.ref(), q.data_ptr(), qs, _dt(q), B, n, hq, tp, wide, lp, max_len, kp, ks, vp, vs, mp,
                                     np_, dim ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr(), nb,
-                                    0 if err is None else err.data_ptr(), _raw_stream(q)), "tq_kv_attend_tree")
+                                    _word(err, dev), _raw_stream(q)), "tq_kv_attend_tree")
     return o
 
 

@@ -998,3 +998,30 @@ def test_cache_handle_is_made_by_two_threads_at_once(lib):
     finally:
         sys.setswitchinterval(interval)
     assert not wrong
+
+
+def test_scratch_error_word_and_device_are_checked(lib, monkeypatch):
+    """Nothing but memory of the calls' own device goes to a kernel."""
+    c = _cache(lib, 4, 16, 2, 32, 256, 8)
+    k = torch.zeros((3, 2, D), device="cuda", dtype=torch.bfloat16)
+    s, pos = (torch.zeros(3, dtype=torch.int32, device="cuda") for _ in range(2))
+    q = torch.zeros((1, 3, 4, D), device="cuda", dtype=torch.bfloat16)
+    table, lens = torch.zeros((1, 4), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    nb = c.tree_bytes(1, 3, 4, 64)
+    ws = torch.empty(2 * nb, dtype=torch.uint8, device="cuda")
+    calls = [lambda **kw: lib.kv_append(c, k, k, s, **kw), lambda **kw: lib.kv_fetch(c, s, **kw),
+             lambda **kw: lib.kv_attend_tree(c, q, table, lens, **kw)]
+    for call in calls:
+        call(err=torch.zeros(1, dtype=torch.int32, device="cuda"))
+        for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int16, device="cuda"),
+                    torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")):
+            with pytest.raises(ValueError):
+                call(err=bad)
+    calls[2](ws=ws)
+    for bad in (ws.cpu(), ws[::2]):
+        with pytest.raises(ValueError):
+            calls[2](ws=bad)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: torch.cuda.device_count())  # as if another device were current
+    for call in (*calls, lambda: lib.rope(k, pos, lib.Rope(D))):
+        with pytest.raises(ValueError):
+            call()
