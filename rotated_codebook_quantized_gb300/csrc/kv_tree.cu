@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(32 * Ctx<ROWS>::kWarps, 1) kv_tree_context_ker
         float o[kTiles][4];
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        // the two rows' running maxima (log2), their negatives (0 while there is none), and sums
+        // the two rows' running maxima (log2), the biases of their weights, and sums
         float m0 = -INFINITY, m1 = -INFINITY, b0 = 0.f, b1 = 0.f, l[4] = {0.f, 0.f, 0.f, 0.f};
         // scale places of the lane: keys' dims 32 j and 32 j + 16, values' dims 16 r
         const int gk0 = (32 * j) >> a.c.lgroup, gk1 = (32 * j + 16) >> a.c.lgroup, gv = (16 * r) >> a.c.lgroup;
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(32 * Ctx<ROWS>::kWarps, 1) kv_tree_context_ker
                 // log2 scores are products times f0 and f1, which are not negative
                 const float x0 = f0 * (kFew ? fmaxf(sc[0][0], sc[0][2]) : fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])));
                 const float x1 = f1 * (kFew ? fmaxf(sc[0][1], sc[0][3]) : fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])));
-                // the maximum follows only when a score passes it by kSlack: weights stay below 2^8, well inside fp16
-                if (__any_sync(kFull, x0 > m0 + kSlack || x1 > m1 + kSlack)) {
+                // the maximum follows only when a score passes it by kSlack (a difference of near numbers is exact)
+                if (__any_sync(kFull, x0 - m0 > kSlack || x1 - m1 > kSlack)) {
                     float n0 = x0, n1 = x1;
 #pragma unroll
                     for (int m = kFew ? 4 : 1; m < (kFew ? 32 : 4); m <<= 1) {
@@ -301,11 +301,12 @@ __global__ void __launch_bounds__(32 * Ctx<ROWS>::kWarps, 1) kv_tree_context_ker
                     }
                     n0 = fmaxf(n0, m0);
                     n1 = fmaxf(n1, m1);
-                    const float g0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0), g1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
+                    const float c0 = weight_bias(n0), c1 = weight_bias(n1);
+                    const float g0 = m0 == -INFINITY ? 0.f : fast_exp2(c0 - b0), g1 = m1 == -INFINITY ? 0.f : fast_exp2(c1 - b1);
                     m0 = n0;
                     m1 = n1;
-                    b0 = m0 == -INFINITY ? 0.f : -m0;
-                    b1 = m1 == -INFINITY ? 0.f : -m1;
+                    b0 = c0;
+                    b1 = c1;
                     l[0] *= g0;
                     l[kFew ? 1 : 2] *= g1;
 #pragma unroll
@@ -430,8 +431,8 @@ __global__ void __launch_bounds__(32 * Ctx<ROWS>::kWarps, 1) kv_tree_context_ker
 #pragma unroll
                 for (int c = 0; c < 4; ++c) f[(4 * i + c) * kFragPad] = o[i][c];
             if ((kFew ? r : j) == 0) {
-                ml(warp)[kFew ? 2 * j : r] = make_float2(m0, l[0]);
-                ml(warp)[kFew ? 2 * j + 1 : r + 8] = make_float2(m1, l[kFew ? 1 : 2]);
+                ml(warp)[kFew ? 2 * j : r] = make_float2(level(m0, b0), l[0]);
+                ml(warp)[kFew ? 2 * j + 1 : r + 8] = make_float2(level(m1, b1), l[kFew ? 1 : 2]);
             }
         }
         __syncthreads();

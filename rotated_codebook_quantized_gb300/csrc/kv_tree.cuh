@@ -12,6 +12,13 @@ namespace tree {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInvSqrtD = 0.08838834764831845f;  // 1 / sqrt(128)
 constexpr float kSlack = 8.0f;                      // a running maximum may be this far (log2) below the true one
+// A row's weights are 2^(score + bias), bias = kLift - maximum: at most 2^15, inside fp16, and the smallest that fp16 holds is
+// 2^-31 of the maximum's (without the lift 2^-24: 131072 tokens a little below that are 0.4 % of a sum).  Rounded down, so that it
+// is never more than the lift, however large the maximum.  Sums belong to the bias: what is kept and joined is its negative.
+constexpr float kLift = 7.0f;
+static_assert(kSlack + kLift <= 15.0f, "weights fit fp16");
+TQ_DEVFN float weight_bias(float m) { return m == -INFINITY ? 0.f : __fadd_rd(kLift, -m); }
+TQ_DEVFN float level(float m, float bias) { return m == -INFINITY ? m : -bias; }  // that sums belong to: -infinity where there are none
 
 struct TreeArgs {
     KvPages c;
@@ -28,7 +35,7 @@ struct TreeArgs {
     int ctas, trows, stoks, least, pad;
     float scale2;                       // scale * log2(e)
     __nv_bfloat16* o;
-    float2* stat;  // [slot][trows]: running maximum (log2 units) and sum of a row
+    float2* stat;  // [slot][trows]: level (log2 units) and sum of a row
     float* part;   // [slot][trows][128]: weighted values, rotated
     uint4* turned;   // more than 16 rows: rotated queries [unit][16 pieces][trows] and their exponents
     int32_t* power;  // [unit][trows]

@@ -4,7 +4,7 @@
 // once into shared memory, as fp16 keys (K-major) and values (MN-major, so that neither needs a transpose), for one or two
 // tiles of 128 query rows:
 //   scores   S[128 x 32]   = Q (TMEM, fp16) . K^T (shared)          8 MMAs of K = 16
-//   weights  P = exp2(S f - m), fp16, written over S in TMEM        one thread to a row
+//   weights  P = exp2(S f + bias), fp16, written over S in TMEM     one thread to a row
 //   values   O[128 x 128] += P (TMEM) . V (shared)                  2 MMAs of K = 16
 // Two streams of four softmax warps each, with scores and sums of their own: the two tiles (T = 2), or the even and the odd
 // steps of one tile (T = 1), joined at the end of the run.  A stream's scores alternate between two places, so that its
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
     constexpr uint32_t kO = 0, kS = 256, kQ = 384;
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* const space = smem - (uint32_t)__cvta_generic_to_shared(smem);  // shared address 0
-    float* const odd = reinterpret_cast<float*>(space + kOdd);              // [2][128] maxima and sums of the odd steps (T = 1)
+    float* const odd = reinterpret_cast<float*>(space + kOdd);              // [2][128] levels and sums of the odd steps (T = 1)
     // full / empty: of a decoded step's place.  Of a place of a stream's scores: scores, weights, values written.  Of a stream:
     // queries written, and read for the last time.  Odd steps' statistics ready, and the sums they go with read (T = 1).
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], s_ready[2][2], p_ready[2][2], o_done[2][2], q_ready[2], q_free[2],
@@ -354,10 +354,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
 #pragma unroll
                         for (int c = 28; c < 32; ++c) x4[c & 3] = fmaxf(x4[c & 3], __uint_as_float(s[c]));
                         const float top = f * fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
-                        if (__any_sync(kFull, top > m + kSlack)) {
-                            const float n = fmaxf(m, top), r = m == -INFINITY ? 0.f : fast_exp2(m - n);
+                        if (__any_sync(kFull, top - m > kSlack)) {
+                            const float n = fmaxf(m, top), to = weight_bias(n), r = m == -INFINITY ? 0.f : fast_exp2(to - bias);
                             m = n;
-                            bias = m == -INFINITY ? 0.f : -m;
+                            bias = to;
                             l *= r;
                             if (i != first) {  // the sums so far, once the last product has written them
                                 ok = __all_sync(kFull, mbar_wait(&o_done[stream][e ^ 1], ((done - 1) >> 1) & 1, abort_flag, a.wait_cycles));
@@ -374,6 +374,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                                 }
                             }
                         }
+                        // (the sum takes the weights before their rounding to fp16, which moves one by 2^-12 of itself or, where it is
+                        // subnormal, by 2^-32 of the maximum's at most)
                         const f2 ff = pk(f, f), bb = pk(bias, bias);
                         f2 ls[2] = {0, 0};
 #pragma unroll
@@ -401,6 +403,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                 if (!ok) break;
                 tc_fence_after();
             }
+            m = level(m, bias);
             float m1 = -INFINITY, l1 = 0.f;
             if (T == 1) {  // the even steps' warps add the odd steps' sums, which lie in the same TMEM lanes
                 if (stream == 1) {
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                 if (!idle) {
                     const bool two = T == 1 && ge - g > 1;
                     const float n = two ? fmaxf(m, m1) : m;
-                    // weight 1 for the joint maximum's own (also where both saw nothing); a NaN sum stays one
+                    // weight 1 for the higher level's own (also where both saw nothing); a NaN sum stays one
                     const float w0 = m == n ? 1.f : fast_exp2(m - n), w1 = m1 == n ? 1.f : fast_exp2(m1 - n);
                     const int64_t to = ((int64_t)blockIdx.x + x.unit) * kRows + row;
                     const float vscale = exp2f((float)ev);

@@ -109,3 +109,32 @@ def test_nothing_of_a_call_is_left_running(lib, n):
         assert bool((ws == 0x5A).all())
         assert not bool(got.any())
         assert torch.equal(ref, lib.kv_attend_tree(c, q, table, lens, k_new=kn, v_new=vn, ws=ws))
+
+
+@pytest.mark.parametrize("n", [1, 4, 16, 64])  # 4, 16, 64 and 256 rows to a kv head
+def test_many_small_weights_beside_a_large_one(lib, n):
+    """One token far above 32767 equal ones, whose values are 4000 times as large: their weights, 2^-20 to 2^-28 of its own,
+    decide the result.  A weight is off by 2^-32 of the largest at most, beside the usual roundings."""
+    g = base._rng(104)
+    T, B, page, at = 32768, 152, 256, 5
+    c = base._cache(lib, T // page, page, 1, 32, 256, 8)
+    k, v = (torch.empty((T, 1, D), device="cuda") for _ in range(2))
+    k[:] = base._dev(g.normal(size=D), torch.float32)
+    v[:] = base._dev(g.normal(size=D) * 4000, torch.float32)
+    k[at], v[at] = (base._dev(g.normal(size=(1, D)), torch.float32) for _ in range(2))
+    lib.kv_append(c, k, v, torch.arange(T, dtype=torch.int32, device="cuda"))
+    (k1, k0), (v1, v0) = ((x[0, 0], x[1, 0]) for x in base._values(c, np.array([at, 0])))
+    q = torch.stack([base._dev((k1 - k0) * w, torch.bfloat16) for w in (20, 24.4, 25.1, 28)])
+    q64 = base._f64(q)
+    scale = np.log(2.0) / ((k1 - k0) @ (k1 - k0))
+    weight = np.exp(-scale * (q64 @ (k1 - k0)))[:, None]  # of the others
+    assert np.all(weight < 2.0 ** -19) and np.all(weight > 2.0 ** -29)
+    ref = (v1 + (T - 1) * weight * v0) / (1 + (T - 1) * weight)
+    table = torch.arange(T // page, dtype=torch.int32, device="cuda").repeat(B, 1)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = lib.kv_attend_tree(c, q.expand(B, n, 4, D).contiguous(), table, torch.full((B,), T, dtype=torch.int32, device="cuda"),
+                             scale=float(scale), err=err)
+    assert lib.check_error(err) == 0
+    bound = base.ATTEND_ROW * np.linalg.norm(ref, axis=-1) + T * 2.0 ** -32 * np.linalg.norm(v0)
+    off = np.linalg.norm(base._f64(got) - ref, axis=-1)
+    assert np.all(off <= bound), (off / bound).max()
