@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(32 * Ctx<ROWS>::kWarps, 1) kv_tree_context_ker
 #pragma unroll
         for (int it = 0; it < kDepth - 1; ++it) issue();
 
-        // queries of the tile: rotated, over a power of two of their own, fp16
+        // queries of the tile: rotated, over a power of two of their own, times the scale's mantissa, fp16
         for (int row = warp; row < ROWS; row += kCtxWarps) {
             float v[4] = {0.f, 0.f, 0.f, 0.f};
             if (row < rows) {
@@ -182,10 +182,10 @@ __global__ void __launch_bounds__(32 * Ctx<ROWS>::kWarps, 1) kv_tree_context_ker
 #pragma unroll
             for (int m = 16; m; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, m));
             const int e = exponent_above(mx);
-            const float d = a.scale2 < 0.f ? -exp2f((float)-e) : exp2f((float)-e);  // a factor below is not negative
+            const float d = query_factor(e, a.qmant);  // takes the scale's sign: the factor below is not negative
             *reinterpret_cast<uint2*>(qh + row * kPD + lane * 4) =
                 make_uint2(pack_f16(v[0] * d, v[1] * d), pack_f16(v[2] * d, v[3] * d));
-            if (lane == 0) qf[row] = score_factor(e + ek, a.scale2);
+            if (lane == 0) qf[row] = score_factor(e + ek, a.qexp);
         }
         __syncthreads();
         // Operand of product step s: the lane's row r (A: and r + 8), dims 32 j + 4 s .. + 3.  Any order
@@ -912,8 +912,11 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
     a.least = p.least;
     a.pad = p.pad;
     a.wait_cycles = wait_budget();
-    // a scale of 0 (all weights equal) as one that no score feels: masked scores are -infinity times a factor
-    a.scale2 = fabsf(scale) < 1e-30f ? 1e-30f : scale * kLog2e;
+    a.scale2 = scale * kLog2e;
+    int qexp = 0;
+    const double qmant = 2.0 * frexp((double)scale * kLog2e * kInvSqrtD, &qexp);
+    a.qmant = (float)qmant;
+    a.qexp = qexp - 1;
     a.o = static_cast<__nv_bfloat16*>(o);
     a.part = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));  // 32-byte stores
     a.stat = reinterpret_cast<float2*>(a.part + (size_t)p.slots * p.trows * kPD);

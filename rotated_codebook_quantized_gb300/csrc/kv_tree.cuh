@@ -34,6 +34,8 @@ struct TreeArgs {
     // context launch: CTAs, query rows of a tile, tokens of a step, fewest steps of a run, steps that beginning a tile weighs
     int ctas, trows, stoks, least, pad;
     float scale2;                       // scale * log2(e)
+    float qmant;                        // scale2 / sqrt(128) as qmant 2^qexp, 1 <= |qmant| <= 2 (or 0)
+    int qexp;
     __nv_bfloat16* o;
     float2* stat;  // [slot][trows]: level (log2 units) and sum of a row
     float* part;   // [slot][trows][128]: weighted values, rotated
@@ -288,9 +290,12 @@ TQ_DEVFN int exponent_above(float x) {
     return e == 0 || e == 255 ? 0 : e - 126;
 }
 
-// From a row's products, of operands over 2^e together, to log2 scores.  Never 0, so that a masked score, -infinity times it, is
-// no NaN; products are below 2^24, so a score that the bound changes stays below 2^-98.
-TQ_DEVFN float score_factor(int e, float scale2) { return fmaxf(exp2f((float)e) * (kInvSqrtD * fabsf(scale2)), 1e-37f); }
+// The scale's mantissa goes into the rotated queries, with their own power of two: what a row's element is multiplied by.
+TQ_DEVFN float query_factor(int e, float qmant) { return exp2f((float)-e) * qmant; }
+// From a row's products, of operands over 2^e together, to log2 scores: a power of two, so that a product times it is exact, and
+// the highest score less itself is 0 however large it is.  Never 0, so that a masked score, -infinity times it, is no NaN; products
+// are below 2^24, so a score that the bound changes stays below 2^-98.
+TQ_DEVFN float score_factor(int e, int qexp) { return exp2f((float)min(max(e + qexp, -122), 127)); }
 
 }  // namespace tree
 }  // namespace tq

@@ -131,7 +131,7 @@ TQ_DEVFN void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d
 
 constexpr int kSoft = 8, kMma = kSoft + kDec, kWarps = kMma + 2;  // 22 warps: 80 registers a thread
 
-// The queries, rotated, over a power of two of their own, fp16: a warp to a row.  Of a tile of `trows` rows the 16-byte pieces
+// The queries, rotated, over a power of two of their own, times the scale's mantissa, fp16: a warp to a row.  Of a tile of `trows` rows the 16-byte pieces
 // [16][trows] lie together, a thread of the next kernel reading its row's; the power's exponent beside them.
 __global__ void __launch_bounds__(256) kv_tree_turn_kernel(TreeArgs a, int tiles) {
     pdl_trigger();
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(256) kv_tree_turn_kernel(TreeArgs a, int tiles
         kFull, max(max(__float_as_uint(fabsf(v[0])), __float_as_uint(fabsf(v[1]))),
                    max(__float_as_uint(fabsf(v[2])), __float_as_uint(fabsf(v[3]))))));
     const int e = exponent_above(top);
-    const float d = a.scale2 < 0.f ? -exp2f((float)-e) : exp2f((float)-e);  // a negative scale's sign goes here
+    const float d = query_factor(e, a.qmant);  // a negative scale's sign goes here
     const int64_t unit = ((int64_t)b * a.c.Hkv + h) * tiles + tile;
     uint8_t* to = reinterpret_cast<uint8_t*>(a.turned) + ((unit * 16 + (lane >> 1)) * a.trows + row) * 16 + (lane & 1) * 8;
     *reinterpret_cast<uint2*>(to) = make_uint2(pack_f16(v[0] * d, v[1] * d), pack_f16(v[2] * d, v[3] * d));
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                     }
                     tc_wait_st();
                 }
-                f = score_factor((in ? a.power[unit * kRows + row] : 0) + ek, a.scale2);
+                f = score_factor((in ? a.power[unit * kRows + row] : 0) + ek, a.qexp);
             }
             if (writer) {
                 tc_fence_before();

@@ -1025,3 +1025,33 @@ def test_scratch_error_word_and_device_are_checked(lib, monkeypatch):
     for call in (*calls, lambda: lib.rope(k, pos, lib.Rope(D))):
         with pytest.raises(ValueError):
             call()
+
+
+FORMS = [(1, 4), (4, 4), (20, 4), (33, 4)]  # drafts and heads: 4, 16, 80 and 132 rows to a kv head
+
+
+@pytest.mark.parametrize("n,Hq", FORMS)
+def test_tree_large_queries_and_small_scales(lib, n, Hq):
+    """Queries of 2^118 under a scale of 2^-118: every score is an ordinary number."""
+    g, c, table, dlens, ctx, q, kn, vn = _setup(lib, (40, n), [333, 20], n, Hq, 1, 32)
+    see = _tree(g, 2, n)
+    q = (q.float() * 2.0 ** 118).bfloat16()
+    scale = D ** -0.5 * 2.0 ** -118
+    for sign in (1, -1):
+        got = lib.kv_attend_tree(c, q, table, dlens, k_new=kn, v_new=vn, mask=_dev(_pack_mask(see)), scale=sign * scale)
+        _check(got, _attend(_f64(q), ctx, _f64(kn), _f64(vn), see, None, sign * scale))
+
+
+@pytest.mark.parametrize("power", [3, 18, 22, 24, 30, 100])
+@pytest.mark.parametrize("n,Hq", FORMS)
+def test_tree_scores_of_any_size(lib, n, Hq, power):
+    """Each row's query points at one token's key: that token's value, up to scores of 2^107."""
+    g, c, table, dlens, ctx, q, kn, vn = _setup(lib, (41, n), [500], n, Hq, 1, 32)
+    k, v = ctx[0]
+    picks = g.integers(0, 500, (n, Hq))
+    q = _dev(k[picks, 0], torch.bfloat16)[None]
+    got = lib.kv_attend_tree(c, q, table, dlens, scale=2.0 ** power * D ** -0.5)
+    ref = _attend(_f64(q), ctx, None, None, None, None, 2.0 ** power * D ** -0.5)
+    if power > 3:
+        np.testing.assert_array_equal(ref[0], v[picks, 0])
+    _check(got, ref)
