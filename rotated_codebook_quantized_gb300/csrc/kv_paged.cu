@@ -695,7 +695,9 @@ extern "C" tq_status tq_kv_append(const tq_kv_pages_t* cache, const void* k, int
         if (!(rope->rotary == 32 || rope->rotary == 64 || rope->rotary == 128)) return TQ_ERR_UNSUPPORTED;
     }
     if (T == 0) return TQ_OK;
-    if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16)) return TQ_ERR_INVALID;
+    if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(positions, 4) || !aligned(err, 4))
+        return TQ_ERR_INVALID;
+    if (T > kMaxTokens) return TQ_ERR_UNSUPPORTED;
     AppendArgs a{};
     a.c = kv_pages_view(cache);
     a.k = k;
@@ -750,7 +752,8 @@ extern "C" tq_status tq_kv_fetch(const tq_kv_pages_t* cache, const int32_t* slot
     if (ok != TQ_OK) return ok;
     if (T < 0 || (dt != TQ_F32 && dt != TQ_BF16 && dt != TQ_F16)) return TQ_ERR_INVALID;
     if (T == 0 || (!k && !v)) return TQ_OK;
-    if (!slots || !aligned(k, 16) || !aligned(v, 16)) return TQ_ERR_INVALID;
+    if (!slots || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(err, 4)) return TQ_ERR_INVALID;
+    if (T > kMaxTokens) return TQ_ERR_UNSUPPORTED;
     FetchArgs a{};
     a.c = kv_pages_view(cache);
     a.slots = slots;

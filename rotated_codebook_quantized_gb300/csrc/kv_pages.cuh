@@ -7,6 +7,8 @@
 namespace tq {
 
 constexpr int kPD = 128;  // head length of the cache
+constexpr int64_t kMaxRows = 1ll << 48;    // rows that a cache's strides may span
+constexpr int64_t kMaxTokens = 1ll << 40;  // of a call: times the kv heads they fit 63 bits
 
 // Device view of a tq_kv_pages_t.
 struct KvPages {
@@ -33,9 +35,11 @@ inline tq_status kv_pages_check(const tq_kv_pages_t* c, bool write) {
     if (c->D != kPD) return TQ_ERR_UNSUPPORTED;
     if (!(c->group == 16 || c->group == 32 || c->group == 64 || c->group == 128)) return TQ_ERR_INVALID;
     if (!is_pow2(c->page) || c->page < 16 || c->page > 256) return TQ_ERR_INVALID;
-    if (c->pages * c->page > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;  // slots are int32
+    if (c->pages > 0x7fffffffll / c->page) return TQ_ERR_UNSUPPORTED;  // slots are int32
     if (c->page_stride < c->page || c->head_stride < c->page || c->page_stride % 16 || c->head_stride % 16)
         return TQ_ERR_INVALID;
+    // rows (and bytes) of the arrays fit 63 bits
+    if ((c->pages && c->page_stride > kMaxRows / c->pages) || c->head_stride > kMaxRows / c->Hkv) return TQ_ERR_UNSUPPORTED;
     if (!c->rot.signs || !aligned(c->rot.signs, 16) || c->rot.dim != kPD || c->rot.block != kPD) return TQ_ERR_INVALID;
     if (!c->kcb.centroids || !c->vcb.centroids || (write && (!c->kcb.thresholds || !c->vcb.thresholds)))
         return TQ_ERR_INVALID;

@@ -795,9 +795,18 @@ int sm_count() {
 }
 
 struct Plan {
-    int64_t tiles, slots, steps, turned;  // output tiles of 16 rows; partial results, steps, rows of turned queries at most
+    int64_t tiles, slots, turned;  // output tiles of 16 rows; partial results, rows of turned queries at most
     int ctas, trows, stoks, least, pad;
 };
+
+// Rows, tiles and steps of a call within 30 bits, which the kernels count in 32 (B, n, Hq and Hkv positive).
+bool plan_fits(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len) {
+    constexpr double kMost = 0x3fffffff;  // products are compared in doubles: they may pass 64 bits
+    const int64_t rows = (int64_t)n * (Hq / Hkv);
+    if (rows > 0x3fffffffll || max_len > 0x7fffffffll - 64) return false;
+    const double heads = (double)Hkv * B, step = rows <= kStep ? kStep : 32, tile = rows <= kStep ? kStep : (rows <= 128 ? 128 : 256);
+    return heads * ((rows + kStep - 1) / kStep) <= kMost && heads * ceil(rows / tile) * (ceil(max_len / step) + 24) <= kMost;
+}
 
 // Context launch and workspace of a call.  Runs (CTAs) and units both ascend along the work, so run + unit numbers every
 // partial result once.  Up to 16 rows to a kv head go to the kernel above, more to the one that decodes a step once for
@@ -813,7 +822,6 @@ Plan make_plan(int32_t Hkv, int32_t B, int32_t n, int32_t Hq, int64_t max_len, i
     p.pad = p.trows == kStep ? 24 : (p.trows == 128 ? 8 : 14);
     p.tiles = (rows + kStep - 1) / kStep;
     const int64_t units = (rows + p.trows - 1) / p.trows * Hkv * B, steps = max_len ? (max_len + p.stoks - 1) / p.stoks + p.pad : 0;
-    p.steps = units * steps;
     p.ctas = (int)std::min<int64_t>(sms, (units * steps + p.least - 1) / p.least);
     p.slots = p.ctas ? units + p.ctas : 0;
     p.turned = p.ctas && p.trows != kStep ? units * p.trows : 0;
@@ -856,6 +864,7 @@ constexpr int kMaxSms = 256;  // bound on the SMs that the workspace is sized fo
 extern "C" size_t tq_kv_attend_tree_workspace_bytes(const tq_kv_pages_t* cache, int32_t B, int32_t n, int32_t Hq,
                                                     int64_t max_len) {
     if (kv_pages_check(cache, false) != TQ_OK || B <= 0 || n <= 0 || Hq <= 0 || Hq % cache->Hkv || max_len < 0) return 0;
+    if (!plan_fits(cache->Hkv, B, n, Hq, max_len)) return 0;
     return plan_bytes(make_plan(cache->Hkv, B, n, Hq, max_len, kMaxSms));
 }
 
@@ -878,14 +887,13 @@ extern "C" tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q
     if (B == 0 || n == 0) return TQ_OK;
     if (!q || !o || !lens || !ws || (max_len && !table)) return TQ_ERR_INVALID;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(ws, 16) ||
-        !aligned(mask, 8))
+        !aligned(mask, 8) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(n_tok, 4) || !aligned(err, 4))
         return TQ_ERR_INVALID;
+    if (!plan_fits(cache->Hkv, B, n, Hq, max_len)) return TQ_ERR_UNSUPPORTED;
     if (ws_bytes < tq_kv_attend_tree_workspace_bytes(cache, B, n, Hq, max_len)) return TQ_ERR_INVALID;
     // (the size above is for the most SMs; a plan for fewer takes no more, and is held to it)
     const Plan p = make_plan(cache->Hkv, B, n, Hq, max_len, std::min(sm_count(), kMaxSms));
     if (ws_bytes < plan_bytes(p)) return TQ_ERR_INVALID;
-    if ((int64_t)n * (Hq / cache->Hkv) > 0x3fffffffll || p.tiles * B * cache->Hkv > 0x3fffffffll || p.steps > 0x3fffffffll || max_len > 0x7fffffffll - 64)
-        return TQ_ERR_UNSUPPORTED;
     // cache rows by the 8 are 32-bit numbers
     if ((cache->pages * cache->page_stride + cache->Hkv * cache->head_stride) / 8 > 0xffffffffll) return TQ_ERR_UNSUPPORTED;
     TreeArgs a{};

@@ -195,7 +195,8 @@ extern "C" tq_status tq_rope(const tq_rope_t* rope, const int32_t* positions, in
     if (Hq && (q_stride < Hq * dim || yq_stride < Hq * dim)) return TQ_ERR_INVALID;
     if (Hkv && (k_stride < Hkv * dim || yk_stride < Hkv * dim)) return TQ_ERR_INVALID;
     if (tokens == 0 || Hq + Hkv == 0) return TQ_OK;
-    if (!positions || (Hq && (!q || !yq)) || (Hkv && (!k || !yk))) return TQ_ERR_INVALID;
+    if (!positions || !aligned(positions, 4) || (Hq && (!q || !yq)) || (Hkv && (!k || !yk))) return TQ_ERR_INVALID;
+    if (tokens > (1ll << 40)) return TQ_ERR_UNSUPPORTED;  // threads are counted in 64 bits
     const size_t es = dt == TQ_F32 ? 4 : 2;
     if ((Hq && (!aligned(q, es) || !aligned(yq, es))) || (Hkv && (!aligned(k, es) || !aligned(yk, es))))
         return TQ_ERR_INVALID;

@@ -182,3 +182,47 @@ def test_wide_kernel_places_are_never_taken_early(streams_share_steps):
                 frees[place] += 1
                 if frees[place] == need:
                     frees[place], freed[place] = 0, freed[place] + 1
+
+
+@pytest.mark.parametrize("change", [dict(pages=1 << 58), dict(pages=1 << 57, page=128, hs=128), dict(ps=1 << 60, pages=16), dict(ps=1 << 48),
+                                    dict(hs=1 << 61), dict(hs=1 << 48)], ids=str)
+def test_pools_past_64_bits_are_refused(lib, change):
+    """Products of page counts, pages and strides that wrap around."""
+    c = ctypes.byref(_pages(**change))
+    assert lib.tq_kv_append(c, FAKE, 1024, FAKE, 1024, 1, 4, FAKE, None, None, None, None) == tq.TQ_ERR_UNSUPPORTED
+    assert lib.tq_kv_fetch(c, FAKE, 4, FAKE, FAKE, 1, None, None) == tq.TQ_ERR_UNSUPPORTED
+    assert lib.tq_kv_attend_tree(c, FAKE, 1024, 1, 1, 1, 8, FAKE, 4, FAKE, 64, None, 0, None, 0, None, None, 1.0, FAKE,
+                                 FAKE, 1 << 30, None, None) == tq.TQ_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("T", [1 << 61, (1 << 61) + 1, 1 << 60])
+def test_token_counts_past_64_bits_are_refused(lib, T):
+    """Eight heads to a token: the count of (token, head) pairs wraps around to a small one."""
+    c = ctypes.byref(_pages())
+    assert lib.tq_kv_append(c, FAKE, 1024, FAKE, 1024, 1, T, FAKE, None, None, None, None) == tq.TQ_ERR_UNSUPPORTED
+    assert lib.tq_kv_fetch(c, FAKE, T, FAKE, FAKE, 1, None, None) == tq.TQ_ERR_UNSUPPORTED
+    assert lib.tq_rope(ctypes.byref(_rope()), FAKE, T, tq.TQ_BF16, 0, FAKE, 1024, 8, FAKE, 1024, None, 0, 0, None, 0,
+                       None) == tq.TQ_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("B,n,hq,most", [(1 << 30, 1 << 20, 8, 64), (1 << 30, 1 << 30, 8, 64), (2 ** 31 - 1, 64, 65528, 0), (1, 1 << 30, 65528, 256),
+                                         (1 << 28, 16, 8, 256), (1, 1, 8, 2 ** 31 - 1), (1 << 24, 1, 8, 1 << 20)])
+def test_trees_past_the_counters_are_refused(lib, B, n, hq, most):
+    """Rows, tiles or steps that the kernels' 32-bit counters do not hold, some of which wrap 64 bits too."""
+    c = ctypes.byref(_pages())
+    assert lib.tq_kv_attend_tree_workspace_bytes(c, B, n, hq, most) == 0
+    assert lib.tq_kv_attend_tree(c, FAKE, hq * 128, 1, B, n, hq, FAKE, 1 << 26, FAKE, most, None, 0, None, 0, None, None, 1.0, FAKE,
+                                 FAKE, 2 ** 63, None, None) == tq.TQ_ERR_UNSUPPORTED
+
+
+def test_integer_arrays_are_aligned(lib):
+    """Positions, slots, tables, lengths, counts and the error word are read as 32-bit numbers."""
+    odd, c, r = ctypes.c_void_p(0x1002), ctypes.byref(_pages()), ctypes.byref(_rope())
+    nb = lib.tq_kv_attend_tree_workspace_bytes(c, 1, 1, 8, 64)
+    app = lambda slots=FAKE, pos=FAKE, err=None: lib.tq_kv_append(c, FAKE, 1024, FAKE, 1024, 1, 4, slots, r, pos, err, None)  # noqa: E731
+    get = lambda slots=FAKE, err=None: lib.tq_kv_fetch(c, slots, 4, FAKE, FAKE, 1, err, None)  # noqa: E731
+    tree = lambda table=FAKE, lens=FAKE, n_tok=None, err=None: lib.tq_kv_attend_tree(  # noqa: E731
+        c, FAKE, 1024, 1, 1, 1, 8, table, 4, lens, 64, None, 0, None, 0, None, n_tok, 1.0, FAKE, FAKE, nb, err, None)
+    for bad in (app(slots=odd), app(pos=odd), app(err=odd), get(slots=odd), get(err=odd), tree(table=odd), tree(lens=odd), tree(n_tok=odd),
+                tree(err=odd), lib.tq_rope(r, odd, 4, 1, 0, FAKE, 1024, 8, FAKE, 1024, None, 0, 0, None, 0, None)):
+        assert bad == tq.TQ_ERR_INVALID
