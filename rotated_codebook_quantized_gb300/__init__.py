@@ -792,17 +792,24 @@ class PagedKVCache:
     _kept = None
 
     def _now(self):
-        """(key, descriptor, workspace sizes, tensors): the key is all that the descriptor is made of, compared on every call."""
+        """(tensors, descriptor, workspace sizes, addresses, sizes), kept while all that the descriptor is made of, compared on
+        every call, is the same."""
         kcb, vcb, rot = self.kcb, self.vcb, self.rot
-        t = (self.kcodes, self.kscales, self.vcodes, self.vscales, kcb.centroids, kcb.thresholds, vcb.centroids, vcb.thresholds,
-             rot.signs)
-        # a tensor may be another object at the same address (a view of other strides) or the same object at another
-        key = (*map(id, t), *[x.data_ptr() for x in t], kcb.levels, vcb.levels, rot.dim, rot.block, self.pages, self.page,
-               self.heads, self.dim, self.group, self.page_stride, self.head_stride)
+        sizes = (kcb.levels, vcb.levels, rot.dim, rot.block, self.pages, self.page, self.heads, self.dim, self.group,
+                 self.page_stride, self.head_stride)
         kept = self._kept
-        if kept is None or kept[0] != key:
-            # in one piece: another thread finds the old or the new; the tensors are held, so that no id comes back
-            kept = self._kept = (key, self.c(), {}, t)
+        if kept is not None and kept[4] == sizes:
+            # a tensor may be another object at the same address (a view of other strides) or the same object at another
+            (a, b, c, d, e, f, g, h, i), (pa, pb, pc, pd, pe, pf, pg, ph, pi) = kept[0], kept[3]
+            if (self.kcodes is a and self.kscales is b and self.vcodes is c and self.vscales is d and kcb.centroids is e
+                    and kcb.thresholds is f and vcb.centroids is g and vcb.thresholds is h and rot.signs is i
+                    and a.data_ptr() == pa and b.data_ptr() == pb and c.data_ptr() == pc and d.data_ptr() == pd and e.data_ptr() == pe
+                    and f.data_ptr() == pf and g.data_ptr() == pg and h.data_ptr() == ph and i.data_ptr() == pi):
+                return kept
+        tensors = (self.kcodes, self.kscales, self.vcodes, self.vscales, kcb.centroids, kcb.thresholds, vcb.centroids,
+                   vcb.thresholds, rot.signs)
+        kept = (tensors, self.c(), {}, tuple(t.data_ptr() for t in tensors), sizes)
+        self._kept = kept  # in one piece: another thread finds the old or the new
         return kept
 
     def ref(self):
@@ -810,7 +817,10 @@ class PagedKVCache:
 
     def tree_bytes(self, B, n, hq, max_len) -> int:
         """Workspace of kv_attend_tree at these sizes."""
-        _, c, sizes, _ = self._now()
+        return self._tree_bytes(self._now(), B, n, hq, max_len)
+
+    def _tree_bytes(self, now, B, n, hq, max_len) -> int:
+        c, sizes = now[1], now[2]
         key = (B, n, hq, max_len)
         nb = sizes.get(key)
         if nb is None:
@@ -889,12 +899,13 @@ def kv_attend_tree(cache: PagedKVCache, q, table, lens, k_new=None, v_new=None, 
     max_len = wide * cache.page if max_len is None else int(max_len)
     torch, device = _torch(), q.device
     o = torch.empty((B, n, hq, dim), dtype=torch.bfloat16, device=device)
-    nb = cache.tree_bytes(B, n, hq, max_len)
+    now = cache._now()
+    nb = cache._tree_bytes(now, B, n, hq, max_len)
     if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
         raise ValueError("ws must be contiguous, on q's device")
     if ws is None or ws.numel() * ws.element_size() < nb:
         ws = torch.empty(nb, dtype=torch.uint8, device=device)
-    _check(load().tq_kv_attend_tree(cache.ref(), q.data_ptr(), qs, _dt(q), B, n, hq, tp, wide, lp, max_len, kp, ks, vp, vs, mp,
+    _check(load().tq_kv_attend_tree(ctypes.byref(now[1]), q.data_ptr(), qs, _dt(q), B, n, hq, tp, wide, lp, max_len, kp, ks, vp, vs, mp,
                                     np_, dim ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr(), nb,
                                     _word(err, dev), _raw_stream(q)), "tq_kv_attend_tree")
     return o
