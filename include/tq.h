@@ -427,7 +427,8 @@ typedef struct tq_rope_t {
  * the slowest one's w by `factor`.  PARTS (YaRN, Peng et al. 2023): with r = the
  * turns of pair i over `original` positions, w_i keeps its value where r >=
  * fast_turns, is divided by `factor` where r <= slow_turns, and is a linear blend
- * between; the factor on the elements is 0.1 ln(factor) + 1. */
+ * in r between; the factor on the elements is 0.1 ln(factor) + 1.  (A model that
+ * blends over the pair's number i between two bounds brings its own steps.) */
 typedef enum tq_rope_scaling_kind {
     TQ_ROPE_NONE = 0, TQ_ROPE_LINEAR = 1, TQ_ROPE_BASE = 2, TQ_ROPE_PARTS = 3
 } tq_rope_scaling_kind;
@@ -516,8 +517,14 @@ tq_status tq_kv_fetch(const tq_kv_pages_t* cache, const int32_t* slots, int64_t 
  * length outside [0, max_len], or a page id outside the pool among those a length
  * reaches, sets TQ_DEVERR_BAD_PAGE; the length is clamped, the page's tokens are
  * left out.  Entries of table past a sequence's pages are not read.
- * o: device bf16 [B][n][Hq][D].  Cached keys, values and their weights are fp16
- * tensor-core operands; scores, softmax statistics and sums are fp32.  ws: 16-byte
+ * o: device bf16 [B][n][Hq][D].  Cached keys and values, rotated queries and softmax
+ * weights are fp16 tensor-core operands, each rounding 2^-11 of itself at most (a
+ * decoded element has two: its centroid, and that times the group's scale).  Where
+ * fp16 is subnormal a decoded element is within 2^-25 of the power of two above its
+ * book, which shows for group scales below about 1e-5; a query's within 2^-24 of its
+ * row's largest; a weight within 2^-32 of its row's largest.  Scores (of any size),
+ * softmax statistics and sums are fp32.  TQ_ERR_UNSUPPORTED, and a workspace of 0
+ * bytes, for more rows, tiles or steps of 16 tokens than 2^30.  ws: 16-byte
  * aligned device scratch of tq_kv_attend_tree_workspace_bytes(...) bytes; calls that
  * may run at the same time must not share it.  A bounded wait that ran out (more than
  * 16 rows, n*Hq/Hkv, to a kv head) sets TQ_DEVERR_TIMEOUT; o is then incomplete. */

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_tree_wide_kernel(TreeArgs a
                                 }
                             }
                         }
-                        // (the sum takes the weights before their rounding to fp16, which moves one by 2^-12 of itself or, where it is
+                        // (the sum takes the weights before their rounding to fp16, which moves one by 2^-11 of itself or, where it is
                         // subnormal, by 2^-32 of the maximum's at most)
                         const f2 ff = pk(f, f), bb = pk(bias, bias);
                         f2 ls[2] = {0, 0};

@@ -1055,3 +1055,16 @@ def test_tree_scores_of_any_size(lib, n, Hq, power):
     if power > 3:
         np.testing.assert_array_equal(ref[0], v[picks, 0])
     _check(got, ref)
+
+
+@pytest.mark.parametrize("size", [1e-5, 1e-6, 1e-7])
+@pytest.mark.parametrize("n,Hq", FORMS)
+def test_tree_group_scales_of_fp16_subnormals(lib, n, Hq, size):
+    """Where group scales are fp16 subnormals a decoded element is off by 2^-25 of the power of two above the book at most
+    (4 for 8 value levels), so a row by that times sqrt(128), beside the usual roundings."""
+    g, c, table, dlens, ctx, q, kn, vn = _setup(lib, (42, n), [77], n, Hq, 1, 32, spread=size)
+    assert float(c.vcb.centroids.abs().max()) < 4
+    got = lib.kv_attend_tree(c, q, table, dlens)
+    ref = _attend(_f64(q), ctx, None, None, None, None)
+    off, norm = (np.linalg.norm(x, axis=-1) for x in (_f64(got) - ref, ref))
+    assert np.all(off <= ATTEND_ROW * norm + math.sqrt(D) * 4 * 2.0 ** -25), (off / norm).max()
