@@ -9,11 +9,11 @@
 // steps of the whole batch, whatever the sequences' lengths, and leaves a partial result (maximum, sum, weighted values
 // of the rows) wherever its run crosses into another tile.  kv_tree_finish_kernel: the drafted tokens, then the join of a
 // tile's partial results, the de-rotation and the output.  More rows: kv_tree_wide.cu's two kernels take the place of the
-// first.  One row over a few thousand tokens would be as fast there (100 tokens of one sequence: 12.7 us against 13.8),
-// over 65536 it takes 63 us against 44.
+// first.  (Up to a few thousand tokens those are as fast for few rows too: one row over 100 tokens of one sequence 12.7 us there
+// and 13.8 here, over 65536 63 and 44.  A rule on lengths, which are on the device, is not worth the 1 us.)
 //
 // The context kernel is bound by instruction issue: a lane decodes 128 codes of a step by a table read or two byte
-// permutes each (131072 tokens of 8 heads: 3.1 TB/s of codes and scales, 47 % of the copy rate).
+// permutes each (131072 tokens of 8 heads: 59 us alone, 3.5 TB/s of codes and scales, 52 % of the copy rate; the call 67).
 #include <math.h>
 
 #include <algorithm>

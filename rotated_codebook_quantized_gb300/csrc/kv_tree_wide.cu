@@ -15,8 +15,9 @@
 // reads of K and V.  A row's running maximum follows only when a score passes it by 2^kSlack, so O is seldom rescaled.
 //
 // Bound by the softmax's chain of latencies (1100 of 1290 cycles a step and stream; the products alone take 514) and by issue
-// slots (62 % of them): 256 rows to each of 8 heads over 131072 tokens 144 us, 950 TFLOP/s, half of the measured bf16 rate;
-// 32 rows to each of 8 heads of 16 sequences of up to 8192 tokens: 59 us, 1.9 TB/s of codes and scales.
+// slots (62 % of them): 256 rows to each of 8 heads over 131072 tokens 146 us alone, 940 TFLOP/s, half of the measured bf16 rate
+// (the call 156); 32 rows to each of 8 heads of 16 sequences of up to 8192 tokens: 64 us alone, 1.7 TB/s of codes and scales (the
+// call 70).
 // Every wait on an mbarrier is bounded; on expiry the CTA sets TQ_DEVERR_TIMEOUT, drains and frees TMEM.
 #include <math.h>
 
@@ -131,7 +132,8 @@ TQ_DEVFN void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d
 
 constexpr int kSoft = 8, kMma = kSoft + kDec, kWarps = kMma + 2;  // 22 warps: 80 registers a thread
 
-// The queries, rotated, over a power of two of their own, times the scale's mantissa, fp16: a warp to a row.  Of a tile of `trows` rows the 16-byte pieces
+// The queries, rotated, over a power of two of their own, times the scale's mantissa, fp16: a warp to a row.  Of a tile of `trows`
+// rows the 16-byte pieces
 // [16][trows] lie together, a thread of the next kernel reading its row's; the power's exponent beside them.
 __global__ void __launch_bounds__(256) kv_tree_turn_kernel(TreeArgs a, int tiles) {
     pdl_trigger();
