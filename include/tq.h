@@ -65,6 +65,7 @@ typedef enum tq_status {
 #define TQ_DEVERR_TIMEOUT 2u     /* a bounded spin-wait gave up */
 #define TQ_DEVERR_BAD_BOOK 4u    /* a ternary codebook that is not {c0, c0+d, c0+2d} */
 #define TQ_DEVERR_BAD_PAGE 8u    /* a cache slot, page id or sequence length out of range */
+#define TQ_DEVERR_NO_PAGE 16u    /* a page pool held too few free pages */
 
 typedef enum tq_dtype { TQ_F32 = 0, TQ_BF16 = 1, TQ_F16 = 2 } tq_dtype;
 
@@ -534,6 +535,122 @@ tq_status tq_kv_attend_tree(const tq_kv_pages_t* cache, const void* q, int64_t q
                             const uint64_t* mask, const int32_t* n_tok, float scale, void* o, void* ws,
                             size_t ws_bytes, uint32_t* err, void* stream);
 size_t tq_kv_attend_tree_workspace_bytes(const tq_kv_pages_t* cache, int32_t B, int32_t n, int32_t Hq, int64_t max_len);
+
+/* ------------------------------------------------------------------ pages of a step */
+
+/* Which pages each sequence of a paged cache holds, kept on the device: a step is planned without the host.
+ * free is a stack, its lowest n_free[0] entries the ids of free pages.  table[b] holds sequence b's pages in order,
+ * held[b] of them; entries from held[b] on are -1.  pages * page is at most 2^31 - 1. */
+typedef struct tq_page_pool_t {
+    int32_t* table;  /* device [batch][width] */
+    int32_t* held;   /* device [batch] */
+    int32_t* free;   /* device [pages] */
+    int32_t* n_free; /* device [1] */
+    int32_t batch, width;
+    int32_t page;    /* tokens of a page: a power of two, 16 to 256 */
+    int64_t pages;
+} tq_page_pool_t;
+
+/* Plans a step: sequence b holds lens[b] tokens and n_new[b] join it.  Afterwards it holds ceil((lens + n_new) / page) pages:
+ * those it has too many of go back, those it lacks come off the stack.  A call with fewer tokens than pages held gives pages
+ * back: n_new = 0 after drafts that were rejected, lens = 0 as well when a request ends.
+ *   given back: first, all sequences' in the reverse of their order (b, then place in the table), so that undoing a step leaves
+ *     the stack as it was; taken: then, by sequences in order, each page from the top.
+ *   a sequence with too few pages left for it and those that take pages before it is refused as a whole, and so is every
+ *     later one that takes pages (TQ_DEVERR_NO_PAGE); sequences that take none are always served.
+ *   a sequence whose lens, n_new or held is below 0, that would hold more than `width` pages or has more than its rows of slots is
+ *     refused too and gives nothing back (TQ_DEVERR_BAD_PAGE).
+ * slots, positions: of the new tokens, the slot (page id * page + offset) where kv_append and latent_append write, and the position
+ * lens[b] + i.  n >= 1: device [batch][n]; token i of sequence b in column i, or in column path[b*n + i] where path (device
+ * [batch][n]) is given: the accepted nodes that tq_verify_tree writes; an entry outside [0, n) drops its token
+ * (TQ_DEVERR_BAD_PAGE), of two alike either is kept.  n = 0: device [tokens], sequences one after another, path NULL, starts device
+ * [batch + 1] written: sequence b's tokens from starts[b] on (a refused one keeps its place unless n_new is out of range or its
+ * tokens pass `tokens`).  Places without a token, and those of a refused sequence, have slot -1 and position 0.
+ * new_lens: device [batch], lens + n_new, or lens where refused.  Outputs overlap neither the inputs nor each other.
+ * batch <= 2^20, batch * n and tokens <= 2^30. */
+tq_status tq_kv_plan(const tq_page_pool_t* pool, const int32_t* lens, const int32_t* n_new, const int32_t* path, int32_t n,
+                     int64_t tokens, int32_t* slots, int32_t* positions, int32_t* new_lens, int32_t* starts, uint32_t* err,
+                     void* stream);
+
+/* ------------------------------------------------------------------ verification of drafted tokens */
+
+/* Verifies B trees of up to n tokens against the target's probabilities, from given uniform numbers: the tokens that come out
+ * are distributed as if each had been sampled from the target (speculative sampling, Leviathan et al. 2023; several children of
+ * a node as Miao et al. 2024).
+ * Node 0 of a tree is its root, a token already accepted; node i >= 1 has token tokens[b*n + i] and parent parent[b*n + i] < i.
+ * p: device [B][n][V] of dt (f32, bf16 or f16), node (b, i) at (b*n + i)*p_stride: the target's distribution after node i.  q: the
+ * same of the distribution that the children of node i were drawn from, or NULL: then they were chosen, not drawn.  u: device
+ * f32 [B][n], uniform in [0, 1).
+ * The walk: node = 0, r = p[node], R = 1; for each child c of node, in order,
+ *   accepted if u[c] q[node](x) R < r(x) (x its token; q(x) = 1 without q): node = c, r = p[c], R = 1;
+ *   else r = max(r - R q[node], 0) (without q: r(x) = 0), R = its sum (without q: R less the old r(x)).
+ * path: device int32 [B][n], the accepted nodes in order, node 0 first, then -1; count: device int32 [B], how many; next: device
+ * int32 [B], the first token t with r(0) + ... + r(t) > u[0] (r(0) + ... + r(V-1)), r as the walk leaves it; p of the last node
+ * where that r is all 0, -1 where that is too.
+ * n_tok: device int32 [B] nodes in use (NULL: n); a tree without any has path -1, count 0 and next -1.  A node whose parent is
+ * not below it, or whose token is outside [0, V), is never accepted (TQ_DEVERR_BAD_ID).  Rows are taken as they are: an entry
+ * below 0 or NaN counts as 0, above 1 as 1, each in steps of 2^-50; sums are exact integers, so results do not depend on
+ * how the work is split.  n <= 1024, V <= 2^20.  Rows of a node without children that are in use are not read from q. */
+tq_status tq_verify_tree(const void* p, int64_t p_stride, const void* q, int64_t q_stride, tq_dtype dt, int32_t B, int32_t n,
+                         int32_t V, const int32_t* tokens, const int32_t* parent, const float* u, const int32_t* n_tok,
+                         int32_t* path, int32_t* count, int32_t* next, uint32_t* err, void* stream);
+
+/* ------------------------------------------------------------------ latent attention */
+
+/* A paged cache of latent attention (multi-head latent attention, DeepSeek-AI 2024): of a token, for all heads together, one
+ * latent vector, of which keys and values are projections, and one rotary key.  Row p*page_stride + i of `rows` holds token i of page p:
+ * `latent` elements, then `rope` elements with their positions.
+ * latent: 512, rope: 64.  dt: BF16 or F16.  page: 16, 32, 64, 128 or 256.  page_stride: rows, >= page.  rows 16-byte aligned. */
+typedef struct tq_latent_pages_t {
+    void* rows;
+    tq_dtype dt;
+    int32_t latent, rope, page;
+    int64_t pages, page_stride;
+} tq_latent_pages_t;
+
+/* Writes T tokens to their slots.  c: device [T][latent] of dt (f32, bf16 or f16), tokens c_stride elements apart; k_rope: device
+ * [T][rope] of dt, k_stride; both 16-byte aligned, strides a multiple of 16 bytes.  slots: device int32 [T]; a negative slot is
+ * skipped, one past the pool too, with TQ_DEVERR_BAD_PAGE.  Two tokens with one slot leave either's row, or a mixture.
+ * rope: rotary positions of k_rope on the way (its dim = cache->rope; NULL: none; positions: device int32 [T]).  Results are
+ * rounded once to the cache's type. */
+tq_status tq_latent_append(const tq_latent_pages_t* cache, const void* c, int64_t c_stride, const void* k_rope, int64_t k_stride,
+                           tq_dtype dt, int64_t T, const int32_t* slots, const tq_rope_t* rope, const int32_t* positions,
+                           uint32_t* err, void* stream);
+
+/* Attention over the latent cache itself (the absorbed form), of B trees of up to n drafted tokens each: keys are whole rows,
+ * values their latent part, one for all heads.
+ *   o[b, i, h] = sum_t p_t c_t,  p = softmax(scale * q[b, i, h] . [c_t, k_t])
+ * q: device [B][n][H][latent + rope] of the cache's type, token (b, i) at (b*n + i)*q_stride: a head's query through its key
+ * projection, then its rotary part with positions.  fresh: the drafted tokens' own rows [B][n][latent + rope] with fresh_stride,
+ * or NULL: only the context is seen.  Strides are multiples of 8 elements, pointers 16-byte aligned.
+ * table, table_stride, lens, max_len, mask, n_tok, err: as of tq_kv_attend_tree.  o: device [B][n][H][latent] of the cache's
+ * type (each head's value projection is the caller's).  A row that sees nothing gives zeros, so do rows i >= n_tok[b].
+ * What a row does not see never reaches it, whatever it holds; a row that sees a draft with an element that is not finite is NaN.
+ * Scores, softmax statistics and sums are fp32; softmax weights are rounded to the cache's type.
+ * ws: 16-byte aligned device scratch of tq_latent_attend_tree_workspace_bytes(...) bytes; calls that may run at the
+ * same time must not share it.  H <= 65535; TQ_ERR_UNSUPPORTED for more rows or steps of 64 tokens than 2^30. */
+tq_status tq_latent_attend_tree(const tq_latent_pages_t* cache, const void* q, int64_t q_stride, int32_t B, int32_t n, int32_t H,
+                                const int32_t* table, int32_t table_stride, const int32_t* lens, int64_t max_len,
+                                const void* fresh, int64_t fresh_stride, const uint64_t* mask, const int32_t* n_tok, float scale,
+                                void* o, void* ws, size_t ws_bytes, uint32_t* err, void* stream);
+size_t tq_latent_attend_tree_workspace_bytes(const tq_latent_pages_t* cache, int32_t B, int32_t n, int32_t H, int64_t max_len);
+
+/* Attention of prompts over keys and values expanded from the latents (the expanded form).
+ * Sequence b has queries q_starts[b] .. q_starts[b+1] - 1 and keys kv_starts[b] .. kv_starts[b+1] - 1 of the packed arrays (device
+ * int32 [B + 1], ascending from 0); its last query stands at its last key, and a query sees the keys up to its own place
+ * (causal = 0: all of them).
+ *   o[t, h] = sum_j p_j v[j, h],  p = softmax(scale * (q[t, h, :128] . k[j, h] + q[t, h, 128:] . k_rope[j]))
+ * q: device [Tq][H][192] of dt (BF16 or F16), tokens q_stride elements apart, heads 192; k, v: device [Tkv][H][128], tokens
+ * kv_stride and heads kv_head_stride elements apart (the expansion's own output [Tkv][H][256] serves as both); k_rope: device
+ * [Tkv][64], tokens k_rope_stride apart.  Strides are multiples of 8 elements, pointers 16-byte aligned.  o: device
+ * [Tq][H][128] of dt.  A query that sees no key gives zeros; queries from q_starts[B] on are left as they were.
+ * What a query does not see never reaches it, whatever it holds; one that sees a value that is not finite is NaN.
+ * Scores, softmax statistics and sums are fp32; softmax weights are rounded to dt.  starts out of order or past Tq or Tkv set
+ * TQ_DEVERR_BAD_PAGE and their sequence is left out. */
+tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
+                                  int64_t kv_head_stride, const void* k_rope, int64_t k_rope_stride, tq_dtype dt, int32_t B,
+                                  int32_t H, int64_t Tq, int64_t Tkv, const int32_t* q_starts, const int32_t* kv_starts,
+                                  int32_t causal, float scale, void* o, uint32_t* err, void* stream);
 
 /* ------------------------------------------------------------------ fused decode layer */
 

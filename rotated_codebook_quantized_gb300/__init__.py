@@ -8,6 +8,7 @@ raises.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -18,7 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libtq.so")
 
 TQ_F32, TQ_BF16, TQ_F16 = 0, 1, 2
 TQ_OK, TQ_ERR_INVALID, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA, TQ_ERR_TIMEOUT, TQ_ERR_DEVICE = range(6)
-TQ_DEVERR_BAD_ID, TQ_DEVERR_TIMEOUT, TQ_DEVERR_BAD_BOOK, TQ_DEVERR_BAD_PAGE = 1, 2, 4, 8
+TQ_DEVERR_BAD_ID, TQ_DEVERR_TIMEOUT, TQ_DEVERR_BAD_BOOK, TQ_DEVERR_BAD_PAGE, TQ_DEVERR_NO_PAGE = 1, 2, 4, 8, 16
 TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
 TQ_ROPE_NONE, TQ_ROPE_LINEAR, TQ_ROPE_BASE, TQ_ROPE_PARTS = range(4)
 
@@ -56,6 +57,16 @@ class tq_kv_pages_t(ctypes.Structure):
     _fields_ = [("kcodes", _c_p), ("kscales", _c_p), ("vcodes", _c_p), ("vscales", _c_p), ("Hkv", _i32), ("D", _i32),
                 ("group", _i32), ("page", _i32), ("pages", _i64), ("page_stride", _i64), ("head_stride", _i64),
                 ("kcb", tq_codebook_t), ("vcb", tq_codebook_t), ("rot", tq_rotation_t)]
+
+
+class tq_page_pool_t(ctypes.Structure):
+    _fields_ = [("table", _c_p), ("held", _c_p), ("free", _c_p), ("n_free", _c_p), ("batch", _i32), ("width", _i32),
+                ("page", _i32), ("pages", _i64)]
+
+
+class tq_latent_pages_t(ctypes.Structure):
+    _fields_ = [("rows", _c_p), ("dt", _i32), ("latent", _i32), ("rope", _i32), ("page", _i32), ("pages", _i64),
+                ("page_stride", _i64)]
 
 
 class tq_layer_desc_t(ctypes.Structure):
@@ -120,6 +131,16 @@ _SIGS = {
     "tq_kv_attend_tree": (_i32, [_P(tq_kv_pages_t), _c_p, _i64, _i32, _i32, _i32, _i32, _c_p, _i32, _c_p, _i64, _c_p,
                                  _i64, _c_p, _i64, _c_p, _c_p, ctypes.c_float, _c_p, _c_p, _sz, _c_p, _c_p]),
     "tq_kv_attend_tree_workspace_bytes": (_sz, [_P(tq_kv_pages_t), _i32, _i32, _i32, _i64]),
+    "tq_kv_plan": (_i32, [_P(tq_page_pool_t), _c_p, _c_p, _c_p, _i32, _i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "tq_verify_tree": (_i32, [_c_p, _i64, _c_p, _i64, _i32, _i32, _i32, _i32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
+                              _c_p]),
+    "tq_latent_append": (_i32, [_P(tq_latent_pages_t), _c_p, _i64, _c_p, _i64, _i32, _i64, _c_p, _P(tq_rope_t), _c_p, _c_p,
+                                _c_p]),
+    "tq_latent_attend_tree": (_i32, [_P(tq_latent_pages_t), _c_p, _i64, _i32, _i32, _i32, _c_p, _i32, _c_p, _i64, _c_p, _i64,
+                                     _c_p, _c_p, ctypes.c_float, _c_p, _c_p, _sz, _c_p, _c_p]),
+    "tq_latent_attend_tree_workspace_bytes": (_sz, [_P(tq_latent_pages_t), _i32, _i32, _i32, _i64]),
+    "tq_latent_attend_prompt": (_i32, [_c_p, _i64, _c_p, _c_p, _i64, _i64, _c_p, _i64, _i32, _i32, _i32, _i64, _i64, _c_p, _c_p,
+                                       _i32, ctypes.c_float, _c_p, _c_p, _c_p]),
     "tq_check_error": (_i32, [_c_p, _P(_u32), _c_p]),
     "tq_set_wait_budget": (_i32, [_i64]),
     "tq_rotation_dense": (_i32, [ctypes.c_uint64, _i32, _P(ctypes.c_double)]),
@@ -908,6 +929,222 @@ def kv_attend_tree(cache: PagedKVCache, q, table, lens, k_new=None, v_new=None, 
     _check(load().tq_kv_attend_tree(ctypes.byref(now[1]), q.data_ptr(), qs, _dt(q), B, n, hq, tp, wide, lp, max_len, kp, ks, vp, vs, mp,
                                     np_, dim ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr(), nb,
                                     _word(err, dev), _raw_stream(q)), "tq_kv_attend_tree")
+    return o
+
+
+# ---------------------------------------------------------------- pages of a step
+
+class PagePool:
+    """The pages of a paged cache and which sequence holds which, on the device.
+
+    ``table`` int32 [batch, width] (page ids in order, -1 past the pages held), ``held`` int32 [batch], ``free`` int32 [pages] (a
+    stack: its first ``n_free`` entries) and ``n_free`` int32 [1]; ``storage``: these four instead of new ones."""
+
+    def __init__(self, pages: int, page: int, batch: int, width: int, device="cuda", storage=None):
+        torch = _torch()
+        self.pages, self.page, self.batch, self.width = int(pages), int(page), int(batch), int(width)
+        if storage is None:
+            self.table = torch.full((self.batch, self.width), -1, dtype=torch.int32, device=device)
+            self.held = torch.zeros(self.batch, dtype=torch.int32, device=device)
+            self.free = torch.arange(self.pages - 1, -1, -1, dtype=torch.int32, device=device)  # page 0 is the first to go
+            self.n_free = torch.full((1,), self.pages, dtype=torch.int32, device=device)
+        else:
+            self.table, self.held, self.free, self.n_free = storage
+
+    def _refs(self):
+        """(descriptor, device) of the tensors as they are now."""
+        dev = self.table.get_device()
+        if not self.table.is_cuda:
+            raise ValueError("a pool's tensors must be on a CUDA device")
+        return tq_page_pool_t(_ints(self.table, "table", self.batch * self.width, dev), _ints(self.held, "held", self.batch, dev),
+                              _ints(self.free, "free", self.pages, dev), _ints(self.n_free, "n_free", 1, dev), self.batch,
+                              self.width, self.page, self.pages), dev
+
+
+Plan = collections.namedtuple("Plan", "slots positions lens starts")
+
+
+def kv_plan(pool: PagePool, lens, n_new, n: int | None = None, tokens: int | None = None, path=None, err=None) -> Plan:
+    """Pages for n_new[b] tokens that join sequences of lens[b] tokens (int32 [batch]), taken from or given back to the pool.
+
+    ``n``: slots and positions as int32 [batch, n], token i of a sequence in column i, or in column path[b, i] (int32 [batch, n]:
+    the accepted nodes of ``verify_tree``).  ``tokens`` instead: packed as int32 [tokens], sequence b's from starts[b] on.  Places
+    without a token have slot -1.  Returns (slots, positions, the lengths afterwards, starts or None)."""
+    if (n is None) == (tokens is None):
+        raise ValueError("either n (padded) or tokens (packed) is given")
+    if n is not None and n < 1 or tokens is not None and (tokens < 0 or path is not None):
+        raise ValueError("n must be at least 1, tokens at least 0 and without a path")
+    torch = _torch()
+    (c, dev), B = pool._refs(), pool.batch
+    lp, wp = _ints(lens, "lens", B, dev), _ints(n_new, "n_new", B, dev)
+    pp = 0 if path is None else _ints(path, "path", B * n, dev)
+    shape, device = ((B, n) if n is not None else (tokens,)), lens.device
+    slots = torch.empty(shape, dtype=torch.int32, device=device)
+    positions = torch.empty(shape, dtype=torch.int32, device=device)
+    after = torch.empty(B, dtype=torch.int32, device=device)
+    starts = None if n is not None else torch.empty(B + 1, dtype=torch.int32, device=device)
+    _check(load().tq_kv_plan(ctypes.byref(c), lp, wp, pp, n or 0, tokens or 0, slots.data_ptr(), positions.data_ptr(), after.data_ptr(),
+                             0 if starts is None else starts.data_ptr(), _word(err, dev), _raw_stream(pool.table)), "tq_kv_plan")
+    return Plan(slots, positions, after, starts)
+
+
+# ---------------------------------------------------------------- verification of drafted tokens
+
+def _distributions(t, name, B, n, V):
+    """Row stride of distributions [B, n, V] whose rows lie at one stride."""
+    if t.shape != (B, n, V) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor [{B}, {n}, {V}]")
+    sb, sn, sv = t.stride()
+    if (V > 1 and sv != 1) or (B > 1 and n > 1 and sb != n * sn):
+        raise ValueError(f"{name}'s rows must be contiguous and lie at one stride")
+    return max(V, sn if n > 1 else sb if B > 1 else V)
+
+
+def verify_tree(p, tokens, parent, u, q=None, n_tok=None, err=None):
+    """Verifies drafted trees against the target's probabilities p [B, n, V] (f32, bf16 or f16) from uniform numbers u f32 [B, n].
+
+    Node 0 of a tree is its root; node i has tokens[b, i], parent[b, i] < i (int32 [B, n]).  q [B, n, V]: the distributions that each
+    node's children were drawn from (None: they were chosen, not drawn).  n_tok: int32 [B] nodes in use.
+    Returns (path int32 [B, n]: the accepted nodes in order, then -1; count int32 [B]; next int32 [B]: the token after them)."""
+    if p.dim() != 3:
+        raise ValueError("p must be [B, n, V]")
+    torch, dev = _torch(), p.get_device()
+    B, n, V = p.shape
+    ps, qs, qp = _distributions(p, "p", B, n, V), 0, 0
+    if q is not None:
+        if q.dtype is not p.dtype or q.get_device() != dev:
+            raise ValueError("q must have p's dtype and device")
+        qs, qp = _distributions(q, "q", B, n, V), q.data_ptr()
+    tp, pp = _ints(tokens, "tokens", B * n, dev), _ints(parent, "parent", B * n, dev)
+    up = _ints(u, "u", B * n, dev, torch.float32)
+    cp = 0 if n_tok is None else _ints(n_tok, "n_tok", B, dev)
+    path = torch.empty((B, n), dtype=torch.int32, device=p.device)
+    count = torch.empty(B, dtype=torch.int32, device=p.device)
+    following = torch.empty(B, dtype=torch.int32, device=p.device)
+    _check(load().tq_verify_tree(p.data_ptr(), ps, qp, qs, _dt(p), B, n, V, tp, pp, up, cp, path.data_ptr(), count.data_ptr(),
+                                 following.data_ptr(), _word(err, dev), _raw_stream(p)), "tq_verify_tree")
+    return path, count, following
+
+
+# ---------------------------------------------------------------- latent attention
+
+class LatentCache:
+    """A paged cache of latent attention: rows [pages, page, latent + rope] (bf16 or f16), a token's latent vector and its rotary
+    key, shared by all heads.  ``storage``: a tensor to use instead of a new one."""
+
+    def __init__(self, pages: int, page: int, latent: int = 512, rope: int = 64, dtype=None, device="cuda", storage=None):
+        torch = _torch()
+        self.pages, self.page, self.latent, self.rope = int(pages), int(page), int(latent), int(rope)
+        self.rows = storage
+        if storage is None:
+            self.rows = torch.zeros((self.pages, self.page, self.latent + self.rope), dtype=dtype or torch.bfloat16, device=device)
+        elif dtype is not None and storage.dtype is not dtype:
+            raise ValueError("storage must have the cache's dtype")
+        self.c()
+
+    def c(self) -> tq_latent_pages_t:
+        """The descriptor of what the handle holds now."""
+        t = self.rows
+        if not t.is_cuda or tuple(t.shape) != (self.pages, self.page, self.latent + self.rope) or not t.is_contiguous():
+            raise ValueError(f"rows must be a contiguous CUDA tensor [{self.pages}, {self.page}, {self.latent + self.rope}]")
+        if t.element_size() != 2 or not t.is_floating_point():
+            raise ValueError("rows must be bf16 or f16")
+        return tq_latent_pages_t(t.data_ptr(), _dt(t), self.latent, self.rope, self.page, self.pages, self.page)
+
+
+def _rows_at(t, name, width):
+    """(rows, row stride) of t [..., width] whose rows lie at one stride."""
+    tokens, _, stride = _heads(t.unsqueeze(-2), name, width)
+    return tokens, stride
+
+
+def latent_append(cache: LatentCache, c, k_rope, slots, rope: Rope | None = None, positions=None, err=None):
+    """Write latent vectors c [..., latent] and rotary keys k_rope [..., rope] (f32, bf16 or f16; views of a fused projection are
+    fine) to ``slots`` (int32, one per token; negative: skipped).  With ``rope`` and ``positions`` the keys get their rotary
+    positions on the way."""
+    T, cs = _rows_at(c, "c", cache.latent)
+    Tk, ks = _rows_at(k_rope, "k_rope", cache.rope)
+    dev = c.get_device()
+    if T != Tk or c.dtype is not k_rope.dtype or k_rope.get_device() != dev or cache.rows.get_device() != dev:
+        raise ValueError("c, k_rope and the cache must have the same tokens, dtype and device")
+    at = _ints(slots, "slots", T, dev)
+    turn, pos = None, 0
+    if rope is not None:
+        if positions is None:
+            raise ValueError("rope needs positions")
+        if rope.steps.get_device() != dev:
+            raise ValueError("the rotary frequencies must be on the tokens' device")
+        turn, pos = rope.ref(), _ints(positions, "positions", T, dev)
+    _check(load().tq_latent_append(ctypes.byref(cache.c()), c.data_ptr(), cs, k_rope.data_ptr(), ks, _dt(c), T, at, turn, pos,
+                                   _word(err, dev), _raw_stream(c)), "tq_latent_append")
+
+
+def latent_attend_tree(cache: LatentCache, q, table, lens, scale: float, new=None, mask=None, n_tok=None,
+                       max_len: int | None = None, err=None, ws=None):
+    """Attention of drafted tokens over the latent cache (the absorbed form): q [B, n, H, latent + rope] of the cache's dtype, each
+    head's query through its key projection and its rotary part.
+
+    table, lens, max_len, mask, n_tok: as of ``kv_attend_tree``; new: the drafts' own rows [B, n, latent + rope].  scale: of the
+    scores, 1 / sqrt(length of an expanded query) in a model.  Returns [B, n, H, latent] (each head's value projection is to follow)."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, n, heads, latent + rope]")
+    width, dev = cache.latent + cache.rope, q.get_device()
+    _, H, qs = _heads(q, "q", width)
+    B, n, _, _ = q.shape
+    if q.dtype is not cache.rows.dtype or cache.rows.get_device() != dev:
+        raise ValueError("q must have the cache's dtype and device")
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"table must be [{B}, pages]")
+    wide = table.shape[1]
+    tp, lp = _ints(table, "table", B * wide, dev), _ints(lens, "lens", B, dev)
+    fp = fs = 0
+    if new is not None:
+        if new.shape != (B, n, width) or new.dtype is not q.dtype or new.get_device() != dev:
+            raise ValueError(f"new must be {[B, n, width]} of q's dtype and device")
+        fp, fs = new.data_ptr(), _rows_at(new, "new", width)[1]
+    mp = 0 if mask is None else _ints(mask, "mask", B * n * (-(-n // 64)), dev, _torch().int64)
+    np_ = 0 if n_tok is None else _ints(n_tok, "n_tok", B, dev)
+    max_len = wide * cache.page if max_len is None else int(max_len)
+    torch, device, c = _torch(), q.device, cache.c()
+    o = torch.empty((B, n, H, cache.latent), dtype=q.dtype, device=device)
+    nb = int(load().tq_latent_attend_tree_workspace_bytes(ctypes.byref(c), B, n, H, max_len))
+    if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError("ws must be contiguous, on q's device")
+    if ws is None or ws.numel() * ws.element_size() < nb:
+        ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    _check(load().tq_latent_attend_tree(ctypes.byref(c), q.data_ptr(), qs, B, n, H, tp, wide, lp, max_len, fp, fs, mp, np_, scale,
+                                        o.data_ptr(), ws.data_ptr(), nb, _word(err, dev), _raw_stream(q)), "tq_latent_attend_tree")
+    return o
+
+
+def latent_attend_prompt(q, k, v, k_rope, q_starts, kv_starts, scale: float, causal: bool = True, err=None):
+    """Attention of packed prompts over keys and values expanded from the latents (the expanded form).
+
+    q [Tq, H, 192] (the last 64 with rotary positions), k and v [Tkv, H, 128] (the two halves of one expansion [Tkv, H, 256] are
+    fine), k_rope [Tkv, 64] for all heads, bf16 or f16; q_starts, kv_starts: int32 [B + 1], sequence b's queries and keys.  Its
+    last query stands at its last key; a query sees the keys up to its own place (causal=False: all).  Returns [Tq, H, 128]."""
+    torch, dev = _torch(), q.get_device()
+    Tq, H, qs = _heads(q, "q", 192)
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (H, 128):
+        raise ValueError("q must be [Tq, H, 192], k and v [Tkv, H, 128]")
+    Tkv = k.shape[0]
+    if k.stride() != v.stride() or k.stride(-1) != 1:
+        raise ValueError("k and v must have the same strides, their heads' elements one after another")
+    Tr, rs = _rows_at(k_rope, "k_rope", 64)
+    if Tr != Tkv or not k.dtype is v.dtype is k_rope.dtype is q.dtype:
+        raise ValueError("k, v and k_rope must have the same tokens and q's dtype")
+    if not k.get_device() == v.get_device() == k_rope.get_device() == dev:
+        raise ValueError("k, v and k_rope must be on q's device")
+    B = q_starts.numel() - 1
+    if B < 0:
+        raise ValueError("q_starts must have an entry more than there are sequences")
+    qp, kp = _ints(q_starts, "q_starts", B + 1, dev), _ints(kv_starts, "kv_starts", B + 1, dev)
+    hs = k.stride(1) if H > 1 else 128
+    ks = k.stride(0) if Tkv > 1 else max(k.stride(0), (H - 1) * hs + 128)
+    o = torch.empty((Tq, H, 128), dtype=q.dtype, device=q.device)
+    _check(load().tq_latent_attend_prompt(q.data_ptr(), qs, k.data_ptr(), v.data_ptr(), ks, hs, k_rope.data_ptr(), rs, _dt(q), B, H, Tq,
+                                          Tkv, qp, kp, int(causal), scale, o.data_ptr(), _word(err, dev), _raw_stream(q)),
+           "tq_latent_attend_prompt")
     return o
 
 
