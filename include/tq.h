@@ -626,9 +626,11 @@ tq_status tq_latent_append(const tq_latent_pages_t* cache, const void* c, int64_
  * table, table_stride, lens, max_len, mask, n_tok, err: as of tq_kv_attend_tree.  o: device [B][n][H][latent] of the cache's
  * type (each head's value projection is the caller's).  A row that sees nothing gives zeros, so do rows i >= n_tok[b].
  * What a row does not see never reaches it, whatever it holds; a row that sees a draft with an element that is not finite is NaN.
- * Scores, softmax statistics and sums are fp32; softmax weights are rounded to the cache's type.
- * ws: 16-byte aligned device scratch of tq_latent_attend_tree_workspace_bytes(...) bytes; calls that may run at the
- * same time must not share it.  H <= 65535; TQ_ERR_UNSUPPORTED for more rows or steps of 64 tokens than 2^30. */
+ * Scores, softmax statistics and sums are fp32; softmax weights are rounded to the cache's type.  A bounded wait that ran out
+ * sets TQ_DEVERR_TIMEOUT; o is then incomplete.
+ * ws: 32-byte aligned device scratch of tq_latent_attend_tree_workspace_bytes(...) bytes; calls that may run at the
+ * same time must not share it.  B, H <= 65535; TQ_ERR_UNSUPPORTED for more rows, or steps of 64 tokens over all tiles of 64 rows,
+ * than 2^29. */
 tq_status tq_latent_attend_tree(const tq_latent_pages_t* cache, const void* q, int64_t q_stride, int32_t B, int32_t n, int32_t H,
                                 const int32_t* table, int32_t table_stride, const int32_t* lens, int64_t max_len,
                                 const void* fresh, int64_t fresh_stride, const uint64_t* mask, const int32_t* n_tok, float scale,
@@ -643,10 +645,11 @@ size_t tq_latent_attend_tree_workspace_bytes(const tq_latent_pages_t* cache, int
  * q: device [Tq][H][192] of dt (BF16 or F16), tokens q_stride elements apart, heads 192; k, v: device [Tkv][H][128], tokens
  * kv_stride and heads kv_head_stride elements apart (the expansion's own output [Tkv][H][256] serves as both); k_rope: device
  * [Tkv][64], tokens k_rope_stride apart.  Strides are multiples of 8 elements, pointers 16-byte aligned.  o: device
- * [Tq][H][128] of dt.  A query that sees no key gives zeros; queries from q_starts[B] on are left as they were.
- * What a query does not see never reaches it, whatever it holds; one that sees a value that is not finite is NaN.
- * Scores, softmax statistics and sums are fp32; softmax weights are rounded to dt.  starts out of order or past Tq or Tkv set
- * TQ_DEVERR_BAD_PAGE and their sequence is left out. */
+ * [Tq][H][128] of dt, 32-byte aligned.  A query that sees no key gives zeros; queries from q_starts[B] on are left as they were.
+ * What a query does not see never reaches it, whatever it holds; of one that sees a value that is not finite that element is
+ * NaN or infinite, and others may be NaN.  Scores, softmax statistics and sums are fp32; softmax weights are rounded to dt.  starts
+ * out of order or past Tq or Tkv set TQ_DEVERR_BAD_PAGE and their sequence is left out.  A bounded wait that ran out sets
+ * TQ_DEVERR_TIMEOUT; o is then incomplete. */
 tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
                                   int64_t kv_head_stride, const void* k_rope, int64_t k_rope_stride, tq_dtype dt, int32_t B,
                                   int32_t H, int64_t Tq, int64_t Tkv, const int32_t* q_starts, const int32_t* kv_starts,
@@ -808,7 +811,8 @@ tq_status tq_expert_cache_stats(const tq_expert_cache* cache, int64_t* hits, int
 tq_status tq_check_error(uint32_t* err, uint32_t* bits, void* stream);
 
 /* Test hook for the bounded waits of the tensor-core kernels (tq_gather_qmm,
- * tq_qmv_tc, tq_kv_attend_tree for more than 16 rows to a kv head) and of the three-level tensor-copy matvec (the ternary kernel of
+ * tq_qmv_tc, tq_kv_attend_tree for more than 16 rows to a kv head,
+ * tq_latent_attend_tree, tq_latent_attend_prompt) and of the three-level tensor-copy matvec (the ternary kernel of
  * calls without scratch, of groups other than 16 and of the fused input
  * stages): every wait of a pipeline role on another (an mbarrier phase)
  * gives up after `cycles` SM clock cycles, raises TQ_DEVERR_TIMEOUT in the

@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                     for (int j = 0; j < 2; ++j) {
                         top[j] = fmaxf(top[j], __shfl_xor_sync(kFull, top[j], 1));
                         top[j] = fmaxf(top[j], __shfl_xor_sync(kFull, top[j], 2));
-                        const float n = fmaxf(m[j], top[j]), to = weight_bias(n);
+                        // (each row by its own scores alone: its result must not hang on what its neighbours see)
+                        const float n = top[j] - m[j] > kSlack ? top[j] : m[j], to = weight_bias(n);
                         r[j] = m[j] == -INFINITY ? 0.f : exp2_fast(to - bias[j]);
                         m[j] = n;
                         bias[j] = to;
@@ -693,11 +694,11 @@ extern "C" tq_status tq_latent_attend_tree(const tq_latent_pages_t* cache, const
         return TQ_ERR_INVALID;
     if (B == 0 || n == 0) return TQ_OK;
     const int64_t steps = most_steps(cache, B, n, H, max_len);
-    if (!steps || B > 65535 || (int64_t)B * n > 1ll << 30) return TQ_ERR_UNSUPPORTED;
+    if (!steps || B > 65535) return TQ_ERR_UNSUPPORTED;
     if (q_stride > 1ll << 32 || fresh_stride > 1ll << 32) return TQ_ERR_UNSUPPORTED;
     const size_t need = tq_latent_attend_tree_workspace_bytes(cache, B, n, H, max_len);
     if (!q || !o || !lens || (max_len && !table) || !ws || ws_bytes < need) return TQ_ERR_INVALID;
-    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(fresh, 16) || !aligned(ws, 16) || !aligned(mask, 8) || !aligned(table, 4) ||
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(fresh, 16) || !aligned(ws, 32) || !aligned(mask, 8) || !aligned(table, 4) ||
         !aligned(lens, 4) || !aligned(n_tok, 4))
         return TQ_ERR_INVALID;
     AttendArgs a{};

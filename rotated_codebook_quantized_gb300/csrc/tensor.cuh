@@ -74,6 +74,12 @@ TQ_DEVFN void st32(uint32_t at, const uint32_t* v) {
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " TQ_L32 ";" ::TQ_I8(0), TQ_I8(8), TQ_I8(16), TQ_I8(24), "r"(at)
         : "memory");
 }
+TQ_DEVFN void ld8(uint32_t at, uint32_t* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : TQ_O8(0) : "r"(at) : "memory");
+}
+TQ_DEVFN void st8(uint32_t at, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::TQ_I8(0), "r"(at) : "memory");
+}
 // 64 columns of 16 lanes: thread t has, of each 8 columns c, elements 4 c + {0, 1} of lane t / 4, columns 8 c + 2 (t % 4) + {0, 1},
 // and 4 c + {2, 3} of lane t / 4 + 8.
 TQ_DEVFN void ld16x64(uint32_t at, uint32_t* v) {
@@ -86,6 +92,27 @@ TQ_DEVFN void ld16x64(uint32_t at, uint32_t* v) {
 #undef TQ_I8
 #undef TQ_L32
 
+using f2 = unsigned long long;  // two packed fp32
+TQ_DEVFN f2 pk(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+TQ_DEVFN float2 un(f2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+TQ_DEVFN f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+TQ_DEVFN f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 TQ_DEVFN float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

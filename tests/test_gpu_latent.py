@@ -439,7 +439,7 @@ def test_expanded_what_is_not_seen_does_not_matter(lib, what):
             end = 200 if first < 200 else 350
             assert torch.equal(got[:first], o[:first]) and torch.equal(got[end:], o[end:])
             if what == "v":
-                assert bool(got[first:end].isnan().all())
+                assert not bool(got[first:end, :, 3].isfinite().any())
             elif x != x:
                 assert bool(got[first:end].isnan().all())
 
@@ -476,6 +476,24 @@ def test_expanded_in_a_graph_and_on_another_stream(lib):
         graph.replay()
     stream.synchronize()
     _check_prompts(got, q, k, v, kr, [0, 30, 260], [0, 50, 400])
+
+
+def test_expired_waits_are_reported(lib):
+    """A wait budget of 0: a status and not a hang, and the next call as before."""
+    s = Scene(lib, 3, 2, 64, 700, 64, "bfloat16")
+    q, kv, kr, qs, ks = _prompts([300, 50], [700, 50], 2, "bfloat16", 13)
+    prompt = lambda err=None: lib.latent_attend_prompt(q, kv[..., :128], kv[..., 128:], kr, _int(qs), _int(ks), SCALE, err=err)  # noqa: E731
+    want, want2 = s.run(), prompt()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lib.set_wait_budget(0)
+    try:
+        s.run(err=err)
+        assert lib.check_error(err) & 2
+        prompt(err=err)
+        assert lib.check_error(err) & 2
+    finally:
+        lib.set_wait_budget(-1)
+    assert torch.equal(s.run(err=err), want) and torch.equal(prompt(err), want2) and lib.check_error(err) == 0
 
 
 # ---------------------------------------------------------------- together
