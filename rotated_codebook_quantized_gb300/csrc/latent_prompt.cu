@@ -7,7 +7,7 @@
 // One thread issues: values of a stream, then its next scores, then the same of the other stream, so that each stream's softmax
 // runs beside the other's products.  TMEM is full: scores and sums of two streams.  Tokens come by tensor copies into a ring of eight
 // units of 128 tokens by 64 elements; a step takes three for keys and two for values.  A row's running maximum follows only when
-// a score passes it by 2^kSlack, so O is seldom rescaled.
+// a score passes it by a set amount, so O is seldom rescaled.
 //
 // Values of steps that some row sees in part are looked through by two guard warps: those past the sequence's end are zeroed, and
 // those that are not finite, which become NaN in the rows that see them (a masked weight of 0 times NaN would reach the others).
@@ -333,9 +333,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
 #pragma unroll
             for (int k = 124; k < 128; ++k) x4[k & 3] = fmaxf(x4[k & 3], __uint_as_float(s[k]));
             const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
-            if (__any_sync(kFull, top - m > kSlack)) {
+            if (__any_sync(kFull, top - m > Weights<BF>::kSlack)) {
                 // (each row by its own scores alone: its result must not hang on what its neighbours see)
-                const float to_m = top - m > kSlack ? top : m, to = weight_bias(to_m);
+                const float to_m = top - m > Weights<BF>::kSlack ? top : m, to = Weights<BF>::bias(to_m);
                 const float r = m == -INFINITY ? 0.f : exp2_fast(to - bias);
                 m = to_m;
                 bias = to;

@@ -80,11 +80,11 @@ TQ_DEVFN void ld8(uint32_t at, uint32_t* v) {
 TQ_DEVFN void st8(uint32_t at, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::TQ_I8(0), "r"(at) : "memory");
 }
-// 64 columns of 16 lanes: thread t has, of each 8 columns c, elements 4 c + {0, 1} of lane t / 4, columns 8 c + 2 (t % 4) + {0, 1},
-// and 4 c + {2, 3} of lane t / 4 + 8.
-TQ_DEVFN void ld16x64(uint32_t at, uint32_t* v) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 " TQ_L32 ", [%32];"
-                 : TQ_O8(0), TQ_O8(8), TQ_O8(16), TQ_O8(24)
+// 32 columns of 16 lanes: thread t has, of each 8 columns k, elements 4 k + {0, 1} of lane t / 4, columns 8 k + 2 (t % 4) + {0, 1},
+// and 4 k + {2, 3} of lane t / 4 + 8.
+TQ_DEVFN void ld16x32(uint32_t at, uint32_t* v) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : TQ_O8(0), TQ_O8(8)
                  : "r"(at)
                  : "memory");
 }
@@ -123,10 +123,18 @@ TQ_DEVFN void stg256(float* p, const float* v) {
                  "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                  : "memory");
 }
-// A running maximum may be kSlack (log2) below the true one; weights are 2^(score + bias), bias = kLift - maximum rounded down: at
-// most 2^15, inside fp16, whose smallest is then 2^-31 of the largest's.
-constexpr float kSlack = 8.0f, kLift = 7.0f;
-TQ_DEVFN float weight_bias(float m) { return m == -INFINITY ? 0.f : __fadd_rd(kLift, -m); }
+TQ_DEVFN void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+// A row's weights are 2^(score + bias), bias = kLift - maximum rounded down, the maximum a running one that may be kSlack (log2) below
+// the true one before it follows.  fp16: at most 2^15, inside its range, and the smallest that it holds is 2^-31 of the largest's.
+// bf16 has fp32's range: there the maximum seldom follows after the first tokens (each time costs the rescaling of a row's
+// sums, and the products wait for it), and sums stay below 2^37 times the largest value.
+template <bool BF>
+struct Weights {
+    static constexpr float kSlack = BF ? 20.0f : 8.0f, kLift = BF ? 0.0f : 7.0f;
+    TQ_DEVFN static float bias(float m) { return m == -INFINITY ? 0.f : __fadd_rd(kLift, -m); }
+};
 // What sums of weights belong to, for joining them: -infinity where there are none.
 TQ_DEVFN float level(float m, float bias) { return m == -INFINITY ? m : -bias; }
 
