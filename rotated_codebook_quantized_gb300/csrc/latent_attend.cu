@@ -7,7 +7,8 @@
 // and as the MN-major operand of
 //   values   O[64 x 512] += P (shared) . V       2 x 2 MMAs of K = 16, N = 256
 // M = 64 takes 16 of the 32 TMEM lanes of each warp: O's upper half of the elements lies in the other 16, so that O takes 256
-// columns.  The issuing thread takes scores and values as they become ready.  A row's running maximum follows only when a score
+// columns.  Scores and values are issued by a thread each: behind its own products a thread's next
+// wait is held up, so that one for both leaves the tensor cores idle between them (1810 clocks a step, scores and values alone 1320).  A row's running maximum follows only when a score
 // passes it by a set amount.
 //
 // Tokens past the end and drafts that hold something that is not finite are zeroed in shared memory by two guard warps (a
@@ -25,19 +26,19 @@ namespace {
 
 using namespace tc;
 
-constexpr int kRows = 64, kTok = 32, kPlaces = 4;  // query rows of a tile; tokens of a step; steps in the ring
+constexpr int kRows = 64, kTok = 32, kPlaces = 5;  // query rows of a tile; tokens of a step; steps in the ring
 constexpr int kBlocks = kLatentRow / 64;           // 128-byte pieces of a row
-constexpr int kMaxSms = 256, kRoom = 4 * kMaxSms;
-constexpr int kSoft = 4, kMma = 4, kCopy = 5, kGuard = 6, kWarps = 8;
+constexpr int kMaxSms = 256;
+constexpr int kSoft = 4, kMma = 4, kCopy = 6, kGuard = 7, kWarps = 9;
 constexpr uint32_t kRingBlock = kPlaces * kTok * 128, kQBlock = kRows * 128;  // bytes of 64 elements of the ring's tokens, of the queries
-constexpr uint32_t kQ = 0, kRing = kQ + kBlocks * kQBlock, kP = kRing + kBlocks * kRingBlock, kControl = kP + kRows * 128;
+constexpr int kQTmem = 6;  // blocks of the queries that lie in TMEM; the others in shared memory
+constexpr uint32_t kQ = 0, kRing = kQ + (kBlocks - kQTmem) * kQBlock, kP = kRing + kBlocks * kRingBlock, kControl = kP + 2 * kQBlock;  // (a spare tile behind the weights)
 constexpr uint32_t kSmem = kControl + 1024 + 1024;  // the last for the start's alignment
 
 struct AttendArgs {
     LatentArgs l;
     int ctas, pad, least;  // of the schedule: CTAs, places that beginning a unit weighs, fewest places of a run
     int fresh_box;         // rows of a copy of drafts
-    bool q_copied;         // queries come by tensor copies: their tokens lie one after another
     float* part;           // [2 ctas][64][512]
     float2* stat;          // [2 ctas][64]: level and sum
     int2* units;           // [B][tiles]: first and last CTA of each unit, written by the first
@@ -186,8 +187,8 @@ struct Walk {
 };
 
 struct Control {
-    uint64_t full[kPlaces], empty[kPlaces], guarded[kPlaces], s_ready[kPlaces];  // of the ring's places
-    uint64_t p_ready[2], o_done[2], q_ready, drain;                              // [2]: of even and odd steps
+    uint64_t full[kPlaces], empty[kPlaces], guarded[kPlaces];  // of the ring's places
+    uint64_t s_ready[2], p_ready[2], o_done[2], q_ready, drain;                              // [2]: of even and odd steps
     uint32_t valid[kPlaces], odd[kPlaces][2];  // of a step's tokens: those that exist; drafts that are not finite
     Walk walk;      // past the CTA's first stretch
     Stretch first;  // which it is
@@ -212,7 +213,7 @@ TQ_DEVFN int64_t part_at(int64_t slot, int row, int e) {
 template <bool BF>
 __global__ void __launch_bounds__(32 * kWarps, 1)
     latent_attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map_rows,
-                         const __grid_constant__ CUtensorMap map_fresh, const __grid_constant__ CUtensorMap map_q) {
+                         const __grid_constant__ CUtensorMap map_fresh) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     uint8_t* const smem = raw + (base - smem_u32(raw));
@@ -229,14 +230,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                 mbar_init(c.full + i, 1);
                 mbar_init(c.empty + i, 3);  // the products and the guards
                 mbar_init(c.guarded + i, 2);
-                mbar_init(c.s_ready + i, 1);
             }
             for (int i = 0; i < 2; ++i) {
+                mbar_init(c.s_ready + i, 1);
                 mbar_init(c.p_ready + i, 32 * kSoft);
                 mbar_init(c.o_done + i, 1);
             }
-            mbar_init(&c.q_ready, a.q_copied ? 1 : 32 * kSoft);
-            mbar_init(&c.drain, 1);
+            mbar_init(&c.q_ready, 32 * kSoft);
+            mbar_init(&c.drain, 2);
             fence_mbar_init();
         }
         __syncwarp();
@@ -245,7 +246,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
         if (lane == 0) {
             prefetch_map(&map_rows);
             prefetch_map(&map_fresh);
-            prefetch_map(&map_q);
         }
         pdl_wait();
         const Run run = find_run(a, blockIdx.x);
@@ -254,12 +254,20 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             c.some = walk.next(l, c.first);
             c.walk = walk;
         }
+        __syncwarp();
+        // the first tile's queries, before the tokens' copies: they are what the products wait for
+        const uint32_t lines = c.some ? min(kRows, c.first.s.live * l.H - c.first.tile * kRows) * kBlocks : 0;
+        for (uint32_t i = lane; i < lines; i += 32) {
+            const uint32_t y = c.first.tile * kRows + i / kBlocks, token = y / (uint32_t)l.H;
+            const uint16_t* at = l.q + ((int64_t)c.first.b * l.n + token) * l.qs + (int64_t)(y - token * l.H) * kLatentRow + i % kBlocks * 64;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
     }
     pdl_wait();
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = c.tmem, to_s = tmem + 256;
+    const uint32_t tmem = c.tmem, to_s = tmem + 256, to_q = tmem + 320;
     Walk walk = c.walk;
     Stretch x = c.first;
     bool some = c.some;
@@ -337,67 +345,69 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             if (fills) mbar_wait_drain(c.full + at, (fills - 1) & 1);
         }
     } else if (warp == kMma) {
-        // ------------------------------------------------------------ MMA issue
+        // ------------------------------------------------------------ MMA issue: scores
         if (elected()) {
             bool ok = true;
-            const uint64_t dq = desc(base + kQ, 16), dk = desc(base + kRing, 16), dv = desc(base + kRing, kRingBlock),
-                           dp = desc(base + kP, 16);
-            for (; ok && some; some = walk.next(l, x)) {
-                const uint32_t ge = g + (x.s1 - x.s0);
+            const uint64_t dq = desc(base + kQ, 16), dk = desc(base + kRing, 16);
+            for (; ok && some; some = walk.next(l, x), ++seg) {
                 ok = mbar_wait(&c.q_ready, seg & 1, abort_flag, a.wait_cycles);
-                uint32_t js = g, jv = g;  // steps whose scores, and values, have been issued
-                long long since = clock64();
-                while (ok && jv < ge) {
-                    // Whatever is ready: the scores of up to two steps ahead first (their softmax is the longer way), then values, which
-                    // free their place of the ring.
-                    const uint32_t place = js % kPlaces, phase = (js / kPlaces) & 1;
-                    const bool more = js < ge && js - jv < kPlaces && mbar_peek(c.full + place, phase);
-                    const bool weights = jv < js && mbar_peek(c.p_ready + (jv & 1), (jv >> 1) & 1);
-                    if (more && (js - jv < 2 || !weights)) {
-                        const uint32_t valid = c.valid[place];
-                        if ((valid != ~0u || x.s0 + (int)(js - g) >= x.s.ctx) &&
-                            !mbar_wait(c.guarded + place, phase, abort_flag, a.wait_cycles)) {
-                            ok = false;
-                            break;
-                        }
-                        fence_after();
-                        const uint32_t id = idesc(BF, kRows, used_of(valid), 0);
-                        const uint64_t k0 = dk + place * (kTok * 128 / 16);
+                for (int s = x.s0; s < x.s1; ++s, ++g) {
+                    const uint32_t place = g % kPlaces, phase = (g / kPlaces) & 1;
+                    ok = mbar_wait(c.full + place, phase, abort_flag, a.wait_cycles);
+                    if (!ok) break;
+                    const uint32_t valid = c.valid[place];
+                    if (valid != ~0u || s >= x.s.ctx) ok = mbar_wait(c.guarded + place, phase, abort_flag, a.wait_cycles);
+                    // the scores of two steps before have been read when their weights are there
+                    if (ok && g > 1) ok = mbar_wait(c.p_ready + (g & 1), ((g - 2) >> 1) & 1, abort_flag, a.wait_cycles);
+                    if (!ok) break;
+                    fence_after();
+                    const uint32_t id = idesc(BF, kRows, used_of(valid), 0), to = to_s + kTok * (g & 1);
+                    const uint64_t k0 = dk + place * (kTok * 128 / 16);
 #pragma unroll
-                        for (int d = 0; d < kBlocks; ++d)
+                    for (int d = 0; d < kQTmem; ++d)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_ss(to_s + kTok * place, dq + d * (kQBlock / 16) + 2 * k, k0 + d * (kRingBlock / 16) + 2 * k, id,
-                                       (d | k) != 0);
-                        commit(c.s_ready + place);
-                        ++js;
-                    } else if (weights) {
-                        const uint32_t at = jv % kPlaces;
-                        fence_after();
-                        const uint64_t v0 = dv + at * (kTok * 128 / 16), p0 = dp + 4 * (jv & 1);
-                        constexpr uint32_t id = idesc(BF, kRows, 256, 1);
-                        const bool both = used_of(c.valid[at]) == 32;
-                        mma_ss(tmem, p0, v0, id, jv != g);
-                        mma_ss(tmem + (16u << 16), p0, v0 + 4 * (kRingBlock / 16), id, jv != g);
-                        if (both) {
-                            mma_ss(tmem, p0 + 2, v0 + 128, id, 1);
-                            mma_ss(tmem + (16u << 16), p0 + 2, v0 + 128 + 4 * (kRingBlock / 16), id, 1);
-                        }
-                        commit(c.empty + at);
-                        commit(c.o_done + (jv & 1));
-                        ++jv;
-                    } else {
-                        if (*abort_flag) ok = false;
-                        if (clock64() - since > a.wait_cycles) *abort_flag = 1;
-                        continue;
-                    }
-                    since = clock64();
+                        for (int k = 0; k < 4; ++k)
+                            mma_ts(to, to_q + 32 * d + 8 * k, k0 + d * (kRingBlock / 16) + 2 * k, id, (d | k) != 0);
+#pragma unroll
+                    for (int d = kQTmem; d < kBlocks; ++d)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss(to, dq + (d - kQTmem) * (kQBlock / 16) + 2 * k, k0 + d * (kRingBlock / 16) + 2 * k, id, 1);
+                    commit(c.s_ready + (g & 1));
                 }
-                g = ge;
-                ++seg;
             }
             commit(&c.drain);  // completes when every MMA issued above has finished
-            if (!mbar_wait_drain(&c.drain, 0)) *abort_flag = 1;
+        }
+        __syncwarp();
+    } else if (warp == kMma + 1) {
+        // ------------------------------------------------------------ MMA issue: values
+        if (elected()) {
+            bool ok = true;
+            const uint64_t dv = desc(base + kRing, kRingBlock), dp = desc(base + kP, 16);
+            for (; ok && some; some = walk.next(l, x)) {
+                for (int s = x.s0; s < x.s1; ++s, ++g) {
+                    const uint32_t place = g % kPlaces;
+                    ok = mbar_wait(c.p_ready + (g & 1), (g >> 1) & 1, abort_flag, a.wait_cycles);
+                    if (!ok) break;
+                    // (complete since before the scores; waiting on it too orders `valid` before its read)
+                    ok = mbar_wait(c.full + place, (g / kPlaces) & 1, abort_flag, a.wait_cycles);
+                    if (!ok) break;
+                    fence_after();
+                    const uint64_t v0 = dv + place * (kTok * 128 / 16), p0 = dp + 4 * (g & 1);
+                    constexpr uint32_t id = idesc(BF, kRows, 256, 1);
+                    const uint32_t more = s != x.s0;
+                    const bool both = used_of(c.valid[place]) == 32;
+                    mma_ss(tmem, p0, v0, id, more);
+                    mma_ss(tmem + (16u << 16), p0, v0 + 4 * (kRingBlock / 16), id, more);
+                    if (both) {
+                        mma_ss(tmem, p0 + 2, v0 + 128, id, 1);
+                        mma_ss(tmem + (16u << 16), p0 + 2, v0 + 128 + 4 * (kRingBlock / 16), id, 1);
+                    }
+                    commit(c.empty + place);
+                    commit(c.o_done + (g & 1));
+                }
+            }
+            commit(&c.drain);
         }
         __syncwarp();
     } else if (warp >= kGuard) {
@@ -460,35 +470,55 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
         const float2 scale2 = make_float2(l.scale2, l.scale2);
         const f2 ff = pk(scale2.x, scale2.y);
         bool ok = true;
-        uint32_t asked = 0;  // tiles of queries
         for (; ok && some; some = walk.next(l, x)) {
             const uint32_t ge = g + (x.s1 - x.s0);
             const uint32_t y0 = x.tile * kRows;
             const int rows = min(kRows, x.s.live * l.H - (int)y0);
             // ---- the tile's queries (the last scores of the stretch before have been read, so its queries are free)
-            ++asked;
-            if (a.q_copied) {
-                if (tid == 0) {
-                    mbar_expect_tx(&c.q_ready, kBlocks * kQBlock);
-#pragma unroll 1
-                    for (int d = 0; d < kBlocks; ++d)
-                        tma_load_2d(base + kQ + d * kQBlock, &map_q, d * 64, x.b * l.n * l.H + (int)y0, &c.q_ready);
-                }
-                __syncwarp();
-            } else {  // eight threads to a row, 128 bytes at a time
-#pragma unroll 1
-                for (int k = 0; k < kRows / 16; ++k) {
-                    const int r = 16 * k + (tid >> 3), piece = tid & 7;
-                    const uint32_t y = y0 + min(r, rows - 1), token = y / (uint32_t)l.H;
-                    const uint16_t* src = l.q + ((int64_t)x.b * l.n + token) * l.qs + (int64_t)(y - token * l.H) * kLatentRow + piece * 8;
-                    const uint32_t dst = base + kQ + r * 128 + ((piece ^ (r & 7)) << 4), size = r < rows ? 16 : 0;
+            // Six blocks go to TMEM, whose lanes 16 .. 31 of a warp repeat its 16 rows (M = 64 wants A in both halves), by way of
+            // shared memory: five where the others, the weights and a spare tile lie, then one beside the others.
+            {
+                const int r0 = warp * 16, r = r0 + (lane & 15);
+                const uint16_t* src[4];  // eight lanes to a row, 16 bytes each
 #pragma unroll
-                    for (int d = 0; d < kBlocks; ++d)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + d * kQBlock), "l"(src + d * 64),
-                                     "r"(size)
-                                     : "memory");
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t y = y0 + min(r0 + 4 * k + (lane >> 3), rows - 1), token = y / (uint32_t)l.H;
+                    src[k] = l.q + ((int64_t)x.b * l.n + token) * l.qs + (int64_t)(y - token * l.H) * kLatentRow + (lane & 7) * 8;
                 }
+                auto bring = [&](int d, uint32_t tile) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = r0 + 4 * k + (lane >> 3);
+                        const uint32_t dst = base + tile + row * 128 + (((lane ^ row) & 7) << 4);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src[k] + d * 64) : "memory");
+                    }
+                };
+                auto move = [&](int d, uint32_t tile) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        const uint4 z = *reinterpret_cast<const uint4*>(smem + tile + r * 128 + ((p ^ (r & 7)) << 4));
+                        v[4 * p] = z.x, v[4 * p + 1] = z.y, v[4 * p + 2] = z.z, v[4 * p + 3] = z.w;
+                    }
+                    st32(to_q + 32 * d + lanes, v);
+                };
+                auto tile_of = [](int d) { return d < 3 ? kQ + d * kQBlock : kP + (d - 3) * kQBlock; };
+#pragma unroll
+                for (int d = 0; d < kQTmem - 1; ++d) bring(d, tile_of(d));
                 asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
+#pragma unroll 1
+                for (int d = 0; d < kQTmem - 1; ++d) move(d, tile_of(d));
+                __syncwarp();
+                bring(kQTmem - 1, kP);
+#pragma unroll
+                for (int d = kQTmem; d < kBlocks; ++d) bring(d, kQ + (d - kQTmem) * kQBlock);
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
+                move(kQTmem - 1, kP);
+                wait_st();
+                __syncwarp();  // (its tile takes weights next)
+                fence_before();
                 fence_async_smem();
                 mbar_arrive(&c.q_ready);
             }
@@ -499,11 +529,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             for (uint32_t i = g; i < ge; ++i) {
                 const uint32_t place = i % kPlaces, phase = (i / kPlaces) & 1;
                 const int s = x.s0 + (int)(i - g);
-                ok = __all_sync(kFull, mbar_wait(c.s_ready + place, phase, abort_flag, a.wait_cycles));
+                ok = __all_sync(kFull, mbar_wait(c.s_ready + (i & 1), (i >> 1) & 1, abort_flag, a.wait_cycles));
                 if (!ok) break;
                 fence_after();
                 uint32_t v[16];  // of 8 columns k: element 4 k + 2 j + e is row j, column 8 k + 2 (lane % 4) + e
-                ld16x32(to_s + kTok * place + lanes, v);
+                ld16x32(to_s + kTok * (i & 1) + lanes, v);
                 // (its tokens' barrier has completed before the scores; waiting on it too orders `valid` before its read)
                 ok = __all_sync(kFull, mbar_wait(c.full + place, phase, abort_flag, a.wait_cycles));
                 if (!ok) break;
@@ -658,9 +688,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             g = ge;
             ++seg;
         }
-        if (a.q_copied && tid == 0 && asked) mbar_wait_drain(&c.q_ready, (asked - 1) & 1);  // (as the tokens' copies)
     }
 
+    if (warp == kMma && elected() && !mbar_wait_drain(&c.drain, 0)) *abort_flag = 1;
+    __syncwarp();
     fence_before();
     __syncthreads();
     if (tid == 0 && *abort_flag && l.err) atomicOr(l.err, TQ_DEVERR_TIMEOUT);
@@ -674,8 +705,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
 // 1 / gridDim.z of the rows of a tile.
 template <bool BF>
 __global__ void __launch_bounds__(256) latent_join_kernel(AttendArgs a) {
-    __shared__ float s_weight[kRoom];  // [parts][rows of this CTA], as many as fit at a time
-    __shared__ float s_top[kRows], s_over[kRows];
     pdl_trigger();
     pdl_wait();
     const LatentArgs& l = a.l;
@@ -693,57 +722,43 @@ __global__ void __launch_bounds__(256) latent_join_kernel(AttendArgs a) {
     const int c0 = unit.x, c1 = unit.y;
     if (c0 == c1) return;  // one CTA has written its rows
     auto slot_of = [&](int c) { return 2ll * c + (c == c0); };
-    // ---- weights of a row's parts: 2^level over the highest, over the sum
-    if (tid < live) {
-        float top = -INFINITY, total = 0.f;
-        for (int c = c0; c <= c1; ++c) top = fmaxf(top, a.stat[slot_of(c) * kRows + r0 + tid].x);
-        for (int c = c0; c <= c1; ++c) {
-            const float2 z = a.stat[slot_of(c) * kRows + r0 + tid];
-            total += z.y * (z.x == top ? 1.f : exp2_fast(z.x - top));
-        }
-        s_top[tid] = top;
-        s_over[tid] = total == 0.f ? 0.f : 1.f / total;
-    }
-    __syncthreads();
-    // two rows at a time, 128 threads to a row; each round of parts as many as have room for their weights
-    const int room = kRoom / own_rows;
-    for (int first = c0; first <= c1; first += room) {
-        const int last = min(first + room - 1, c1);
-        __syncthreads();
-        for (int i = tid; i < (last - first + 1) * live; i += 256) {
-            const int c = first + i / live, r = i % live;
-            const float level = a.stat[slot_of(c) * kRows + r0 + r].x;
-            s_weight[(c - first) * own_rows + r] = (level == s_top[r] ? 1.f : exp2_fast(level - s_top[r])) * s_over[r];
-        }
-        __syncthreads();
-        // a thread to a row and 8 elements; neighbours have the rows of a store's run
-        for (int i = tid; i < own_rows * (kLatent / 8); i += 256) {
-            const int r = i % own_rows, e = i / own_rows * 2;
-            if (r >= live) continue;
-            float o[8] = {};
-            float* const kept[2] = {a.part + part_at(slot_of(c0), r0 + r, e), a.part + part_at(slot_of(c0), r0 + r, e + 1)};  // what rounds hand on
-            auto add = [&](int c, float w) {
+    // A thread to a row and 8 elements; neighbours have the rows of a store's run.  Four parts on their way at a time.
+    constexpr int kAhead = 4;
+    for (int i = tid; i < own_rows * (kLatent / 8); i += 256) {
+        const int r = i % own_rows, e = i / own_rows * 2;
+        if (r >= live) continue;
+        float o[8] = {}, top = -INFINITY, total = 0.f;
+        for (int c = c0; c <= c1; c += kAhead) {
+            float2 stat[kAhead];
+            float4 z[kAhead][2];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int64_t slot = slot_of(min(c + k, c1));
+                stat[k] = a.stat[slot * kRows + r0 + r];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) z[k][h] = *reinterpret_cast<const float4*>(a.part + part_at(slot, r0 + r, e + h));
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (c + k > c1) break;
+                // both to the higher level: weight 1 for its own (also where neither saw anything)
+                const float n = fmaxf(top, stat[k].x), w0 = top == n ? 1.f : exp2_fast(top - n),
+                            w1 = stat[k].x == n ? 1.f : exp2_fast(stat[k].x - n);
+                top = n;
+                total = total * w0 + stat[k].y * w1;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float4 z = *reinterpret_cast<const float4*>(a.part + part_at(slot_of(c), r0 + r, e + h));
-                    o[4 * h] = fmaf(z.x, w, o[4 * h]);
-                    o[4 * h + 1] = fmaf(z.y, w, o[4 * h + 1]);
-                    o[4 * h + 2] = fmaf(z.z, w, o[4 * h + 2]);
-                    o[4 * h + 3] = fmaf(z.w, w, o[4 * h + 3]);
+                    o[4 * h] = fmaf(o[4 * h], w0, z[k][h].x * w1);
+                    o[4 * h + 1] = fmaf(o[4 * h + 1], w0, z[k][h].y * w1);
+                    o[4 * h + 2] = fmaf(o[4 * h + 2], w0, z[k][h].z * w1);
+                    o[4 * h + 3] = fmaf(o[4 * h + 3], w0, z[k][h].w * w1);
                 }
-            };
-            if (first != c0) add(c0, 1.f);
-#pragma unroll 4
-            for (int c = first; c <= last; ++c) add(c, s_weight[(c - first) * own_rows + r]);
-            if (last == c1) {
-                *reinterpret_cast<uint4*>(out + (int64_t)r * kLatent + e * 4) =
-                    make_uint4(pack16<BF>(o[0], o[1]), pack16<BF>(o[2], o[3]), pack16<BF>(o[4], o[5]), pack16<BF>(o[6], o[7]));
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<float4*>(kept[h]) = make_float4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
             }
         }
+        const float over = total == 0.f ? 0.f : 1.f / total;  // (a NaN sum stays one)
+        *reinterpret_cast<uint4*>(out + (int64_t)r * kLatent + e * 4) =
+            make_uint4(pack16<BF>(o[0] * over, o[1] * over), pack16<BF>(o[2] * over, o[3] * over), pack16<BF>(o[4] * over, o[5] * over),
+                       pack16<BF>(o[6] * over, o[7] * over));
     }
 }
 
@@ -765,9 +780,9 @@ int64_t most_steps(const tq_latent_pages_t* cache, int32_t B, int32_t n, int32_t
 }
 
 template <bool BF>
-tq_status launch(const AttendArgs& a, const CUtensorMap& rows, const CUtensorMap& fresh, const CUtensorMap& q, cudaStream_t st) {
+tq_status launch(const AttendArgs& a, const CUtensorMap& rows, const CUtensorMap& fresh, cudaStream_t st) {
     if (ensure_smem((const void*)latent_attend_kernel<BF>, kSmem) != cudaSuccess) return TQ_ERR_CUDA;
-    tq_status s = launch_pdl(latent_attend_kernel<BF>, dim3((unsigned)a.ctas), dim3(32 * kWarps), kSmem, st, a, rows, fresh, q);
+    tq_status s = launch_pdl(latent_attend_kernel<BF>, dim3((unsigned)a.ctas), dim3(32 * kWarps), kSmem, st, a, rows, fresh);
     if (s != TQ_OK) return s;
     const int64_t tiles = ((int64_t)a.l.n * a.l.H + kRows - 1) / kRows;
     const int64_t units = tiles * a.l.B;
@@ -837,15 +852,13 @@ extern "C" tq_status tq_latent_attend_tree(const tq_latent_pages_t* cache, const
     a.part = reinterpret_cast<float*>(ws);
     a.stat = reinterpret_cast<float2*>(a.part + 2ll * a.ctas * kRows * kLatent);
     a.units = reinterpret_cast<int2*>(a.stat + 2ll * a.ctas * kRows);
-    a.q_copied = q_stride == (int64_t)H * kLatentRow;
     a.wait_cycles = wait_budget();
     const bool bf = cache->dt == TQ_BF16;
-    CUtensorMap rows, drafts, queries;
+    CUtensorMap rows, drafts;
     // (an empty pool has no page that a copy could reach)
     if (!tensor_map(&rows, bf, cache->pages ? cache->rows : q, std::max<int64_t>(cache->pages * cache->page_stride, 1), kLatentRow,
                     kLatentRow, std::min(cache->page, kTok)) ||
-        !tensor_map(&drafts, bf, fresh ? fresh : q, (int64_t)B * n, kLatentRow, fresh ? fresh_stride : kLatentRow, a.fresh_box) ||
-        !tensor_map(&queries, bf, q, (int64_t)B * n * H, kLatentRow, kLatentRow, kRows))
+        !tensor_map(&drafts, bf, fresh ? fresh : q, (int64_t)B * n, kLatentRow, fresh ? fresh_stride : kLatentRow, a.fresh_box))
         return TQ_ERR_CUDA;
-    return bf ? launch<true>(a, rows, drafts, queries, as_stream(stream)) : launch<false>(a, rows, drafts, queries, as_stream(stream));
+    return bf ? launch<true>(a, rows, drafts, as_stream(stream)) : launch<false>(a, rows, drafts, as_stream(stream));
 }
