@@ -38,56 +38,101 @@ struct PromptArgs {
     const int32_t* kv_starts;
     uint16_t* o;
     uint32_t* err;
-    int B, H;
+    int B, H, heads;  // heads: of a group
     bool causal;
     float scale2;  // scale * log2(e)
     long long wait_cycles;
 };
 
-// Of a CTA: its rows and keys as places of the packed arrays, and what its first row stands at.
+// A job: a tile of a sequence and head.  Its rows and keys as places of the packed arrays.
 struct Job {
-    int q0, rows;   // rows in use
-    int k0, keys;   // of the sequence
-    int at;         // key of the first row's own place, less k0; the rows' are at + row (causal)
+    int q0, rows;  // rows in use; -1: no more jobs
+    int k0, keys;  // of the sequence
+    int at;        // key of the first row's own place, less k0; the rows' are at + row (causal)
+    int head;
 };
-TQ_DEVFN bool span(const PromptArgs& a, int b, int& q0, int& q1, int& k0, int& k1) {
-    q0 = a.q_starts[b], q1 = a.q_starts[b + 1], k0 = a.kv_starts[b], k1 = a.kv_starts[b + 1];
-    return q0 >= 0 && q0 <= q1 && q1 <= a.Tq && k0 >= 0 && k0 <= k1 && k1 <= a.Tkv;
+struct Span {
+    int q0, q1, k0, k1, tiles;
+    bool bad;
+};
+TQ_DEVFN Span span(const PromptArgs& a, int b) {
+    Span s{};
+    if (b >= a.B) return s;
+    s.q0 = a.q_starts[b], s.q1 = a.q_starts[b + 1], s.k0 = a.kv_starts[b], s.k1 = a.kv_starts[b + 1];
+    s.bad = !(s.q0 >= 0 && s.q0 <= s.q1 && s.q1 <= a.Tq && s.k0 >= 0 && s.k0 <= s.k1 && s.k1 <= a.Tkv);
+    s.tiles = s.bad ? 0 : (s.q1 - s.q0 + kTile - 1) / kTile;
+    return s;
 }
-// Tile `at` of the batch, counted from the last (late rows of a sequence see most: they go first); rows 0 where there is none (one
-// warp).
-TQ_DEVFN Job find_job(const PromptArgs& a, int at, bool report) {
+// Tiles of a sequence that take more than `steps` steps: its last ones.
+TQ_DEVFN int tiles_above(const PromptArgs& a, const Span& s, int steps) {
+    if (steps < 0 || !s.tiles) return s.tiles;
+    if (s.k1 - s.k0 <= steps * kTok) return 0;
+    if (!a.causal) return s.tiles;
+    // a tile whose last row is the e-th sees keys - queries + e of them
+    return s.tiles - max(steps * kTok + (s.q1 - s.q0) - (s.k1 - s.k0), 0) / kTile;
+}
+// Jobs go in groups of `heads` heads, whose keys and values the L2 cache holds; in a group those with the most steps first.  A CTA
+// takes every gridDim.x-th, in turns from the front and from the back.
+struct Jobs {
+    int tiles, most;  // of a head; steps of the longest
+};
+TQ_DEVFN Jobs count_jobs(const PromptArgs& a, bool report) {  // (one warp)
+    int tiles = 0, most = 0;
+    bool bad = false;
+    for (int b = threadIdx.x & 31; b < a.B; b += 32) {
+        const Span s = span(a, b);
+        bad |= s.bad;
+        tiles += s.tiles;
+        if (s.tiles) most = max(most, (s.k1 - s.k0 + kTok - 1) / kTok);
+    }
+    if (report && bad && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
+    return {(int)__reduce_add_sync(kFull, tiles), (int)__reduce_max_sync(kFull, most)};
+}
+TQ_DEVFN Job find_job(const PromptArgs& a, const Jobs& jobs, int64_t at) {  // (one warp)
     const int lane = threadIdx.x & 31;
     Job j{};
-    bool bad = false;
-    for (int end = a.B; end > 0; end -= 32) {  // sequences end - 1, end - 2, ...
-        const int b = end - 1 - lane;
-        int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-        bool ok = b >= 0 && span(a, b, q0, q1, k0, k1);
-        bad |= b >= 0 && !ok;
-        const int tiles = ok ? (q1 - q0 + kTile - 1) / kTile : 0;
-        int upto = tiles;
+    j.rows = -1;
+    if (at >= (int64_t)jobs.tiles * a.H) return j;
+    const int group = (int)(at / ((int64_t)jobs.tiles * a.heads)), in = min(a.heads, a.H - group * a.heads);
+    const int left = (int)(at - (int64_t)group * jobs.tiles * a.heads);
+    j.head = group * a.heads + left % in;
+    int rank = left / in;
+    // the fewest steps s that no more than `rank` tiles pass
+    auto above = [&](int steps) {
+        int n = 0;
+        for (int b = lane; b < a.B; b += 32) n += tiles_above(a, span(a, b), steps);
+        return (int)__reduce_add_sync(kFull, n);
+    };
+    int lo = 0, hi = jobs.most;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (above(mid) <= rank) hi = mid;
+        else lo = mid + 1;
+    }
+    rank -= above(lo);  // of the tiles of exactly lo steps, in order
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const Span s = span(a, b0 + lane);
+        const int over = tiles_above(a, s, lo), own = tiles_above(a, s, lo - 1) - over;
+        int upto = own;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const int x = __shfl_up_sync(kFull, upto, m);
             if (lane >= m) upto += x;
         }
-        const unsigned hit = __ballot_sync(kFull, upto > at);
-        if (hit && j.rows == 0) {
+        const unsigned hit = __ballot_sync(kFull, upto > rank);
+        if (hit) {
             const int src = __ffs(hit) - 1;
-            const int tile = __shfl_sync(kFull, tiles, src) - 1 - (at - __shfl_sync(kFull, upto - tiles, src));
-            q0 = __shfl_sync(kFull, q0, src), q1 = __shfl_sync(kFull, q1, src);
-            k0 = __shfl_sync(kFull, k0, src), k1 = __shfl_sync(kFull, k1, src);
+            const int tile = __shfl_sync(kFull, s.tiles - over - 1 - (rank - (upto - own)), src);
+            const int q0 = __shfl_sync(kFull, s.q0, src), q1 = __shfl_sync(kFull, s.q1, src);
+            j.k0 = __shfl_sync(kFull, s.k0, src);
+            j.keys = __shfl_sync(kFull, s.k1, src) - j.k0;
             j.q0 = q0 + tile * kTile;
             j.rows = min(kTile, q1 - j.q0);
-            j.k0 = k0;
-            j.keys = k1 - k0;
             j.at = j.keys - (q1 - q0) + tile * kTile;
-            if (!report) break;
+            break;
         }
-        at -= __shfl_sync(kFull, upto, 31);
+        rank -= __shfl_sync(kFull, upto, 31);
     }
-    if (report && bad && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
     return j;
 }
 // Keys that row r of the job sees: the first `seen_by`.
@@ -100,14 +145,43 @@ TQ_DEVFN int steps_of(const PromptArgs& a, const Job& j, int t) {
 TQ_DEVFN int whole_of(const PromptArgs& a, const Job& j, int t) { return seen_by(a, j, t * kRows) / kTok; }
 
 struct Control {
-    uint64_t q_full[kStreams], k_full[2], v_full[2], k_empty[2], v_empty[2], guarded[2];  // [2]: of even and odd steps
-    uint64_t s_ready[kStreams], p_ready[kStreams], o_done[kStreams], drain;
+    uint64_t q_full[kStreams], q_empty[kStreams], k_full[2], v_full[2], k_empty[2], v_empty[2], guarded[2];  // [2]: even, odd steps
+    uint64_t s_ready[kStreams], p_ready[kStreams], o_done[kStreams], job_full[2], job_empty[2], drain;
     uint32_t odd[2][4];  // values of a step that are not finite
-    Job job;
+    Job job[2];          // of even and odd jobs of the CTA
     uint32_t tmem;
     int abort;
 };
 static_assert(sizeof(Control) <= 1024, "control block");
+
+// A role's way through the CTA's jobs.
+struct Way {
+    Control& c;
+    volatile int* abort_flag;
+    long long wait_cycles;
+    uint32_t n = 0;  // jobs so far
+    Job j{};
+    int n0 = 0, n1 = 0, steps = 0, part = 0;  // steps of the streams, of both, and those that need no guard
+    TQ_DEVFN Way(Control& c, volatile int* abort_flag, long long wait_cycles) : c(c), abort_flag(abort_flag), wait_cycles(wait_cycles) {}
+    TQ_DEVFN void see(const PromptArgs& a) {
+        n0 = steps_of(a, j, 0);
+        n1 = steps_of(a, j, 1);
+        steps = max(n0, n1);
+        part = min(n0 ? whole_of(a, j, 0) : steps, n1 ? whole_of(a, j, 1) : steps);
+    }
+    // The next job: false where there is none (`ok` false: the CTA gives up).
+    TQ_DEVFN bool next(const PromptArgs& a, bool& ok) {
+        ok = mbar_wait(c.job_full + (n & 1), (n >> 1) & 1, abort_flag, wait_cycles);
+        if (!ok) return false;
+        j = c.job[n & 1];
+        if (j.rows < 0) return false;
+        see(a);
+        return true;
+    }
+    TQ_DEVFN void done() {  // (one thread of the warp)
+        mbar_arrive(c.job_empty + (n & 1));
+    }
+};
 
 template <bool BF>
 __global__ void __launch_bounds__(32 * kWarps, 1)
@@ -119,7 +193,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     uint8_t* const smem = raw + (base - smem_u32(raw));
     Control& c = *reinterpret_cast<Control*>(smem + kControl);
     volatile int* abort_flag = &c.abort;
-    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31, h = blockIdx.y;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
 
     pdl_trigger();
     if (warp == kMma) {
@@ -127,6 +201,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             c.abort = 0;
             for (int i = 0; i < 2; ++i) {
                 mbar_init(c.q_full + i, 1);
+                mbar_init(c.q_empty + i, 1);
                 mbar_init(c.k_full + i, 1);
                 mbar_init(c.v_full + i, 1);
                 mbar_init(c.k_empty + i, 1);
@@ -135,109 +210,155 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                 mbar_init(c.s_ready + i, 1);
                 mbar_init(c.p_ready + i, 128);
                 mbar_init(c.o_done + i, 1);
+                mbar_init(c.job_full + i, 1);
+                mbar_init(c.job_empty + i, kWarps - 1);  // every warp but the one that finds them
             }
             mbar_init(&c.drain, 1);
             fence_mbar_init();
         }
         __syncwarp();
         alloc512(&c.tmem);
+    } else if (warp == kCopy && lane == 0) {
+        prefetch_map(&map_q);
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+        prefetch_map(&map_r);
     }
     pdl_wait();
-    if (warp == kCopy) {
-        const Job j = find_job(a, blockIdx.x, blockIdx.x == 0 && h == 0);
-        if (lane == 0) c.job = j;
-    }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = c.tmem;
-    const Job j = c.job;
-    const int n0 = steps_of(a, j, 0), n1 = steps_of(a, j, 1), n = max(n0, n1);
-    // steps from here on are looked through by the guards
-    const int part = min(n0 ? whole_of(a, j, 0) : n, n1 ? whole_of(a, j, 1) : n);
+    Way w(c, abort_flag, a.wait_cycles);
+    uint32_t g = 0;  // steps of the CTA so far: the ring's places and the phases of its barriers
 
     if (warp == kCopy) {
-        // ------------------------------------------------------------ tensor copies
+        // ------------------------------------------------------------ jobs and tensor copies
+        const Jobs jobs = count_jobs(a, blockIdx.x == 0);
         bool ok = true;
-        int k_done = 0, v_done = 0;
-        if (n && elected()) {
-            for (int t = 0; t < kStreams; ++t) {
-                mbar_expect_tx(c.q_full + t, kQUnits * kUnit);
-                for (int d = 0; d < kQUnits; ++d)
-                    tma_load_2d(base + (t * kQUnits + d) * kUnit, &map_q, h * kHeadQuery + d * 64, j.q0 + t * kRows, c.q_full + t);
+        uint32_t k_done = 0, v_done = 0, q_done[kStreams] = {0, 0};
+        for (; ok; ++w.n) {
+            const uint32_t from = w.n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+            w.j = find_job(a, jobs, (int64_t)w.n * gridDim.x + from);
+            if (w.n >= 2) ok = __all_sync(kFull, mbar_wait(c.job_empty + (w.n & 1), ((w.n - 2) >> 1) & 1, abort_flag, a.wait_cycles));
+            if (!ok) break;
+            if (lane == 0) {
+                c.job[w.n & 1] = w.j;
+                mbar_arrive(c.job_full + (w.n & 1));
             }
-            for (int i = 0; i < n && ok; ++i) {
-                const int e = i & 1, row = j.k0 + i * kTok, x = (int)(h * a.kvh);
-                auto unit = [&](int u) { return base + kRing + ((i * kStep + u) % kUnits) * kUnit; };
+            __syncwarp();
+            if (w.j.rows < 0) break;
+            w.see(a);
+            const int row0 = w.j.k0, x = (int)(w.j.head * a.kvh);
+            for (int i = 0; i < w.steps && ok; ++i, ++g) {
+                const uint32_t e = g & 1;
+                const int row = row0 + i * kTok;
+                auto unit = [&](uint32_t u) { return base + kRing + ((g * kStep + u) % kUnits) * kUnit; };
                 // its keys lie where the last keys and the values of two steps before did, its values where keys of the step before did
-                if (i >= 2) ok = mbar_wait(c.v_empty + e, ((i - 2) >> 1) & 1, abort_flag, a.wait_cycles);
+                if (g >= 2) ok = __all_sync(kFull, mbar_wait(c.v_empty + e, ((g - 2) >> 1) & 1, abort_flag, a.wait_cycles));
                 if (!ok) break;
-                mbar_expect_tx(c.k_full + e, kQUnits * kUnit);
-                tma_load_2d(unit(0), &map_k, x, row, c.k_full + e);
-                tma_load_2d(unit(1), &map_k, x + 64, row, c.k_full + e);
-                tma_load_2d(unit(2), &map_r, 0, row, c.k_full + e);
+                if (elected()) {
+                    mbar_expect_tx(c.k_full + e, kQUnits * kUnit);
+                    tma_load_2d(unit(0), &map_k, x, row, c.k_full + e);
+                    tma_load_2d(unit(1), &map_k, x + 64, row, c.k_full + e);
+                    tma_load_2d(unit(2), &map_r, 0, row, c.k_full + e);
+                }
+                __syncwarp();
                 ++k_done;
-                if (i >= 1) ok = mbar_wait(c.k_empty + (e ^ 1), ((i - 1) >> 1) & 1, abort_flag, a.wait_cycles);
+                if (i == 0)  // the job's queries, once the last products of the job before have read theirs
+                    for (int t = 0; t < kStreams && ok; ++t) {
+                        if (!(t ? w.n1 : w.n0)) continue;
+                        if (q_done[t])
+                            ok = __all_sync(kFull, mbar_wait(c.q_empty + t, (q_done[t] - 1) & 1, abort_flag, a.wait_cycles));
+                        if (!ok) break;
+                        if (elected()) {
+                            mbar_expect_tx(c.q_full + t, kQUnits * kUnit);
+                            for (int d = 0; d < kQUnits; ++d)
+                                tma_load_2d(base + (t * kQUnits + d) * kUnit, &map_q, w.j.head * kHeadQuery + d * 64,
+                                            w.j.q0 + t * kRows, c.q_full + t);
+                        }
+                        __syncwarp();
+                        ++q_done[t];
+                    }
+                if (g >= 1 && ok) ok = __all_sync(kFull, mbar_wait(c.k_empty + (e ^ 1), ((g - 1) >> 1) & 1, abort_flag, a.wait_cycles));
                 if (!ok) break;
-                mbar_expect_tx(c.v_full + e, kVUnits * kUnit);
-                tma_load_2d(unit(3), &map_v, x, row, c.v_full + e);
-                tma_load_2d(unit(4), &map_v, x + 64, row, c.v_full + e);
+                if (elected()) {
+                    mbar_expect_tx(c.v_full + e, kVUnits * kUnit);
+                    tma_load_2d(unit(3), &map_v, x, row, c.v_full + e);
+                    tma_load_2d(unit(4), &map_v, x + 64, row, c.v_full + e);
+                }
+                __syncwarp();
                 ++v_done;
             }
-            // no copy may be in flight when the CTA ends (on an abort: nobody else has waited for them)
-            for (int t = 0; t < kStreams; ++t) mbar_wait_drain(c.q_full + t, 0);
-            for (int i = max(k_done - 2, 0); i < k_done; ++i) mbar_wait_drain(c.k_full + (i & 1), (i >> 1) & 1);
-            for (int i = max(v_done - 2, 0); i < v_done; ++i) mbar_wait_drain(c.v_full + (i & 1), (i >> 1) & 1);
         }
-        __syncwarp();
+        // no copy may be in flight when the CTA ends (on an abort: nobody else has waited for them)
+        for (int t = 0; t < kStreams; ++t)
+            if (q_done[t]) mbar_wait_drain(c.q_full + t, (q_done[t] - 1) & 1);
+        for (uint32_t i = k_done < 2 ? 0 : k_done - 2; i < k_done; ++i) mbar_wait_drain(c.k_full + (i & 1), (i >> 1) & 1);
+        for (uint32_t i = v_done < 2 ? 0 : v_done - 2; i < v_done; ++i) mbar_wait_drain(c.v_full + (i & 1), (i >> 1) & 1);
     } else if (warp == kMma) {
         // ------------------------------------------------------------ MMA issue
         if (elected()) {
             const uint64_t dq = desc(base, 16), dk = desc(base + kRing, 16), dv = desc(base + kRing, kUnit);
-            auto scores = [&](int t, int i) {
-                if (!mbar_wait(c.k_full + (i & 1), (i >> 1) & 1, abort_flag, a.wait_cycles)) return false;
-                fence_after();
-                constexpr uint32_t id = idesc(BF, kRows, kTok, 0);
-#pragma unroll
-                for (int d = 0; d < kQUnits; ++d) {
-                    const uint64_t from = dk + (uint32_t)((i * kStep + d) % kUnits) * (kUnit / 16);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(tmem + 256 * t, dq + (t * kQUnits + d) * (kUnit / 16) + 2 * k, from + 2 * k, id, (d | k) != 0);
-                }
-                commit(c.s_ready + t);
-                if (t == 1 || i >= n1) commit(c.k_empty + (i & 1));  // the last to read these keys
-                return true;
-            };
+            uint32_t p_seen[kStreams] = {0, 0}, q_seen[kStreams] = {0, 0};  // steps and jobs of the streams so far
             bool ok = true;
-            if (n0) ok = mbar_wait(c.q_full, 0, abort_flag, a.wait_cycles) && scores(0, 0);
-            if (n1 && ok) ok = mbar_wait(c.q_full + 1, 0, abort_flag, a.wait_cycles) && scores(1, 0);
-            for (int i = 0; i < n && ok; ++i)
-#pragma unroll
-                for (int t = 0; t < kStreams; ++t) {
-                    if (!ok || i >= (t ? n1 : n0)) continue;
-                    ok = mbar_wait(c.v_full + (i & 1), (i >> 1) & 1, abort_flag, a.wait_cycles) &&
-                         (i < part || mbar_wait(c.guarded + (i & 1), (i >> 1) & 1, abort_flag, a.wait_cycles)) &&
-                         mbar_wait(c.p_ready + t, i & 1, abort_flag, a.wait_cycles);
-                    if (!ok) break;
+            for (; w.next(a, ok); ++w.n) {
+                // Scores of stream t and the job's step i.
+                auto scores = [&](int t, int i) {
+                    const uint32_t at = g + i;
+                    if (!mbar_wait(c.k_full + (at & 1), (at >> 1) & 1, abort_flag, a.wait_cycles)) return false;
                     fence_after();
-                    constexpr uint32_t id = idesc(BF, kRows, kHeadValue, 1);
-                    // (its two units may lie at the ring's end and start: then each is a product of its own)
-                    const uint32_t u = (uint32_t)(i * kStep + kQUnits) % kUnits;
-                    const uint64_t from = dv + u * (kUnit / 16);
+                    constexpr uint32_t id = idesc(BF, kRows, kTok, 0);
 #pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k) {
-                        if (u + 1 < kUnits) {
-                            mma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * k, from + 128 * k, id, (i | k) != 0);
-                        } else {
-                            mma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * k, from + 128 * k, idesc(BF, kRows, 64, 1), (i | k) != 0);
-                            mma_ts(tmem + 256 * t + 192, tmem + 256 * t + 8 * k, dv + 128 * k, idesc(BF, kRows, 64, 1), (i | k) != 0);
-                        }
+                    for (int d = 0; d < kQUnits; ++d) {
+                        const uint64_t from = dk + (uint32_t)((at * kStep + d) % kUnits) * (kUnit / 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss(tmem + 256 * t, dq + (t * kQUnits + d) * (kUnit / 16) + 2 * k, from + 2 * k, id, (d | k) != 0);
                     }
-                    commit(c.o_done + t);
-                    if (t == 1 || i >= n1) commit(c.v_empty + (i & 1));
-                    if (i + 1 < (t ? n1 : n0)) ok = scores(t, i + 1);
-                }
+                    commit(c.s_ready + t);
+                    if (t == 1 || i >= w.n1) commit(c.k_empty + (at & 1));  // the last to read these keys
+                    if (i + 1 == (t ? w.n1 : w.n0)) commit(c.q_empty + t);
+                    return true;
+                };
+#pragma unroll
+                for (int t = 0; t < kStreams; ++t)
+                    if (ok && (t ? w.n1 : w.n0)) {
+                        ok = mbar_wait(c.q_full + t, q_seen[t] & 1, abort_flag, a.wait_cycles) && scores(t, 0);
+                        ++q_seen[t];
+                    }
+                for (int i = 0; i < w.steps && ok; ++i)
+#pragma unroll
+                    for (int t = 0; t < kStreams; ++t) {
+                        if (!ok || i >= (t ? w.n1 : w.n0)) continue;
+                        const uint32_t at = g + i;
+                        ok = mbar_wait(c.v_full + (at & 1), (at >> 1) & 1, abort_flag, a.wait_cycles) &&
+                             (i < w.part || mbar_wait(c.guarded + (at & 1), (at >> 1) & 1, abort_flag, a.wait_cycles)) &&
+                             mbar_wait(c.p_ready + t, p_seen[t] & 1, abort_flag, a.wait_cycles);
+                        if (!ok) break;
+                        ++p_seen[t];
+                        fence_after();
+                        constexpr uint32_t id = idesc(BF, kRows, kHeadValue, 1), half = idesc(BF, kRows, 64, 1);
+                        // (its two units may lie at the ring's end and start: then each is a product of its own)
+                        const uint32_t u = (at * kStep + kQUnits) % kUnits;
+                        const uint64_t from = dv + u * (kUnit / 16);
+#pragma unroll
+                        for (int k = 0; k < kTok / 16; ++k) {
+                            if (u + 1 < kUnits) {
+                                mma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * k, from + 128 * k, id, (i | k) != 0);
+                            } else {
+                                mma_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * k, from + 128 * k, half, (i | k) != 0);
+                                mma_ts(tmem + 256 * t + 192, tmem + 256 * t + 8 * k, dv + 128 * k, half, (i | k) != 0);
+                            }
+                        }
+                        commit(c.o_done + t);
+                        if (t == 1 || i >= w.n1) commit(c.v_empty + (at & 1));
+                        if (i + 1 < (t ? w.n1 : w.n0)) ok = scores(t, i + 1);
+                    }
+                if (!ok) break;
+                g += w.steps;
+                w.done();
+            }
             commit(&c.drain);  // completes when every MMA issued above has finished
             if (!mbar_wait_drain(&c.drain, 0)) *abort_flag = 1;
         }
@@ -246,140 +367,149 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
         // ------------------------------------------------------------ guards: a thread to two tokens
         const int id = tid - kGuard * 32;
         bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
-            const int e = i & 1;
-            ok = __all_sync(kFull, mbar_wait(c.v_full + e, (i >> 1) & 1, abort_flag, a.wait_cycles));
-            if (!ok) break;
-            if (i >= part) {
-                bool wrote = false;
-                for (int z = 0; z < 2; ++z) {
-                    const int t = id + 64 * z;
-                    uint8_t* rows[2];
-                    for (int d = 0; d < 2; ++d) rows[d] = smem + kRing + ((i * kStep + kQUnits + d) % kUnits) * kUnit + t * 128;
-                    bool odd = false, wipe = i * kTok + t >= j.keys;
-                    constexpr uint32_t kTop = BF ? 0x7f80u : 0x7c00u;
-                    for (int d = 0; d < 2 && !wipe; ++d)
+        for (; __all_sync(kFull, w.next(a, ok)); ++w.n) {
+            for (int i = 0; i < w.steps && ok; ++i, ++g) {
+                const uint32_t e = g & 1;
+                ok = __all_sync(kFull, mbar_wait(c.v_full + e, (g >> 1) & 1, abort_flag, a.wait_cycles));
+                if (!ok) break;
+                if (i >= w.part) {
+                    bool wrote = false;
+                    for (int z = 0; z < 2; ++z) {
+                        const int t = id + 64 * z;
+                        uint8_t* rows[2];
+                        for (int d = 0; d < 2; ++d) rows[d] = smem + kRing + ((g * kStep + kQUnits + d) % kUnits) * kUnit + t * 128;
+                        bool odd = false;
+                        const bool wipe = i * kTok + t >= w.j.keys;
+                        constexpr uint32_t kTop = BF ? 0x7f807f80u : 0x7c007c00u;
+                        for (int d = 0; d < 2 && !wipe; ++d)
 #pragma unroll
-                        for (int p = 0; p < 8; ++p) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(rows[d] + ((p + t) & 7) * 16);
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            for (int p = 0; p < 8; ++p) {
+                                const uint4 v = *reinterpret_cast<const uint4*>(rows[d] + ((p + t) & 7) * 16);
+                                odd |= (__vcmpeq2(v.x & kTop, kTop) | __vcmpeq2(v.y & kTop, kTop) | __vcmpeq2(v.z & kTop, kTop) |
+                                        __vcmpeq2(v.w & kTop, kTop)) != 0;
+                            }
+                        __syncwarp();
+                        const uint32_t bits = __ballot_sync(kFull, odd);
+                        if (lane == 0) c.odd[e][2 * z + warp - kGuard] = bits;
+                        if (wipe || odd) {
+                            wrote = true;
+                            for (int d = 0; d < 2; ++d)
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) odd |= (w[q] & kTop) == kTop || ((w[q] >> 16) & kTop) == kTop;
+                                for (int p = 0; p < 8; ++p)
+                                    *reinterpret_cast<uint4*>(rows[d] + ((p + t) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
-                    const uint32_t bits = __ballot_sync(kFull, odd);
-                    if (lane == 0) c.odd[e][2 * z + warp - kGuard] = bits;
-                    if (wipe || odd) {
-                        wrote = true;
-                        for (int d = 0; d < 2; ++d)
-#pragma unroll
-                            for (int p = 0; p < 8; ++p)
-                                *reinterpret_cast<uint4*>(rows[d] + ((p + t) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
+                    if (wrote) fence_async_smem();
                 }
-                if (wrote) fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(c.guarded + e);
+                    mbar_arrive(c.v_empty + e);
+                }
             }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(c.guarded + e);
-                mbar_arrive(c.v_empty + e);
-            }
+            if (!ok) break;
+            if (lane == 0) w.done();
         }
     } else {
         // ------------------------------------------------------------ softmax: a thread to a row
-        const int t = warp >> 2, row = t * kRows + (warp & 3) * 32 + lane, steps = t ? n1 : n0, whole = steps ? whole_of(a, j, t) : 0;
+        const int t = warp >> 2, row = t * kRows + (warp & 3) * 32 + lane;
         const uint32_t at = tmem + 256 * t + ((uint32_t)(warp & 3) << 21), col_o = at + 128;
-        const int seen = row < j.rows ? seen_by(a, j, row) : 0;
         const f2 ff = pk(a.scale2, a.scale2);
-        float m = -INFINITY, sum = 0.f, bias = 0.f;
+        uint32_t done = 0;  // steps of this stream so far
         bool ok = true;
-        for (int i = 0; i < steps; ++i) {
-            ok = __all_sync(kFull, mbar_wait(c.s_ready + t, i & 1, abort_flag, a.wait_cycles));
-            if (!ok) break;
-            fence_after();
-            uint32_t s[128];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) ld32(at + 32 * q, s + 32 * q);
-            wait_ld();
-#pragma unroll
-            for (int k = 0; k < 64; ++k) {
-                const float2 y = un(mul2(pk(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), ff));
-                s[2 * k] = __float_as_uint(y.x);
-                s[2 * k + 1] = __float_as_uint(y.y);
-            }
-            bool spoilt = false;
-            if (i >= whole) {
-                const int limit = seen - i * kTok;  // keys of this step that the row sees
-#pragma unroll
-                for (int k = 0; k < 128; ++k)
-                    if (k >= limit) s[k] = __float_as_uint(-INFINITY);
-            }
-            if (i >= part) {
-                ok = __all_sync(kFull, mbar_wait(c.guarded + (i & 1), (i >> 1) & 1, abort_flag, a.wait_cycles));
+        for (; __all_sync(kFull, w.next(a, ok)); ++w.n) {
+            const Job j = w.j;
+            const int steps = t ? w.n1 : w.n0, whole = steps ? whole_of(a, j, t) : 0, part = w.part;
+            const int seen = row < j.rows ? seen_by(a, j, row) : 0;
+            const uint32_t g1 = g + w.steps;
+            if (lane == 0) w.done();
+            float m = -INFINITY, sum = 0.f, bias = 0.f;
+            for (int i = 0; i < steps; ++i, ++g, ++done) {
+                ok = __all_sync(kFull, mbar_wait(c.s_ready + t, done & 1, abort_flag, a.wait_cycles));
                 if (!ok) break;
-                const int limit = seen - i * kTok;
+                fence_after();
+                uint32_t s[128];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int bits = min(max(limit - 32 * w, 0), 32);
-                    spoilt |= (c.odd[i & 1][w] & (bits == 32 ? ~0u : (1u << bits) - 1)) != 0;
+                for (int q = 0; q < 4; ++q) ld32(at + 32 * q, s + 32 * q);
+                wait_ld();
+#pragma unroll
+                for (int k = 0; k < 64; ++k) {
+                    const float2 y = un(mul2(pk(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), ff));
+                    s[2 * k] = __float_as_uint(y.x);
+                    s[2 * k + 1] = __float_as_uint(y.y);
                 }
-            }
-            float x4[4];
+                bool spoilt = false;
+                if (i >= whole) {
+                    const int limit = seen - i * kTok;  // keys of this step that the row sees
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x4[k] = __uint_as_float(s[k]);
-#pragma unroll
-            for (int k = 4; k < 124; k += 8)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) x4[z] = fmaxf(fmaxf(x4[z], __uint_as_float(s[k + z])), __uint_as_float(s[k + z + 4]));
-#pragma unroll
-            for (int k = 124; k < 128; ++k) x4[k & 3] = fmaxf(x4[k & 3], __uint_as_float(s[k]));
-            const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
-            if (__any_sync(kFull, top - m > Weights<BF>::kSlack)) {
-                // (each row by its own scores alone: its result must not hang on what its neighbours see)
-                const float to_m = top - m > Weights<BF>::kSlack ? top : m, to = Weights<BF>::bias(to_m);
-                const float r = m == -INFINITY ? 0.f : exp2_fast(to - bias);
-                m = to_m;
-                bias = to;
-                sum *= r;
-                if (i) {  // the sums so far, once the last product has written them
-                    ok = __all_sync(kFull, mbar_wait(c.o_done + t, (i - 1) & 1, abort_flag, a.wait_cycles));
+                    for (int k = 0; k < 128; ++k)
+                        if (k >= limit) s[k] = __float_as_uint(-INFINITY);
+                }
+                if (i >= part) {
+                    ok = __all_sync(kFull, mbar_wait(c.guarded + (g & 1), (g >> 1) & 1, abort_flag, a.wait_cycles));
                     if (!ok) break;
-                    fence_after();
-#pragma unroll 1
-                    for (int q = 0; q < 16; ++q) {
-                        uint32_t o[8];
-                        ld8(col_o + 8 * q, o);
-                        wait_ld();
+                    const int limit = seen - i * kTok;
 #pragma unroll
-                        for (int z = 0; z < 8; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * r);
-                        st8(col_o + 8 * q, o);
+                    for (int z = 0; z < 4; ++z) {
+                        const int bits = min(max(limit - 32 * z, 0), 32);
+                        spoilt |= (c.odd[g & 1][z] & (bits == 32 ? ~0u : (1u << bits) - 1)) != 0;
                     }
                 }
-            }
-            // ---- weights; the sum takes them before their rounding
-            const f2 bb = pk(bias, bias);
-            f2 ls[2] = {0, 0};
+                float x4[4];
 #pragma unroll
-            for (int k = 0; k < 64; ++k) {
-                const float2 y = un(add2(pk(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), bb));
-                const float u = exp2_fast(y.x), v = exp2_fast(y.y);
-                ls[k & 1] = add2(ls[k & 1], pk(u, v));
-                s[k] = pack16<BF>(u, v);
-                if ((k & 31) == 31) st32(at + (k & 32), s + (k & 32));
+                for (int k = 0; k < 4; ++k) x4[k] = __uint_as_float(s[k]);
+#pragma unroll
+                for (int k = 4; k < 124; k += 8)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) x4[z] = fmaxf(fmaxf(x4[z], __uint_as_float(s[k + z])), __uint_as_float(s[k + z + 4]));
+#pragma unroll
+                for (int k = 124; k < 128; ++k) x4[k & 3] = fmaxf(x4[k & 3], __uint_as_float(s[k]));
+                const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
+                if (__any_sync(kFull, top - m > Weights<BF>::kSlack)) {
+                    // (each row by its own scores alone: its result must not hang on what its neighbours see)
+                    const float to_m = top - m > Weights<BF>::kSlack ? top : m, to = Weights<BF>::bias(to_m);
+                    const float r = m == -INFINITY ? 0.f : exp2_fast(to - bias);
+                    m = to_m;
+                    bias = to;
+                    sum *= r;
+                    if (i) {  // the sums so far (the scores were issued behind the products that wrote them)
+#pragma unroll 1
+                        for (int q = 0; q < 16; ++q) {
+                            uint32_t o[8];
+                            ld8(col_o + 8 * q, o);
+                            wait_ld();
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * r);
+                            st8(col_o + 8 * q, o);
+                        }
+                    }
+                }
+                // ---- weights; the sum takes them before their rounding
+                const f2 bb = pk(bias, bias);
+                f2 ls[2] = {0, 0};
+#pragma unroll
+                for (int k = 0; k < 64; ++k) {
+                    const float2 y = un(add2(pk(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), bb));
+                    const float u = exp2_fast(y.x), v = exp2_fast(y.y);
+                    ls[k & 1] = add2(ls[k & 1], pk(u, v));
+                    s[k] = pack16<BF>(u, v);
+                    if ((k & 31) == 31) st32(at + (k & 32), s + (k & 32));
+                }
+                const float2 z = un(add2(ls[0], ls[1]));
+                sum += z.x + z.y;
+                if (spoilt) sum = NAN;
+                wait_st();
+                fence_before();
+                mbar_arrive(c.p_ready + t);
             }
-            const float2 z = un(add2(ls[0], ls[1]));
-            sum += z.x + z.y;
-            if (spoilt) sum = NAN;
-            wait_st();
-            fence_before();
-            mbar_arrive(c.p_ready + t);
-        }
-        if (ok && steps) {
-            ok = __all_sync(kFull, mbar_wait(c.o_done + t, (steps - 1) & 1, abort_flag, a.wait_cycles));
-            fence_after();
-        }
-        if (ok) {
+            if (!ok) break;
+            if (steps) {
+                ok = __all_sync(kFull, mbar_wait(c.o_done + t, (done - 1) & 1, abort_flag, a.wait_cycles));
+                if (!ok) break;
+                fence_after();
+            }
             const float over = sum == 0.f ? 0.f : 1.f / sum;  // (a NaN sum stays one)
-            uint16_t* out = a.o + ((int64_t)(j.q0 + row) * a.H + h) * kHeadValue;
+            uint16_t* out = a.o + ((int64_t)(j.q0 + row) * a.H + j.head) * kHeadValue;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 uint32_t o[32];
@@ -399,6 +529,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                 }
                 __syncwarp();
             }
+            fence_before();
+            g = g1;
         }
     }
 
@@ -409,6 +541,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
         fence_after();
         dealloc512(tmem);
     }
+}
+
+int sm_count() {
+    static const int n = [] {
+        int dev = 0, v = 0;
+        return cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? v : 152;
+    }();
+    return n;
 }
 
 }  // namespace
@@ -454,10 +594,12 @@ extern "C" tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, co
         !tensor_map(&mk, bf, Tkv ? k : q, keys, cols, kv_stride, kTok) || !tensor_map(&mv, bf, Tkv ? v : q, keys, cols, kv_stride, kTok) ||
         !tensor_map(&mr, bf, Tkv ? k_rope : q, keys, kLatentRope, k_rope_stride, kTok))
         return TQ_ERR_CUDA;
-    const int64_t tiles = (Tq + kTile - 1) / kTile + B;  // at most
-    if (tiles > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
+    // heads of a group: as many as the L2 cache (129 MB) holds the keys and values of twice over
+    a.heads = (int)std::min<int64_t>(H, std::max<int64_t>(1, (64ll << 20) / (keys * (kHeadKey + kHeadValue) * 2)));
+    const int64_t jobs = std::min((Tq + kTile - 1) / kTile + B, Tq) * H;  // at most
     void (*kernel)(PromptArgs, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap) =
         bf ? latent_prompt_kernel<true> : latent_prompt_kernel<false>;
     if (ensure_smem((const void*)kernel, kSmem) != cudaSuccess) return TQ_ERR_CUDA;
-    return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(tiles, Tq), (unsigned)H), dim3(32 * kWarps), kSmem, as_stream(stream), a, mq, mk, mv, mr);
+    return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(jobs, sm_count())), dim3(32 * kWarps), kSmem, as_stream(stream), a, mq, mk, mv,
+                      mr);
 }
