@@ -140,7 +140,8 @@ _SIGS = {
                                      _c_p, _c_p, ctypes.c_float, _c_p, _c_p, _sz, _c_p, _c_p]),
     "tq_latent_attend_tree_workspace_bytes": (_sz, [_P(tq_latent_pages_t), _i32, _i32, _i32, _i64]),
     "tq_latent_attend_prompt": (_i32, [_c_p, _i64, _c_p, _c_p, _i64, _i64, _c_p, _i64, _i32, _i32, _i32, _i64, _i64, _c_p, _c_p,
-                                       _i32, ctypes.c_float, _c_p, _c_p, _c_p]),
+                                       _i32, ctypes.c_float, _c_p, _c_p, _sz, _c_p, _c_p]),
+    "tq_latent_attend_prompt_workspace_bytes": (_sz, []),
     "tq_check_error": (_i32, [_c_p, _P(_u32), _c_p]),
     "tq_set_wait_budget": (_i32, [_i64]),
     "tq_rotation_dense": (_i32, [ctypes.c_uint64, _i32, _P(ctypes.c_double)]),
@@ -1117,7 +1118,7 @@ def latent_attend_tree(cache: LatentCache, q, table, lens, scale: float, new=Non
     return o
 
 
-def latent_attend_prompt(q, k, v, k_rope, q_starts, kv_starts, scale: float, causal: bool = True, err=None):
+def latent_attend_prompt(q, k, v, k_rope, q_starts, kv_starts, scale: float, causal: bool = True, err=None, ws=None):
     """Attention of packed prompts over keys and values expanded from the latents (the expanded form).
 
     q [Tq, H, 192] (the last 64 with rotary positions), k and v [Tkv, H, 128] (the two halves of one expansion [Tkv, H, 256] are
@@ -1142,8 +1143,13 @@ def latent_attend_prompt(q, k, v, k_rope, q_starts, kv_starts, scale: float, cau
     hs = k.stride(1) if H > 1 else 128
     ks = k.stride(0) if Tkv > 1 else max(k.stride(0), (H - 1) * hs + 128)
     o = torch.empty((Tq, H, 128), dtype=q.dtype, device=q.device)
+    nb = int(load().tq_latent_attend_prompt_workspace_bytes())
+    if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError("ws must be contiguous, on q's device")
+    if ws is None or ws.numel() * ws.element_size() < nb:
+        ws = torch.empty(nb, dtype=torch.uint8, device=q.device)
     _check(load().tq_latent_attend_prompt(q.data_ptr(), qs, k.data_ptr(), v.data_ptr(), ks, hs, k_rope.data_ptr(), rs, _dt(q), B, H, Tq,
-                                          Tkv, qp, kp, int(causal), scale, o.data_ptr(), _word(err, dev), _raw_stream(q)),
+                                          Tkv, qp, kp, int(causal), scale, o.data_ptr(), ws.data_ptr(), nb, _word(err, dev), _raw_stream(q)),
            "tq_latent_attend_prompt")
     return o
 

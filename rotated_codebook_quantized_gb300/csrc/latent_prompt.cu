@@ -40,7 +40,8 @@ struct PromptArgs {
     uint32_t* err;
     int B, H, heads;  // heads: of a group
     bool causal;
-    float scale2;  // scale * log2(e)
+    uint32_t* taken;  // jobs taken beyond each CTA's first; NULL: there are no others
+    float scale2;     // scale * log2(e)
     long long wait_cycles;
 };
 
@@ -72,7 +73,8 @@ TQ_DEVFN int tiles_above(const PromptArgs& a, const Span& s, int steps) {
     return s.tiles - max(steps * kTok + (s.q1 - s.q0) - (s.k1 - s.k0), 0) / kTile;
 }
 // Jobs go in groups of `heads` heads, whose keys and values the L2 cache holds; in a group those with the most steps first.  A CTA
-// takes every gridDim.x-th, in turns from the front and from the back.
+// takes the next one when its copies of the last are under way (shared out beforehand, seven chunks of prompts left a quarter of the
+// SMs' time idle).
 struct Jobs {
     int tiles, most;  // of a head; steps of the longest
 };
@@ -238,8 +240,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
         bool ok = true;
         uint32_t k_done = 0, v_done = 0, q_done[kStreams] = {0, 0};
         for (; ok; ++w.n) {
-            const uint32_t from = w.n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-            w.j = find_job(a, jobs, (int64_t)w.n * gridDim.x + from);
+            uint32_t at = blockIdx.x;
+            if (w.n) {
+                if (!a.taken) at = ~0u;
+                else if (lane == 0) at = gridDim.x + atomicAdd(a.taken, 1u);
+                at = __shfl_sync(kFull, at, 0);
+            }
+            w.j = find_job(a, jobs, at);
             if (w.n >= 2) ok = __all_sync(kFull, mbar_wait(c.job_empty + (w.n & 1), ((w.n - 2) >> 1) & 1, abort_flag, a.wait_cycles));
             if (!ok) break;
             if (lane == 0) {
@@ -556,11 +563,13 @@ int sm_count() {
 
 using namespace tq;
 
+extern "C" size_t tq_latent_attend_prompt_workspace_bytes(void) { return sizeof(uint32_t); }
+
 extern "C" tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
                                              int64_t kv_head_stride, const void* k_rope, int64_t k_rope_stride, tq_dtype dt,
                                              int32_t B, int32_t H, int64_t Tq, int64_t Tkv, const int32_t* q_starts,
-                                             const int32_t* kv_starts, int32_t causal, float scale, void* o, uint32_t* err,
-                                             void* stream) {
+                                             const int32_t* kv_starts, int32_t causal, float scale, void* o, void* ws,
+                                             size_t ws_bytes, uint32_t* err, void* stream) {
     if (B < 0 || H <= 0 || H > 65535 || Tq < 0 || Tkv < 0 || !isfinite(scale)) return TQ_ERR_INVALID;
     if (!(dt == TQ_BF16 || dt == TQ_F16 || dt == TQ_F32)) return TQ_ERR_INVALID;
     if (dt == TQ_F32 || Tq > 1ll << 30 || Tkv > 1ll << 30) return TQ_ERR_UNSUPPORTED;
@@ -569,8 +578,8 @@ extern "C" tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, co
         return TQ_ERR_INVALID;
     if (q_stride > 1ll << 32 || kv_stride > 1ll << 32 || k_rope_stride > 1ll << 32) return TQ_ERR_UNSUPPORTED;
     if (B == 0 || Tq == 0) return TQ_OK;
-    if (!q || !o || !q_starts || !kv_starts || (Tkv && (!k || !v || !k_rope))) return TQ_ERR_INVALID;
-    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_rope, 16) || !aligned(o, 32) || !aligned(q_starts, 4) ||
+    if (!q || !o || !ws || ws_bytes < sizeof(uint32_t) || !q_starts || !kv_starts || (Tkv && (!k || !v || !k_rope))) return TQ_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_rope, 16) || !aligned(o, 32) || !aligned(ws, 4) || !aligned(q_starts, 4) ||
         !aligned(kv_starts, 4))
         return TQ_ERR_INVALID;
     PromptArgs a{};
@@ -597,9 +606,14 @@ extern "C" tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, co
     // heads of a group: as many as the L2 cache (129 MB) holds the keys and values of twice over
     a.heads = (int)std::min<int64_t>(H, std::max<int64_t>(1, (64ll << 20) / (keys * (kHeadKey + kHeadValue) * 2)));
     const int64_t jobs = std::min((Tq + kTile - 1) / kTile + B, Tq) * H;  // at most
+    if (jobs > 1ll << 30) return TQ_ERR_UNSUPPORTED;
     void (*kernel)(PromptArgs, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap) =
         bf ? latent_prompt_kernel<true> : latent_prompt_kernel<false>;
     if (ensure_smem((const void*)kernel, kSmem) != cudaSuccess) return TQ_ERR_CUDA;
+    if (jobs > sm_count()) {
+        a.taken = reinterpret_cast<uint32_t*>(ws);
+        if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), as_stream(stream)) != cudaSuccess) return TQ_ERR_CUDA;
+    }
     return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(jobs, sm_count())), dim3(32 * kWarps), kSmem, as_stream(stream), a, mq, mk, mv,
                       mr);
 }

@@ -104,13 +104,14 @@ def test_latent_attend_tree_refusals(tq):
 def test_latent_attend_prompt_refusals(tq):
     lib = tq.load()
 
-    def call(q=F, qs=16 * 192, k=F, v=F, kvs=16 * 256, kvh=256, kr=F, krs=64, dt=tq.TQ_BF16, B=2, H=16, Tq=9, Tkv=9, starts=F, scale=0.1, o=F):
-        return lib.tq_latent_attend_prompt(q, qs, k, v, kvs, kvh, kr, krs, dt, B, H, Tq, Tkv, starts, F, 1, scale, o, None, None)
+    def call(q=F, qs=16 * 192, k=F, v=F, kvs=16 * 256, kvh=256, kr=F, krs=64, dt=tq.TQ_BF16, B=2, H=16, Tq=9, Tkv=9, starts=F, scale=0.1, o=F, ws=F, nb=4):
+        return lib.tq_latent_attend_prompt(q, qs, k, v, kvs, kvh, kr, krs, dt, B, H, Tq, Tkv, starts, F, 1, scale, o, ws, nb, None, None)
 
     for kw in (dict(q=None), dict(qs=16 * 192 - 8), dict(qs=16 * 192 + 4), dict(k=None), dict(v=None), dict(kr=None), dict(kvs=15 * 256),
                dict(kvh=120), dict(kvh=252), dict(krs=56), dict(krs=68), dict(dt=5), dict(B=-1), dict(H=0), dict(H=65536), dict(Tq=-1),
                dict(Tkv=-1), dict(starts=None), dict(scale=float("nan")), dict(o=None), dict(q=F + 8), dict(k=F + 8), dict(v=F + 8),
-               dict(kr=F + 8), dict(o=F + 8), dict(starts=F + 2)):
+               dict(kr=F + 8), dict(o=F + 8), dict(starts=F + 2), dict(ws=None),
+               dict(ws=F + 2), dict(nb=3)):
         assert call(**kw) == tq.TQ_ERR_INVALID, kw
     for kw in (dict(dt=tq.TQ_F32), dict(Tq=2 ** 30 + 1), dict(Tkv=2 ** 30 + 1), dict(kvs=2 ** 33)):
         assert call(**kw) == tq.TQ_ERR_UNSUPPORTED, kw
