@@ -481,8 +481,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
         // ------------------------------------------------------------ softmax: rows lane / 4 and lane / 4 + 8 of the warp's 16
         const uint32_t lanes = (uint32_t)warp << 21;
         const int words = (l.n + 63) / 64;
-        const float2 scale2 = make_float2(l.scale2, l.scale2);
-        const f2 ff = pk(scale2.x, scale2.y);
+        const float f = fabsf(l.scale2);
+        const f2 ff = pk(f, f);
         bool ok = true;
         for (; ok && some; some = walk.next(l, x)) {
             const uint32_t ge = g + (x.s1 - x.s0);
@@ -571,12 +571,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                 }
                 wait_ld();
                 float top[2] = {-INFINITY, -INFINITY};
+                if (l.scale2 < 0)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 y = un(mul2(pk(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), ff));
-                    v[2 * k] = __float_as_uint(y.x);
-                    v[2 * k + 1] = __float_as_uint(y.y);
-                }
+                    for (int k = 0; k < 16; ++k) v[k] ^= 0x80000000u;
                 if (!whole)
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
@@ -584,6 +581,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     top[k & 1] = fmaxf(fmaxf(top[k & 1], __uint_as_float(v[2 * k])), __uint_as_float(v[2 * k + 1]));
+                top[0] *= f;
+                top[1] *= f;
                 if (__any_sync(kFull, top[0] - m[0] > Weights<BF>::kSlack || top[1] - m[1] > Weights<BF>::kSlack)) {
                     float r[2];
 #pragma unroll
@@ -603,14 +602,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                         fence_after();
                         // row lane % 16 of O's two halves
                         const float lo = __shfl_sync(kFull, r[0], (lane & 7) * 4), hi = __shfl_sync(kFull, r[1], (lane & 7) * 4);
-                        const float f = lane & 8 ? hi : lo;
+                        const float by = lane & 8 ? hi : lo;
 #pragma unroll 1
                         for (int q = 0; q < 8; ++q) {
                             uint32_t o[32];
                             ld32(tmem + lanes + 32 * q, o);
                             wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
                             st32(tmem + lanes + 32 * q, o);
                         }
                         wait_st();
@@ -619,10 +618,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                 // ---- weights; the sum takes them before their rounding
                 uint32_t w[8];
                 const f2 bb[2] = {pk(bias[0], bias[0]), pk(bias[1], bias[1])};
-                f2 ls[2] = {0, 0};
+                f2 ls[2] = {0, 0}, by = ff;
+                if (__any_sync(kFull, huge(m[0]) || huge(m[1]))) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__fmul_rn(__uint_as_float(v[k]), f));
+                    by = pk(1.f, 1.f);
+                }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float2 y = un(add2(pk(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), bb[k & 1]));
+                    const float2 y = un(fma2(pk(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), by, bb[k & 1]));
                     const float p0 = exp2_fast(y.x), p1 = exp2_fast(y.y);
                     ls[k & 1] = add2(ls[k & 1], pk(p0, p1));
                     w[k] = pack16<BF>(p0, p1);
@@ -856,7 +860,7 @@ extern "C" tq_status tq_latent_attend_tree(const tq_latent_pages_t* cache, const
     a.l.H = H;
     a.l.table_stride = table_stride;
     a.l.lpage = ilog2(cache->page);
-    a.l.scale2 = scale * 1.4426950408889634f;
+    a.l.scale2 = score_factor(scale);
     a.l.o = reinterpret_cast<uint16_t*>(o);
     a.l.err = err;
     a.ctas = (int)std::min<int64_t>(steps, std::min(sm_count(), kMaxSms));

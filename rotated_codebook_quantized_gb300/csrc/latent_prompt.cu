@@ -343,7 +343,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                              (i < w.part || mbar_wait(c.guarded + (at & 1), (at >> 1) & 1, abort_flag, a.wait_cycles)) &&
                              mbar_wait(c.p_ready + t, p_seen[t] & 1, abort_flag, a.wait_cycles);
                         if (!ok) break;
-                        ++p_seen[t];
                         fence_after();
                         constexpr uint32_t id = idesc(BF, kRows, kHeadValue, 1), half = idesc(BF, kRows, 64, 1);
                         // (its two units may lie at the ring's end and start: then each is a product of its own)
@@ -358,6 +357,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                                 mma_ts(tmem + 256 * t + 192, tmem + 256 * t + 8 * k, dv + 128 * k, half, (i | k) != 0);
                             }
                         }
+                        ++p_seen[t];
                         commit(c.o_done + t);
                         if (t == 1 || i >= w.n1) commit(c.v_empty + (at & 1));
                         if (i + 1 < (t ? w.n1 : w.n0)) ok = scores(t, i + 1);
@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
         // ------------------------------------------------------------ softmax: a thread to a row
         const int t = warp >> 2, row = t * kRows + (warp & 3) * 32 + lane;
         const uint32_t at = tmem + 256 * t + ((uint32_t)(warp & 3) << 21), col_o = at + 128;
-        const f2 ff = pk(a.scale2, a.scale2);
+        const float f = fabsf(a.scale2);
+        const f2 ff = pk(f, f);
         uint32_t done = 0;  // steps of this stream so far
         bool ok = true;
         for (; __all_sync(kFull, w.next(a, ok)); ++w.n) {
@@ -439,12 +440,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) ld32(at + 32 * q, s + 32 * q);
                 wait_ld();
+                if (a.scale2 < 0)
 #pragma unroll
-                for (int k = 0; k < 64; ++k) {
-                    const float2 y = un(mul2(pk(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), ff));
-                    s[2 * k] = __float_as_uint(y.x);
-                    s[2 * k + 1] = __float_as_uint(y.y);
-                }
+                    for (int k = 0; k < 128; ++k) s[k] ^= 0x80000000u;
                 bool spoilt = false;
                 if (i >= whole) {
                     const int limit = seen - i * kTok;  // keys of this step that the row sees
@@ -471,7 +469,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                     for (int z = 0; z < 4; ++z) x4[z] = fmaxf(fmaxf(x4[z], __uint_as_float(s[k + z])), __uint_as_float(s[k + z + 4]));
 #pragma unroll
                 for (int k = 124; k < 128; ++k) x4[k & 3] = fmaxf(x4[k & 3], __uint_as_float(s[k]));
-                const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
+                const float top = f * fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
                 if (__any_sync(kFull, top - m > Weights<BF>::kSlack)) {
                     // (each row by its own scores alone: its result must not hang on what its neighbours see)
                     const float to_m = top - m > Weights<BF>::kSlack ? top : m, to = Weights<BF>::bias(to_m);
@@ -493,10 +491,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                 }
                 // ---- weights; the sum takes them before their rounding
                 const f2 bb = pk(bias, bias);
+                f2 by = ff;
+                if (__any_sync(kFull, huge(m))) {
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__fmul_rn(__uint_as_float(s[k]), f));
+                    by = pk(1.f, 1.f);
+                }
                 f2 ls[2] = {0, 0};
 #pragma unroll
                 for (int k = 0; k < 64; ++k) {
-                    const float2 y = un(add2(pk(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), bb));
+                    const float2 y = un(fma2(pk(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), by, bb));
                     const float u = exp2_fast(y.x), v = exp2_fast(y.y);
                     ls[k & 1] = add2(ls[k & 1], pk(u, v));
                     s[k] = pack16<BF>(u, v);
@@ -593,7 +597,7 @@ extern "C" tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, co
     a.B = B;
     a.H = H;
     a.causal = causal != 0;
-    a.scale2 = scale * 1.4426950408889634f;
+    a.scale2 = score_factor(scale);
     a.wait_cycles = wait_budget();
     const bool bf = dt == TQ_BF16;
     CUtensorMap mq, mk, mv, mr;

@@ -1,6 +1,8 @@
 // tcgen05 (5th-generation tensor core) helpers of the latent attention kernels: descriptors, products, TMEM loads and stores.
 #pragma once
 
+#include <math.h>
+
 #include "common.cuh"
 #include "tma.cuh"
 
@@ -108,9 +110,9 @@ TQ_DEVFN f2 add2(f2 a, f2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-TQ_DEVFN f2 mul2(f2 a, f2 b) {
+TQ_DEVFN f2 fma2(f2 a, f2 b, f2 c) {
     f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 TQ_DEVFN float exp2_fast(float x) {
@@ -131,15 +133,23 @@ TQ_DEVFN void prefetch_2d(const CUtensorMap* map, int x, int y) {
 TQ_DEVFN void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-// A row's weights are 2^(score + bias), bias = kLift - maximum rounded down, the maximum a running one that may be kSlack (log2) below
-// the true one before it follows.  fp16: at most 2^15, inside its range, and the smallest that it holds is 2^-31 of the largest's.
+// A row's weights are 2^(f s + bias), f s the score in log2 and bias = kLift - maximum rounded down, the maximum a running one that may
+// be kSlack (log2) below the true one before it follows.  fp16: at most 2^14, with half a step of the
+// maximum's where the product is not rounded by itself; and the smallest that it holds is 2^-31 of the largest's.
 // bf16 has fp32's range: there the maximum seldom follows after the first tokens (each time costs the rescaling of a row's
 // sums, and the products wait for it), and sums stay below 2^37 times the largest value.
 template <bool BF>
 struct Weights {
-    static constexpr float kSlack = BF ? 20.0f : 8.0f, kLift = BF ? 0.0f : 7.0f;
+    static constexpr float kSlack = BF ? 20.0f : 7.0f, kLift = BF ? 0.0f : 7.0f;
     TQ_DEVFN static float bias(float m) { return m == -INFINITY ? 0.f : __fadd_rd(kLift, -m); }
 };
+// A factor on scores that is never 0, so that a masked score, -infinity times it, is no NaN.
+inline float score_factor(float scale) {
+    const float f = scale * 1.4426950408889634f, least = 1.8807909613156600e-37f;  // 2^-122
+    return f < 0 ? fminf(f, -least) : fmaxf(f, least);
+}
+// Maxima whose products have to be rounded before the bias is added: the product's own rounding no longer counts for little.
+TQ_DEVFN bool huge(float m) { return fabsf(m) > 4194304.f && m != -INFINITY; }
 // What sums of weights belong to, for joining them: -infinity where there are none.
 TQ_DEVFN float level(float m, float bias) { return m == -INFINITY ? m : -bias; }
 
