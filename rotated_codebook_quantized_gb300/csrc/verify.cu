@@ -1,13 +1,15 @@
 // Verification of drafted trees: speculative sampling from given uniform numbers.
 //
 // A cluster of CTAs walks one tree.  What a node's test needs besides its token's two probabilities (gathered for all nodes at the
-// start) is the sum R of the residual r after each rejection: one pass over the vocabulary, a part of it to each CTA.  The walk
-// itself is a few hundred instructions that every thread repeats, so it needs no exchange.  r is never stored: it is computed from
-// the rows and the R of the node's rejections whenever it is needed.
-// All of r and R are integers, in steps of 2^-50 of the largest value they may have: sums are exact, in any order, so that
-// neither the split over CTAs nor the number of warps can change the sampled token.
-// Bound by the latency of the chain: tokens, their probabilities, one or two passes (rows where the walk ends: 1 MB a tree of two
-// rows of 131072 in 32 bits) and one search.
+// start) is the sum R of the residual r after each rejection: one pass over the vocabulary, a part of it to each CTA, whose r stays in
+// shared memory for the next pass and for the search.  The walk itself is a few hundred instructions that every thread repeats, so
+// it needs no exchange.
+// All of r and R are integers, in steps of 2^-50, and tests compare products of 112 bits: sums are exact, in any order, so
+// that neither the split over CTAs nor the number of warps can change the sampled token.  (Sums in fp64 would be off by
+// little, but this GPU adds two of them a clock and SM.)
+// Bound by the latency of the chain: tokens, their probabilities (launch and walk 4 us), a pass and the search (1.5 to 3 us), and 3.7 us
+// for each further rejection of a node, 54 instructions an element.  8 chains of 5 drafts over 131072 tokens, fp32: 10.1 us; 48
+// trees of up to 23 drafts over 50001, bf16: 32 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,7 +23,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kRun = 256;          // elements of a run, whose sum is kept for the search
 constexpr int kNodes = 1024;       // largest tree
 constexpr int kVocab = 1 << 20;    // largest vocabulary
-constexpr int kCluster = 8;        // most CTAs of a tree
+constexpr int kCluster = 16;       // most CTAs of a tree (more than 8 have to be asked for)
 constexpr u64 kOne = 1ull << 50;
 
 struct VerifyArgs {
@@ -46,26 +48,40 @@ TQ_DEVFN float load_p(const void* p, int64_t i) {
     return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(p) + i)));
 }
 
-// x in steps of 2^-50, rounded to nearest; below 0 and NaN: 0, above 1: 1.
+// A probability's bits: below 0 and NaN 0, above 1 those of 1.
+TQ_DEVFN uint32_t bits_of(float x) {
+    const uint32_t b = __float_as_uint(x);  // (above one's bits as integers: larger, negative or NaN)
+    return b > 0x3f800000u ? (x > 1.f ? 0x3f800000u : 0u) : b;
+}
+// x in steps of 2^-50, rounded to nearest (subnormal numbers are 0).
 TQ_DEVFN u64 fixed(float x) {
-    const uint32_t b = __float_as_uint(x);
-    if (b > 0x3f800000u) return x > 1.f ? kOne : 0ull;  // (above one's bits as integers: larger, negative or NaN)
-    const int e = b >> 23;
-    const u64 m = (u64)((b & 0x7fffffu) | (e ? 0x800000u : 0u)) << 28;  // x = m 2^(e - 178), a subnormal's is 0 below
-    const int down = 127 - e;
-    return down > 62 ? 0ull : ((m >> down) + 1) >> 1;
+    const uint32_t b = bits_of(x);
+    const u64 m = (u64)((b & 0x7fffffu) | 0x800000u) << 28;  // x = m 2^(e - 178)
+    return ((m >> min(127 - (int)(b >> 23), 63)) + 1) >> 1;
+}
+// max(r - R q, 0), R q rounded as `fixed` rounds (R = 1 gives q's own value): q's 24 bits times R's, shifted to steps of 2^-50.
+TQ_DEVFN u64 step_down(u64 r, float q, u64 R) {
+    const uint32_t b = bits_of(q), m = (b & 0x7fffffu) | 0x800000u;
+    const u64 low = (u64)(uint32_t)R * m, high = (u64)(uint32_t)(R >> 32) * m + (low >> 32);  // R m = high 2^32 + the low word
+    const u64 x = high << 10 | (uint32_t)low >> 22;                                           // R q = x 2^(e - 128)
+    const u64 rq = ((x >> min(127 - (int)(b >> 23), 63)) + 1) >> 1;
+    return r > rq ? r - rq : 0ull;
 }
 
-// The residual after `k` rejections of a node: R of each rejection before it, and the shift that brought its sum up to 2^49 .. 2^50.
-struct Steps {
-    u64 R[kNodes];
-    int shift[kNodes];
-};
-// max(r - R q, 0) 2^shift, q and R in steps of 2^-50.
-TQ_DEVFN u64 step_down(u64 r, u64 q, u64 R, int shift) {
-    const u64 hi = __umul64hi(R, q), lo = R * q;
-    const u64 rq = (hi << 14) | (lo >> 50);
-    return r > rq ? (r - rq) << shift : 0ull;
+// u q < p, exactly: the sum's sign is not rounded (the powers of two keep it from underflow).
+TQ_DEVFN bool below(float u, float q, float p) { return fmaf(u * 4294967296.f, q * 4294967296.f, -p * 18446744073709551616.f) < 0.f; }
+// u q R < r, exactly, as integers: u and q are 24 bits and a power of two each.
+TQ_DEVFN bool below(float u, float q, u64 R, u64 r) {
+    if (!(u > 0.f)) return u <= 0.f && r > 0;  // (a NaN accepts nothing)
+    const uint32_t bu = __float_as_uint(fminf(u, 2.f)), bq = __float_as_uint(q);
+    const int eu = bu >> 23, eq = bq >> 23;
+    const u64 m = (u64)((bu & 0x7fffffu) | (eu ? 0x800000u : 0u)) * ((bq & 0x7fffffu) | (eq ? 0x800000u : 0u));
+    const u64 high = __umul64hi(m, R), low = m * R;  // u q R = (high 2^64 + low) 2^-s, below 2^112
+    const int s = 300 - max(eu, 1) - max(eq, 1);     // 45 at least
+    if (s >= 128) return r > 0;
+    if (s > 64 && r >> (128 - s)) return true;  // r 2^s has more than 128 bits
+    const u64 rh = s >= 64 ? r << (s - 64) : r >> (64 - s), rl = s >= 64 ? 0 : r << s;
+    return high < rh || (high == rh && low < rl);
 }
 
 TQ_DEVFN uint32_t cluster_rank() {
@@ -103,13 +119,19 @@ TQ_DEVFN u64 warp_prefix(u64 x) {
     return x;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) verify_tree_kernel(VerifyArgs a) {
-    extern __shared__ u64 run_sum[];          // [runs]
-    __shared__ float s_p[kNodes], s_q[kNodes], s_u[kNodes];  // of each node: its token's probabilities, its number
-    __shared__ int s_parent[kNodes], s_token[kNodes], s_path[kNodes];
-    __shared__ Steps steps;
-    __shared__ u64 s_total[2][kCluster];      // by turns, so that one exchange needs one barrier
+// KEPT: the residual lies in shared memory, an element of the CTA's part after another; else it is computed from the rows and all
+// rejections of the node.
+template <int DT, bool Q, bool KEPT>
+__global__ void __launch_bounds__(kThreads) verify_tree_kernel(const __grid_constant__ VerifyArgs a) {
+    extern __shared__ u64 shared[];
+    u64* const run_sum = shared;                                  // [runs]
+    u64* const kept = run_sum + a.runs;                           // [runs][kRun]
+    u64* const s_R = kept + (KEPT ? (size_t)a.runs * kRun : 0);   // [n]: of each rejection of the node, R before it
+    float* const s_p = reinterpret_cast<float*>(s_R + a.n);       // of each node: its token's probabilities, its number
+    float *const s_q = s_p + a.n, *const s_u = s_q + a.n;
+    int *const s_parent = reinterpret_cast<int*>(s_u + a.n), *const s_token = s_parent + a.n, *const s_path = s_token + a.n;
+    int* const s_shift = s_path + a.n;         // of each rejection: how much finer its steps became; without q: its token
+    __shared__ u64 s_total[2][kCluster];       // by turns, so that one exchange needs one barrier
     __shared__ u64 s_part[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), size = cluster_size();
@@ -119,94 +141,112 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(VerifyArgs a) {
     pdl_wait();
     const int used = a.n_tok ? min(max(a.n_tok[b], 0), a.n) : a.n;
     uint32_t wrong = 0;
-    for (int i = tid; i < used; i += kThreads) {
+    for (int i = tid; i < a.n; i += kThreads) {
         const int parent = a.parent[row0 + i], token = a.tokens[row0 + i];
-        const bool ok = i > 0 && (uint32_t)parent < (uint32_t)i && (uint32_t)token < (uint32_t)a.V;
-        if (i > 0 && !ok) wrong |= TQ_DEVERR_BAD_ID;
+        const bool ok = i > 0 && i < used && (uint32_t)parent < (uint32_t)i && (uint32_t)token < (uint32_t)a.V;
+        if (i > 0 && i < used && !ok) wrong |= TQ_DEVERR_BAD_ID;
         s_parent[i] = ok ? parent : -1;
         s_token[i] = token;
         s_u[i] = a.u[row0 + i];
         // (fmaxf drops a NaN)
         s_p[i] = ok ? fminf(fmaxf(load_p<DT>(a.p, (row0 + parent) * a.p_stride + token), 0.f), 1.f) : 0.f;
-        s_q[i] = ok && a.q ? fminf(fmaxf(load_p<DT>(a.q, (row0 + parent) * a.q_stride + token), 0.f), 1.f) : 1.f;
+        s_q[i] = Q && ok ? fminf(fmaxf(load_p<DT>(a.q, (row0 + parent) * a.q_stride + token), 0.f), 1.f) : 1.f;
     }
     if (wrong && a.err && rank == 0) atomicOr(a.err, wrong);
     __syncthreads();
 
     const int first = (int)rank * a.runs;  // of this CTA's runs
-    int turn = 0;
-    // r of element x of the rows of `node`, after `k` rejections.
-    auto residual = [&](const void* prow, const void* qrow, int x, int k, const int* gone) {
-        u64 r = fixed(load_p<DT>(prow, x));
-        if (a.q) {
-            if (k) {
-                const u64 q = fixed(load_p<DT>(qrow, x));
-                for (int j = 0; j < k; ++j) r = step_down(r, q, steps.R[j], steps.shift[j]);
-            }
+    int turn = 0, node = 0, length = 1, k = 0;  // k: rejections of the node
+    u64 R = kOne, mine = 0, before = 0;         // of the whole vocabulary, this CTA's part, the parts before it
+    auto row_p = [&](int at) { return reinterpret_cast<const char*>(a.p) + (row0 + at) * a.p_stride * (DT == TQ_F32 ? 4 : 2); };
+    auto row_q = [&](int at) { return reinterpret_cast<const char*>(a.q) + (row0 + at) * a.q_stride * (DT == TQ_F32 ? 4 : 2); };
+    // An element's residual after the node's k rejections, from its probabilities.
+    auto residual = [&](float p, float q, int x) {
+        u64 r = fixed(p);
+        if (Q) {
+            for (int j = 0; j < k; ++j) r = step_down(r, q, s_R[j]) << s_shift[j];
         } else {
             for (int j = 0; j < k; ++j)
-                if (x == gone[j]) r = 0;
+                if (x == s_shift[j]) r = 0;
         }
         return r;
     };
-    // The sum of r over the vocabulary; run_sum holds this CTA's runs, `mine` and `before` its own total and that of the CTAs before.
-    auto pass = [&](const void* prow, const void* qrow, int k, const int* gone, u64& mine, u64& before) {
+    // The residual after k rejections, and its sums: from the rows, after a node's first rejection, or by one more step from what is kept.
+    auto sums_of = [&](auto how) {
+        constexpr bool AGAIN = decltype(how)::value == 2, FIRST = decltype(how)::value == 1;
+        const char *prow = row_p(node), *qrow = row_q(node);
+        const u64 R1 = R;
         u64 sum = 0;
-        for (int i = warp; i < a.runs; i += kWarps) {
-            const int x0 = (first + i) * kRun;
-            u64 r = 0;
+        constexpr int N = kRun / 32, kTwo = 2;  // elements a lane, runs on their way at a time
+        for (int i0 = warp; i0 < a.runs; i0 += kTwo * kWarps) {
+            float p[kTwo][N], q[kTwo][N];
 #pragma unroll
-            for (int c = 0; c < kRun / 32; ++c) {
-                const int x = x0 + c * 32 + lane;
-                if (x < a.V) r += residual(prow, qrow, x, k, gone);
+            for (int z = 0; z < kTwo; ++z) {
+                const int i = i0 + z * kWarps, x0 = (first + i) * kRun + lane;
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    const int x = x0 + c * 32;
+                    const bool in = i < a.runs && x < a.V;
+                    p[z][c] = in && !AGAIN ? load_p<DT>(prow, x) : 0.f;
+                    q[z][c] = Q && in && k ? load_p<DT>(qrow, x) : 0.f;
+                }
             }
-            r = warp_sum(r);
-            if (lane == 0) run_sum[i] = r;
-            sum += r;
+#pragma unroll
+            for (int z = 0; z < kTwo; ++z) {
+                const int i = i0 + z * kWarps;
+                if (i >= a.runs) break;
+                u64 r = 0;
+                u64* const at = kept + (KEPT ? i * kRun + lane : 0);
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    u64 v;
+                    if (AGAIN) {
+                        v = step_down(at[c * 32], q[z][c], R1);
+                    } else if (FIRST) {  // R is 1
+                        const u64 f = fixed(p[z][c]), g = fixed(q[z][c]);
+                        v = f > g ? f - g : 0;
+                    } else {
+                        v = residual(p[z][c], q[z][c], (first + i) * kRun + lane + c * 32);
+                    }
+                    if (KEPT) at[c * 32] = v;
+                    r += v;
+                }
+                r = warp_sum(r);
+                if (lane == 0) run_sum[i] = r;
+                sum += r;
+            }
         }
+        return sum;
+    };
+    auto pass = [&]() {
+        u64 sum;
+        if (KEPT && Q && k > 1) sum = sums_of(std::integral_constant<int, 2>{});
+        else if (Q && k == 1) sum = sums_of(std::integral_constant<int, 1>{});
+        else sum = sums_of(std::integral_constant<int, 0>{});
         if (lane == 0) s_part[warp] = sum;
         __syncthreads();
         mine = warp_sum(lane < kWarps ? s_part[lane] : 0ull);
         if (warp == 0 && lane < (int)size) store_remote(&s_total[turn][rank], lane, mine);
         cluster_sync();
-        u64 all = 0;
-        before = 0;
+        R = before = 0;
         for (uint32_t c = 0; c < size; ++c) {
             if (c < rank) before += s_total[turn][c];
-            all += s_total[turn][c];
+            R += s_total[turn][c];
         }
         turn ^= 1;
-        return all;
     };
 
-    auto row_p = [&](int node) {
-        return reinterpret_cast<const char*>(a.p) + (row0 + node) * a.p_stride * (DT == TQ_F32 ? 4 : 2);
-    };
-    auto row_q = [&](int node) {
-        return reinterpret_cast<const char*>(a.q) + (row0 + node) * a.q_stride * (DT == TQ_F32 ? 4 : 2);
-    };
-    int* const gone = steps.shift;  // without q: the tokens of the rejected children
-    int node = 0, length = 1, k = 0;
-    u64 R = kOne, mine = 0, before = 0;
-    bool summed = false;  // run_sum holds the sums of r as it is
+    bool summed = false;  // run_sum and what is kept are those of r as it is
     if (tid == 0) s_path[0] = 0;
     for (int i = 1; i < used; ++i) {
         if (s_parent[i] != node) continue;
-        const int x = s_token[i];
         bool yes;
         u64 r = 0;
         if (k == 0) {
-            yes = (double)s_u[i] * (double)s_q[i] < (double)s_p[i];  // (the product is exact)
+            yes = below(s_u[i], s_q[i], s_p[i]);
         } else {
-            r = fixed(s_p[i]);
-            if (a.q) {
-                const u64 q = fixed(s_q[i]);
-                for (int j = 0; j < k; ++j) r = step_down(r, q, steps.R[j], steps.shift[j]);
-            } else {
-                for (int j = 0; j < k; ++j)
-                    if (gone[j] == x) r = 0;
-            }
-            yes = (double)s_u[i] * (double)s_q[i] * (double)R < (double)r;
+            r = residual(s_p[i], s_q[i], s_token[i]);
+            yes = below(s_u[i], s_q[i], R, r);
         }
         if (yes) {
             node = i;
@@ -217,40 +257,40 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(VerifyArgs a) {
             ++length;
             continue;
         }
-        __syncthreads();  // the last reads of steps
-        if (a.q) {
-            if (tid == 0) {
-                steps.R[k] = R;
-                steps.shift[k] = 0;
-            }
-            __syncthreads();
-            R = pass(row_p(node), row_q(node), ++k, gone, mine, before);
+        if (!Q && k == 0) r = fixed(s_p[i]);
+        if (!KEPT || !Q || k == 0) __syncthreads();  // the last reads of the rejections
+        if (tid == 0) {
+            s_R[k] = R;
+            s_shift[k] = Q ? 0 : s_token[i];
+        }
+        ++k;
+        if (!KEPT || !Q) __syncthreads();  // (else they are read again behind the pass's barriers)
+        if (Q) {
+            pass();
             summed = true;
-            const int up = R ? max(__clzll((long long)R) - 14, 0) : 0;
-            if (up) {  // keep 2^-50 of what is left, however little that is
+            if (R && R < 1ull << 34) {  // little is left: its steps are made finer, 2^-50 of it to 2^-49
+                const int up = __clzll((long long)R) - 14;
                 __syncthreads();
-                if (tid == 0) steps.shift[k - 1] = up;
+                if (tid == 0) s_shift[k - 1] = up;
                 for (int j = tid; j < a.runs; j += kThreads) run_sum[j] <<= up;
+                if (KEPT)
+                    for (int j = tid; j < a.runs * kRun; j += kThreads) kept[j] <<= up;
                 R <<= up;
                 mine <<= up;
                 before <<= up;
                 __syncthreads();
             }
         } else {
-            if (k == 0) r = fixed(s_p[i]);
             R = R > r ? R - r : 0;
-            if (tid == 0) gone[k] = x;
-            ++k;
-            __syncthreads();
         }
     }
     if (used == 0) {
         length = 0;
     } else {
-        if (!summed) R = pass(row_p(node), row_q(node), k, gone, mine, before);
+        if (!summed) pass();
         if (R == 0) {
             k = 0;
-            R = pass(row_p(node), row_q(node), 0, gone, mine, before);
+            pass();
         }
     }
     __syncthreads();
@@ -284,7 +324,9 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(VerifyArgs a) {
             u64 r[kEach], own = 0;
 #pragma unroll
             for (int c = 0; c < kEach; ++c) {
-                r[c] = x0 + c < a.V ? residual(row_p(node), row_q(node), x0 + c, k, gone) : 0;
+                const int x = x0 + c;
+                if (KEPT) r[c] = kept[run * kRun + lane * kEach + c];
+                else r[c] = x < a.V ? residual(load_p<DT>(row_p(node), x), Q && k ? load_p<DT>(row_q(node), x) : 0.f, x) : 0;
                 own += r[c];
             }
             const u64 upto = warp_prefix(own);
@@ -302,6 +344,24 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(VerifyArgs a) {
         }
     }
     cluster_sync();  // no CTA ends while another may still write its totals here
+}
+
+// Clusters of more than 8 CTAs, allowed once a kernel.
+cudaError_t allow_wide(const void* kernel) {
+    static std::mutex mu;
+    static std::unordered_map<const void*, bool> done;
+    std::lock_guard<std::mutex> lock(mu);
+    bool& yes = done[kernel];
+    if (yes) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    yes = e == cudaSuccess;
+    return e;
+}
+
+template <int DT>
+void (*kernel_of(bool q, bool kept))(VerifyArgs) {
+    if (q) return kept ? verify_tree_kernel<DT, true, true> : verify_tree_kernel<DT, true, false>;
+    return kept ? verify_tree_kernel<DT, false, true> : verify_tree_kernel<DT, false, false>;
 }
 
 }  // namespace
@@ -327,15 +387,20 @@ extern "C" tq_status tq_verify_tree(const void* p, int64_t p_stride, const void*
         if (!aligned(x, 4)) return TQ_ERR_INVALID;
     VerifyArgs a{p, q, p_stride, q ? q_stride : 0, tokens, parent, u, n_tok, path, count, next, err, n, V, 0};
     const int runs = (V + kRun - 1) / kRun;
-    // few trees: each over several CTAs, as long as each has two runs to a warp
+    // Each tree over several CTAs, since it waits for the slowest of its passes: as many as four to an SM make, each with a run for
+    // every warp; sixteen to a cluster where the trees are few.
     int size_c = 1;
-    while (size_c < kCluster && B * size_c < 152 && runs >= 2 * kWarps * 2 * size_c) size_c *= 2;
+    while (size_c < kCluster && B * size_c * 2 <= (size_c < 8 ? 4 * 152 : 64) && runs >= 32 * size_c) size_c *= 2;
     a.runs = (runs + size_c - 1) / size_c;
-    void (*kernel)(VerifyArgs) = dt == TQ_F32 ? verify_tree_kernel<TQ_F32>
-                                              : (dt == TQ_BF16 ? verify_tree_kernel<TQ_BF16> : verify_tree_kernel<TQ_F16>);
-    const size_t smem = (size_t)a.runs * sizeof(u64);
-    constexpr size_t kStatic = 40 * 1024;  // above the kernel's own arrays: the limit that is raised holds for both together
+    const size_t nodes = (size_t)n * (sizeof(u64) + 3 * sizeof(float) + 4 * sizeof(int)), sums = (size_t)a.runs * sizeof(u64);
+    // The residual stays in shared memory where it fits (five rejections in each of 48 trees over 131072 tokens: 130 us in parts that
+    // fit, 367 us in parts twice as large, computed anew in each pass).
+    const bool kept = nodes + sums * (1 + kRun) <= 200 * 1024;
+    const size_t smem = nodes + sums * (1 + (kept ? kRun : 0));
+    void (*kernel)(VerifyArgs) = dt == TQ_F32 ? kernel_of<TQ_F32>(q, kept) : (dt == TQ_BF16 ? kernel_of<TQ_BF16>(q, kept) : kernel_of<TQ_F16>(q, kept));
+    constexpr size_t kStatic = 1024;  // above the kernel's own arrays: the limit that is raised holds for both together
     if (ensure_smem((const void*)kernel, smem + kStatic) != cudaSuccess) return TQ_ERR_CUDA;
+    if (size_c > 8 && allow_wide((const void*)kernel) != cudaSuccess) return TQ_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(B * size_c));
     cfg.blockDim = dim3(kThreads);
