@@ -952,14 +952,25 @@ class PagePool:
         else:
             self.table, self.held, self.free, self.n_free = storage
 
+    _kept = None
+
     def _refs(self):
-        """(descriptor, device) of the tensors as they are now."""
-        dev = self.table.get_device()
+        """(descriptor, device, tensors, what they and the sizes were), kept while all of it, compared on every call, is the same."""
+        table, held, free, n_free = tensors = self.table, self.held, self.free, self.n_free
+        now = (table.data_ptr(), held.data_ptr(), free.data_ptr(), n_free.data_ptr(), self.batch, self.width, self.page, self.pages)
+        kept = self._kept
+        if kept is not None and kept[3] == now:
+            a, b, c, d = kept[2]
+            if table is a and held is b and free is c and n_free is d:
+                return kept
+        dev = table.get_device()
         if not self.table.is_cuda:
             raise ValueError("a pool's tensors must be on a CUDA device")
-        return tq_page_pool_t(_ints(self.table, "table", self.batch * self.width, dev), _ints(self.held, "held", self.batch, dev),
-                              _ints(self.free, "free", self.pages, dev), _ints(self.n_free, "n_free", 1, dev), self.batch,
-                              self.width, self.page, self.pages), dev
+        c = tq_page_pool_t(_ints(table, "table", self.batch * self.width, dev), _ints(held, "held", self.batch, dev),
+                           _ints(free, "free", self.pages, dev), _ints(n_free, "n_free", 1, dev), self.batch, self.width, self.page,
+                           self.pages)
+        self._kept = kept = (c, dev, tensors, now)  # in one piece: another thread finds the old or the new
+        return kept
 
 
 Plan = collections.namedtuple("Plan", "slots positions lens starts")
@@ -976,7 +987,7 @@ def kv_plan(pool: PagePool, lens, n_new, n: int | None = None, tokens: int | Non
     if n is not None and n < 1 or tokens is not None and (tokens < 0 or path is not None):
         raise ValueError("n must be at least 1, tokens at least 0 and without a path")
     torch = _torch()
-    (c, dev), B = pool._refs(), pool.batch
+    (c, dev, _, _), B = pool._refs(), pool.batch
     lp, wp = _ints(lens, "lens", B, dev), _ints(n_new, "n_new", B, dev)
     pp = 0 if path is None else _ints(path, "path", B * n, dev)
     shape, device = ((B, n) if n is not None else (tokens,)), lens.device
@@ -1052,6 +1063,26 @@ class LatentCache:
             raise ValueError("rows must be bf16 or f16")
         return tq_latent_pages_t(t.data_ptr(), _dt(t), self.latent, self.rope, self.page, self.pages, self.page)
 
+    _kept = None
+
+    def _now(self):
+        """(rows, descriptor, workspace sizes, what they were), kept while all that the descriptor is made of is the same."""
+        rows = self.rows
+        now = (rows.data_ptr(), self.latent, self.rope, self.page, self.pages)
+        kept = self._kept
+        if kept is None or kept[0] is not rows or kept[3] != now:
+            self._kept = kept = (rows, self.c(), {}, now)  # in one piece: another thread finds the old or the new
+        return kept
+
+    def _tree_bytes(self, now, B, n, H, max_len) -> int:
+        sizes, key = now[2], (B, n, H, max_len)
+        nb = sizes.get(key)
+        if nb is None:
+            if len(sizes) > 4096:
+                sizes.clear()
+            nb = sizes[key] = int(load().tq_latent_attend_tree_workspace_bytes(ctypes.byref(now[1]), B, n, H, max_len))
+        return nb
+
 
 def _rows_at(t, name, width):
     """(rows, row stride) of t [..., width] whose rows lie at one stride."""
@@ -1076,7 +1107,7 @@ def latent_append(cache: LatentCache, c, k_rope, slots, rope: Rope | None = None
         if rope.steps.get_device() != dev:
             raise ValueError("the rotary frequencies must be on the tokens' device")
         turn, pos = rope.ref(), _ints(positions, "positions", T, dev)
-    _check(load().tq_latent_append(ctypes.byref(cache.c()), c.data_ptr(), cs, k_rope.data_ptr(), ks, _dt(c), T, at, turn, pos,
+    _check(load().tq_latent_append(ctypes.byref(cache._now()[1]), c.data_ptr(), cs, k_rope.data_ptr(), ks, _dt(c), T, at, turn, pos,
                                    _word(err, dev), _raw_stream(c)), "tq_latent_append")
 
 
@@ -1106,14 +1137,14 @@ def latent_attend_tree(cache: LatentCache, q, table, lens, scale: float, new=Non
     mp = 0 if mask is None else _ints(mask, "mask", B * n * (-(-n // 64)), dev, _torch().int64)
     np_ = 0 if n_tok is None else _ints(n_tok, "n_tok", B, dev)
     max_len = wide * cache.page if max_len is None else int(max_len)
-    torch, device, c = _torch(), q.device, cache.c()
+    torch, device, now = _torch(), q.device, cache._now()
     o = torch.empty((B, n, H, cache.latent), dtype=q.dtype, device=device)
-    nb = int(load().tq_latent_attend_tree_workspace_bytes(ctypes.byref(c), B, n, H, max_len))
+    nb = cache._tree_bytes(now, B, n, H, max_len)
     if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
         raise ValueError("ws must be contiguous, on q's device")
     if ws is None or ws.numel() * ws.element_size() < nb:
         ws = torch.empty(nb, dtype=torch.uint8, device=device)
-    _check(load().tq_latent_attend_tree(ctypes.byref(c), q.data_ptr(), qs, B, n, H, tp, wide, lp, max_len, fp, fs, mp, np_, scale,
+    _check(load().tq_latent_attend_tree(ctypes.byref(now[1]), q.data_ptr(), qs, B, n, H, tp, wide, lp, max_len, fp, fs, mp, np_, scale,
                                         o.data_ptr(), ws.data_ptr(), nb, _word(err, dev), _raw_stream(q)), "tq_latent_attend_tree")
     return o
 
@@ -1143,7 +1174,7 @@ def latent_attend_prompt(q, k, v, k_rope, q_starts, kv_starts, scale: float, cau
     hs = k.stride(1) if H > 1 else 128
     ks = k.stride(0) if Tkv > 1 else max(k.stride(0), (H - 1) * hs + 128)
     o = torch.empty((Tq, H, 128), dtype=q.dtype, device=q.device)
-    nb = int(load().tq_latent_attend_prompt_workspace_bytes())
+    nb = 4  # (tq_latent_attend_prompt_workspace_bytes: a counter)
     if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
         raise ValueError("ws must be contiguous, on q's device")
     if ws is None or ws.numel() * ws.element_size() < nb:
