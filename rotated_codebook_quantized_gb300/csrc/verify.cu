@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(const __grid_cons
         s_q[i] = Q && ok ? fminf(fmaxf(load_p<DT>(a.q, (row0 + parent) * a.q_stride + token), 0.f), 1.f) : 1.f;
     }
     if (wrong && a.err && rank == 0) atomicOr(a.err, wrong);
+    if (rank == 0 && tid == 0) a.next[b] = -1;  // until the search finds one, behind a pass's barrier of the cluster
     __syncthreads();
 
     const int first = (int)rank * a.runs;  // of this CTA's runs
@@ -296,10 +297,7 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(const __grid_cons
     __syncthreads();
     if (rank == 0) {
         for (int i = tid; i < a.n; i += kThreads) a.path[row0 + i] = i < length ? s_path[i] : -1;
-        if (tid == 0) {
-            a.count[b] = length;
-            if (R == 0 || used == 0) a.next[b] = -1;
-        }
+        if (tid == 0) a.count[b] = length;
     }
     if (used && R && warp == 0) {
         // the first token whose prefix sum passes u R: in this CTA where the threshold falls into its part

@@ -514,6 +514,55 @@ def test_expired_waits_are_reported(lib):
     assert torch.equal(s.run(err=err), want) and torch.equal(prompt(err), want2) and lib.check_error(err) == 0
 
 
+def test_expanded_more_jobs_than_sms_in_a_graph(lib):
+    """Jobs that CTAs take as they come free, the counter in a workspace that holds anything; replayed, and another call between."""
+    q, kv, kr, qs, ks = _prompts([700, 300, 513, 40], [900, 300, 600, 1000], 40, "bfloat16", 15)
+    k, v, dq, dk = kv[..., :128], kv[..., 128:], _int(qs), _int(ks)
+    ws = torch.full((64,), 255, dtype=torch.uint8, device="cuda")
+    want = lib.latent_attend_prompt(q, k, v, kr, dq, dk, SCALE, ws=ws)
+    _check_prompts(want[:, :2], q[:, :2], k[:, :2], v[:, :2], kr, qs, ks)
+    _check_prompts(want[:, 39:], q[:, 39:], k[:, 39:], v[:, 39:], kr, qs, ks)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            got = lib.latent_attend_prompt(q, k, v, kr, dq, dk, SCALE, ws=ws)
+            twice = lib.latent_attend_prompt(q, k, v, kr, dq, dk, SCALE, ws=ws)
+        for _ in range(3):
+            got.zero_()
+            twice.zero_()
+            graph.replay()
+            assert torch.equal(lib.latent_attend_prompt(q, k, v, kr, dq, dk, SCALE, ws=ws), want)
+            assert torch.equal(got, want) and torch.equal(twice, want)
+    torch.cuda.current_stream().wait_stream(stream)
+
+
+@pytest.mark.parametrize("B,n,H,context", [(200, 1, 64, 300), (60, 9, 64, 100), (1, 64, 128, 900), (170, 2, 24, 64)])
+def test_absorbed_more_units_than_sms(lib, B, n, H, context):
+    """Runs that cross units: several tiles to a CTA, tiles that two of them share."""
+    s = Scene(lib, B, n, H, context, 32, "bfloat16")
+    o = s.run()
+    s.check(o)
+    assert torch.equal(o, s.run())
+
+
+def test_two_streams_at_once(lib):
+    """Calls on two streams with scratch of their own."""
+    s, t = Scene(lib, 6, 2, 64, 3000, 64, "bfloat16"), Scene(lib, 9, 1, 32, 2000, 16, "float16")
+    want = s.run(), t.run()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(a):
+            x = s.run()
+        with torch.cuda.stream(b):
+            y = t.run()
+        a.synchronize()
+        b.synchronize()
+        assert torch.equal(x, want[0]) and torch.equal(y, want[1])
+
+
 # ---------------------------------------------------------------- together
 
 def test_both_forms_agree_over_a_served_prompt(lib):
@@ -542,3 +591,18 @@ def test_both_forms_agree_over_a_served_prompt(lib):
     got = torch.einsum("hc,hdc->hd", o[0, 0].float(), wv)
     # relative 2-norms: bf16 roundings of keys, values, queries, weights and results, each 2^-8 / sqrt(3) rms at most: eight of them
     assert float((got - full[-1].float()).norm() / full[-1].float().norm()) < math.sqrt(8) * 2.0 ** -8
+
+
+def test_served_requests_with_drafts(lib):
+    """The example of all of them in a row: planned, written, attended in both forms, verified; nothing reported, every accepted token
+    counted, and both forms the same up to eight bf16 roundings (as above)."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "latent_decode.py")
+    spec = importlib.util.spec_from_file_location("latent_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    worst, bits, lens, accepted = example.main()
+    assert bits == 0 and sum(lens) == sum(example.PROMPTS) + accepted
+    assert worst < math.sqrt(8) * 2.0 ** -8

@@ -392,6 +392,15 @@ def test_verify_edges(lib):
     assert path.tolist() == [[-1, -1, -1]] and count.tolist() == [0] and token.tolist() == [-1]
 
 
+def test_verify_rows_that_are_no_distributions(lib):
+    """Sums past 64 bits and others: some token of the vocabulary, or -1."""
+    for x, V in ((1.0, 1 << 17), (3.0, 20000), (0.01, 50000), (float("inf"), 1000)):
+        p = torch.full((2, 3, V), x, device="cuda")
+        u = torch.full((2, 3), 0.7, device="cuda")
+        path, count, token = lib.verify_tree(p, _int([[0, 1, 2]] * 2), _int([[-1, 0, 1]] * 2), u, q=p)
+        assert all(-1 <= t < V for t in token.tolist()) and all(1 <= c <= 3 for c in count.tolist())
+
+
 def test_verify_bad_nodes_are_never_accepted(lib):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     p = torch.full((1, 5, 4), 0.25, device="cuda")
