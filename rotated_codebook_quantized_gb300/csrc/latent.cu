@@ -48,66 +48,49 @@ struct Eight {
     }
 };
 
-// A warp to N tokens at a time, all of whose loads it has on their way: a lane to 16 of a latent vector's elements and to a pair of the
-// rotary key's, so that every lane has one sine and cosine a token.  (16-byte pieces dealt to threads one after another left those of
-// the rotary keys, four sines each, to an eighth of them: 48 us for 65536 tokens.)
-template <int DT, bool BF, int N>
+// A warp to a token, a lane to 16 of its latent vector's elements and to a pair of its rotary key's, so that every lane has one sine and
+// cosine.  (16-byte pieces dealt to threads one after another left those of the rotary keys, four sines each, to an eighth of
+// them.)  Bound by HBM: 65536 tokens 23 to 24 us, 6.3 to 6.6 TB/s (pieces: 48 us; four tokens to a warp at a time: 23.3, and 10.0 for
+// 8.5 over 32768 tokens).  48 tokens: 1.7 us, the launch.
+template <int DT, bool BF>
 __global__ void __launch_bounds__(256) latent_append_kernel(AppendArgs a) {
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     // the lane's two elements of the rotary key
     const bool turned = a.rope.steps && lane < a.rope.rotary / 2;
     int e0 = 2 * lane, e1 = e0 + 1;
-    if (a.rope.steps && a.rope.layout == TQ_ROPE_HALF && turned) e0 = lane, e1 = lane + a.rope.rotary / 2;
+    if (a.rope.layout == TQ_ROPE_HALF && turned) e0 = lane, e1 = lane + a.rope.rotary / 2;
     pdl_wait();
     const uint64_t step = turned ? a.rope.steps[lane] : 0;
-    const int64_t warps = (int64_t)gridDim.x * 8;
-    for (int64_t t0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * N; t0 < a.T; t0 += warps * N) {
-        int slot[N], pos[N];
-        Eight<DT> c[N][2];
-        float x[N], y[N];
+    for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * 8) {
+        const int slot = a.slots[t], pos = a.rope.steps ? a.positions[t] : 0;
+        Eight<DT> c[2];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int64_t t = min(t0 + i, a.T - 1);
-            slot[i] = t0 + i < a.T ? a.slots[t] : -1;
-            pos[i] = a.rope.steps ? a.positions[t] : 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) c[i][h].load(a.c, t * a.cs + h * 256 + lane * 8);
-            x[i] = load_as_float(a.k, t * a.ks + e0, DT);
-            y[i] = load_as_float(a.k, t * a.ks + e1, DT);
+        for (int h = 0; h < 2; ++h) c[h].load(a.c, t * a.cs + h * 256 + lane * 8);
+        const float x = load_as_float(a.k, t * a.ks + e0, DT), y = load_as_float(a.k, t * a.ks + e1, DT);
+        if (slot < 0) continue;
+        if ((slot >> a.lpage) >= a.pages) {
+            if (lane == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
+            continue;
         }
+        const int64_t row = (int64_t)(slot >> a.lpage) * a.page_stride + (slot & ((1 << a.lpage) - 1));
+        uint16_t* const to = reinterpret_cast<uint16_t*>(a.rows) + row * kLatentRow;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (slot[i] < 0) continue;
-            if ((slot[i] >> a.lpage) >= a.pages) {
-                if (lane == 0 && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
-                continue;
-            }
-            const int64_t row = (int64_t)(slot[i] >> a.lpage) * a.page_stride + (slot[i] & ((1 << a.lpage) - 1));
-            uint16_t* const to = reinterpret_cast<uint16_t*>(a.rows) + row * kLatentRow;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(to + h * 256 + lane * 8) = c[i][h].template packed<BF>();
-            float u = x[i], v = y[i];
-            if (turned) {
-                float sn, cs;
-                rope_angle(pos[i], step, sn, cs);
-                u = a.rope.factor * (x[i] * cs - y[i] * sn);
-                v = a.rope.factor * (x[i] * sn + y[i] * cs);
-            }
-            if (e1 == e0 + 1 && !(e0 & 1)) {
-                *reinterpret_cast<uint32_t*>(to + kLatent + e0) = pack16<BF>(u, v);
-            } else {
-                to[kLatent + e0] = to16<BF>(u);
-                to[kLatent + e1] = to16<BF>(v);
-            }
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(to + h * 256 + lane * 8) = c[h].template packed<BF>();
+        float u = x, v = y;
+        if (turned) {
+            float sn, cs;
+            rope_angle(pos, step, sn, cs);
+            u = a.rope.factor * (x * cs - y * sn);
+            v = a.rope.factor * (x * sn + y * cs);
+        }
+        if (e1 == e0 + 1 && !(e0 & 1)) {
+            *reinterpret_cast<uint32_t*>(to + kLatent + e0) = pack16<BF>(u, v);
+        } else {
+            to[kLatent + e0] = to16<BF>(u);
+            to[kLatent + e1] = to16<BF>(v);
         }
     }
-}
-
-template <int DT>
-void (*append_of(bool bf, bool many))(AppendArgs) {
-    if (bf) return many ? latent_append_kernel<DT, true, 4> : latent_append_kernel<DT, true, 1>;
-    return many ? latent_append_kernel<DT, false, 4> : latent_append_kernel<DT, false, 1>;
 }
 
 }  // namespace
@@ -143,11 +126,11 @@ extern "C" tq_status tq_latent_append(const tq_latent_pages_t* cache, const void
     a.err = err;
     a.lpage = ilog2(cache->page);
     if (rope) a.rope = *rope;
-    // four tokens a warp hide the loads' latency where there are warps enough; fewer tokens go one to a warp
-    const bool many = T >= 8192, bf = cache->dt == TQ_BF16;
-    const int64_t warps = many ? (T + 3) / 4 : T;
-    const unsigned grid = (unsigned)std::min<int64_t>((warps + 7) / 8, 152 * 8);
+    const unsigned grid = (unsigned)std::min<int64_t>((T + 7) / 8, 152 * 8);
+    const bool bf = cache->dt == TQ_BF16;
     void (*kernel)(AppendArgs) =
-        dt == TQ_F32 ? append_of<TQ_F32>(bf, many) : dt == TQ_BF16 ? append_of<TQ_BF16>(bf, many) : append_of<TQ_F16>(bf, many);
+        dt == TQ_F32 ? (bf ? latent_append_kernel<TQ_F32, true> : latent_append_kernel<TQ_F32, false>)
+        : dt == TQ_BF16 ? (bf ? latent_append_kernel<TQ_BF16, true> : latent_append_kernel<TQ_BF16, false>)
+                        : (bf ? latent_append_kernel<TQ_F16, true> : latent_append_kernel<TQ_F16, false>);
     return launch_pdl(kernel, dim3(grid), dim3(256), 0, as_stream(stream), a);
 }

@@ -1,19 +1,24 @@
 // Attention of drafted trees over the paged latent cache (the absorbed form), on the 5th-generation tensor cores.
 //
 // A cached row of 576 elements is the key of every head and its first 512 the value, so 64 query rows (heads of drafts) share
-// each token that is read.  A persistent CTA takes a run of steps of 32 tokens; tokens come by tensor copies into a ring of four
-// places, one 128-byte swizzled row a token for each 64 elements, which serves as the K-major operand of
-//   scores   S[64 x 32]   = Q (shared) . K^T     36 MMAs of K = 16
+// each token that is read.  A persistent CTA takes steps of 32 tokens; they come by tensor copies into a ring of five places, one 128-byte
+// swizzled row a token for each 64 elements, which serves as the K-major operand of
+//   scores   S[64 x 32]   = Q (TMEM; a third in shared memory) . K^T     36 MMAs of K = 16
 // and as the MN-major operand of
-//   values   O[64 x 512] += P (shared) . V       2 x 2 MMAs of K = 16, N = 256
+//   values   O[64 x 512] += P (shared) . V                               2 x 2 MMAs of K = 16, N = 256
 // M = 64 takes 16 of the 32 TMEM lanes of each warp: O's upper half of the elements lies in the other 16, so that O takes 256
-// columns.  Scores and values are issued by a thread each: behind its own products a thread's next
-// wait is held up, so that one for both leaves the tensor cores idle between them (1810 clocks a step, scores and values alone 1320).  A row's running maximum follows only when a score
-// passes it by a set amount.
+// columns, six blocks of Q (in both halves of the lanes) 192 and two places of scores 64.  Q in shared memory as a whole would leave
+// room for four steps (193 us for 204 over trees).  Scores and values are issued by a thread each: behind its own products a
+// thread's next wait is held up, so that one for both leaves the tensor cores idle between them (1810 clocks a step for 1560).
+// A row's running maximum follows only when a score passes it by a set amount.
 //
 // Tokens past the end and drafts that hold something that is not finite are zeroed in shared memory by two guard warps (a
 // masked weight of 0 times NaN would reach the rows that do not see it); only steps that have such tokens wait for them.
 // Every wait on an mbarrier is bounded; on expiry the CTA sets TQ_DEVERR_TIMEOUT, drains and frees TMEM.
+//
+// Up to 64 rows a sequence: bound by HBM, 1600 clocks a step of 1575 at the copy rate, and by its beginning and end: 32 ragged sequences
+// of up to 16384 tokens, 64 heads: 68 us, 4.6 TB/s of 6.75 over the whole call; 64 rows over 131072 tokens: 50 us.  More rows: by the
+// products, 1090 of 1360 clocks a step (M = 64 runs at half rate): 512 rows over 65536 tokens, two sequences: 183 us, 795 TFLOP/s.
 #include <math.h>
 
 #include <algorithm>
@@ -719,64 +724,80 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     }
 }
 
-// What the CTAs left in parts, joined in their order; rows that see nothing, and drafts that are not in use, are zeros.  A CTA to
-// 1 / gridDim.z of the rows of a tile.
-template <bool BF>
-__global__ void __launch_bounds__(256) latent_join_kernel(AttendArgs a) {
+// What the CTAs left in parts, joined in their order; rows that see nothing, and drafts that are not in use, are zeros.  A warp's lanes
+// have the 512 bytes that a warp of the attention stored at a time, and the 512 after them: 8 elements of 16 rows and two halves;
+// 128 such pieces make a tile.  SPLIT: the parts are dealt to the CTA's 8 warps, a CTA to a piece, where few units are in many parts
+// (64 rows over 131072 tokens, one unit in 152 parts: the call 118 us without).
+template <bool BF, bool SPLIT>
+__global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr int kJoin = 8, kAhead = 4;  // warps; parts on their way at a time
+    __shared__ float s_sum[SPLIT ? kJoin : 1][10][32];
     pdl_trigger();
     pdl_wait();
     const LatentArgs& l = a.l;
-    const int b = blockIdx.y, tile = blockIdx.x, tid = threadIdx.x, own_rows = kRows / gridDim.z, r0 = blockIdx.z * own_rows;
+    const int b = blockIdx.y, tile = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (l.err && tile == 0 && blockIdx.z == 0 && tid == 0 && l.lens[b] != latent_len(l, b)) atomicOr(l.err, TQ_DEVERR_BAD_PAGE);
     const Seq s = seq(l, b);
-    const int64_t y0 = (int64_t)tile * kRows + r0;
-    const int rows = (int)max(min((int64_t)own_rows, (int64_t)l.n * l.H - y0), (int64_t)0);  // of the output
+    const int64_t y0 = (int64_t)tile * kRows;
+    const int rows = (int)max(min((int64_t)kRows, (int64_t)l.n * l.H - y0), (int64_t)0);  // of the output
     const int live = s.steps ? (int)max(min((int64_t)rows, (int64_t)s.live * l.H - y0), (int64_t)0) : 0;
     uint16_t* const out = l.o + ((int64_t)b * l.n * l.H + y0) * kLatent;
-    for (int i = live * (kLatent / 8) + tid; i < rows * (kLatent / 8); i += 256)
+    for (int i = live * (kLatent / 8) + blockIdx.z * 256 + tid; i < rows * (kLatent / 8); i += gridDim.z * 256)
         *reinterpret_cast<uint4*>(out + (int64_t)i * 8) = make_uint4(0u, 0u, 0u, 0u);
     if (live == 0) return;
     const int2 unit = a.units[(int64_t)b * gridDim.x + tile];
     const int c0 = unit.x, c1 = unit.y;
     if (c0 == c1) return;  // one CTA has written its rows
     auto slot_of = [&](int c) { return 2ll * c + (c == c0); };
-    // A thread to a row and 8 elements; neighbours have the rows of a store's run.  Four parts on their way at a time.
-    constexpr int kAhead = 4;
-    for (int i = tid; i < own_rows * (kLatent / 8); i += 256) {
-        const int r = i % own_rows, e = i / own_rows * 2;
-        if (r >= live) continue;
+    for (int piece = SPLIT ? blockIdx.z : blockIdx.z * kJoin + warp; piece < 128; piece += SPLIT ? 128 : gridDim.z * kJoin) {
+        const int row = (piece >> 5) * 16 + (lane & 15), e = (lane >> 4) * 64 + (piece & 31) * 2;
         float o[8] = {}, top = -INFINITY, total = 0.f;
-        for (int c = c0; c <= c1; c += kAhead) {
+        auto add = [&](float level, float sum, const float4 (&z)[2]) {
+            // both to the higher level: weight 1 for its own (also where neither saw anything)
+            const float n = fmaxf(top, level), w0 = top == n ? 1.f : exp2_fast(top - n), w1 = level == n ? 1.f : exp2_fast(level - n);
+            top = n;
+            total = total * w0 + sum * w1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                o[4 * h] = fmaf(o[4 * h], w0, z[h].x * w1);
+                o[4 * h + 1] = fmaf(o[4 * h + 1], w0, z[h].y * w1);
+                o[4 * h + 2] = fmaf(o[4 * h + 2], w0, z[h].z * w1);
+                o[4 * h + 3] = fmaf(o[4 * h + 3], w0, z[h].w * w1);
+            }
+        };
+        constexpr int kDeal = SPLIT ? kJoin : 1;
+        for (int c = c0 + (SPLIT ? warp : 0); c <= c1; c += kAhead * kDeal) {
             float2 stat[kAhead];
             float4 z[kAhead][2];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const int64_t slot = slot_of(min(c + k, c1));
-                stat[k] = a.stat[slot * kRows + r0 + r];
+                const int64_t slot = slot_of(min(c + k * kDeal, c1));
+                stat[k] = a.stat[slot * kRows + row];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) z[k][h] = *reinterpret_cast<const float4*>(a.part + part_at(slot, r0 + r, e + h));
+                for (int h = 0; h < 2; ++h) z[k][h] = *reinterpret_cast<const float4*>(a.part + part_at(slot, row, e + h));
             }
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                if (c + k > c1) break;
-                // both to the higher level: weight 1 for its own (also where neither saw anything)
-                const float n = fmaxf(top, stat[k].x), w0 = top == n ? 1.f : exp2_fast(top - n),
-                            w1 = stat[k].x == n ? 1.f : exp2_fast(stat[k].x - n);
-                top = n;
-                total = total * w0 + stat[k].y * w1;
+            for (int k = 0; k < kAhead; ++k)
+                if (c + k * kDeal <= c1) add(stat[k].x, stat[k].y, z[k]);
+        }
+        if (SPLIT) {
+            s_sum[warp][8][lane] = top;
+            s_sum[warp][9][lane] = total;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    o[4 * h] = fmaf(o[4 * h], w0, z[k][h].x * w1);
-                    o[4 * h + 1] = fmaf(o[4 * h + 1], w0, z[k][h].y * w1);
-                    o[4 * h + 2] = fmaf(o[4 * h + 2], w0, z[k][h].z * w1);
-                    o[4 * h + 3] = fmaf(o[4 * h + 3], w0, z[k][h].w * w1);
-                }
+            for (int k = 0; k < 8; ++k) s_sum[warp][k][lane] = o[k];
+            __syncthreads();
+            if (warp) return;
+            for (int w = 1; w < kJoin; ++w) {
+                const float4 z[2] = {make_float4(s_sum[w][0][lane], s_sum[w][1][lane], s_sum[w][2][lane], s_sum[w][3][lane]),
+                                     make_float4(s_sum[w][4][lane], s_sum[w][5][lane], s_sum[w][6][lane], s_sum[w][7][lane])};
+                add(s_sum[w][8][lane], s_sum[w][9][lane], z);
             }
         }
         const float over = total == 0.f ? 0.f : 1.f / total;  // (a NaN sum stays one)
-        *reinterpret_cast<uint4*>(out + (int64_t)r * kLatent + e * 4) =
-            make_uint4(pack16<BF>(o[0] * over, o[1] * over), pack16<BF>(o[2] * over, o[3] * over), pack16<BF>(o[4] * over, o[5] * over),
-                       pack16<BF>(o[6] * over, o[7] * over));
+        if (row < live)
+            *reinterpret_cast<uint4*>(out + (int64_t)row * kLatent + e * 4) =
+                make_uint4(pack16<BF>(o[0] * over, o[1] * over), pack16<BF>(o[2] * over, o[3] * over),
+                           pack16<BF>(o[4] * over, o[5] * over), pack16<BF>(o[6] * over, o[7] * over));
     }
 }
 
@@ -798,14 +819,19 @@ int64_t most_steps(const tq_latent_pages_t* cache, int32_t B, int32_t n, int32_t
 }
 
 template <bool BF>
-tq_status launch(const AttendArgs& a, const CUtensorMap& rows, const CUtensorMap& fresh, cudaStream_t st) {
+tq_status launch(const AttendArgs& a, const CUtensorMap& rows, const CUtensorMap& fresh, int64_t steps, cudaStream_t st) {  // steps: of a unit
     if (ensure_smem((const void*)latent_attend_kernel<BF>, kSmem) != cudaSuccess) return TQ_ERR_CUDA;
     tq_status s = launch_pdl(latent_attend_kernel<BF>, dim3((unsigned)a.ctas), dim3(32 * kWarps), kSmem, st, a, rows, fresh);
     if (s != TQ_OK) return s;
     const int64_t tiles = ((int64_t)a.l.n * a.l.H + kRows - 1) / kRows;
     const int64_t units = tiles * a.l.B;
-    const int parts = units <= 64 ? 16 : units <= 256 ? 8 : units <= 1024 ? 2 : 1;
-    return launch_pdl(latent_join_kernel<BF>, dim3((unsigned)tiles, (unsigned)a.l.B, (unsigned)parts), dim3(256), 0, st, a);
+    // The parts of a tile dealt to warps: where there are few tiles in many parts (64 rows over 131072 tokens: 50 us for 96; over 30000
+    // tokens, 4 sequences 42 for 54, 8 sequences 63 for 67, 16 sequences 107 for 102).  Else 128 pieces to a tile, over more CTAs
+    // where there are fewer tiles (32 ragged sequences of up to 16384: 71, 73, 79 and 130 us with 16, 8, 4 and one; 200 sequences of
+    // up to 1500: 71, 69, 69 and 91).
+    const bool split = units <= 8 && steps >= 64;
+    const dim3 grid((unsigned)tiles, (unsigned)a.l.B, split ? 128 : units <= 64 ? 16 : units <= 256 ? 8 : units <= 1024 ? 2 : 1);
+    return launch_pdl(split ? latent_join_kernel<BF, true> : latent_join_kernel<BF, false>, grid, dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -864,8 +890,8 @@ extern "C" tq_status tq_latent_attend_tree(const tq_latent_pages_t* cache, const
     a.l.o = reinterpret_cast<uint16_t*>(o);
     a.l.err = err;
     a.ctas = (int)std::min<int64_t>(steps, std::min(sm_count(), kMaxSms));
-    a.pad = 4;
-    a.least = 4;
+    a.pad = 8;    // what beginning a unit costs (200 sequences of up to 1500 tokens: 65.5 us; 4: 69, 0: 78)
+    a.least = 4;  // (a segment of fewer steps costs more to join than it saves: three contexts of up to 300 tokens 15.4 us; 1: 16.4)
     a.fresh_box = n <= 8 ? 8 : n <= 16 ? 16 : kTok;  // (a divisor of a step)
     a.part = reinterpret_cast<float*>(ws);
     a.stat = reinterpret_cast<float2*>(a.part + 2ll * a.ctas * kRows * kLatent);
@@ -878,5 +904,6 @@ extern "C" tq_status tq_latent_attend_tree(const tq_latent_pages_t* cache, const
                     kLatentRow, std::min(cache->page, kTok)) ||
         !tensor_map(&drafts, bf, fresh ? fresh : q, (int64_t)B * n, kLatentRow, fresh ? fresh_stride : kLatentRow, a.fresh_box))
         return TQ_ERR_CUDA;
-    return bf ? launch<true>(a, rows, drafts, as_stream(stream)) : launch<false>(a, rows, drafts, as_stream(stream));
+    const int64_t own = (max_len + kTok - 1) / kTok;
+    return bf ? launch<true>(a, rows, drafts, own, as_stream(stream)) : launch<false>(a, rows, drafts, own, as_stream(stream));
 }
