@@ -630,7 +630,7 @@ tq_status tq_latent_append(const tq_latent_pages_t* cache, const void* c, int64_
  * sets TQ_DEVERR_TIMEOUT; o is then incomplete.
  * ws: 32-byte aligned device scratch of tq_latent_attend_tree_workspace_bytes(...) bytes; calls that may run at the
  * same time must not share it.  B, H <= 65535; TQ_ERR_UNSUPPORTED for more rows, or steps of 32 tokens over all tiles of 64 rows,
- * than 2^29. */
+ * than 2^27. */
 tq_status tq_latent_attend_tree(const tq_latent_pages_t* cache, const void* q, int64_t q_stride, int32_t B, int32_t n, int32_t H,
                                 const int32_t* table, int32_t table_stride, const int32_t* lens, int64_t max_len,
                                 const void* fresh, int64_t fresh_stride, const uint64_t* mask, const int32_t* n_tok, float scale,

@@ -1009,7 +1009,10 @@ def _distributions(t, name, B, n, V):
     sb, sn, sv = t.stride()
     if (V > 1 and sv != 1) or (B > 1 and n > 1 and sb != n * sn):
         raise ValueError(f"{name}'s rows must be contiguous and lie at one stride")
-    return max(V, sn if n > 1 else sb if B > 1 else V)
+    step = sn if n > 1 else sb if B > 1 else V
+    if step < V:
+        raise ValueError(f"{name}'s rows must not overlap (an expanded tensor has to be made contiguous)")
+    return step
 
 
 def verify_tree(p, tokens, parent, u, q=None, n_tok=None, err=None):

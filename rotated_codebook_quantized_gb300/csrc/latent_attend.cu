@@ -812,7 +812,7 @@ int sm_count() {
 // Steps of the whole batch at most; 0 where there are too many.
 int64_t most_steps(const tq_latent_pages_t* cache, int32_t B, int32_t n, int32_t H, int64_t max_len) {
     if (latent_check(cache) != TQ_OK || B <= 0 || n <= 0 || H <= 0 || H > 65535 || max_len < 0) return 0;
-    const int64_t most = 1ll << 29;
+    const int64_t most = 1ll << 27;  // (with the places of their beginnings below 2^31)
     const int64_t tiles = ((int64_t)n * H + kRows - 1) / kRows, steps = (std::min<int64_t>(max_len, 1ll << 40) + kTok - 1) / kTok + (n + kTok - 1) / kTok;
     if ((int64_t)n * H > most || steps > most || tiles > most / B || tiles * B > most / steps) return 0;
     return tiles * B * steps;

@@ -583,7 +583,9 @@ extern "C" tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, co
     if (q_stride < (int64_t)H * kHeadQuery || kv_head_stride < kHeadKey || kv_stride < (H - 1) * kv_head_stride + kHeadKey ||
         k_rope_stride < kLatentRope || q_stride % 8 || kv_stride % 8 || kv_head_stride % 8 || k_rope_stride % 8)
         return TQ_ERR_INVALID;
-    if (q_stride > 1ll << 32 || kv_stride > 1ll << 32 || k_rope_stride > 1ll << 32) return TQ_ERR_UNSUPPORTED;
+    // (a tensor copy's column is an int)
+    if (q_stride > 1ll << 32 || kv_stride > 1ll << 32 || k_rope_stride > 1ll << 32 || (H - 1) * kv_head_stride + kHeadKey > 0x7fffffffll)
+        return TQ_ERR_UNSUPPORTED;
     if (B == 0 || Tq == 0) return TQ_OK;
     if (!q || !o || !ws || ws_bytes < sizeof(uint32_t) || !q_starts || !kv_starts || (Tkv && (!k || !v || !k_rope))) return TQ_ERR_INVALID;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_rope, 16) || !aligned(o, 32) || !aligned(ws, 4) || !aligned(q_starts, 4) ||

@@ -484,6 +484,10 @@ def test_refusals(lib):
         lib.verify_tree(p, t, t, u.double())
     with pytest.raises(ValueError):
         lib.verify_tree(p.transpose(1, 2), t, t, u)
+    for x in (p[:, :1].expand(1, 2, 8), torch.zeros((1, 1, 8), device="cuda").expand(3, 1, 8)):  # rows that lie on one another
+        with pytest.raises(ValueError):
+            lib.verify_tree(x, _int([[0, 0]] if len(x) == 1 else [[0]] * 3), _int([[0, 0]] if len(x) == 1 else [[0]] * 3),
+                            torch.zeros(x.shape[:2], device="cuda"))
     with pytest.raises(lib.TQError):
         big = torch.zeros((1, 1025, 8), device="cuda")
         lib.verify_tree(big, _int(np.zeros((1, 1025))), _int(np.zeros((1, 1025))), torch.zeros((1, 1025), device="cuda"))

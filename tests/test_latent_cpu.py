@@ -96,7 +96,7 @@ def test_latent_attend_tree_refusals(tq):
                dict(most=641), dict(most=-1), dict(lens=None), dict(fs=568), dict(fs=580), dict(scale=float("nan")), dict(scale=float("inf")),
                dict(o=None), dict(ws=None), dict(nb=8), dict(q=F + 2), dict(fresh=F + 2), dict(o=F + 8), dict(ws=F + 8), dict(mask=F + 4)):
         assert call(**kw) == tq.TQ_ERR_INVALID, kw
-    for kw in (dict(B=2 ** 20, n=2 ** 10), dict(qs=2 ** 41), dict(fs=2 ** 41)):
+    for kw in (dict(B=2 ** 20, n=2 ** 10), dict(B=2 ** 16), dict(B=60000, n=400), dict(qs=2 ** 41), dict(fs=2 ** 41)):
         assert call(**kw) == tq.TQ_ERR_UNSUPPORTED, kw
     assert call(B=0) == tq.TQ_OK and call(n=0) == tq.TQ_OK
 
@@ -113,6 +113,6 @@ def test_latent_attend_prompt_refusals(tq):
                dict(kr=F + 8), dict(o=F + 8), dict(starts=F + 2), dict(ws=None),
                dict(ws=F + 2), dict(nb=3)):
         assert call(**kw) == tq.TQ_ERR_INVALID, kw
-    for kw in (dict(dt=tq.TQ_F32), dict(Tq=2 ** 30 + 1), dict(Tkv=2 ** 30 + 1), dict(kvs=2 ** 33)):
+    for kw in (dict(dt=tq.TQ_F32), dict(Tq=2 ** 30 + 1), dict(Tkv=2 ** 30 + 1), dict(kvs=2 ** 33), dict(kvs=2 ** 32, kvh=2 ** 28)):
         assert call(**kw) == tq.TQ_ERR_UNSUPPORTED, kw
     assert call(B=0) == tq.TQ_OK and call(Tq=0) == tq.TQ_OK
