@@ -648,15 +648,15 @@ size_t tq_latent_attend_tree_workspace_bytes(const tq_latent_pages_t* cache, int
  * [Tq][H][128] of dt, 32-byte aligned.  A query that sees no key gives zeros; queries from q_starts[B] on are left as they were.
  * What a query does not see never reaches it, whatever it holds; of one that sees a value that is not finite that element is
  * NaN or infinite, and others may be NaN.  Scores, softmax statistics and sums are fp32; softmax weights are rounded to dt.  starts
- * out of order or past Tq or Tkv set TQ_DEVERR_BAD_PAGE and their sequence is left out.  ws: 4-byte aligned device scratch of
- * tq_latent_attend_prompt_workspace_bytes() bytes (a counter, set to 0 by the call); calls that may run at the same time must not
- * share it.  TQ_ERR_UNSUPPORTED for more tiles of 256 rows over all heads than 2^30.  A bounded wait that ran out sets
+ * out of order or past Tq or Tkv set TQ_DEVERR_BAD_PAGE and their sequence is left out.  ws: 32-byte aligned device scratch of
+ * tq_latent_attend_prompt_workspace_bytes(...) bytes (a counter, set to 0 by the call, or partial results); calls that may run at
+ * the same time must not share it.  TQ_ERR_UNSUPPORTED for more tiles of 256 rows over all heads than 2^30.  A bounded wait that ran out sets
  * TQ_DEVERR_TIMEOUT; o is then incomplete. */
 tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
                                   int64_t kv_head_stride, const void* k_rope, int64_t k_rope_stride, tq_dtype dt, int32_t B,
                                   int32_t H, int64_t Tq, int64_t Tkv, const int32_t* q_starts, const int32_t* kv_starts,
                                   int32_t causal, float scale, void* o, void* ws, size_t ws_bytes, uint32_t* err, void* stream);
-size_t tq_latent_attend_prompt_workspace_bytes(void);
+size_t tq_latent_attend_prompt_workspace_bytes(int32_t B, int32_t H, int64_t Tq, int64_t Tkv);
 
 /* ------------------------------------------------------------------ fused decode layer */
 

@@ -141,7 +141,7 @@ _SIGS = {
     "tq_latent_attend_tree_workspace_bytes": (_sz, [_P(tq_latent_pages_t), _i32, _i32, _i32, _i64]),
     "tq_latent_attend_prompt": (_i32, [_c_p, _i64, _c_p, _c_p, _i64, _i64, _c_p, _i64, _i32, _i32, _i32, _i64, _i64, _c_p, _c_p,
                                        _i32, ctypes.c_float, _c_p, _c_p, _sz, _c_p, _c_p]),
-    "tq_latent_attend_prompt_workspace_bytes": (_sz, []),
+    "tq_latent_attend_prompt_workspace_bytes": (_sz, [_i32, _i32, _i64, _i64]),
     "tq_check_error": (_i32, [_c_p, _P(_u32), _c_p]),
     "tq_set_wait_budget": (_i32, [_i64]),
     "tq_rotation_dense": (_i32, [ctypes.c_uint64, _i32, _P(ctypes.c_double)]),
@@ -1177,7 +1177,7 @@ def latent_attend_prompt(q, k, v, k_rope, q_starts, kv_starts, scale: float, cau
     hs = k.stride(1) if H > 1 else 128
     ks = k.stride(0) if Tkv > 1 else max(k.stride(0), (H - 1) * hs + 128)
     o = torch.empty((Tq, H, 128), dtype=q.dtype, device=q.device)
-    nb = 4  # (tq_latent_attend_prompt_workspace_bytes: a counter)
+    nb = int(load().tq_latent_attend_prompt_workspace_bytes(B, H, Tq, Tkv))
     if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
         raise ValueError("ws must be contiguous, on q's device")
     if ws is None or ws.numel() * ws.element_size() < nb:

@@ -41,9 +41,11 @@ struct PromptArgs {
     const int32_t* kv_starts;
     uint16_t* o;
     uint32_t* err;
-    int B, H, heads;  // heads: of a group
+    int B, H, heads, ctas;  // heads: of a group
     bool causal;
     uint32_t* taken;  // jobs taken beyond each CTA's first; NULL: there are no others
+    float* part;      // [CTAs][256 rows][128], where jobs may be cut; NULL: they are not
+    float2* stat;     // [CTAs][256]: level and sum
     float scale2;     // scale * log2(e)
     long long wait_cycles;
 };
@@ -54,6 +56,7 @@ struct Job {
     int k0, keys;  // of the sequence
     int at;        // key of the first row's own place, less k0; the rows' are at + row (causal)
     int head;
+    bool cut;      // one of several parts: the result is a partial one
 };
 struct Span {
     int q0, q1, k0, k1, tiles;
@@ -75,11 +78,15 @@ TQ_DEVFN int tiles_above(const PromptArgs& a, const Span& s, int steps) {
     // a tile whose last row is the e-th sees keys - queries + e of them
     return s.tiles - max(steps * kTok + (s.q1 - s.q0) - (s.k1 - s.k0), 0) / kTile;
 }
+// Few jobs over many keys (a chunk of a prompt late in a long one) are cut into parts along the keys, one to a CTA, and joined: 16
+// tokens after 8000, 8 heads 29 us (whole: 105), 700 after 1300, 4 heads 27 (47), 256 after 744, 32 heads 26 (27).
+constexpr int kLeast = 4, kParts = 32;  // fewest steps of a part, most parts
 // Jobs go in groups of `heads` heads, whose keys and values the L2 cache holds; in a group those with the most steps first.  A CTA
 // takes the next one when its copies of the last are under way (shared out beforehand, seven chunks of prompts left a quarter of the
 // SMs' time idle).
 struct Jobs {
     int tiles, most;  // of a head; steps of the longest
+    int parts, per;   // into how many parts jobs are cut, of how many steps at most
 };
 TQ_DEVFN Jobs count_jobs(const PromptArgs& a, bool report) {  // (one warp)
     int tiles = 0, most = 0;
@@ -91,13 +98,19 @@ TQ_DEVFN Jobs count_jobs(const PromptArgs& a, bool report) {  // (one warp)
         if (s.tiles) most = max(most, (s.k1 - s.k0 + kTok - 1) / kTok);
     }
     if (report && bad && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
-    return {(int)__reduce_add_sync(kFull, tiles), (int)__reduce_max_sync(kFull, most)};
+    Jobs j{(int)__reduce_add_sync(kFull, tiles), (int)__reduce_max_sync(kFull, most), 1, 0};
+    const int64_t all = (int64_t)j.tiles * a.H;
+    if (a.part && all > 0) j.parts = (int)max(min((int64_t)(a.ctas / all), (int64_t)min(j.most / kLeast, kParts)), (int64_t)1);
+    j.per = (j.most + j.parts - 1) / j.parts;
+    return j;
 }
 TQ_DEVFN Job find_job(const PromptArgs& a, const Jobs& jobs, int64_t at) {  // (one warp)
     const int lane = threadIdx.x & 31;
     Job j{};
     j.rows = -1;
-    if (at >= (int64_t)jobs.tiles * a.H) return j;
+    if (at >= (int64_t)jobs.tiles * a.H * jobs.parts) return j;
+    const int part = (int)(at % jobs.parts);
+    at /= jobs.parts;
     const int group = (int)(at / ((int64_t)jobs.tiles * a.heads)), in = min(a.heads, a.H - group * a.heads);
     const int left = (int)(at - (int64_t)group * jobs.tiles * a.heads);
     j.head = group * a.heads + left % in;
@@ -137,6 +150,13 @@ TQ_DEVFN Job find_job(const PromptArgs& a, const Jobs& jobs, int64_t at) {  // (
             break;
         }
         rank -= __shfl_sync(kFull, upto, 31);
+    }
+    if (jobs.parts > 1) {  // a part is a job over some of the keys: the rows stand as far before or behind them as they do
+        const int from = part * jobs.per * kTok;
+        j.cut = true;
+        j.k0 += from;
+        j.keys = min(max(j.keys - from, 0), jobs.per * kTok);
+        j.at -= from;
     }
     return j;
 }
@@ -522,6 +542,27 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                 if (!ok) break;
                 fence_after();
             }
+            if (j.cut) {  // 16-byte pieces [8 warps][4 x 32 elements][8][32 lanes]: each store is one run of 512 bytes
+                a.stat[(int64_t)blockIdx.x * kTile + row] = make_float2(level(m, bias), sum);
+                float* const part_to = a.part + ((int64_t)blockIdx.x * kTile * (kHeadValue / 4) + warp * 1024 + lane) * 4;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[32];
+                    if (steps) {
+                        ld32(col_o + 32 * q, o);
+                        wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4*>(part_to + (q * 8 + e) * 128) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+                fence_before();
+                g = g1;
+                continue;
+            }
             const float over = sum == 0.f ? 0.f : 1.f / sum;  // (a NaN sum stays one)
             uint16_t* out = a.o + ((int64_t)(j.q0 + row) * a.H + j.head) * kHeadValue;
 #pragma unroll 1
@@ -557,6 +598,67 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     }
 }
 
+// The parts of jobs, joined in their order: a warp to 8 elements of 32 rows.
+template <bool BF>
+__global__ void __launch_bounds__(256) latent_prompt_join_kernel(const __grid_constant__ PromptArgs a) {
+    __shared__ Jobs s_jobs;
+    __shared__ Job s_job;
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == 0) {
+        Jobs jobs = count_jobs(a, false);
+        const int parts = jobs.parts, per = jobs.per;
+        jobs.parts = 1;  // (the whole job, not one of its parts)
+        const Job j = find_job(a, jobs, blockIdx.x);
+        jobs.parts = parts, jobs.per = per;
+        if (lane == 0) s_jobs = jobs, s_job = j;
+    }
+    __syncthreads();
+    const Jobs jobs = s_jobs;
+    const Job j = s_job;
+    if (jobs.parts <= 1 || j.rows < 0) return;
+    constexpr int kAhead = 4;
+    const int piece = blockIdx.y * 8 + warp, row = (piece >> 4) * 32 + lane, e = (piece & 15) * 2;  // pieces of 4 elements e, e + 1
+    if (row >= j.rows) return;
+    // parts that hold keys that some row of the job sees: the others' levels are -infinity
+    const int64_t slot0 = (int64_t)blockIdx.x * jobs.parts;
+    float o[8] = {}, top = -INFINITY, total = 0.f;
+    for (int c = 0; c < jobs.parts; c += kAhead) {
+        float2 stat[kAhead];
+        float4 z[kAhead][2];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t slot = slot0 + min(c + k, jobs.parts - 1);
+            stat[k] = a.stat[slot * kTile + row];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                z[k][h] = *reinterpret_cast<const float4*>(
+                    a.part + (slot * kTile * (kHeadValue / 4) + (row >> 5) * 1024 + (((e + h) >> 3) * 8 + ((e + h) & 7)) * 32 + lane) * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (c + k >= jobs.parts) break;
+            // both to the higher level: weight 1 for its own (also where neither saw anything)
+            const float n = fmaxf(top, stat[k].x), w0 = top == n ? 1.f : exp2_fast(top - n),
+                        w1 = stat[k].x == n ? 1.f : exp2_fast(stat[k].x - n);
+            top = n;
+            total = total * w0 + stat[k].y * w1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                o[4 * h] = fmaf(o[4 * h], w0, z[k][h].x * w1);
+                o[4 * h + 1] = fmaf(o[4 * h + 1], w0, z[k][h].y * w1);
+                o[4 * h + 2] = fmaf(o[4 * h + 2], w0, z[k][h].z * w1);
+                o[4 * h + 3] = fmaf(o[4 * h + 3], w0, z[k][h].w * w1);
+            }
+        }
+    }
+    const float over = total == 0.f ? 0.f : 1.f / total;  // (a NaN sum stays one)
+    *reinterpret_cast<uint4*>(a.o + ((int64_t)(j.q0 + row) * a.H + j.head) * kHeadValue + e * 4) =
+        make_uint4(pack16<BF>(o[0] * over, o[1] * over), pack16<BF>(o[2] * over, o[3] * over), pack16<BF>(o[4] * over, o[5] * over),
+                   pack16<BF>(o[6] * over, o[7] * over));
+}
+
 int sm_count() {
     static const int n = [] {
         int dev = 0, v = 0;
@@ -570,7 +672,17 @@ int sm_count() {
 
 using namespace tq;
 
-extern "C" size_t tq_latent_attend_prompt_workspace_bytes(void) { return sizeof(uint32_t); }
+namespace {
+constexpr int kMaxSms = 256;
+// Tiles over all heads, at most; and whether they may be cut: half the SMs would be idle, and a sequence can have 8 steps.
+int64_t most_jobs(int32_t B, int32_t H, int64_t Tq) { return std::min((Tq + kTile - 1) / kTile + B, Tq) * H; }
+bool may_cut(int64_t jobs, int64_t Tkv, int sms) { return jobs * 2 <= sms && Tkv >= 2 * kLeast * kTok; }
+}  // namespace
+
+extern "C" size_t tq_latent_attend_prompt_workspace_bytes(int32_t B, int32_t H, int64_t Tq, int64_t Tkv) {
+    if (B <= 0 || H <= 0 || Tq <= 0 || Tkv < 0 || Tq > 1ll << 30) return sizeof(uint32_t);
+    return may_cut(most_jobs(B, H, Tq), Tkv, kMaxSms) ? (size_t)kMaxSms * kTile * (kHeadValue * sizeof(float) + sizeof(float2)) : sizeof(uint32_t);
+}
 
 extern "C" tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
                                              int64_t kv_head_stride, const void* k_rope, int64_t k_rope_stride, tq_dtype dt,
@@ -587,8 +699,8 @@ extern "C" tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, co
     if (q_stride > 1ll << 32 || kv_stride > 1ll << 32 || k_rope_stride > 1ll << 32 || (H - 1) * kv_head_stride + kHeadKey > 0x7fffffffll)
         return TQ_ERR_UNSUPPORTED;
     if (B == 0 || Tq == 0) return TQ_OK;
-    if (!q || !o || !ws || ws_bytes < sizeof(uint32_t) || !q_starts || !kv_starts || (Tkv && (!k || !v || !k_rope))) return TQ_ERR_INVALID;
-    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_rope, 16) || !aligned(o, 32) || !aligned(ws, 4) || !aligned(q_starts, 4) ||
+    if (!q || !o || !ws || ws_bytes < tq_latent_attend_prompt_workspace_bytes(B, H, Tq, Tkv) || !q_starts || !kv_starts || (Tkv && (!k || !v || !k_rope))) return TQ_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_rope, 16) || !aligned(o, 32) || !aligned(ws, 32) || !aligned(q_starts, 4) ||
         !aligned(kv_starts, 4))
         return TQ_ERR_INVALID;
     PromptArgs a{};
@@ -615,15 +727,24 @@ extern "C" tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, co
     // heads of a group: as many as the L2 cache (129 MB) holds the keys and values of twice over (8192 tokens: 915 us with 16 to 96 MB, 958
     // ungrouped; seven chunks 99 us with 64 MB, 108 with 16)
     a.heads = (int)std::min<int64_t>(H, std::max<int64_t>(1, (64ll << 20) / (keys * (kHeadKey + kHeadValue) * 2)));
-    const int64_t jobs = std::min((Tq + kTile - 1) / kTile + B, Tq) * H;  // at most
+    const int64_t jobs = most_jobs(B, H, Tq);
     if (jobs > 1ll << 30) return TQ_ERR_UNSUPPORTED;
     void (*kernel)(PromptArgs, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap) =
         bf ? latent_prompt_kernel<true> : latent_prompt_kernel<false>;
     if (ensure_smem((const void*)kernel, kSmem) != cudaSuccess) return TQ_ERR_CUDA;
-    if (jobs > sm_count()) {
+    if (jobs > std::min(sm_count(), kMaxSms)) {
         a.taken = reinterpret_cast<uint32_t*>(ws);
         if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), as_stream(stream)) != cudaSuccess) return TQ_ERR_CUDA;
     }
-    return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(jobs, sm_count())), dim3(32 * kWarps), kSmem, as_stream(stream), a, mq, mk, mv,
-                      mr);
+    const int sms = std::min(sm_count(), kMaxSms);
+    const bool cut = may_cut(jobs, Tkv, sms);
+    a.ctas = (int)(cut ? sms : std::min<int64_t>(jobs, sms));
+    if (cut) {
+        a.part = reinterpret_cast<float*>(ws);
+        a.stat = reinterpret_cast<float2*>(a.part + (int64_t)sms * kTile * kHeadValue);
+    }
+    const tq_status s = launch_pdl(kernel, dim3((unsigned)a.ctas), dim3(32 * kWarps), kSmem, as_stream(stream), a, mq, mk, mv, mr);
+    if (s != TQ_OK || !cut) return s;
+    return launch_pdl(bf ? latent_prompt_join_kernel<true> : latent_prompt_join_kernel<false>, dim3((unsigned)jobs, 16), dim3(256), 0,
+                      as_stream(stream), a);
 }

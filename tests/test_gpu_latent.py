@@ -514,6 +514,25 @@ def test_expired_waits_are_reported(lib):
     assert torch.equal(s.run(err=err), want) and torch.equal(prompt(err), want2) and lib.check_error(err) == 0
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("ql,kl,H", [([1], [5000], 2), ([16], [9000], 1), ([300], [4200], 3), ([5, 0, 260], [3000, 2000, 1030], 4),
+                                     ([700], [1100], 1), ([2, 3, 4], [1024, 0, 7], 5), ([3000], [2500], 1)])
+def test_expanded_few_rows_over_many_keys(lib, dtype, causal, ql, kl, H):
+    """Jobs cut along the keys and joined: parts that a row sees all, part and nothing of, rows that see nothing, short sequences beside."""
+    q, kv, kr, qs, ks = _prompts(ql, kl, H, dtype, 16, sum(ql), H)
+    k, v = kv[..., :128], kv[..., 128:]
+    ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device="cuda")
+    o = lib.latent_attend_prompt(q, k, v, kr, _int(qs), _int(ks), SCALE, causal=causal, ws=ws)
+    _check_prompts(o, q, k, v, kr, qs, ks, causal=causal)
+    assert torch.equal(o, lib.latent_attend_prompt(q, k, v, kr, _int(qs), _int(ks), SCALE, causal=causal))
+    # what the rows do not see: past the sequence's keys, and the last key of all (its last row alone)
+    if causal and len(ql) == 1 and 1 < ql[0] < kl[0]:
+        kv[-1] = float("nan")
+        got = lib.latent_attend_prompt(q, k, v, kr, _int(qs), _int(ks), SCALE)
+        assert torch.equal(got[:-1], o[:-1]) and bool(got[-1].isnan().all())
+
+
 def test_expanded_more_jobs_than_sms_in_a_graph(lib):
     """Jobs that CTAs take as they come free, the counter in a workspace that holds anything; replayed, and another call between."""
     q, kv, kr, qs, ks = _prompts([700, 300, 513, 40], [900, 300, 600, 1000], 40, "bfloat16", 15)

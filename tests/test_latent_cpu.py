@@ -104,7 +104,7 @@ def test_latent_attend_tree_refusals(tq):
 def test_latent_attend_prompt_refusals(tq):
     lib = tq.load()
 
-    def call(q=F, qs=16 * 192, k=F, v=F, kvs=16 * 256, kvh=256, kr=F, krs=64, dt=tq.TQ_BF16, B=2, H=16, Tq=9, Tkv=9, starts=F, scale=0.1, o=F, ws=F, nb=4):
+    def call(q=F, qs=16 * 192, k=F, v=F, kvs=16 * 256, kvh=256, kr=F, krs=64, dt=tq.TQ_BF16, B=2, H=16, Tq=9, Tkv=9, starts=F, scale=0.1, o=F, ws=F, nb=1 << 30):
         return lib.tq_latent_attend_prompt(q, qs, k, v, kvs, kvh, kr, krs, dt, B, H, Tq, Tkv, starts, F, 1, scale, o, ws, nb, None, None)
 
     for kw in (dict(q=None), dict(qs=16 * 192 - 8), dict(qs=16 * 192 + 4), dict(k=None), dict(v=None), dict(kr=None), dict(kvs=15 * 256),
@@ -115,4 +115,6 @@ def test_latent_attend_prompt_refusals(tq):
         assert call(**kw) == tq.TQ_ERR_INVALID, kw
     for kw in (dict(dt=tq.TQ_F32), dict(Tq=2 ** 30 + 1), dict(Tkv=2 ** 30 + 1), dict(kvs=2 ** 33), dict(kvs=2 ** 32, kvh=2 ** 28)):
         assert call(**kw) == tq.TQ_ERR_UNSUPPORTED, kw
+    need = lib.tq_latent_attend_prompt_workspace_bytes(2, 16, 9, 9000)  # (few tiles, many keys: partial results)
+    assert need > 1 << 20 and call(Tkv=9000, nb=need - 1) == tq.TQ_ERR_INVALID
     assert call(B=0) == tq.TQ_OK and call(Tq=0) == tq.TQ_OK
