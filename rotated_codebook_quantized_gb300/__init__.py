@@ -1089,6 +1089,16 @@ class LatentCache:
 
 def _rows_at(t, name, width):
     """(rows, row stride) of t [..., width] whose rows lie at one stride."""
+    if t.is_cuda:  # the usual cases, without a view (which takes as long as the call itself)
+        shape, strides = t.shape, t.stride()
+        if len(shape) == 2 and shape[1] == width and strides[1] == 1:
+            return shape[0], strides[0] if shape[0] > 1 else width
+        if len(shape) == 3 and shape[2] == width and strides[2] == 1:
+            (a, b, _), (sa, sb, _) = shape, strides
+            if b == 1:
+                return a, sa if a > 1 else width
+            if a == 1 or (a > 1 and b > 1 and sa == b * sb):
+                return a * b, sb
     tokens, _, stride = _heads(t.unsqueeze(-2), name, width)
     return tokens, stride
 
