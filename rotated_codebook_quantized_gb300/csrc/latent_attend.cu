@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             const uint64_t dq = desc(base + kQ, 16), dk = desc(base + kRing, 16);
             for (; ok && some; some = walk.next(l, x), ++seg) {
                 ok = mbar_wait(&c.q_ready, seg & 1, abort_flag, a.wait_cycles);
+                if (!ok) break;  // (else it would issue on queries that are still being copied)
                 for (int s = x.s0; s < x.s1; ++s, ++g) {
                     const uint32_t place = g % kPlaces, phase = (g / kPlaces) & 1;
                     ok = mbar_wait(c.full + place, phase, abort_flag, a.wait_cycles);
