@@ -494,6 +494,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             const uint32_t ge = g + (x.s1 - x.s0);
             const uint32_t y0 = x.tile * kRows;
             const int rows = min(kRows, x.s.live * l.H - (int)y0);
+            if (x.s0 == 0 && tid == 0)  // (before any wait: the join takes these for indices)
+                a.units[(int64_t)x.b * ((l.n * l.H + kRows - 1) / kRows) + x.tile] = make_int2(blockIdx.x, x.last);
             // ---- the tile's queries (the last scores of the stretch before have been read, so its queries are free)
             // Six blocks go to TMEM, whose lanes 16 .. 31 of a warp repeat its 16 rows (M = 64 wants A in both halves), by way of
             // shared memory: five where the others, the weights and a spare tile lie, then one beside the others.
@@ -674,8 +676,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             const float total = lane & 8 ? s_hi : s_lo, lev = lane & 8 ? l_hi : l_lo;
             const bool mine = row < rows;
             const int64_t slot = 2ll * blockIdx.x + (x.s0 == 0);
-            if (x.s0 == 0 && tid == 0)
-                a.units[(int64_t)x.b * ((l.n * l.H + kRows - 1) / kRows) + x.tile] = make_int2(blockIdx.x, x.last);
             if (x.s0 == 0 && x.s1 == x.s.steps) {
                 const float over = total == 0.f ? 0.f : 1.f / total;  // (a NaN sum stays one)
                 uint16_t* out = l.o + ((int64_t)x.b * l.n * l.H + y0 + min(row, rows - 1)) * kLatent + (lane >> 4) * 256;
@@ -748,6 +748,11 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     if (live == 0) return;
     const int2 unit = a.units[(int64_t)b * gridDim.x + tile];
     const int c0 = unit.x, c1 = unit.y;
+    if (c0 < 0 || c1 < c0 || c1 >= a.ctas) {  // not written: a CTA gave up in a stretch before this unit, and has reported it
+        for (int i = blockIdx.z * 256 + tid; i < live * (kLatent / 8); i += gridDim.z * 256)
+            *reinterpret_cast<uint4*>(out + (int64_t)i * 8) = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
     if (c0 == c1) return;  // one CTA has written its rows
     auto slot_of = [&](int c) { return 2ll * c + (c == c0); };
     for (int piece = SPLIT ? blockIdx.z : blockIdx.z * kJoin + warp; piece < 128; piece += SPLIT ? 128 : gridDim.z * kJoin) {

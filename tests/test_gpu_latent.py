@@ -514,6 +514,25 @@ def test_expired_waits_are_reported(lib):
     assert torch.equal(s.run(err=err), want) and torch.equal(prompt(err), want2) and lib.check_error(err) == 0
 
 
+@pytest.mark.parametrize("B,n,H,context", [(3, 2, 64, 700), (1, 1, 64, 6000), (200, 1, 64, 300)])
+@pytest.mark.parametrize("word", [-1, 0, 0x01010101, 0x7fffffff, 151])
+def test_expired_waits_over_scratch_that_holds_anything(lib, word, B, n, H, context):
+    """A wait budget of 0 over scratch whose words name no CTAs, or others': a status, and the next call as before."""
+    s = Scene(lib, B, n, H, context, 64, "bfloat16")
+    ws = torch.full((1 << 26,), word, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lib.set_wait_budget(0)
+    try:
+        s.run(err=err, ws=ws)
+        assert lib.check_error(err) & 2
+    finally:
+        lib.set_wait_budget(-1)
+    ws.fill_(word)
+    o = s.run(err=err, ws=ws)
+    s.check(o)
+    assert lib.check_error(err) == 0
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("ql,kl,H", [([1], [5000], 2), ([16], [9000], 1), ([300], [4200], 3), ([5, 0, 260], [3000, 2000, 1030], 4),
