@@ -94,9 +94,17 @@ TQ_DEVFN uint32_t cluster_size() {
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-TQ_DEVFN void cluster_sync() {
+TQ_DEVFN void cluster_arrive() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+TQ_DEVFN void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+TQ_DEVFN void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
 }
 TQ_DEVFN void store_remote(u64* local, uint32_t rank, u64 v) {
     uint32_t at;
@@ -138,6 +146,7 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(const __grid_cons
     const int b = blockIdx.x / size;
     const int64_t row0 = (int64_t)b * a.n;
     pdl_trigger();
+    cluster_arrive();
     pdl_wait();
     const int used = a.n_tok ? min(max(a.n_tok[b], 0), a.n) : a.n;
     uint32_t wrong = 0;
@@ -155,6 +164,7 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(const __grid_cons
     if (wrong && a.err && rank == 0) atomicOr(a.err, wrong);
     if (rank == 0 && tid == 0) a.next[b] = -1;  // until the search finds one, behind a pass's barrier of the cluster
     __syncthreads();
+    cluster_wait();  // every CTA of the cluster has started: before that none may store into another's shared memory
 
     const int first = (int)rank * a.runs;  // of this CTA's runs
     int turn = 0, node = 0, length = 1, k = 0;  // k: rejections of the node

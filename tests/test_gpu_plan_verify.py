@@ -464,6 +464,29 @@ def test_verify_in_a_graph_and_on_another_stream(lib):
     assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
+@pytest.mark.parametrize("B,V", [(1, 131072), (3, 131072), (40, 50001)])
+def test_verify_beside_other_work(lib, B, V):
+    """Clusters whose CTAs find the SMs taken by another stream's kernels and start when these let them: the same results."""
+    gen = torch.Generator(device="cuda").manual_seed(V + B)
+    n = 4
+    p, q = (torch.softmax(2 * torch.randn((B, n, V), generator=gen, device="cuda"), -1) for _ in range(2))
+    tokens = torch.multinomial(q.flatten(0, 1)[::n].repeat_interleave(n, 0), 1, generator=gen).view(B, n).int()
+    parent, u = _int([[-1, 0, 0, 0]] * B), torch.rand((B, n), generator=gen, device="cuda")
+    want = lib.verify_tree(p, tokens, parent, u, q=q)
+    x = torch.randn((4096, 4096), generator=gen, device="cuda").bfloat16()
+    other, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(other):
+            for _ in range(4):
+                y = x @ x
+        with torch.cuda.stream(mine):
+            got = [lib.verify_tree(p, tokens, parent, u, q=q) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+    del y
+
+
 def test_refusals(lib):
     pool = lib.PagePool(4, 16, 2, 4)
     a = _int([0, 0])

@@ -1,7 +1,9 @@
-"""Bounded waits in the CUDA sources: a wait that ran out ends its role.
+"""Waits in the CUDA sources.
 
-A role keeps the outcome of its waits in `ok`.  Where the next wait overwrites it before anything has looked at it, a role whose
+A bounded wait that ran out ends its role.  A role keeps the outcome of its waits in `ok`.  Where the next wait overwrites it before anything has looked at it, a role whose
 first wait ran out goes on as if it had not (a completed phase answers yes whatever has happened elsewhere).
+
+A CTA stores into the shared memory of its cluster's others only when all of them are known to have started.
 """
 import os
 import re
@@ -36,3 +38,17 @@ def test_a_lost_outcome_is_found():
 @pytest.mark.parametrize("name", sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))))
 def test_the_outcome_of_a_wait_is_looked_at(name):
     assert _lost(open(os.path.join(CSRC, name)).read()) == []
+
+
+def test_a_cluster_has_started_before_its_shared_memory_is_written():
+    """In the verification kernel an arrival and a wait that every thread passes, on any road through it, come before the first store."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "verify.cu")).read())
+    body = text[text.index("verify_tree_kernel(const __grid_constant__"):]
+    body = body[body.index("{"):body.index("store_remote(")]
+    depth, unconditional = 0, []
+    for part in re.finditer(r"[{}]|\bcluster_(?:arrive|wait|sync)\(\);|\breturn\b", body):
+        if part[0] in "{}":
+            depth += 1 if part[0] == "{" else -1
+        elif depth == 1:
+            unconditional.append(part[0])
+    assert unconditional in (["cluster_arrive();", "cluster_wait();"], ["cluster_sync();"])
