@@ -10,6 +10,7 @@
 #include <type_traits>
 #include <unordered_map>
 
+#include "per_device.h"
 #include "tq.h"
 
 #define TQ_DEVFN __device__ __forceinline__
@@ -62,20 +63,6 @@ inline tq_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
-}
-
-// Raise a kernel's dynamic shared-memory limit once per process (not on every
-// launch, so launches can be captured into CUDA graphs without extra API calls).
-inline cudaError_t ensure_smem(const void* kernel, size_t bytes) {
-    static std::mutex mu;
-    static std::unordered_map<const void*, size_t> done;
-    if (bytes <= 48 * 1024) return cudaSuccess;
-    std::lock_guard<std::mutex> lock(mu);
-    size_t& cur = done[kernel];
-    if (cur >= bytes) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) cur = bytes;
-    return e;
 }
 
 inline bool is_pow2(long long v) { return v > 0 && (v & (v - 1)) == 0; }

@@ -126,7 +126,7 @@ extern "C" tq_status tq_latent_append(const tq_latent_pages_t* cache, const void
     a.err = err;
     a.lpage = ilog2(cache->page);
     if (rope) a.rope = *rope;
-    const unsigned grid = (unsigned)std::min<int64_t>((T + 7) / 8, 152 * 8);
+    const unsigned grid = (unsigned)std::min<int64_t>((T + 7) / 8, device_sms() * 8);
     const bool bf = cache->dt == TQ_BF16;
     void (*kernel)(AppendArgs) =
         dt == TQ_F32 ? (bf ? latent_append_kernel<TQ_F32, true> : latent_append_kernel<TQ_F32, false>)

@@ -807,14 +807,6 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     }
 }
 
-int sm_count() {
-    static const int n = [] {
-        int dev = 0, v = 0;
-        return cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? v : 152;
-    }();
-    return n;
-}
-
 // Steps of the whole batch at most; 0 where there are too many.
 int64_t most_steps(const tq_latent_pages_t* cache, int32_t B, int32_t n, int32_t H, int64_t max_len) {
     if (latent_check(cache) != TQ_OK || B <= 0 || n <= 0 || H <= 0 || H > 65535 || max_len < 0) return 0;
@@ -895,7 +887,7 @@ extern "C" tq_status tq_latent_attend_tree(const tq_latent_pages_t* cache, const
     a.l.scale2 = score_factor(scale);
     a.l.o = reinterpret_cast<uint16_t*>(o);
     a.l.err = err;
-    a.ctas = (int)std::min<int64_t>(steps, std::min(sm_count(), kMaxSms));
+    a.ctas = (int)std::min<int64_t>(steps, std::min(device_sms(), kMaxSms));
     a.pad = 8;    // what beginning a unit costs (200 sequences of up to 1500 tokens: 65.5 us; 4: 69, 0: 78)
     a.least = 4;  // (a segment of fewer steps costs more to join than it saves: three contexts of up to 300 tokens 15.4 us; 1: 16.4)
     a.fresh_box = n <= 8 ? 8 : n <= 16 ? 16 : kTok;  // (a divisor of a step)

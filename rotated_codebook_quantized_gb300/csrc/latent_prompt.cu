@@ -659,14 +659,6 @@ __global__ void __launch_bounds__(256) latent_prompt_join_kernel(const __grid_co
                    pack16<BF>(o[6] * over, o[7] * over));
 }
 
-int sm_count() {
-    static const int n = [] {
-        int dev = 0, v = 0;
-        return cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? v : 152;
-    }();
-    return n;
-}
-
 }  // namespace
 }  // namespace tq
 
@@ -732,11 +724,11 @@ extern "C" tq_status tq_latent_attend_prompt(const void* q, int64_t q_stride, co
     void (*kernel)(PromptArgs, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap) =
         bf ? latent_prompt_kernel<true> : latent_prompt_kernel<false>;
     if (ensure_smem((const void*)kernel, kSmem) != cudaSuccess) return TQ_ERR_CUDA;
-    if (jobs > std::min(sm_count(), kMaxSms)) {
+    if (jobs > std::min(device_sms(), kMaxSms)) {
         a.taken = reinterpret_cast<uint32_t*>(ws);
         if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), as_stream(stream)) != cudaSuccess) return TQ_ERR_CUDA;
     }
-    const int sms = std::min(sm_count(), kMaxSms);
+    const int sms = std::min(device_sms(), kMaxSms);
     const bool cut = may_cut(jobs, Tkv, sms);
     a.ctas = (int)(cut ? sms : std::min<int64_t>(jobs, sms));
     if (cut) {

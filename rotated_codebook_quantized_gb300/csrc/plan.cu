@@ -292,6 +292,6 @@ extern "C" tq_status tq_kv_plan(const tq_page_pool_t* pool, const int32_t* lens,
     const tq_status s = launch_pdl(kv_plan_kernel, dim3(1), dim3(threads), 0, as_stream(stream), a);
     if (s != TQ_OK || rows == 0) return s;
     const int64_t warps = n ? pool->batch : (tokens + 31) / 32;
-    return launch_pdl(kv_plan_slots_kernel, dim3((unsigned)std::min<int64_t>((warps + 7) / 8, 152 * 8)), dim3(256), 0,
+    return launch_pdl(kv_plan_slots_kernel, dim3((unsigned)std::min<int64_t>((warps + 7) / 8, device_sms() * 8)), dim3(256), 0,
                       as_stream(stream), a);
 }

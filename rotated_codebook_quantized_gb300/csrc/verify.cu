@@ -354,18 +354,6 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(const __grid_cons
     cluster_sync();  // no CTA ends while another may still write its totals here
 }
 
-// Clusters of more than 8 CTAs, allowed once a kernel.
-cudaError_t allow_wide(const void* kernel) {
-    static std::mutex mu;
-    static std::unordered_map<const void*, bool> done;
-    std::lock_guard<std::mutex> lock(mu);
-    bool& yes = done[kernel];
-    if (yes) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    yes = e == cudaSuccess;
-    return e;
-}
-
 template <int DT>
 void (*kernel_of(bool q, bool kept))(VerifyArgs) {
     if (q) return kept ? verify_tree_kernel<DT, true, true> : verify_tree_kernel<DT, true, false>;
@@ -399,17 +387,22 @@ extern "C" tq_status tq_verify_tree(const void* p, int64_t p_stride, const void*
     // every warp (48 trees over 50001 tokens: 35 us with eight to a tree, 41 with four); sixteen where the trees are few (one tree,
     // 131072 tokens, five rejections: 23 us for 34; eight trees gain nothing).
     int size_c = 1;
-    while (size_c < kCluster && B * size_c * 2 <= (size_c < 8 ? 4 * 152 : 64) && runs >= 32 * size_c) size_c *= 2;
-    a.runs = (runs + size_c - 1) / size_c;
-    const size_t nodes = (size_t)n * (sizeof(u64) + 3 * sizeof(float) + 4 * sizeof(int)), sums = (size_t)a.runs * sizeof(u64);
+    while (size_c < kCluster && B * size_c * 2 <= (size_c < 8 ? 4 * device_sms() : 64) && runs >= 32 * size_c) size_c *= 2;
+    const size_t nodes = (size_t)n * (sizeof(u64) + 3 * sizeof(float) + 4 * sizeof(int));
     // The residual stays in shared memory where it fits (five rejections in each of 48 trees over 131072 tokens: 130 us in parts that
     // fit, 367 us in parts twice as large, computed anew in each pass).
-    const bool kept = nodes + sums * (1 + kRun) <= 200 * 1024;
-    const size_t smem = nodes + sums * (1 + (kept ? kRun : 0));
-    void (*kernel)(VerifyArgs) = dt == TQ_F32 ? kernel_of<TQ_F32>(q, kept) : (dt == TQ_BF16 ? kernel_of<TQ_BF16>(q, kept) : kernel_of<TQ_F16>(q, kept));
     constexpr size_t kStatic = 1024;  // above the kernel's own arrays: the limit that is raised holds for both together
-    if (ensure_smem((const void*)kernel, smem + kStatic) != cudaSuccess) return TQ_ERR_CUDA;
-    if (size_c > 8 && allow_wide((const void*)kernel) != cudaSuccess) return TQ_ERR_CUDA;
+    size_t smem = 0;
+    void (*kernel)(VerifyArgs) = nullptr;
+    for (;; size_c = 8) {  // (once more where no cluster of 16 has a place)
+        a.runs = (runs + size_c - 1) / size_c;
+        const size_t sums = (size_t)a.runs * sizeof(u64);
+        const bool kept = nodes + sums * (1 + kRun) <= 200 * 1024;
+        smem = nodes + sums * (1 + (kept ? kRun : 0));
+        kernel = dt == TQ_F32 ? kernel_of<TQ_F32>(q, kept) : (dt == TQ_BF16 ? kernel_of<TQ_BF16>(q, kept) : kernel_of<TQ_F16>(q, kept));
+        if (ensure_smem((const void*)kernel, smem + kStatic) != cudaSuccess) return TQ_ERR_CUDA;
+        if (clusters_fit((const void*)kernel, size_c, kThreads, smem)) break;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(B * size_c));
     cfg.blockDim = dim3(kThreads);

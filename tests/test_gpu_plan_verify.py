@@ -487,6 +487,23 @@ def test_verify_beside_other_work(lib, B, V):
     del y
 
 
+@pytest.mark.parametrize("B,n,V", [(1, 3, 131070), (2, 40, 150001), (4, 3, 131073)])
+def test_verify_first_call_of_a_size_in_a_graph(lib, B, n, V):
+    """Clusters of 16, whose place on the device is asked for while a graph is captured."""
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    p, q = (torch.softmax(2 * torch.randn((B, n, V), generator=gen, device="cuda"), -1) for _ in range(2))
+    tokens = torch.randint(0, V, (B, n), generator=gen, device="cuda", dtype=torch.int32)
+    parent, u = _int([[-1] + [0] * (n - 1)] * B), torch.rand((B, n), generator=gen, device="cuda")
+    lib.verify_tree(p[:, :, :64].contiguous(), tokens % 64, parent, u)  # (the library is loaded)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = lib.verify_tree(p, tokens, parent, u, q=q)
+    graph.replay()
+    torch.cuda.synchronize()
+    want = lib.verify_tree(p, tokens, parent, u, q=q)
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and bool((got[1] >= 1).all())
+
+
 def test_refusals(lib):
     pool = lib.PagePool(4, 16, 2, 4)
     a = _int([0, 0])
