@@ -647,8 +647,9 @@ size_t tq_latent_attend_tree_workspace_bytes(const tq_latent_pages_t* cache, int
  * [Tkv][64], tokens k_rope_stride apart.  Strides are multiples of 8 elements, pointers 16-byte aligned.  o: device
  * [Tq][H][128] of dt, 32-byte aligned.  A query that sees no key gives zeros; queries from q_starts[B] on are left as they were.
  * What a query does not see never reaches it, whatever it holds; of one that sees a value that is not finite that element is
- * NaN or infinite, and others may be NaN.  Scores, softmax statistics and sums are fp32; softmax weights are rounded to dt.  starts
- * out of order or past Tq or Tkv set TQ_DEVERR_BAD_PAGE and their sequence is left out.  ws: 32-byte aligned device scratch of
+ * NaN or infinite, and others may be NaN.  Scores, softmax statistics and sums are fp32; softmax weights are rounded to dt.  A
+ * sequence whose starts are out of order or past Tq or Tkv sets TQ_DEVERR_BAD_PAGE and is left out, and so is one whose queries begin
+ * below an earlier start: no two sequences have a row in common.  ws: 32-byte aligned device scratch of
  * tq_latent_attend_prompt_workspace_bytes(...) bytes (a counter, set to 0 by the call, or partial results); calls that may run at
  * the same time must not share it.  TQ_ERR_UNSUPPORTED for more tiles of 256 rows over all heads than 2^30.  A bounded wait that ran out sets
  * TQ_DEVERR_TIMEOUT; o is then incomplete. */

@@ -70,6 +70,28 @@ TQ_DEVFN Span span(const PromptArgs& a, int b) {
     s.tiles = s.bad ? 0 : (s.q1 - s.q0 + kTile - 1) / kTile;
     return s;
 }
+// What f is to make of every sequence, 32 at a time, until it returns true (all by one warp; f has the span of sequence b + lane).
+// `torn`: some starts are out of order.  A sequence whose queries begin below an earlier start is then left out as well, or
+// sequences would lie on one another: rows written by two jobs, and more tiles than the host has counted.
+template <class F>
+TQ_DEVFN void each_span(const PromptArgs& a, bool torn, F&& f) {
+    const int lane = threadIdx.x & 31;
+    int top = 0;  // highest start so far, of those within the array
+    for (int b = 0; b < a.B; b += 32) {
+        Span s = span(a, b + lane);
+        if (torn) {
+            int upto = max(top, b + lane < a.B && s.q0 <= a.Tq ? s.q0 : 0);
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int x = __shfl_up_sync(kFull, upto, m);
+                if (lane >= m) upto = max(upto, x);
+            }
+            if (b + lane < a.B && s.q0 < upto) s.bad = true, s.tiles = 0;
+            top = __shfl_sync(kFull, upto, 31);
+        }
+        if (f(s, b)) return;
+    }
+}
 // Tiles of a sequence that take more than `steps` steps: its last ones.
 TQ_DEVFN int tiles_above(const PromptArgs& a, const Span& s, int steps) {
     if (steps < 0 || !s.tiles) return s.tiles;
@@ -87,18 +109,25 @@ constexpr int kLeast = 4, kParts = 32;  // fewest steps of a part, most parts
 struct Jobs {
     int tiles, most;  // of a head; steps of the longest
     int parts, per;   // into how many parts jobs are cut, of how many steps at most
+    bool torn;        // some sequence is left out
 };
 TQ_DEVFN Jobs count_jobs(const PromptArgs& a, bool report) {  // (one warp)
     int tiles = 0, most = 0;
-    bool bad = false;
-    for (int b = threadIdx.x & 31; b < a.B; b += 32) {
-        const Span s = span(a, b);
+    bool bad = false, torn = false;
+    auto count = [&](const Span& s, int) {
         bad |= s.bad;
         tiles += s.tiles;
         if (s.tiles) most = max(most, (s.k1 - s.k0 + kTok - 1) / kTok);
+        return false;
+    };
+    each_span(a, false, count);
+    if (__any_sync(kFull, bad)) {
+        torn = true;
+        tiles = most = 0;
+        each_span(a, true, count);
+        if (report && bad && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
     }
-    if (report && bad && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
-    Jobs j{(int)__reduce_add_sync(kFull, tiles), (int)__reduce_max_sync(kFull, most), 1, 0};
+    Jobs j{(int)__reduce_add_sync(kFull, tiles), (int)__reduce_max_sync(kFull, most), 1, 0, torn};
     const int64_t all = (int64_t)j.tiles * a.H;
     if (a.part && all > 0) j.parts = (int)max(min((int64_t)(a.ctas / all), (int64_t)min(j.most / kLeast, kParts)), (int64_t)1);
     j.per = (j.most + j.parts - 1) / j.parts;
@@ -118,7 +147,10 @@ TQ_DEVFN Job find_job(const PromptArgs& a, const Jobs& jobs, int64_t at) {  // (
     // the fewest steps s that no more than `rank` tiles pass
     auto above = [&](int steps) {
         int n = 0;
-        for (int b = lane; b < a.B; b += 32) n += tiles_above(a, span(a, b), steps);
+        each_span(a, jobs.torn, [&](const Span& s, int) {
+            n += tiles_above(a, s, steps);
+            return false;
+        });
         return (int)__reduce_add_sync(kFull, n);
     };
     int lo = 0, hi = jobs.most;
@@ -128,8 +160,7 @@ TQ_DEVFN Job find_job(const PromptArgs& a, const Jobs& jobs, int64_t at) {  // (
         else lo = mid + 1;
     }
     rank -= above(lo);  // of the tiles of exactly lo steps, in order
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const Span s = span(a, b0 + lane);
+    each_span(a, jobs.torn, [&](const Span& s, int) {
         const int over = tiles_above(a, s, lo), own = tiles_above(a, s, lo - 1) - over;
         int upto = own;
 #pragma unroll
@@ -147,10 +178,11 @@ TQ_DEVFN Job find_job(const PromptArgs& a, const Jobs& jobs, int64_t at) {  // (
             j.q0 = q0 + tile * kTile;
             j.rows = min(kTile, q1 - j.q0);
             j.at = j.keys - (q1 - q0) + tile * kTile;
-            break;
+            return true;
         }
         rank -= __shfl_sync(kFull, upto, 31);
-    }
+        return false;
+    });
     if (jobs.parts > 1) {  // a part is a job over some of the keys: the rows stand as far before or behind them as they do
         const int from = part * jobs.per * kTok;
         j.cut = true;

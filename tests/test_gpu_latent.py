@@ -475,6 +475,33 @@ def test_expanded_rows_behind_the_last_sequence_and_bad_starts(lib):
     assert torch.equal(o[:100], want[:100]) and lib.check_error(err) == 8
 
 
+@pytest.mark.parametrize("H", [2, 64])
+@pytest.mark.parametrize("starts,kept", [
+    ([0, 500, 100, 600], [0]),  # the third begins within the first
+    ([0, 1 << 30, 300, 600], [2]), ([0, -7, 300, 600], [2]),  # one start alone is wrong
+    ([0, 600] * 12, [0]),  # far more tiles than there are rows, were they all taken
+    ([0] * 40 + [300, 299, 300, 600], [39, 42]),  # the last begins where an earlier one ends
+    ([0, 200, 1 << 30, 100, 600], [0]), ([100, 50, 600, 50, 600], [])])
+def test_expanded_sequences_that_would_overlap_are_left_out(lib, H, starts, kept):
+    """Starts that fall and rise again: the sequences before the fall as they are alone, and nothing written over them."""
+    q, kv, kr, _, _ = _prompts([600], [600], H, "bfloat16", 17)
+    k, v, B = kv[..., :128], kv[..., 128:], len(starts) - 1
+    keys = np.minimum(np.arange(B + 1) * 15, 600)
+    if B < 8:
+        keys = np.linspace(0, 600, B + 1).astype(int)
+    fits = [b for b in range(B) if 0 <= starts[b] <= starts[b + 1] <= 600
+            and all(not 0 <= x <= 600 or x <= starts[b] for x in starts[:b])]
+    assert [b for b in fits if starts[b + 1] > starts[b]] == kept
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = lib.latent_attend_prompt(q, k, v, kr, _int(starts), _int(keys), SCALE, err=err)
+    assert lib.check_error(err) == 8
+    for b in fits:
+        q0, q1, k0, k1 = starts[b], starts[b + 1], keys[b], keys[b + 1]
+        if q1 > q0:
+            alone = lib.latent_attend_prompt(q[q0:q1], k[k0:k1], v[k0:k1], kr[k0:k1], _int([0, q1 - q0]), _int([0, k1 - k0]), SCALE)
+            assert torch.equal(o[q0:q1], alone)
+
+
 def test_expanded_in_a_graph_and_on_another_stream(lib):
     q, kv, kr, qs, ks = _prompts([100, 160], [100, 300], 2, "bfloat16", 11)
     k, v, dq, dk = kv[..., :128], kv[..., 128:], _int(qs), _int(ks)
