@@ -645,11 +645,12 @@ size_t tq_latent_attend_tree_workspace_bytes(const tq_latent_pages_t* cache, int
  * q: device [Tq][H][192] of dt (BF16 or F16), tokens q_stride elements apart, heads 192; k, v: device [Tkv][H][128], tokens
  * kv_stride and heads kv_head_stride elements apart (the expansion's own output [Tkv][H][256] serves as both); k_rope: device
  * [Tkv][64], tokens k_rope_stride apart.  Strides are multiples of 8 elements, pointers 16-byte aligned.  o: device
- * [Tq][H][128] of dt, 32-byte aligned.  A query that sees no key gives zeros; queries from q_starts[B] on are left as they were.
+ * [Tq][H][128] of dt, 32-byte aligned.  A query that sees no key gives zeros, and so does one that belongs to no
+ * sequence: from q_starts[B] on, before q_starts[0], of a sequence that is left out (nothing is written where B is 0).
  * What a query does not see never reaches it, whatever it holds; of one that sees a value that is not finite that element is
  * NaN or infinite, and others may be NaN.  Scores, softmax statistics and sums are fp32; softmax weights are rounded to dt.  A
- * sequence whose starts are out of order or past Tq or Tkv sets TQ_DEVERR_BAD_PAGE and is left out, and so is one whose queries begin
- * below an earlier start: no two sequences have a row in common.  ws: 32-byte aligned device scratch of
+ * sequence whose starts are out of order or past Tq or Tkv sets TQ_DEVERR_BAD_PAGE and is left out, and so is one whose queries
+ * begin below an earlier start: no two sequences have a row in common.  ws: 32-byte aligned device scratch of
  * tq_latent_attend_prompt_workspace_bytes(...) bytes (a counter, set to 0 by the call, or partial results); calls that may run at
  * the same time must not share it.  TQ_ERR_UNSUPPORTED for more tiles of 256 rows over all heads than 2^30.  A bounded wait that ran out sets
  * TQ_DEVERR_TIMEOUT; o is then incomplete. */

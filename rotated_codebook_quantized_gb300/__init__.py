@@ -1167,7 +1167,8 @@ def latent_attend_prompt(q, k, v, k_rope, q_starts, kv_starts, scale: float, cau
 
     q [Tq, H, 192] (the last 64 with rotary positions), k and v [Tkv, H, 128] (the two halves of one expansion [Tkv, H, 256] are
     fine), k_rope [Tkv, 64] for all heads, bf16 or f16; q_starts, kv_starts: int32 [B + 1], sequence b's queries and keys.  Its
-    last query stands at its last key; a query sees the keys up to its own place (causal=False: all).  Returns [Tq, H, 128]."""
+    last query stands at its last key; a query sees the keys up to its own place (causal=False: all).  Returns [Tq, H, 128]; queries of
+    no sequence (behind the last one, or of starts that are out of order, which err reports) give zeros."""
     torch, dev = _torch(), q.get_device()
     Tq, H, qs = _heads(q, "q", 192)
     if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (H, 128):
@@ -1186,7 +1187,7 @@ def latent_attend_prompt(q, k, v, k_rope, q_starts, kv_starts, scale: float, cau
     qp, kp = _ints(q_starts, "q_starts", B + 1, dev), _ints(kv_starts, "kv_starts", B + 1, dev)
     hs = k.stride(1) if H > 1 else 128
     ks = k.stride(0) if Tkv > 1 else max(k.stride(0), (H - 1) * hs + 128)
-    o = torch.empty((Tq, H, 128), dtype=q.dtype, device=q.device)
+    o = (torch.empty if B else torch.zeros)((Tq, H, 128), dtype=q.dtype, device=q.device)
     nb = int(load().tq_latent_attend_prompt_workspace_bytes(B, H, Tq, Tkv))
     if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
         raise ValueError("ws must be contiguous, on q's device")

@@ -110,24 +110,28 @@ struct Jobs {
     int tiles, most;  // of a head; steps of the longest
     int parts, per;   // into how many parts jobs are cut, of how many steps at most
     bool torn;        // some sequence is left out
+    int64_t rows;     // of the sequences that are not
 };
 TQ_DEVFN Jobs count_jobs(const PromptArgs& a, bool report) {  // (one warp)
     int tiles = 0, most = 0;
+    unsigned rows = 0;
     bool bad = false, torn = false;
     auto count = [&](const Span& s, int) {
         bad |= s.bad;
         tiles += s.tiles;
+        if (s.tiles) rows += s.q1 - s.q0;
         if (s.tiles) most = max(most, (s.k1 - s.k0 + kTok - 1) / kTok);
         return false;
     };
     each_span(a, false, count);
     if (__any_sync(kFull, bad)) {
         torn = true;
-        tiles = most = 0;
+        tiles = most = rows = 0;
         each_span(a, true, count);
         if (report && bad && a.err) atomicOr(a.err, TQ_DEVERR_BAD_PAGE);
     }
-    Jobs j{(int)__reduce_add_sync(kFull, tiles), (int)__reduce_max_sync(kFull, most), 1, 0, torn};
+    Jobs j{(int)__reduce_add_sync(kFull, tiles), (int)__reduce_max_sync(kFull, most), 1, 0, torn,
+           __reduce_add_sync(kFull, rows)};
     const int64_t all = (int64_t)j.tiles * a.H;
     if (a.part && all > 0) j.parts = (int)max(min((int64_t)(a.ctas / all), (int64_t)min(j.most / kLeast, kParts)), (int64_t)1);
     j.per = (j.most + j.parts - 1) / j.parts;
@@ -200,6 +204,28 @@ TQ_DEVFN int steps_of(const PromptArgs& a, const Job& j, int t) {
     return last < t * kRows ? 0 : (seen_by(a, j, last) + kTok - 1) / kTok;
 }
 TQ_DEVFN int whole_of(const PromptArgs& a, const Job& j, int t) { return seen_by(a, j, t * kRows) / kTok; }
+
+// Zeros in the rows that belong to no sequence: behind the last one, before the first, and those of sequences that are left out.  A
+// warp of each CTA.
+TQ_DEVFN void clear_rest(const PromptArgs& a, const Jobs& jobs) {
+    if (jobs.rows == a.Tq) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t pieces = (int64_t)a.H * (kHeadValue / 8);  // of 16 bytes, of a row
+    auto clear = [&](int64_t from, int64_t to) {
+        for (int64_t i = from * pieces + blockIdx.x * 32 + lane; i < to * pieces; i += gridDim.x * 32)
+            *reinterpret_cast<uint4*>(a.o + i * 8) = make_uint4(0u, 0u, 0u, 0u);
+    };
+    int end = 0;  // of the sequence before
+    each_span(a, jobs.torn, [&](const Span& s, int) {
+        for (unsigned own = __ballot_sync(kFull, s.tiles > 0); own; own &= own - 1) {
+            const int src = __ffs(own) - 1, q0 = __shfl_sync(kFull, s.q0, src);
+            clear(end, q0);
+            end = __shfl_sync(kFull, s.q1, src);
+        }
+        return false;
+    });
+    clear(end, a.Tq);
+}
 
 struct Control {
     uint64_t q_full[kStreams], q_empty[kStreams], k_full[2], v_full[2], k_empty[2], v_empty[2], guarded[2];  // [2]: even, odd steps
@@ -358,6 +384,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             if (q_done[t]) mbar_wait_drain(c.q_full + t, (q_done[t] - 1) & 1);
         for (uint32_t i = k_done < 2 ? 0 : k_done - 2; i < k_done; ++i) mbar_wait_drain(c.k_full + (i & 1), (i >> 1) & 1);
         for (uint32_t i = v_done < 2 ? 0 : v_done - 2; i < v_done; ++i) mbar_wait_drain(c.v_full + (i & 1), (i >> 1) & 1);
+        clear_rest(a, jobs);
     } else if (warp == kMma) {
         // ------------------------------------------------------------ MMA issue
         if (elected()) {

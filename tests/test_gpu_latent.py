@@ -502,6 +502,47 @@ def test_expanded_sequences_that_would_overlap_are_left_out(lib, H, starts, kept
             assert torch.equal(o[q0:q1], alone)
 
 
+def _soil(shape, dtype):
+    """Memory that the next result of this shape is likely to lie in, full of NaN."""
+    torch.cuda.synchronize()
+    torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("ql,starts,H,kl", [
+    ([200, 100], [0, 200, 250], 2, [200, 50]),  # 50 rows behind the last sequence
+    ([200, 100], [70, 200, 300], 3, [130, 100]),  # 70 before the first
+    ([600], [0, 500, 100, 600], 64, [200, 0, 300]), ([600], [0, 1 << 30, 300, 600], 2, [100, 100, 300]),  # left out
+    ([4000], [0, 40], 16, [40]), ([300], [0, 20, 20, 20], 1, [2000, 0, 0]), ([3000], [3000, 0], 2, [100]),
+    ([100], [0], 4, []), ([70], [0] * 71, 2, [1] * 70)])
+def test_expanded_rows_of_no_sequence_are_zeros(lib, dtype, ql, starts, H, kl):
+    q, kv, kr, _, ks = _prompts(ql, kl or [10], H, dtype, 18, sum(ql))
+    ks = ks if kl else np.zeros(1, dtype=int)
+    _soil((sum(ql), H, 128), q.dtype)
+    o = lib.latent_attend_prompt(q, kv[..., :128], kv[..., 128:], kr, _int(starts), _int(ks), SCALE)
+    assert not bool(o.isnan().any())
+    rest = torch.ones(sum(ql), dtype=torch.bool, device="cuda")
+    for b in range(len(starts) - 1):
+        if starts[b] <= starts[b + 1] <= len(q) and max((x for x in starts[:b] if x <= len(q)), default=0) <= starts[b]:
+            rest[starts[b]:starts[b + 1]] = False
+            if starts[b + 1] > starts[b] and kl[b]:
+                one = lib.latent_attend_prompt(q[starts[b]:starts[b + 1]], kv[ks[b]:ks[b + 1], :, :128], kv[ks[b]:ks[b + 1], :, 128:],
+                                               kr[ks[b]:ks[b + 1]], _int([0, starts[b + 1] - starts[b]]), _int([0, kl[b]]), SCALE)
+                assert torch.equal(o[starts[b]:starts[b + 1]], one)
+    assert bool(rest.any()) and not bool(o[rest].any())
+
+
+def test_a_plan_and_its_prompts_leave_no_old_memory(lib):
+    """Prompts planned into more packed places than they fill: the attention gives zeros in the places behind the last token."""
+    pool = lib.PagePool(20, 16, 2, 8)
+    plan = lib.kv_plan(pool, _int([0, 0]), _int([30, 21]), tokens=64)
+    q, kv, kr, _, _ = _prompts([64], [64], 2, "bfloat16", 19)
+    _soil((64, 2, 128), q.dtype)
+    o = lib.latent_attend_prompt(q, kv[..., :128], kv[..., 128:], kr, plan.starts, plan.starts, SCALE)
+    assert not bool(o[51:].any()) and bool(o[:51].isfinite().all()) and bool(o[:51].any(-1).all())
+
+
 def test_expanded_in_a_graph_and_on_another_stream(lib):
     q, kv, kr, qs, ks = _prompts([100, 160], [100, 300], 2, "bfloat16", 11)
     k, v, dq, dk = kv[..., :128], kv[..., 128:], _int(qs), _int(ks)
