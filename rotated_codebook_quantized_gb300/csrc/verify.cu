@@ -4,7 +4,7 @@
 // start) is the sum R of the residual r after each rejection: one pass over the vocabulary, a part of it to each CTA, whose r stays in
 // shared memory for the next pass and for the search.  The walk itself is a few hundred instructions that every thread repeats, so
 // it needs no exchange.
-// All of r and R are integers, in steps of 2^-50, and tests compare products of 112 bits: sums are exact, in any order, so
+// All of r and R are integers, in steps of 2^-50, and tests and the search compare products of 112 and 88 bits: sums are exact, in any order, so
 // that neither the split over CTAs nor the number of warps can change the sampled token.  (Sums in fp64 would be off by
 // little, but this GPU adds two of them a clock and SM.)
 // Bound by the latency of the chain: tokens, their probabilities (launch and walk 4 us), a pass and the search (1.5 to 3 us), and 3.7 us
@@ -82,6 +82,17 @@ TQ_DEVFN bool below(float u, float q, u64 R, u64 r) {
     if (s > 64 && r >> (128 - s)) return true;  // r 2^s has more than 128 bits
     const u64 rh = s >= 64 ? r << (s - 64) : r >> (64 - s), rl = s >= 64 ? 0 : r << s;
     return high < rh || (high == rh && low < rl);
+}
+
+// u R without its fraction, exactly, for 0 <= u < 1 (R - 1 above, 0 below and for a NaN): an integer P passes u R where it is larger.
+TQ_DEVFN u64 share(float u, u64 R) {
+    if (!(u > 0.f)) return 0;
+    if (u >= 1.f) return R - 1;
+    const uint32_t b = __float_as_uint(u);
+    const int e = b >> 23, s = 150 - max(e, 1);  // u = m 2^-s, s 24 at least
+    const u64 m = (b & 0x7fffffu) | (e ? 0x800000u : 0u), high = __umul64hi(m, R), low = m * R;
+    if (s >= 64) return s >= 128 ? 0 : high >> (s - 64);
+    return high << (64 - s) | low >> s;
 }
 
 TQ_DEVFN uint32_t cluster_rank() {
@@ -311,8 +322,7 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(const __grid_cons
     }
     if (used && R && warp == 0) {
         // the first token whose prefix sum passes u R: in this CTA where the threshold falls into its part
-        const double want = (double)s_u[0] * (double)R;
-        const u64 t = want > 0 ? min((u64)fmin(want, 9.0e18), R - 1) : 0;
+        const u64 t = share(s_u[0], R);
         if (t >= before && t - before < mine) {
             u64 left = t - before;  // prefix sums within this CTA must pass it
             int run = 0;

@@ -392,6 +392,51 @@ def test_verify_edges(lib):
     assert path.tolist() == [[-1, -1, -1]] and count.tolist() == [0] and token.tolist() == [-1]
 
 
+def _split(x):
+    """The whole number x (steps of 2^-50) as fp32 values that add up to it: 24 bits each."""
+    out = []
+    while x:
+        top = x >> max(x.bit_length() - 24, 0) << max(x.bit_length() - 24, 0)
+        out.append(top * 2.0 ** -50)
+        x -= top
+    return out
+
+
+@pytest.mark.parametrize("V", [40, 100003])
+def test_verify_thresholds_to_the_last_step(lib, V):
+    """Prefix sums at u R itself, one step of 2^-50 below and above it: u R has 74 bits, of which none is rounded."""
+    g = _rng(20, V)
+    rows, us, want = [], [], []
+    ends = [1 - 2.0 ** -24, 2.0 ** -24, 0.5, 2.0 ** -50, 2.0 ** -60, 2.0 ** -149, 0.75, 1 - 3 * 2.0 ** -24]
+    for i in range(64):
+        u = float(np.float32(ends[i] if i < len(ends) else g.random()))
+        total = (1 << 50) + (1, 0, -1, int(g.integers(-(1 << 30), 1 << 30)))[i % 4]
+        at = Fraction(u) * total
+        edge = at.numerator // at.denominator + (0, 1, 2)[i % 3]  # the first tokens' sum: at u R or below it, just above it, beyond
+        first = _split(edge)
+        rest = _split(total - edge)
+        row = np.zeros(V, dtype=np.float32)
+        row[:len(first)] = first
+        row[V - len(rest):] = rest
+        exact = [Fraction(float(x)) for x in np.concatenate([row[:20], row[V - 20:]])]  # (zeros between)
+        assert sum(exact) == Fraction(total, 1 << 50) and len(first) < 20 and len(rest) < 20
+        exact = [min(x, Fraction(1)) for x in exact]  # (as the definition has it: of a total above 1 the first entry may be)
+        cum, token = Fraction(0), None
+        for t, x in enumerate(exact):
+            cum += x
+            if token is None and cum > Fraction(u) * sum(exact):
+                token = t if t < 20 else V - 40 + t
+        rows.append(row)
+        us.append(u)
+        want.append(token)
+    p = torch.tensor(np.stack(rows)[:, None], device="cuda")
+    u = torch.tensor(us, dtype=torch.float32, device="cuda")[:, None]
+    zero = _int(np.zeros((64, 1)))
+    assert lib.verify_tree(p, zero, zero - 1, u)[2].tolist() == want
+    for b in (0, 1, 5):  # alone: other clusters
+        assert lib.verify_tree(p[b:b + 1], zero[:1], zero[:1] - 1, u[b:b + 1])[2].tolist() == want[b:b + 1]
+
+
 def test_verify_rows_that_are_no_distributions(lib):
     """Sums past 64 bits and others: some token of the vocabulary, or -1."""
     for x, V in ((1.0, 1 << 17), (3.0, 20000), (0.01, 50000), (float("inf"), 1000)):
