@@ -580,7 +580,10 @@ tq_status tq_kv_plan(const tq_page_pool_t* pool, const int32_t* lens, const int3
  * Node 0 of a tree is its root, a token already accepted; node i >= 1 has token tokens[b*n + i] and parent parent[b*n + i] < i.
  * p: device [B][n][V] of dt (f32, bf16 or f16), node (b, i) at (b*n + i)*p_stride: the target's distribution after node i.  q: the
  * same of the distribution that the children of node i were drawn from, or NULL: then they were chosen, not drawn.  u: device
- * f32 [B][n], uniform in [0, 1).
+ * f32 [B][n], uniform in [0, 1).  With q the children of a node are independent draws from its row, with replacement (one token may
+ * come twice): for those alone r - R q is what is left to be sampled.  Children drawn without replacement, each from q without the
+ * tokens before it, or a q that was filtered after the draw, make the tokens that come out follow another distribution, which no call
+ * can notice; children that are fixed by q (its likeliest tokens) are chosen, q NULL.
  * The walk: node = 0, r = p[node], R = 1; for each child c of node, in order,
  *   accepted if u[c] q[node](x) R < r(x) (x its token; q(x) = 1 without q): node = c, r = p[c], R = 1;
  *   else r = max(r - R q[node], 0) (without q: r(x) = 0), R = its sum (without q: R less the old r(x)).

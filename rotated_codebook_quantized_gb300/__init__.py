@@ -1019,7 +1019,8 @@ def verify_tree(p, tokens, parent, u, q=None, n_tok=None, err=None):
     """Verifies drafted trees against the target's probabilities p [B, n, V] (f32, bf16 or f16) from uniform numbers u f32 [B, n].
 
     Node 0 of a tree is its root; node i has tokens[b, i], parent[b, i] < i (int32 [B, n]).  q [B, n, V]: the distributions that each
-    node's children were drawn from (None: they were chosen, not drawn).  n_tok: int32 [B] nodes in use.
+    node's children were drawn from, independently of one another and with replacement (else the tokens do not follow the target, without
+    an error); None: they were chosen, as a draft's likeliest tokens are, not drawn.  n_tok: int32 [B] nodes in use.
     Returns (path int32 [B, n]: the accepted nodes in order, then -1; count int32 [B]; next int32 [B]: the token after them)."""
     if p.dim() != 3:
         raise ValueError("p must be [B, n, V]")

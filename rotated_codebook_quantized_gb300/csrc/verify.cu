@@ -2,7 +2,8 @@
 //
 // A cluster of CTAs walks one tree.  What a node's test needs besides its token's two probabilities (gathered for all nodes at the
 // start) is the sum R of the residual r after each rejection: one pass over the vocabulary, a part of it to each CTA, whose r stays in
-// shared memory for the next pass and for the search.  The walk itself is a few hundred instructions that every thread repeats, so
+// shared memory for the next pass and for the search.  (r - R q is the rest of the target for children drawn independently, with
+// replacement, or for a single one.)  The walk itself is a few hundred instructions that every thread repeats, so
 // it needs no exchange.
 // All of r and R are integers, in steps of 2^-50, and tests and the search compare products of 112 and 88 bits: sums are exact, in any order, so
 // that neither the split over CTAs nor the number of warps can change the sampled token.  (Sums in fp64 would be off by
