@@ -91,6 +91,56 @@ def test_append_matches_the_definition(lib, dtype, kept, T, page, layout, rotary
     assert lib.check_error(err) == (8 if T > 2 else 0)
 
 
+@pytest.mark.parametrize("factor", [1.25, 0.5])
+@pytest.mark.parametrize("layout,rotary", [("half", 64), ("interleaved", 64), ("interleaved", 24), ("half", 40)])
+def test_append_with_a_rotary_factor(lib, layout, rotary, factor):
+    """The factor of scaled frequencies: on the rotated part alone."""
+    T, page, gen = 300, 32, _gen(23, rotary)
+    x = torch.randn((T, W), generator=gen, device="cuda")
+    pos = torch.randint(0, 1 << 18, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    rope = lib.Rope(R, rotary, base=50000.0, layout=layout)
+    rope.factor = factor
+    cache = lib.LatentCache(10, page, dtype=torch.float16)
+    lib.latent_append(cache, x[:, :C], x[:, C:], _int(np.arange(T)), rope=rope, positions=pos)
+    got = cache.rows.view(-1, W)[:T].double()
+    k = x[:, C:].double()
+    slack = torch.zeros_like(k)
+    slack[:, :rotary] = 4e-7 * 1.42 * factor * k.abs().amax(1, keepdim=True)
+    want = torch.cat([x[:, :C].double(), _turn(k, pos, 50000.0 ** (-np.arange(0, rotary, 2) / rotary), rotary, layout, factor)], 1)
+    bound = _half_step(torch.float16) * want.abs() * 1.001 + 2.0 ** -25
+    bound[:, C:] += slack
+    assert bool(((got - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("page,stride", [(16, 17), (64, 100), (32, 32 * 3)])
+def test_pages_further_apart_than_they_are_long(lib, page, stride):
+    """Pages inside larger blocks, as the C call takes them: written and attended like pages that follow one another, what lies between
+    them neither read nor written."""
+    import ctypes
+
+    g, gen, pages, lens, H, n = _rng(24, page), _gen(25, page), 40, [150, 3], 16, 2
+    dt = torch.bfloat16
+    close = lib.LatentCache(pages, page, dtype=dt)
+    wide = torch.full((pages, stride, W), float("nan"), dtype=dt, device="cuda")
+    wide[:, :page] = 0
+    apart = lib.tq_latent_pages_t(wide.data_ptr(), lib.TQ_BF16, C, R, page, pages, stride)
+    table = g.permutation(pages)[:20].reshape(2, 10)
+    slots = np.concatenate([[table[b, t // page] * page + t % page for t in range(lens[b])] for b in range(2)])
+    x = torch.randn((len(slots), W), generator=gen, device="cuda").to(dt)
+    lib.latent_append(close, x[:, :C], x[:, C:], _int(slots))
+    stream, at = torch.cuda.current_stream().cuda_stream, _int(slots)
+    assert lib.load().tq_latent_append(ctypes.byref(apart), x.data_ptr(), W, x.data_ptr() + 2 * C, W, lib.TQ_BF16, len(slots),
+                                       at.data_ptr(), None, 0, 0, stream) == 0
+    assert torch.equal(wide[:, :page], close.rows) and bool(wide[:, page:].isnan().all())
+    q, fresh = (torch.randn(s, generator=gen, device="cuda").to(dt) for s in ((2, n, H, W), (2, n, W)))
+    want = lib.latent_attend_tree(close, q, _int(table), _int(lens), SCALE, new=fresh)
+    nb = lib.load().tq_latent_attend_tree_workspace_bytes(ctypes.byref(apart), 2, n, H, 10 * page)
+    ws, o, tab, ln = torch.empty(nb, dtype=torch.uint8, device="cuda"), torch.empty_like(want), _int(table), _int(lens)
+    assert lib.load().tq_latent_attend_tree(ctypes.byref(apart), q.data_ptr(), H * W, 2, n, H, tab.data_ptr(), 10, ln.data_ptr(),
+                                            10 * page, fresh.data_ptr(), W, 0, 0, SCALE, o.data_ptr(), ws.data_ptr(), nb, 0, stream) == 0
+    assert torch.equal(o, want)
+
+
 # ---------------------------------------------------------------- absorbed
 
 def _bound(o, A, d, n, top, dtype):

@@ -392,6 +392,82 @@ def test_verify_edges(lib):
     assert path.tolist() == [[-1, -1, -1]] and count.tolist() == [0] and token.tolist() == [-1]
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("case", ["apart", "alike", "chosen"])
+def test_verify_residuals_computed_anew(lib, dtype, case):
+    """80 trees over 131072 tokens: parts too long for shared memory, so that each pass and the search go over the rows and all the
+    node's rejections again.  Sums are exact, so one tree alone (whose residual is kept) gives the same.  "alike": next to nothing is
+    left after a rejection, so the residual's steps are made finer, again and again."""
+    B, n, V = 80, 7, 131072
+    dt = getattr(torch, dtype)
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    q = torch.softmax(2 * torch.randn((B, n, V), generator=gen, device="cuda"), -1)
+    if case == "alike":
+        p = q * (1 + 2.0 ** -18 * torch.randn((B, n, V), generator=gen, device="cuda")) if dtype == "float32" else q.clone()
+        if dtype != "float32":  # a handful of entries apart, a step of the type each
+            p[:, :, ::9973] *= 1 + 2.0 ** -6
+            p[:, :, 5::9973] *= 1 - 2.0 ** -6
+    else:
+        p = torch.softmax(2 * torch.randn((B, n, V), generator=gen, device="cuda"), -1)
+    p, q = p.to(dt), q.to(dt)
+    tokens = (q[:, 0].float() - p[:, 0].float()).argsort(1, descending=True)[:, :n].int()  # offered too often: rejected at u near 1
+    u = torch.rand((B, n), generator=gen, device="cuda")
+    u[:, 1:4] = 1 - 2.0 ** -24
+    parent = _int([[-1, 0, 0, 0, 0, 4, 4]] * B)
+    kw = {} if case == "chosen" else dict(q=q)
+    got = lib.verify_tree(p, tokens.contiguous(), parent, u, **kw)
+    for b in range(0, B, 7):
+        kw = {} if case == "chosen" else dict(q=q[b:b + 1])
+        one = lib.verify_tree(p[b:b + 1], tokens[b:b + 1].contiguous(), parent[:1], u[b:b + 1], **kw)
+        assert all(torch.equal(x[b:b + 1], y) for x, y in zip(got, one))
+    if case != "apart" or dtype != "float32":
+        return
+    # two rejections and more in 64 bits, for the trees whose other children were rejected as well: steps of 2^-51 over 2^17 entries,
+    # three times, and fp64 sums: thresholds nearer than 2^-30 are taken either way
+    rows = torch.arange(B, device="cuda")
+    out = (got[1] == 1).nonzero().flatten()
+    assert len(out) >= 10
+    P, Q = p[out, 0].double(), q[out, 0].double()
+    r, R = P, torch.ones(len(out), 1, dtype=torch.float64, device="cuda")
+    for _ in range(4):
+        r = torch.clamp(r - R * Q, min=0)
+        R = r.sum(1, keepdim=True)
+    cum, t = r.cumsum(1), got[2][out].long()
+    rows = torch.arange(len(out), device="cuda")
+    at = u[out, 0].double() * cum[:, -1]
+    assert bool((cum[rows, t] > at - 2.0 ** -30).all()) and bool((cum[rows, t] - r[rows, t] <= at + 2.0 ** -30).all())
+
+
+@pytest.mark.parametrize("V", [37, 300])
+def test_verify_next_to_nothing_left(lib, V):
+    """Targets that differ from the proposal by some 2^-18 of a probability: a rejection leaves less than 2^-16, whose steps are made
+    finer before the next test.  Against the walk in rational arithmetic."""
+    g = _rng(22, V)
+    B, n = 40, 6
+    q = _probabilities(g, (B, n, V), torch.float32, peak=0.5)
+    p = (q.double() * (1 + 2.0 ** -17 * torch.tensor(g.normal(size=(B, n, V))))).float()
+    parent = np.array([[-1] + [0] * (n - 1)] * B)
+    tokens = g.integers(0, V, (B, n))
+    u, want, deep = np.zeros((B, n), dtype=np.float32), [], 0
+    for b in range(B):
+        tokens[b, 1] = int((q[b, 0] - p[b, 0]).argmax())
+        P, Q = _exact_rows(p[b]), _exact_rows(q[b])
+        left = sum(max(x - y, Fraction(0)) for x, y in zip(P[0], Q[0]))
+        assert 0 < left < Fraction(1, 1 << 16)
+        while True:
+            u[b] = g.random(n).astype(np.float32)
+            u[b, 1] = 1 - 2.0 ** -24
+            path, token, near = _walk(P, Q, tokens[b].tolist(), parent[b].tolist(), u[b].tolist(), n)
+            if near > 2.0 ** -30:
+                break
+        deep += len(path) == 1 or path[1] > 2
+        want.append((path + [-1] * (n - len(path)), len(path), token))
+    assert deep >= B // 4  # two rejections and more
+    path, count, token = lib.verify_tree(p.cuda(), _int(tokens), _int(parent), torch.tensor(u, device="cuda"), q=q.cuda())
+    assert path.tolist() == [w[0] for w in want] and count.tolist() == [w[1] for w in want]
+    assert token.tolist() == [w[2] for w in want]
+
+
 def _split(x):
     """The whole number x (steps of 2^-50) as fp32 values that add up to it: 24 bits each."""
     out = []
