@@ -593,7 +593,8 @@ tq_status tq_kv_plan(const tq_page_pool_t* pool, const int32_t* lens, const int3
  * n_tok: device int32 [B] nodes in use (NULL: n); a tree without any has path -1, count 0 and next -1.  A node whose parent is
  * not below it, or whose token is outside [0, V), is never accepted (TQ_DEVERR_BAD_ID).  Rows are taken as they are: an entry
  * below 0 or NaN counts as 0, above 1 as 1, each in steps of 2^-50; sums are exact integers and comparisons with them
- * exact too, so results do not depend on how the work is split (rows whose sum is 2^14 or more give any token, or -1).  n <= 1024, V <= 2^20.  Rows of a node without children that are in use are not read from q. */
+ * exact too, so results do not depend on how the work is split (rows whose sum is 2^14 or more give any token, or -1).
+ * n <= 1024, V <= 2^20.  Rows of a node without children that are in use are not read from q. */
 tq_status tq_verify_tree(const void* p, int64_t p_stride, const void* q, int64_t q_stride, tq_dtype dt, int32_t B, int32_t n,
                          int32_t V, const int32_t* tokens, const int32_t* parent, const float* u, const int32_t* n_tok,
                          int32_t* path, int32_t* count, int32_t* next, uint32_t* err, void* stream);

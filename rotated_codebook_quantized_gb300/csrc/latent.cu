@@ -50,8 +50,9 @@ struct Eight {
 
 // A warp to a token, a lane to 16 of its latent vector's elements and to a pair of its rotary key's, so that every lane has one sine and
 // cosine.  (16-byte pieces dealt to threads one after another left those of the rotary keys, four sines each, to an eighth of
-// them.)  Bound by HBM: 65536 tokens 23 to 24 us, 6.3 to 6.6 TB/s (pieces: 48 us; four tokens to a warp at a time: 23.3, and 10.0 for
-// 8.5 over 32768 tokens).  48 tokens: 1.7 us, the launch.
+// them.)  Bound by HBM: 65536 tokens 27.8 us, 5.5 TB/s, where tokens and rows are others at each call, and 24 us over the same ones again,
+// part of which the L2 cache still holds (there pieces took 48 us; four tokens to a warp at a time 23.3, and 10.0 for 8.5 over 32768
+// tokens).  48 tokens: 1.5 us, the launch.
 template <int DT, bool BF>
 __global__ void __launch_bounds__(256) latent_append_kernel(AppendArgs a) {
     pdl_trigger();

@@ -17,8 +17,8 @@
 // Every wait on an mbarrier is bounded; on expiry the CTA sets TQ_DEVERR_TIMEOUT, drains and frees TMEM.
 //
 // Up to 64 rows a sequence: bound by HBM, 1600 clocks a step of 1575 at the copy rate, and by its beginning and end: 32 ragged sequences
-// of up to 16384 tokens, 64 heads: 68 us, 4.6 TB/s of 6.75 over the whole call; 64 rows over 131072 tokens: 50 us.  More rows: by the
-// products, 1090 of 1360 clocks a step (M = 64 runs at half rate): 512 rows over 65536 tokens, two sequences: 183 us, 795 TFLOP/s.
+// of up to 16384 tokens, 64 heads: 69 us, 4.6 TB/s of 6.75 over the whole call (73 over others at each call); 64 rows over 131072
+// tokens: 50 us.  More rows: by the products, 1090 of 1360 clocks a step (M = 64 runs at half rate): 512 rows over 65536 tokens, two sequences: 182 us, 800 TFLOP/s.
 #include <math.h>
 
 #include <algorithm>

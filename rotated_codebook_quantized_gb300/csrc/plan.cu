@@ -3,7 +3,8 @@
 // One CTA moves the pages: prefix sums over the sequences (pages given, pages taken, tokens) fix every place on the stack, in the
 // tables and among the packed tokens, so nothing depends on the order of threads.  Slots and positions come from a second launch
 // over the whole GPU (from the same CTA: 11.1 us for 64 sequences planned and undone, 8.7 with it; 38 and 12 for 1000 of 16 tokens).
-// Bound by latency: a chain of dependent loads (lengths, pages held, the stack, the tables), 4.5 us a call.
+// Bound by latency: a chain of dependent loads (lengths, pages held, the stack, the tables), 4.5 us a call.  A sequence's padded row is
+// one warp's: 65536 tokens of one sequence planned and undone 223 us, packed (a search of each token's sequence) 11 us.
 #include <algorithm>
 
 #include "common.cuh"

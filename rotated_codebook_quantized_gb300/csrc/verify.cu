@@ -395,7 +395,8 @@ extern "C" tq_status tq_verify_tree(const void* p, int64_t p_stride, const void*
     VerifyArgs a{p, q, p_stride, q ? q_stride : 0, tokens, parent, u, n_tok, path, count, next, err, n, V, 0};
     const int runs = (V + kRun - 1) / kRun;
     // Each tree over several CTAs, since it waits for the slowest of its passes: as many as four to an SM make, each with a run for
-    // every warp (48 trees over 50001 tokens: 35 us with eight to a tree, 41 with four); sixteen where the trees are few (one tree,
+    // every warp (48 trees over 50001 tokens: 35 us with eight to a tree, 41 with four, although two of 64 registers by 512 threads are
+    // resident on an SM, so that 384 CTAs come in two waves); sixteen where the trees are few (one tree,
     // 131072 tokens, five rejections: 23 us for 34; eight trees gain nothing).
     int size_c = 1;
     while (size_c < kCluster && B * size_c * 2 <= (size_c < 8 ? 4 * device_sms() : 64) && runs >= 32 * size_c) size_c *= 2;
